@@ -304,6 +304,87 @@ int moe_q4_0_layer(const float* x, const float* Wr, const q4_0_block* Wg, const 
                    const q4_0_block* Wd, float* out, int T, int H, int I, int E, int topk,
                    int n_shared, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense feed-forward over frozen Q4_0 weights: the gated block, the projection
+ * with the low-rank adapters of many requests, and the gradients with respect
+ * to the activations (the Q4_0 weights themselves are not trained). The tutorials'
+ * decoder layers are built of these linears (the fused matmul of §3.4; the
+ * SiLU-gated feed-forward of the experts, here for one matrix pair and any
+ * number of rows).
+ *
+ * Two forms each, as for the plain products:
+ *   decode (q4_0_glu, q4_0_gemv_lora): fp32 activations, 1 <= M <= Q4_GEMV_MAX_M,
+ *     any K the GEMV takes, fp32 sums and results;
+ *   prompt and gradient (the others): fp16 activations, bf16 gradients, any M;
+ *     K % 64 == 0 and N % 64 == 0. Each dequantized weight is rounded to fp16
+ *     before its product (as in q4_0_gemm), sums are fp32, results are rounded
+ *     once.
+ * fp16 and bf16 arrays, fp32 x of q4_0_gemv_lora: 16-byte aligned; Q4_0
+ * matrices 2-byte, other fp32 and int32 arrays 4-byte. Every matrix, activation
+ * and result array is smaller than 2 GiB. Outputs must not overlap inputs or
+ * one another. A call fails with Q4_EWORKSPACE when ws is smaller than its
+ * *_workspace_bytes.
+ * ------------------------------------------------------------------------- */
+typedef enum q4_act {
+  Q4_ACT_SILU = 0, /* z / (1 + exp(-z)) */
+  Q4_ACT_GELU = 1  /* z / 2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) */
+} q4_act;
+
+/* Gated block, decode: h[M x N] = act(x . deq(Wg)) * (x . deq(Wu)).
+ *   x fp32 [M][K]      Wg, Wu Q4_0 [K][N/32] blocks      h fp32 [M][N]
+ * Both products run in one launch; no sum of either is ever rounded below fp32. */
+size_t q4_0_glu_workspace_bytes(int M, int N, int K);
+int q4_0_glu(const float* x, const q4_0_block* Wg, const q4_0_block* Wu, float* h, int M, int N,
+             int K, int act, void* ws, size_t ws_bytes, void* stream);
+
+/* Gated block, prompt: H = act(g) * u with g = X . deq(Wg), u = X . deq(Wu).
+ *   X fp16 [M][K]      H fp16 [M][N]
+ *   G, U fp16 [M][N]: g and u, for q4_0_glu_backward; both or neither NULL.
+ * H is formed from the fp32 g and u, not from the rounded G and U. */
+size_t q4_0_glu_gemm_workspace_bytes(int M, int N, int K);
+int q4_0_glu_gemm(const uint16_t* X, const q4_0_block* Wg, const q4_0_block* Wu, uint16_t* H,
+                  uint16_t* G, uint16_t* U, int M, int N, int K, int act, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/* Gradient of the gated block with respect to X:
+ *   dX = (dH * U * act'(G)) . deq(Wg)^T + (dH * act(G)) . deq(Wu)^T
+ *   dH bf16 [M][N]     G, U fp16 [M][N] as q4_0_glu_gemm left them
+ *   dX bf16 [M][K], overwritten
+ * The factors of dH are formed in fp32; each row is then scaled by a power of
+ * two to the range of fp16 and rounded, and the product is scaled back, so
+ * gradients need no loss scale. */
+size_t q4_0_glu_backward_workspace_bytes(int M, int N, int K);
+int q4_0_glu_backward(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
+                      const q4_0_block* Wg, const q4_0_block* Wu, uint16_t* dX, int M, int N,
+                      int K, int act, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of Y = X . deq(B) with respect to X: dX = dY . deq(B)^T.
+ *   dY bf16 [M][N]     dX bf16 [M][K], overwritten
+ * Rows are scaled as in q4_0_glu_backward. */
+size_t q4_0_gemm_backward_workspace_bytes(int M, int N, int K);
+int q4_0_gemm_backward(const uint16_t* dY, const q4_0_block* B, uint16_t* dX, int M, int N, int K,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* Projection with low-rank adapters, one of L for each row:
+ *   y[m] = x[m] . deq(B) + scale[i] * (x[m] . A[i]^T) . Bl[i]^T,  i = ids[m]
+ *   A  fp16 [L][R][K]     Bl fp16 [L][N][R]     ids int32 [M]     scale fp32 [L]
+ *   1 <= L, R % 8 == 0, 8 <= R <= Q4_LORA_MAX_R, K % 8 == 0 (decode). An adapter
+ *   of a smaller rank has zeros in its last rows of A or columns of Bl.
+ * Data-dependent rule (not checked on the host): a row whose id is outside
+ * [0, L) has no adapter, its y is x . deq(B). Rows may use any ids in any order.
+ * Decode: x, y fp32, M <= Q4_GEMV_MAX_M. Prompt: X, Y fp16; there the narrow
+ * product is held in fp32 or, for the matrix cores, in fp16 relative to its
+ * row's largest value. */
+#define Q4_LORA_MAX_R 128
+size_t q4_0_gemv_lora_workspace_bytes(int M, int N, int K, int R);
+int q4_0_gemv_lora(const float* x, const q4_0_block* B, const uint16_t* A, const uint16_t* Bl,
+                   const int32_t* ids, const float* scale, float* y, int M, int N, int K, int R,
+                   int L, void* ws, size_t ws_bytes, void* stream);
+size_t q4_0_gemm_lora_workspace_bytes(int M, int N, int K, int R);
+int q4_0_gemm_lora(const uint16_t* X, const q4_0_block* B, const uint16_t* A, const uint16_t* Bl,
+                   const int32_t* ids, const float* scale, uint16_t* Y, int M, int N, int K,
+                   int R, int L, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

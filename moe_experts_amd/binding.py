@@ -69,6 +69,23 @@ _lib.moe_q4_0_route_layout.argtypes = [_I, _I, _I, _I, _I, ctypes.POINTER(_Z), c
 _lib.moe_q4_0_prefill_route_layout.restype = _I
 _lib.moe_q4_0_prefill_route_layout.argtypes = [_I, _I, _I, _I, _I] + [ctypes.POINTER(_Z)] * 4
 
+for _name, _ints in (("q4_0_glu", 3), ("q4_0_glu_gemm", 3), ("q4_0_glu_backward", 3),
+                     ("q4_0_gemm_backward", 3), ("q4_0_gemv_lora", 4), ("q4_0_gemm_lora", 4)):
+    _f = getattr(_lib, _name + "_workspace_bytes")
+    _f.restype = _Z
+    _f.argtypes = [_I] * _ints
+_lib.q4_0_glu.restype = _I
+_lib.q4_0_glu.argtypes = [_P] * 4 + [_I] * 4 + [_P, _Z, _P]
+_lib.q4_0_glu_gemm.restype = _I
+_lib.q4_0_glu_gemm.argtypes = [_P] * 6 + [_I] * 4 + [_P, _Z, _P]
+_lib.q4_0_glu_backward.restype = _I
+_lib.q4_0_glu_backward.argtypes = [_P] * 6 + [_I] * 4 + [_P, _Z, _P]
+_lib.q4_0_gemm_backward.restype = _I
+_lib.q4_0_gemm_backward.argtypes = [_P] * 3 + [_I] * 3 + [_P, _Z, _P]
+for _f in (_lib.q4_0_gemv_lora, _lib.q4_0_gemm_lora):
+    _f.restype = _I
+    _f.argtypes = [_P] * 7 + [_I] * 5 + [_P, _Z, _P]
+
 BLOCK_BYTES = 18
 Q8_BLOCK_BYTES = 34
 
@@ -352,3 +369,195 @@ def moe_q4_0_prefill(x16: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: 
     _check(_lib.moe_q4_0_prefill(px, pg, pu, pd, pi, pw_, po, T, H, I, E, topk, pws, nws,
                                  _stream(x16.device)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Dense feed-forward over frozen Q4_0 weights
+# ---------------------------------------------------------------------------
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)} (got {act!r})")
+    return ACTIVATIONS[act]
+
+
+def _on(device, **tensors):
+    """Every tensor given is on `device` (the stream is that device's)."""
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _columns(N: int, block: int):
+    if N <= 0 or N % block:
+        raise ValueError(f"N must be a positive multiple of {block}")
+
+
+def _call(f, device, *args):
+    # the launches go to the tensors' device, which need not be the current one
+    with torch.cuda.device(device):
+        _check(f(*args, _stream(device)))
+
+
+def q4_0_glu_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.q4_0_glu_workspace_bytes(M, N, K))
+
+
+def q4_0_glu(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, act: str = "silu",
+             h: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """h[M, N] = act(x . deq(Wg)) * (x . deq(Wu)) for x [M, K] fp32, M <= 8, and two Q4_0
+    matrices; act "silu" or "gelu" (tanh form)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    _columns(N, 32)
+    mat = K * (N // 32) * BLOCK_BYTES
+    a = _act(act)
+    px = _dev(x, "x", torch.float32, M * K)
+    pg = _dev(Wg, "Wg", torch.uint8, mat)
+    pu = _dev(Wu, "Wu", torch.uint8, mat)
+    if h is None:
+        h = torch.empty((M, N), dtype=torch.float32, device=x.device)
+    ph = _dev(h, "h", torch.float32, M * N)
+    pw, nw = _ws_arg(ws, q4_0_glu_workspace_bytes(M, N, K), x.device)
+    _on(x.device, Wg=Wg, Wu=Wu, h=h, ws=ws)
+    _call(_lib.q4_0_glu, x.device, px, pg, pu, ph, M, N, K, a, pw, nw)
+    return h
+
+
+def q4_0_glu_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.q4_0_glu_gemm_workspace_bytes(M, N, K))
+
+
+def q4_0_glu_gemm(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, act: str = "silu",
+                  H: torch.Tensor | None = None, G: torch.Tensor | None = None,
+                  U: torch.Tensor | None = None, save: bool = False,
+                  ws: torch.Tensor | None = None):
+    """H[M, N] = act(X . deq(Wg)) * (X . deq(Wu)), fp16 in and out, any M; K and N multiples of
+    64. With save, or with G and U given, also returns g = X . deq(Wg) and u = X . deq(Wu) as
+    fp16: (H, G, U), what q4_0_glu_backward reads."""
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    M, K = X.shape
+    _columns(N, 64)
+    mat = K * (N // 32) * BLOCK_BYTES
+    a = _act(act)
+    if (G is None) != (U is None):
+        raise ValueError("G and U are given together")
+    px = _dev(X, "X", torch.float16, M * K)
+    pg = _dev(Wg, "Wg", torch.uint8, mat)
+    pu = _dev(Wu, "Wu", torch.uint8, mat)
+    if H is None:
+        H = torch.empty((M, N), dtype=torch.float16, device=X.device)
+    if save and G is None:
+        G, U = torch.empty_like(H), torch.empty_like(H)
+    ph = _dev(H, "H", torch.float16, M * N)
+    pG = pU = None
+    if G is not None:
+        pG = _dev(G, "G", torch.float16, M * N)
+        pU = _dev(U, "U", torch.float16, M * N)
+    pw, nw = _ws_arg(ws, q4_0_glu_gemm_workspace_bytes(M, N, K), X.device)
+    _on(X.device, Wg=Wg, Wu=Wu, H=H, G=G, U=U, ws=ws)
+    _call(_lib.q4_0_glu_gemm, X.device, px, pg, pu, ph, pG, pU, M, N, K, a, pw, nw)
+    return H if G is None else (H, G, U)
+
+
+def q4_0_glu_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.q4_0_glu_backward_workspace_bytes(M, N, K))
+
+
+def q4_0_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, Wg: torch.Tensor,
+                      Wu: torch.Tensor, K: int, act: str = "silu",
+                      dX: torch.Tensor | None = None,
+                      ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of q4_0_glu_gemm with respect to X: dX [M, K] bf16 from dH [M, N] bf16 and the
+    G and U that the forward call returned. The weights have no gradient."""
+    if dH.dim() != 2:
+        raise ValueError("dH must be [M, N]")
+    M, N = dH.shape
+    _columns(N, 64)
+    mat = K * (N // 32) * BLOCK_BYTES
+    a = _act(act)
+    pd = _dev(dH, "dH", torch.bfloat16, M * N)
+    pG = _dev(G, "G", torch.float16, M * N)
+    pU = _dev(U, "U", torch.float16, M * N)
+    pg = _dev(Wg, "Wg", torch.uint8, mat)
+    pu = _dev(Wu, "Wu", torch.uint8, mat)
+    if dX is None:
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dH.device)
+    px = _dev(dX, "dX", torch.bfloat16, M * K)
+    pw, nw = _ws_arg(ws, q4_0_glu_backward_workspace_bytes(M, N, K), dH.device)
+    _on(dH.device, G=G, U=U, Wg=Wg, Wu=Wu, dX=dX, ws=ws)
+    _call(_lib.q4_0_glu_backward, dH.device, pd, pG, pU, pg, pu, px, M, N, K, a, pw, nw)
+    return dX
+
+
+def q4_0_gemm_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.q4_0_gemm_backward_workspace_bytes(M, N, K))
+
+
+def q4_0_gemm_backward(dY: torch.Tensor, B: torch.Tensor, K: int, dX: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of Y = X . deq(B) with respect to X: dX [M, K] bf16 from dY [M, N] bf16."""
+    if dY.dim() != 2:
+        raise ValueError("dY must be [M, N]")
+    M, N = dY.shape
+    _columns(N, 64)
+    pd = _dev(dY, "dY", torch.bfloat16, M * N)
+    pb = _dev(B, "B", torch.uint8, K * (N // 32) * BLOCK_BYTES)
+    if dX is None:
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dY.device)
+    px = _dev(dX, "dX", torch.bfloat16, M * K)
+    pw, nw = _ws_arg(ws, q4_0_gemm_backward_workspace_bytes(M, N, K), dY.device)
+    _on(dY.device, B=B, dX=dX, ws=ws)
+    _call(_lib.q4_0_gemm_backward, dY.device, pd, pb, px, M, N, K, pw, nw)
+    return dX
+
+
+def q4_0_gemv_lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
+    return int(_lib.q4_0_gemv_lora_workspace_bytes(M, N, K, R))
+
+
+def q4_0_gemm_lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
+    return int(_lib.q4_0_gemm_lora_workspace_bytes(M, N, K, R))
+
+
+def _lora(f, need, x, B, N, A, Bl, ids, scale, y, ws, dtype, block, names):
+    if x.dim() != 2 or A.dim() != 3:
+        raise ValueError(f"{names[0]} must be [M, K] and A [L, R, K]")
+    M, K = x.shape
+    L, R = A.shape[:2]
+    _columns(N, block)
+    px = _dev(x, names[0], dtype, M * K)
+    pb = _dev(B, "B", torch.uint8, K * (N // 32) * BLOCK_BYTES)
+    pA = _dev(A, "A", torch.float16, L * R * K)
+    pB = _dev(Bl, "Bl", torch.float16, L * N * R)
+    pi = _dev(ids, "ids", torch.int32, M)
+    ps = _dev(scale, "scale", torch.float32, L)
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=x.device)
+    py = _dev(y, names[1], dtype, M * N)
+    pw, nw = _ws_arg(ws, need(M, N, K, R), x.device)
+    _on(x.device, B=B, A=A, Bl=Bl, ids=ids, scale=scale, y=y, ws=ws)
+    _call(f, x.device, px, pb, pA, pB, pi, ps, py, M, N, K, R, L, pw, nw)
+    return y
+
+
+def q4_0_gemv_lora(x: torch.Tensor, B: torch.Tensor, N: int, A: torch.Tensor, Bl: torch.Tensor,
+                   ids: torch.Tensor, scale: torch.Tensor, y: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None) -> torch.Tensor:
+    """y[m] = x[m] . deq(B) + scale[i] * (x[m] . A[i]^T) . Bl[i]^T with i = ids[m]: one of L
+    adapters (A [L, R, K], Bl [L, N, R], fp16) for each row, none where ids[m] is outside
+    [0, L). x and y fp32, M <= 8."""
+    return _lora(_lib.q4_0_gemv_lora, q4_0_gemv_lora_workspace_bytes, x, B, N, A, Bl, ids, scale,
+                 y, ws, torch.float32, 32, ("x", "y"))
+
+
+def q4_0_gemm_lora(X: torch.Tensor, B: torch.Tensor, N: int, A: torch.Tensor, Bl: torch.Tensor,
+                   ids: torch.Tensor, scale: torch.Tensor, Y: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None) -> torch.Tensor:
+    """q4_0_gemv_lora for any number of rows, X and Y fp16; K and N multiples of 64."""
+    return _lora(_lib.q4_0_gemm_lora, q4_0_gemm_lora_workspace_bytes, X, B, N, A, Bl, ids, scale,
+                 Y, ws, torch.float16, 64, ("X", "Y"))

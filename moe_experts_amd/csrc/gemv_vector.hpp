@@ -44,6 +44,7 @@ struct GemvArgs {
   float* __restrict__ part;  // [S][M][N] split-K partials
   int M, N, K, NB;
   int Jt, Lr, P, C, Kt, S;
+  const uint8_t* __restrict__ B1;  // the second matrix of a pair launch
 };
 
 // The LDS-staged weight path reads Q4_0 blocks out of 16-block segments.
@@ -59,12 +60,21 @@ constexpr int staged_rows_per_batch() {
 }
 constexpr int kStagedBuffers = 2;
 
-template <class Fmt, int M, int LPB, bool STAGED>
+// PAIR: the grid covers two matrices of one shape (first B, then B1), whose
+// partial sums stand one after the other: part[2][S][M][N], also when S == 1.
+template <class Fmt, int M, int LPB, bool STAGED, bool PAIR = false>
 __global__ __launch_bounds__(kThreads) void gemv_vector_kernel(GemvArgs a) {
   extern __shared__ __attribute__((aligned(16))) float smem[];
   const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
   const int c = L % a.C;
-  const int s = L / a.C;
+  int s = L / a.C;
+  if constexpr (PAIR) {
+    if (s >= a.S) {
+      s -= a.S;
+      a.B = a.B1;
+      a.part += (size_t)a.S * a.M * a.N;
+    }
+  }
   SplitTile g;
   g.B = a.B;
   g.NB = a.NB;
@@ -90,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void gemv_vector_kernel(GemvArgs a) {
   }
   const int n0 = g.j0 * kBlockWeights;
   const int ncols = min(a.Jt, a.NB - g.j0) * kBlockWeights;
-  float* dst = (a.S == 1) ? a.y : a.part + (size_t)s * M * a.N;
+  float* dst = (!PAIR && a.S == 1) ? a.y : a.part + (size_t)s * M * a.N;
   reduce_phases<M, LPB, Fmt>(acc, corr, smem, a.Lr, a.P, ncols,
                              [&](int m, int o, float v) { dst[(size_t)m * a.N + n0 + o] = v; });
 }
@@ -141,8 +151,9 @@ int vector_lds_bytes(int M, int Kt, int P, bool staged_possible) {
 // keep at least 128 rows. S is the largest split within both, then raised
 // further if the activation tile would not fit in LDS (wide matrices, where
 // the grid target alone gives few splits).
+// mats = 2: a pair launch, whose grid holds both matrices.
 template <class Fmt>
-GemvPlan plan_vector(int M, int N, int K) {
+GemvPlan plan_vector(int M, int N, int K, int mats = 1) {
   GemvPlan p{};
   constexpr int kMinTileRows = 128;
   const int NB = N / kBlockWeights;
@@ -163,7 +174,7 @@ GemvPlan plan_vector(int M, int N, int K) {
     const int S = (K + kt - 1) / kt;
     if (S == last_S) continue;
     last_S = S;
-    if (kt < kMinTileRows || p.C * S > target) break;
+    if (kt < kMinTileRows || mats * p.C * S > target) break;
     best_kt = kt;
   }
   const bool staged_possible = stages_in_lds<Fmt>() && p.Jt == kStagedJt;
@@ -172,12 +183,13 @@ GemvPlan plan_vector(int M, int N, int K) {
     best_kt = kt_for(s);
   p.Kt = best_kt;
   p.S = (K + p.Kt - 1) / p.Kt;
-  p.ws_bytes = p.S > 1 ? (size_t)p.S * M * N * sizeof(float) : 0;
+  p.ws_bytes = p.S > 1 || mats > 1 ? (size_t)mats * p.S * M * N * sizeof(float) : 0;
   return p;
 }
 
-template <class Fmt, int M>
-hipError_t launch_vector_m(const GemvArgs& a, bool staged, hipStream_t st) {
+template <class Fmt, int M, bool PAIR>
+hipError_t launch_vector_m(const GemvArgs& a, bool staged, bool sum, hipStream_t st) {
+  const dim3 grid((PAIR ? 2 : 1) * a.C * a.S);
   constexpr int LPB = Fmt::lanes_per_block(M);
   const int rf = 4 * phase_lds_floats<M, LPB, Fmt>();
   int lds;
@@ -188,24 +200,26 @@ hipError_t launch_vector_m(const GemvArgs& a, bool staged, hipStream_t st) {
       const int sb =
           staged_lds_bytes<M, LPB, staged_rows_per_batch<LPB>(), kStagedJt, kStagedBuffers>(a.Kt);
       lds = sb > rf ? sb : rf;
-      hipLaunchKernelGGL((gemv_vector_kernel<Fmt, M, LPB, true>), dim3(a.C * a.S),
-                         dim3(kThreads), lds, st, a);
+      hipLaunchKernelGGL((gemv_vector_kernel<Fmt, M, LPB, true, PAIR>), grid, dim3(kThreads), lds,
+                         st, a);
     }
   } else {
     const int xf = 4 * tile_x_floats<M>(a.Kt, a.P, Fmt::rows_per_batch(M));
     lds = xf > rf ? xf : rf;
-    hipLaunchKernelGGL((gemv_vector_kernel<Fmt, M, LPB, false>), dim3(a.C * a.S), dim3(kThreads),
-                       lds, st, a);
+    hipLaunchKernelGGL((gemv_vector_kernel<Fmt, M, LPB, false, PAIR>), grid, dim3(kThreads), lds,
+                       st, a);
   }
   hipError_t err = hipGetLastError();
-  if (err != hipSuccess || a.S == 1) return err;
+  if (err != hipSuccess || a.S == 1 || !sum) return err;
   return launch_gemv_reduce(a.part, a.y, M * a.N, a.S, st);
 }
 
-// Launch a plan of plan_vector<Fmt> (main kernel, then the split-K sum).
-template <class Fmt>
+// Launch a plan of plan_vector<Fmt> (main kernel, then, with sum, the split-K
+// sum). PAIR: B and B1 by a plan for two matrices, no sum.
+template <class Fmt, bool PAIR = false>
 hipError_t launch_vector(const float* x, const uint8_t* B, float* y, int M, int N, int K, void* ws,
-                         const GemvPlan& p, hipStream_t st) {
+                         const GemvPlan& p, hipStream_t st, bool sum = true,
+                         const uint8_t* B1 = nullptr) {
   GemvArgs a;
   a.x = x;
   a.B = B;
@@ -221,18 +235,20 @@ hipError_t launch_vector(const float* x, const uint8_t* B, float* y, int M, int 
   a.C = p.C;
   a.Kt = p.Kt;
   a.S = p.S;
+  a.B1 = B1;
   // Wave-private staging needs 16-byte aligned 16-block row segments.
   const bool staged = stages_in_lds<Fmt>() && p.Jt == kStagedJt && a.NB % 8 == 0 &&
-                      (reinterpret_cast<uintptr_t>(B) & 15) == 0;
+                      (reinterpret_cast<uintptr_t>(B) & 15) == 0 &&
+                      (!PAIR || (reinterpret_cast<uintptr_t>(B1) & 15) == 0);
   switch (M) {
-    case 1: return launch_vector_m<Fmt, 1>(a, staged, st);
-    case 2: return launch_vector_m<Fmt, 2>(a, staged, st);
-    case 3: return launch_vector_m<Fmt, 3>(a, staged, st);
-    case 4: return launch_vector_m<Fmt, 4>(a, staged, st);
-    case 5: return launch_vector_m<Fmt, 5>(a, staged, st);
-    case 6: return launch_vector_m<Fmt, 6>(a, staged, st);
-    case 7: return launch_vector_m<Fmt, 7>(a, staged, st);
-    case 8: return launch_vector_m<Fmt, 8>(a, staged, st);
+    case 1: return launch_vector_m<Fmt, 1, PAIR>(a, staged, !PAIR && sum, st);
+    case 2: return launch_vector_m<Fmt, 2, PAIR>(a, staged, !PAIR && sum, st);
+    case 3: return launch_vector_m<Fmt, 3, PAIR>(a, staged, !PAIR && sum, st);
+    case 4: return launch_vector_m<Fmt, 4, PAIR>(a, staged, !PAIR && sum, st);
+    case 5: return launch_vector_m<Fmt, 5, PAIR>(a, staged, !PAIR && sum, st);
+    case 6: return launch_vector_m<Fmt, 6, PAIR>(a, staged, !PAIR && sum, st);
+    case 7: return launch_vector_m<Fmt, 7, PAIR>(a, staged, !PAIR && sum, st);
+    case 8: return launch_vector_m<Fmt, 8, PAIR>(a, staged, !PAIR && sum, st);
     default: return hipErrorInvalidValue;
   }
 }

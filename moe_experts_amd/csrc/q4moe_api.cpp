@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "ffn_internal.hpp"
 #include "q4_internal.hpp"
 
 namespace {
@@ -109,6 +110,42 @@ LayerWs layer_ws(int T, int H, int I, int E, int topk, int n_shared) {
   l.bytes = l.off_moe + q4::plan_moe(T, H, I, E + n_shared, slots).ws_bytes;
   return l;
 }
+
+// Shapes of the prompt and gradient forms over one or two K x N matrices.
+int check_ffn_shape(int M, int N, int K) {
+  if (M <= 0 || N <= 0 || K <= 0) return Q4_EINVAL;
+  if (N % 64 != 0 || K % 64 != 0) return Q4_ESHAPE;
+  if ((long long)K * (N / 32) * 18 > kMaxBytes || (long long)M * K * 2 > kMaxBytes ||
+      (long long)M * N * 2 > kMaxBytes)
+    return Q4_ETOOBIG;
+  return Q4_OK;
+}
+
+int check_rank(int R) {
+  if (R <= 0) return Q4_EINVAL;
+  return R % 8 != 0 || R > Q4_LORA_MAX_R ? Q4_ESHAPE : Q4_OK;
+}
+
+int check_gemv_lora_shape(int M, int N, int K, int R) {
+  int rc = check_gemv_shape(M, N, K, 18);
+  if (rc != Q4_OK) return rc;
+  rc = check_rank(R);
+  if (rc != Q4_OK) return rc;
+  return K % 8 != 0 ? Q4_ESHAPE : Q4_OK;
+}
+
+int check_gemm_lora_shape(int M, int N, int K, int R) {
+  const int rc = check_ffn_shape(M, N, K);
+  return rc != Q4_OK ? rc : check_rank(R);
+}
+
+// 16-byte alignment of every array given (NULL is aligned)
+template <class... P>
+bool aligned16(P... p) {
+  return (aligned(p, 16) && ...);
+}
+
+const uint8_t* bytes(const q4_0_block* b) { return reinterpret_cast<const uint8_t*>(b); }
 
 }  // namespace
 
@@ -310,6 +347,127 @@ int moe_q4_0_prefill(const uint16_t* x16, const q4_0_block* Wg, const q4_0_block
                                          reinterpret_cast<const uint8_t*>(Wd), topk_ids, topk_w,
                                          out, T, H, I, E, topk, ws, p,
                                          static_cast<hipStream_t>(stream)));
+}
+
+
+size_t q4_0_glu_workspace_bytes(int M, int N, int K) {
+  if (check_gemv_shape(M, N, K, 18) != Q4_OK) return 0;
+  return q4::plan_glu(M, N, K).ws_bytes;
+}
+
+int q4_0_glu(const float* x, const q4_0_block* Wg, const q4_0_block* Wu, float* h, int M, int N,
+             int K, int act, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_gemv(x, Wg, h, M, N, K);
+  if (!Wu) return Q4_EINVAL;
+  if (rc != Q4_OK) return rc;
+  if (act != Q4_ACT_SILU && act != Q4_ACT_GELU) return Q4_EINVAL;
+  if (!aligned(Wu, 2)) return Q4_EALIGN;
+  const q4::GemvPlan p = q4::plan_glu(M, N, K);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  return from_hip(q4::launch_glu(x, bytes(Wg), bytes(Wu), h, M, N, K, act, ws, p,
+                                 static_cast<hipStream_t>(stream)));
+}
+
+size_t q4_0_glu_gemm_workspace_bytes(int M, int N, int K) {
+  if (check_ffn_shape(M, N, K) != Q4_OK) return 0;
+  return q4::plan_glu_gemm(M, N, K).ws_bytes;
+}
+
+int q4_0_glu_gemm(const uint16_t* X, const q4_0_block* Wg, const q4_0_block* Wu, uint16_t* H,
+                  uint16_t* G, uint16_t* U, int M, int N, int K, int act, void* ws,
+                  size_t ws_bytes, void* stream) {
+  if (!X || !Wg || !Wu || !H || !G != !U) return Q4_EINVAL;
+  if (act != Q4_ACT_SILU && act != Q4_ACT_GELU) return Q4_EINVAL;
+  int rc = check_ffn_shape(M, N, K);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(X, H, G, U) || !aligned(Wg, 2) || !aligned(Wu, 2)) return Q4_EALIGN;
+  const q4::FfnPlan p = q4::plan_glu_gemm(M, N, K);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  return from_hip(q4::launch_glu_gemm(X, bytes(Wg), bytes(Wu), H, G, U, M, N, K, act, ws, p,
+                                      static_cast<hipStream_t>(stream)));
+}
+
+size_t q4_0_glu_backward_workspace_bytes(int M, int N, int K) {
+  if (check_ffn_shape(M, N, K) != Q4_OK) return 0;
+  return q4::plan_gradient(M, N, K, 2).ws_bytes;
+}
+
+int q4_0_glu_backward(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
+                      const q4_0_block* Wg, const q4_0_block* Wu, uint16_t* dX, int M, int N,
+                      int K, int act, void* ws, size_t ws_bytes, void* stream) {
+  if (!dH || !G || !U || !Wg || !Wu || !dX) return Q4_EINVAL;
+  if (act != Q4_ACT_SILU && act != Q4_ACT_GELU) return Q4_EINVAL;
+  int rc = check_ffn_shape(M, N, K);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(dH, G, U, dX) || !aligned(Wg, 2) || !aligned(Wu, 2)) return Q4_EALIGN;
+  const q4::FfnPlan p = q4::plan_gradient(M, N, K, 2);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  return from_hip(q4::launch_gradient(dH, G, U, bytes(Wg), bytes(Wu), dX, M, N, K, act, 2, ws, p,
+                                      static_cast<hipStream_t>(stream)));
+}
+
+size_t q4_0_gemm_backward_workspace_bytes(int M, int N, int K) {
+  if (check_ffn_shape(M, N, K) != Q4_OK) return 0;
+  return q4::plan_gradient(M, N, K, 1).ws_bytes;
+}
+
+int q4_0_gemm_backward(const uint16_t* dY, const q4_0_block* B, uint16_t* dX, int M, int N, int K,
+                       void* ws, size_t ws_bytes, void* stream) {
+  if (!dY || !B || !dX) return Q4_EINVAL;
+  int rc = check_ffn_shape(M, N, K);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(dY, dX) || !aligned(B, 2)) return Q4_EALIGN;
+  const q4::FfnPlan p = q4::plan_gradient(M, N, K, 1);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  return from_hip(q4::launch_gradient(dY, nullptr, nullptr, bytes(B), nullptr, dX, M, N, K,
+                                      Q4_ACT_SILU, 1, ws, p, static_cast<hipStream_t>(stream)));
+}
+
+size_t q4_0_gemv_lora_workspace_bytes(int M, int N, int K, int R) {
+  if (check_gemv_lora_shape(M, N, K, R) != Q4_OK) return 0;
+  return q4::plan_gemv_lora(M, N, K, R).ws_bytes;
+}
+
+int q4_0_gemv_lora(const float* x, const q4_0_block* B, const uint16_t* A, const uint16_t* Bl,
+                   const int32_t* ids, const float* scale, float* y, int M, int N, int K, int R,
+                   int L, void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !B || !A || !Bl || !ids || !scale || !y || L <= 0) return Q4_EINVAL;
+  int rc = check_gemv_lora_shape(M, N, K, R);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(x, A, Bl) || !aligned(B, 2) || !aligned(ids, 4) || !aligned(scale, 4) ||
+      !aligned(y, 4))
+    return Q4_EALIGN;
+  const q4::GemvLoraPlan p = q4::plan_gemv_lora(M, N, K, R);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  const q4::Adapters ad{A, Bl, ids, scale, R, L};
+  return from_hip(q4::launch_gemv_lora(x, bytes(B), ad, y, M, N, K, ws, p,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+size_t q4_0_gemm_lora_workspace_bytes(int M, int N, int K, int R) {
+  if (check_gemm_lora_shape(M, N, K, R) != Q4_OK) return 0;
+  return q4::plan_gemm_lora(M, N, K, R).ws_bytes;
+}
+
+int q4_0_gemm_lora(const uint16_t* X, const q4_0_block* B, const uint16_t* A, const uint16_t* Bl,
+                   const int32_t* ids, const float* scale, uint16_t* Y, int M, int N, int K,
+                   int R, int L, void* ws, size_t ws_bytes, void* stream) {
+  if (!X || !B || !A || !Bl || !ids || !scale || !Y || L <= 0) return Q4_EINVAL;
+  int rc = check_gemm_lora_shape(M, N, K, R);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(X, A, Bl, Y) || !aligned(B, 2) || !aligned(ids, 4) || !aligned(scale, 4))
+    return Q4_EALIGN;
+  const q4::FfnPlan p = q4::plan_gemm_lora(M, N, K, R);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  const q4::Adapters ad{A, Bl, ids, scale, R, L};
+  return from_hip(q4::launch_gemm_lora(X, bytes(B), ad, Y, M, N, K, ws, p,
+                                       static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
