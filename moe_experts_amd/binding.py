@@ -14,6 +14,7 @@ bounds by a kernel.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -107,8 +108,13 @@ def _check(rc: int):
         raise Q4Error(rc)
 
 
+def _raw_stream(index: int) -> int:
+    """Handle of the current stream of a device, without building a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _dev(t: torch.Tensor, name: str, dtype, numel: int):
@@ -126,7 +132,10 @@ def _dev(t: torch.Tensor, name: str, dtype, numel: int):
 
 
 # Workspaces: one scratch buffer per (device, stream), grown on demand. Calls
-# on one stream run in order, so they can share it.
+# on one stream run in order, so they can share it. A call that is being
+# captured takes memory of its own from the graph's pool instead: graphs that
+# are replayed at the same time must not share scratch memory, and a graph must
+# not depend on a buffer that a later, larger call replaces.
 _ws_lock = threading.Lock()
 _ws_cache: dict = {}
 
@@ -135,13 +144,17 @@ def workspace(nbytes: int, device) -> torch.Tensor | None:
     if nbytes == 0:
         return None
     dev = torch.device(device)
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
-    with _ws_lock:
-        buf = _ws_cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
-            _ws_cache[key] = buf
-        return buf
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    key = (dev.index, _raw_stream(dev.index))
+    buf = _ws_cache.get(key)
+    if buf is None or buf.numel() < nbytes:
+        with _ws_lock:
+            buf = _ws_cache.get(key)
+            if buf is None or buf.numel() < nbytes:
+                buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+                _ws_cache[key] = buf
+    return buf
 
 
 def q4_0_gemv_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -372,22 +385,27 @@ def moe_q4_0_prefill(x16: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: 
 
 
 # ---------------------------------------------------------------------------
-# Dense feed-forward over frozen Q4_0 weights
+# Dense feed-forward over frozen Q4_0 weights. These calls take a few
+# microseconds of GPU time at decode, so their host side is kept short: one
+# check per tensor, workspace sizes remembered by shape.
 # ---------------------------------------------------------------------------
 ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 
 def _act(act: str) -> int:
-    if act not in ACTIVATIONS:
+    a = ACTIVATIONS.get(act)
+    if a is None:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)} (got {act!r})")
-    return ACTIVATIONS[act]
+    return a
 
 
-def _on(device, **tensors):
-    """Every tensor given is on `device` (the stream is that device's)."""
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _ptr(t, name: str, dtype, numel: int, index: int) -> int:
+    """Address of a contiguous tensor of this type and size on device `index`."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == index >= 0 and t.dtype is dtype
+            and t.numel() == numel and t.is_contiguous()):
+        return t.data_ptr()
+    _dev(t, name, dtype, numel)
+    raise ValueError(f"{name} is on {t.device}, the first argument on device {index}")
 
 
 def _columns(N: int, block: int):
@@ -395,14 +413,51 @@ def _columns(N: int, block: int):
         raise ValueError(f"N must be a positive multiple of {block}")
 
 
-def _call(f, device, *args):
-    # the launches go to the tensors' device, which need not be the current one
-    with torch.cuda.device(device):
-        _check(f(*args, _stream(device)))
+def _run(f, need: int, ws, index: int, *args):
+    """Call f(*args, workspace, its size, stream) on device `index`, which need not be the
+    current one."""
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _run(f, need, ws, index, *args)
+    if ws is None:
+        ws = workspace(need, torch.device("cuda", index)) if need else None
+        p, n = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    else:
+        n = ws.numel()
+        p = _ptr(ws, "ws", torch.uint8, n, index)
+    rc = f(*args, p, n, _raw_stream(index))
+    if rc != 0:
+        raise Q4Error(rc)
 
 
+@functools.lru_cache(maxsize=1024)
 def q4_0_glu_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(_lib.q4_0_glu_workspace_bytes(M, N, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def q4_0_glu_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.q4_0_glu_gemm_workspace_bytes(M, N, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def q4_0_glu_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.q4_0_glu_backward_workspace_bytes(M, N, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def q4_0_gemm_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.q4_0_gemm_backward_workspace_bytes(M, N, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def q4_0_gemv_lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
+    return int(_lib.q4_0_gemv_lora_workspace_bytes(M, N, K, R))
+
+
+@functools.lru_cache(maxsize=1024)
+def q4_0_gemm_lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
+    return int(_lib.q4_0_gemm_lora_workspace_bytes(M, N, K, R))
 
 
 def q4_0_glu(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, act: str = "silu",
@@ -415,20 +470,15 @@ def q4_0_glu(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, act: s
     _columns(N, 32)
     mat = K * (N // 32) * BLOCK_BYTES
     a = _act(act)
-    px = _dev(x, "x", torch.float32, M * K)
-    pg = _dev(Wg, "Wg", torch.uint8, mat)
-    pu = _dev(Wu, "Wu", torch.uint8, mat)
+    i = x.get_device()
+    px = _ptr(x, "x", torch.float32, M * K, i)
+    pg = _ptr(Wg, "Wg", torch.uint8, mat, i)
+    pu = _ptr(Wu, "Wu", torch.uint8, mat, i)
     if h is None:
         h = torch.empty((M, N), dtype=torch.float32, device=x.device)
-    ph = _dev(h, "h", torch.float32, M * N)
-    pw, nw = _ws_arg(ws, q4_0_glu_workspace_bytes(M, N, K), x.device)
-    _on(x.device, Wg=Wg, Wu=Wu, h=h, ws=ws)
-    _call(_lib.q4_0_glu, x.device, px, pg, pu, ph, M, N, K, a, pw, nw)
+    ph = _ptr(h, "h", torch.float32, M * N, i)
+    _run(_lib.q4_0_glu, q4_0_glu_workspace_bytes(M, N, K), ws, i, px, pg, pu, ph, M, N, K, a)
     return h
-
-
-def q4_0_glu_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(_lib.q4_0_glu_gemm_workspace_bytes(M, N, K))
 
 
 def q4_0_glu_gemm(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, act: str = "silu",
@@ -446,26 +496,23 @@ def q4_0_glu_gemm(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, a
     a = _act(act)
     if (G is None) != (U is None):
         raise ValueError("G and U are given together")
-    px = _dev(X, "X", torch.float16, M * K)
-    pg = _dev(Wg, "Wg", torch.uint8, mat)
-    pu = _dev(Wu, "Wu", torch.uint8, mat)
+    i = X.get_device()
+    px = _ptr(X, "X", torch.float16, M * K, i)
+    pg = _ptr(Wg, "Wg", torch.uint8, mat, i)
+    pu = _ptr(Wu, "Wu", torch.uint8, mat, i)
     if H is None:
         H = torch.empty((M, N), dtype=torch.float16, device=X.device)
     if save and G is None:
-        G, U = torch.empty_like(H), torch.empty_like(H)
-    ph = _dev(H, "H", torch.float16, M * N)
+        G = torch.empty((M, N), dtype=torch.float16, device=X.device)
+        U = torch.empty((M, N), dtype=torch.float16, device=X.device)
+    ph = _ptr(H, "H", torch.float16, M * N, i)
     pG = pU = None
     if G is not None:
-        pG = _dev(G, "G", torch.float16, M * N)
-        pU = _dev(U, "U", torch.float16, M * N)
-    pw, nw = _ws_arg(ws, q4_0_glu_gemm_workspace_bytes(M, N, K), X.device)
-    _on(X.device, Wg=Wg, Wu=Wu, H=H, G=G, U=U, ws=ws)
-    _call(_lib.q4_0_glu_gemm, X.device, px, pg, pu, ph, pG, pU, M, N, K, a, pw, nw)
+        pG = _ptr(G, "G", torch.float16, M * N, i)
+        pU = _ptr(U, "U", torch.float16, M * N, i)
+    _run(_lib.q4_0_glu_gemm, q4_0_glu_gemm_workspace_bytes(M, N, K), ws, i, px, pg, pu, ph, pG, pU,
+         M, N, K, a)
     return H if G is None else (H, G, U)
-
-
-def q4_0_glu_backward_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(_lib.q4_0_glu_backward_workspace_bytes(M, N, K))
 
 
 def q4_0_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, Wg: torch.Tensor,
@@ -480,22 +527,18 @@ def q4_0_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, Wg: to
     _columns(N, 64)
     mat = K * (N // 32) * BLOCK_BYTES
     a = _act(act)
-    pd = _dev(dH, "dH", torch.bfloat16, M * N)
-    pG = _dev(G, "G", torch.float16, M * N)
-    pU = _dev(U, "U", torch.float16, M * N)
-    pg = _dev(Wg, "Wg", torch.uint8, mat)
-    pu = _dev(Wu, "Wu", torch.uint8, mat)
+    i = dH.get_device()
+    pd = _ptr(dH, "dH", torch.bfloat16, M * N, i)
+    pG = _ptr(G, "G", torch.float16, M * N, i)
+    pU = _ptr(U, "U", torch.float16, M * N, i)
+    pg = _ptr(Wg, "Wg", torch.uint8, mat, i)
+    pu = _ptr(Wu, "Wu", torch.uint8, mat, i)
     if dX is None:
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=dH.device)
-    px = _dev(dX, "dX", torch.bfloat16, M * K)
-    pw, nw = _ws_arg(ws, q4_0_glu_backward_workspace_bytes(M, N, K), dH.device)
-    _on(dH.device, G=G, U=U, Wg=Wg, Wu=Wu, dX=dX, ws=ws)
-    _call(_lib.q4_0_glu_backward, dH.device, pd, pG, pU, pg, pu, px, M, N, K, a, pw, nw)
+    px = _ptr(dX, "dX", torch.bfloat16, M * K, i)
+    _run(_lib.q4_0_glu_backward, q4_0_glu_backward_workspace_bytes(M, N, K), ws, i, pd, pG, pU, pg,
+         pu, px, M, N, K, a)
     return dX
-
-
-def q4_0_gemm_backward_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(_lib.q4_0_gemm_backward_workspace_bytes(M, N, K))
 
 
 def q4_0_gemm_backward(dY: torch.Tensor, B: torch.Tensor, K: int, dX: torch.Tensor | None = None,
@@ -505,43 +548,34 @@ def q4_0_gemm_backward(dY: torch.Tensor, B: torch.Tensor, K: int, dX: torch.Tens
         raise ValueError("dY must be [M, N]")
     M, N = dY.shape
     _columns(N, 64)
-    pd = _dev(dY, "dY", torch.bfloat16, M * N)
-    pb = _dev(B, "B", torch.uint8, K * (N // 32) * BLOCK_BYTES)
+    i = dY.get_device()
+    pd = _ptr(dY, "dY", torch.bfloat16, M * N, i)
+    pb = _ptr(B, "B", torch.uint8, K * (N // 32) * BLOCK_BYTES, i)
     if dX is None:
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=dY.device)
-    px = _dev(dX, "dX", torch.bfloat16, M * K)
-    pw, nw = _ws_arg(ws, q4_0_gemm_backward_workspace_bytes(M, N, K), dY.device)
-    _on(dY.device, B=B, dX=dX, ws=ws)
-    _call(_lib.q4_0_gemm_backward, dY.device, pd, pb, px, M, N, K, pw, nw)
+    px = _ptr(dX, "dX", torch.bfloat16, M * K, i)
+    _run(_lib.q4_0_gemm_backward, q4_0_gemm_backward_workspace_bytes(M, N, K), ws, i, pd, pb, px,
+         M, N, K)
     return dX
-
-
-def q4_0_gemv_lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
-    return int(_lib.q4_0_gemv_lora_workspace_bytes(M, N, K, R))
-
-
-def q4_0_gemm_lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
-    return int(_lib.q4_0_gemm_lora_workspace_bytes(M, N, K, R))
 
 
 def _lora(f, need, x, B, N, A, Bl, ids, scale, y, ws, dtype, block, names):
     if x.dim() != 2 or A.dim() != 3:
         raise ValueError(f"{names[0]} must be [M, K] and A [L, R, K]")
     M, K = x.shape
-    L, R = A.shape[:2]
+    L, R, _ = A.shape
     _columns(N, block)
-    px = _dev(x, names[0], dtype, M * K)
-    pb = _dev(B, "B", torch.uint8, K * (N // 32) * BLOCK_BYTES)
-    pA = _dev(A, "A", torch.float16, L * R * K)
-    pB = _dev(Bl, "Bl", torch.float16, L * N * R)
-    pi = _dev(ids, "ids", torch.int32, M)
-    ps = _dev(scale, "scale", torch.float32, L)
+    i = x.get_device()
+    px = _ptr(x, names[0], dtype, M * K, i)
+    pb = _ptr(B, "B", torch.uint8, K * (N // 32) * BLOCK_BYTES, i)
+    pA = _ptr(A, "A", torch.float16, L * R * K, i)
+    pB = _ptr(Bl, "Bl", torch.float16, L * N * R, i)
+    pi = _ptr(ids, "ids", torch.int32, M, i)
+    ps = _ptr(scale, "scale", torch.float32, L, i)
     if y is None:
         y = torch.empty((M, N), dtype=dtype, device=x.device)
-    py = _dev(y, names[1], dtype, M * N)
-    pw, nw = _ws_arg(ws, need(M, N, K, R), x.device)
-    _on(x.device, B=B, A=A, Bl=Bl, ids=ids, scale=scale, y=y, ws=ws)
-    _call(f, x.device, px, pb, pA, pB, pi, ps, py, M, N, K, R, L, pw, nw)
+    py = _ptr(y, names[1], dtype, M * N, i)
+    _run(f, need(M, N, K, R), ws, i, px, pb, pA, pB, pi, ps, py, M, N, K, R, L)
     return y
 
 
