@@ -20,7 +20,10 @@ SOURCES = ["q4moe_api.cpp", "gemv_q4_0.hip", "gemv_mfma_q4_0.hip", "gemv_q8_0.hi
 # allocator rotated the accumulators between loop iterations (register copies
 # on every batch).
 EXTRA = {"gemv_mfma_q4_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "moe_q4_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "moe_q4_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         # With accumulation registers the compiler gave one LDS store of
+         # lora_shrink_tile_kernel a wrong offset (row 1 of a tile at row 0).
+         "ffn_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,4 +1,6 @@
-// Activations of the gated feed-forward block and their slopes, in fp32.
+// Device-side pieces of the dense feed-forward kernels.
+//
+// Activations of the gated block and their slopes, in fp32.
 //   SiLU:  a(z) = z * s(z),        a'(z) = s + z * s * (1 - s)
 //   GELU (tanh form): a(z) = z * s(p), p = 2c (z + 0.044715 z^3), c = sqrt(2/pi),
 //          since (1 + tanh v) / 2 = s(2v);  a'(z) = s + z * s * (1 - s) * p'(z)

@@ -32,7 +32,7 @@
 // as in q4_0_gemm; the sums are fp32.
 #include <type_traits>
 
-#include "ffn_act.hpp"
+#include "ffn_device.hpp"
 #include "ffn_internal.hpp"
 #include "q4_device.hpp"
 
@@ -538,6 +538,10 @@ hipError_t launch_glu_gemm(const uint16_t* X, const uint8_t* Wg, const uint8_t* 
   return launch_glu_finish_f16(g.part, H, G, U, (size_t)M * N, p.S, act, st);
 }
 
+// Up to so many rows most use different adapters (requests that decode), and
+// the narrow product is formed row by row.
+constexpr int kFewRows = 64;
+
 FfnPlan plan_gemm_lora(int M, int N, int K, int R) {
   FfnPlan p{};
   plan_tiles(p, M, (N + BN - 1) / BN, K / BK);
@@ -547,6 +551,7 @@ FfnPlan plan_gemm_lora(int M, int N, int K, int R) {
     at = align256(at + bytes);
     return o;
   };
+  if (M > kFewRows || p.S == 1) p.off_tp = take((size_t)shrink_shares(M, K) * M * R * sizeof(float));
   if (p.S > 1) {
     p.off_part = take((size_t)p.S * M * N * sizeof(float));
     p.off_t = take((size_t)M * R * sizeof(float));
@@ -564,7 +569,8 @@ hipError_t launch_gemm_lora(const uint16_t* X, const uint8_t* B, const Adapters&
   float* t = p.S > 1 ? reinterpret_cast<float*>(w + p.off_t) : nullptr;
   uint16_t* t16 = p.S > 1 ? nullptr : reinterpret_cast<uint16_t*>(w + p.off_t16);
   float* ts = p.S > 1 ? nullptr : reinterpret_cast<float*>(w + p.off_ts);
-  hipError_t err = launch_lora_shrink_f16(X, ad, t, t16, ts, M, K, st);
+  float* tp = M > kFewRows || p.S == 1 ? reinterpret_cast<float*>(w + p.off_tp) : nullptr;
+  hipError_t err = launch_lora_shrink_f16(X, ad, tp, t, t16, ts, M, K, st);
   if (err != hipSuccess) return err;
   TileArgs g{};
   g.X = X;

@@ -45,6 +45,7 @@ struct FfnPlan {
   int nk;           // K steps of the whole contraction
   int S, kper;      // splits, K steps of one
   size_t off_part;  // fp32 [mats][S][M][ncols], only when S > 1
+  size_t off_tp;    // adapters: fp32 [shares of K][M][R], many rows only
   size_t off_t;     // adapters: fp32 [M][R]
   size_t off_t16;   // adapters: fp16 [M][R], rows scaled to their largest value
   size_t off_ts;    // adapters: fp32 [M], what a row of t16 is multiplied by
@@ -77,8 +78,11 @@ hipError_t launch_glu_finish_f16(const float* part, uint16_t* H, uint16_t* G, ui
 // t[m][r] = scale[id] * sum_k x[m][k] * A[id][r][k], 0 for a row without adapter.
 hipError_t launch_lora_shrink(const float* x, const Adapters& ad, float* t, int M, int K,
                               hipStream_t st);
-hipError_t launch_lora_shrink_f16(const uint16_t* X, const Adapters& ad, float* t, uint16_t* t16,
-                                  float* ts, int M, int K, hipStream_t st);
+// Many rows (tp set): tp[shares][M][R] is scratch, the result is t, or, with
+// t16, t16 and ts (FfnPlan). Few rows (tp null): t.
+int shrink_shares(int M, int K);
+hipError_t launch_lora_shrink_f16(const uint16_t* X, const Adapters& ad, float* tp, float* t,
+                                  uint16_t* t16, float* ts, int M, int K, hipStream_t st);
 // y[m][n] = sum_s part[s][m][n] + sum_r t[m][r] * B[id][n][r]
 hipError_t launch_lora_finish(const float* part, const float* t, const Adapters& ad, float* y,
                               int M, int N, int S, hipStream_t st);

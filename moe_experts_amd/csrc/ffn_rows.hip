@@ -9,7 +9,10 @@
 //   gradient_finish  dX from the split-K partial sums
 #include <hip/hip_runtime.h>
 
-#include "ffn_act.hpp"
+#include <algorithm>
+#include <type_traits>
+
+#include "ffn_device.hpp"
 #include "ffn_internal.hpp"
 #include "q4_device.hpp"
 
@@ -35,43 +38,96 @@ __device__ __forceinline__ uint16_t float_to_bf16(float f) {
 }
 
 // ---------------------------------------------------------------------------
-// h = act(g) * u, four consecutive values a lane, both sums in split order.
-// Bound by the round trip of its loads: all of one group of splits are issued
-// before the first addition.
+// Sums of split-K partials, in split order. They are bound by the round trip
+// of their loads, so with SMAX > 0 (S <= SMAX) all SMAX loads are issued before
+// the first addition: split indices past S - 1 repeat the last one and are not
+// added. SMAX = 0 takes any S in groups of 8. V values a lane.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float4v sum_splits4(const float* __restrict__ src, size_t stride,
-                                               int S) {
-  float4v v = {0.0f, 0.0f, 0.0f, 0.0f};
-  int s = 0;
-  for (; s + 4 <= S; s += 4) {
-    float4v t[4];
+template <int V>
+struct Vec;
+template <>
+struct Vec<1> {
+  typedef float T;
+};
+template <>
+struct Vec<4> {
+  typedef float4v T;
+};
+
+template <int SMAX, int V>
+struct Splits {
+  typedef typename Vec<V>::T T;
+  T t[SMAX ? SMAX : 1];
+  const float* src;
+  __device__ __forceinline__ void load(const float* __restrict__ at, size_t stride, int S) {
+    src = at;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      t[i] = *reinterpret_cast<const float4v*>(src + (size_t)(s + i) * stride);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v += t[i];
+    for (int s = 0; s < SMAX; ++s)
+      t[s] = *reinterpret_cast<const T*>(at + (size_t)min(s, S - 1) * stride);
   }
-  for (; s < S; ++s) v += *reinterpret_cast<const float4v*>(src + (size_t)s * stride);
-  return v;
+  __device__ __forceinline__ T sum(size_t stride, int S) const {
+    T v{};
+    if constexpr (SMAX > 0) {
+#pragma unroll
+      for (int s = 0; s < SMAX; ++s)
+        if (s < S) v += t[s];
+    } else {
+      for (int s0 = 0; s0 < S; s0 += 8) {
+        T p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          p[i] = *reinterpret_cast<const T*>(src + (size_t)min(s0 + i, S - 1) * stride);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (s0 + i < S) v += p[i];
+      }
+    }
+    return v;
+  }
+};
+
+// Runs `call` with the smallest compiled SMAX for S as a compile-time number.
+template <class F>
+void by_splits(int S, F&& call) {
+  if (S <= 2)
+    call(std::integral_constant<int, 2>{});
+  else if (S <= 4)
+    call(std::integral_constant<int, 4>{});
+  else if (S <= 8)
+    call(std::integral_constant<int, 8>{});
+  else if (S <= 16)
+    call(std::integral_constant<int, 16>{});
+  else if (S <= 32)
+    call(std::integral_constant<int, 32>{});
+  else if (S <= 48)
+    call(std::integral_constant<int, 48>{});
+  else
+    call(std::integral_constant<int, 0>{});
 }
 
+// h = act(g) * u
+template <int SMAX>
 __global__ __launch_bounds__(64) void glu_finish_kernel(const float* __restrict__ part,
                                                         float* __restrict__ h, size_t mn, int S,
                                                         int act) {
   const size_t i = (size_t)blockIdx.x * 64 + threadIdx.x;
   if (i >= mn) return;
-  const float g = sum_strided(part + i, mn, S);
-  const float u = sum_strided(part + (size_t)S * mn + i, mn, S);
-  h[i] = act_value(g, act) * u;
+  Splits<SMAX, 1> g, u;
+  g.load(part + i, mn, S);
+  u.load(part + (size_t)S * mn + i, mn, S);
+  h[i] = act_value(g.sum(mn, S), act) * u.sum(mn, S);
 }
 
+template <int SMAX>
 __global__ __launch_bounds__(kRowThreads) void glu_finish_f16_kernel(
     const float* __restrict__ part, _Float16* __restrict__ H, _Float16* __restrict__ G,
     _Float16* __restrict__ U, size_t mn, int S, int act) {
   const size_t i = ((size_t)blockIdx.x * kRowThreads + threadIdx.x) * 4;
   if (i >= mn) return;
-  const float4v g = sum_splits4(part + i, mn, S);
-  const float4v u = sum_splits4(part + (size_t)S * mn + i, mn, S);
+  Splits<SMAX, 4> gs, us;
+  gs.load(part + i, mn, S);
+  us.load(part + (size_t)S * mn + i, mn, S);
+  const float4v g = gs.sum(mn, S), u = us.sum(mn, S);
   half4 h, gh, uh;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -153,143 +209,196 @@ __global__ __launch_bounds__(kRowThreads) void lora_shrink_kernel(const X* __res
 
 // ---------------------------------------------------------------------------
 // Adapters, narrow half, many rows, on the matrix cores (fp16 in, fp32 sums).
-// A workgroup owns 16 rows of X and the whole of K; its 8 waves take K steps
-// of 32 in turn. For every adapter that occurs in the 16 rows the tile is
-// multiplied with all R rows of A (v_mfma_f32_16x16x32_f16, both operands read
-// straight from memory, K being contiguous in both) and the rows that use that
-// adapter keep the result. Rows of one prompt stand together, so a tile nearly
-// always holds one or two adapters. The waves' sums are added in wave order.
-// With t16: rows scaled by a power of two to a largest value in [1, 2), as the
-// fp16 operand of the wide half, and ts[m] = scale[id] / that power.
+// Workgroup (i, c) owns 64 rows of X and one of KS shares of K; its 4 waves
+// take the share's K steps of 16 in turn. For every adapter that occurs in the
+// 64 rows the tile is multiplied with 32 rows of A at a time
+// (v_mfma_f32_32x32x16_f16, both operands read straight from memory, K being
+// contiguous in both) and the rows that use that adapter keep the result. Rows
+// of one prompt stand together, so a tile nearly always holds one or two
+// adapters. Bound by its loads: the shares keep enough of them in flight, and
+// A is read once a tile (2000 rows of 11008 at rank 32 in 7 prompts: 60 us in
+// 16-row tiles and one share, 29 us in eight shares, 27 us in 64-row tiles, 21
+// us with two adapters a pass). The waves'
+// sums are added in wave order, the shares' by lora_rows_kernel.
 // ---------------------------------------------------------------------------
-constexpr int kShrinkRows = 16, kShrinkWaves = 8;
-constexpr int kMaxR = Q4_LORA_MAX_R;
+constexpr int kShrinkRows = 64, kShrinkWaves = 4, kShrinkRanks = 32, kShrinkChunk = 64;
 
 __global__ __launch_bounds__(kShrinkWaves * kWaveSize) void lora_shrink_tile_kernel(
-    const _Float16* __restrict__ X, Adapters ad, float* __restrict__ t,
-    _Float16* __restrict__ t16, float* __restrict__ ts, int M, int K) {
-  __shared__ __attribute__((aligned(16))) float sums[kShrinkWaves][kShrinkRows][kMaxR];
+    const _Float16* __restrict__ X, Adapters ad, float* __restrict__ tp, int M, int K, int tiles,
+    int share) {
+  typedef float float16v __attribute__((ext_vector_type(16)));
+  __shared__ float sums[kShrinkWaves][kShrinkRows][kShrinkRanks];
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int m0 = blockIdx.x * kShrinkRows;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = blockIdx.x % tiles;
+  const int c = blockIdx.x / tiles;
+  const int m0 = tile * kShrinkRows;
+  const int kb = c * share, ke = min(K, kb + share);  // multiples of a chunk
   const int R = ad.R;
-  // lane l of every wave holds the adapter of row l % 16
-  const int row = lane & 15;
-  int id = m0 + row < M ? ad.ids[m0 + row] : -1;
+  // lane l of every wave holds the adapter of row l
+  int id = m0 + lane < M ? ad.ids[m0 + lane] : -1;
   if (id < 0 || id >= ad.L) id = -1;
-  for (int i = lane; i < kShrinkRows * R; i += kWaveSize) sums[wave][i / R][i % R] = 0.0f;
+  const int lr = lane & 31, kg = 8 * (lane >> 5);
+  const _Float16* xr[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) xr[i] = X + (size_t)min(m0 + 32 * i + lr, M - 1) * K + kg;
 
-  const _Float16* xr = X + (size_t)min(m0 + row, M - 1) * K + 8 * (lane >> 4);
-  unsigned todo = (unsigned)__ballot(id >= 0) & 0xffffu;
-  while (todo) {
-    const int cur = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-    const unsigned same = (unsigned)__ballot(id == cur) & 0xffffu;
-    todo &= ~same;
-    // 32 rows of A at a time
-    for (int r0 = 0; r0 < R; r0 += 32) {
+  for (int r0 = 0; r0 < R; r0 += kShrinkRanks) {
+    float16v keep[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) keep[i][e] = 0.0f;
+    unsigned long long todo = __ballot(id >= 0);
+    while (todo) {
+      // two adapters a pass, so that a tile across the end of a prompt reads X
+      // once (a lone adapter is taken twice, its second product not kept)
+      const int cur0 = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+      const unsigned long long same0 = __ballot(id == cur0);
+      todo &= ~same0;
+      const bool two = todo != 0;
+      const int cur1 = two ? __builtin_amdgcn_readlane(id, __builtin_ctzll(todo)) : cur0;
+      const unsigned long long same1 = two ? __ballot(id == cur1) : 0;
+      todo &= ~same1;
       const _Float16* ar[2];
 #pragma unroll
       for (int f = 0; f < 2; ++f)  // rank indexes past R repeat the last one, not kept
         ar[f] = reinterpret_cast<const _Float16*>(ad.A) +
-                ((size_t)cur * R + min(r0 + 16 * f + row, R - 1)) * K + 8 * (lane >> 4);
-      float4v acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-      constexpr int kU = 4;  // K steps in flight
-      for (int k0 = wave * 32; k0 < K; k0 += kU * kShrinkWaves * 32) {
-        half8 xa[kU], b[kU][2];
+                ((size_t)(f ? cur1 : cur0) * R + min(r0 + lr, R - 1)) * K + kg;
+      float16v acc[2][2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[f][i][e] = 0.0f;
+      for (int k0 = kb + wave * kShrinkChunk; k0 < ke; k0 += kShrinkWaves * kShrinkChunk) {
+        constexpr int kU = kShrinkChunk / 16;
+        half8 xa[kU][2], b[kU][2];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const int k = k0 + u * kShrinkWaves * 32;
-          const int kc = min(k, K - 32);
-          xa[u] = *reinterpret_cast<const half8*>(xr + kc);
 #pragma unroll
-          for (int f = 0; f < 2; ++f) b[u][f] = *reinterpret_cast<const half8*>(ar[f] + kc);
+          for (int i = 0; i < 2; ++i)
+            xa[u][i] = *reinterpret_cast<const half8*>(xr[i] + k0 + 16 * u);
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            if (f == 0 || two) b[u][f] = *reinterpret_cast<const half8*>(ar[f] + k0 + 16 * u);
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-          if (k0 + u * kShrinkWaves * 32 < K)
+        for (int f = 0; f < 2; ++f)
+          if (f == 0 || two)
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
-              acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xa[u], b[u][f], acc[f], 0, 0, 0);
+            for (int u = 0; u < kU; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                acc[f][i] =
+                    __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[u][i], b[u][f], acc[f][i], 0, 0, 0);
       }
-      // a 16 x 16 result: lane l holds column l % 16, register e row 4 * (l / 16) + e
+      // a 32 x 32 result: lane l holds column l % 32, register e row
+      // 8 * (e / 4) + 4 * (l / 32) + e % 4
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int r = r0 + 16 * f + row;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int mr = 4 * (lane >> 4) + e;
-          if (r < R && ((same >> mr) & 1u)) sums[wave][mr][r] = acc[f][e];
+        for (int e = 0; e < 16; ++e) {
+          const int row = 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+          keep[i][e] = (same0 >> row) & 1ull
+                           ? acc[0][i][e]
+                           : ((same1 >> row) & 1ull ? acc[1][i][e] : keep[i][e]);
         }
-      }
     }
-  }
-  __syncthreads();
-  // each wave finishes two rows: lane l takes r = l and l + 64
+    if (r0) __syncthreads();  // the sums of the ranks before have been read
 #pragma unroll
-  for (int i = 0; i < kShrinkRows / kShrinkWaves; ++i) {
-    const int mr = wave + i * kShrinkWaves;
-    const int m = m0 + mr;
-    if (m >= M) continue;
-    const int mid = __builtin_amdgcn_readlane(id, mr);
-    const float sc = mid >= 0 ? ad.scale[mid] : 0.0f;
-    float v[2], big = 0.0f;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = lane + 64 * h;
-      v[h] = 0.0f;
-      if (r < R && mid >= 0)
-        for (int w = 0; w < kShrinkWaves; ++w) v[h] += sums[w][mr][r];
-      big = fmaxf(big, fabsf(v[h]));
-    }
-    if (t16) {
+      for (int e = 0; e < 16; ++e)
+        sums[wave][32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)][lr] = keep[i][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kShrinkRows * kShrinkRanks; i += kShrinkWaves * kWaveSize) {
+      const int row = i / kShrinkRanks, r = i % kShrinkRanks;
+      float v = 0.0f;
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o));
-      // big in [2^e, 2^(e+1)); infinities and NaN stay what they are under any factor
-      const int e = big > 0.0f ? max(-126, min(127, ilogbf(big))) : 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = lane + 64 * h;
-        if (r < R) t16[(size_t)m * R + r] = (_Float16)ldexpf(v[h], -e);
-      }
-      if (lane == 0) ts[m] = ldexpf(sc, e);
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = lane + 64 * h;
-        if (r < R) t[(size_t)m * R + r] = mid >= 0 ? v[h] * sc : 0.0f;
-      }
+      for (int w = 0; w < kShrinkWaves; ++w) v += sums[w][row][r];
+      if (m0 + row < M && r0 + r < R) tp[((size_t)c * M + m0 + row) * R + r0 + r] = v;
     }
   }
 }
 
+// One wave a row: the shares of t[m] added in order. With t16: the row scaled
+// by a power of two to a largest value in [1, 2), as the fp16 operand of the
+// wide half, and ts[m] = scale[id] / that power; else t[m] times scale[id].
+__global__ __launch_bounds__(kRowThreads) void lora_rows_kernel(const float* __restrict__ tp,
+                                                                Adapters ad,
+                                                                float* __restrict__ t,
+                                                                _Float16* __restrict__ t16,
+                                                                float* __restrict__ ts, int M,
+                                                                int KS) {
+  const int lane = threadIdx.x & 63;
+  const int m = blockIdx.x * (kRowThreads / kWaveSize) + (threadIdx.x >> 6);
+  if (m >= M) return;
+  const int R = ad.R;
+  const int id = ad.ids[m];
+  const bool live = id >= 0 && id < ad.L;
+  const float sc = live ? ad.scale[id] : 0.0f;
+  float v[2], big = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = lane + 64 * h;
+    v[h] = r < R && live ? sum_strided(tp + (size_t)m * R + r, (size_t)M * R, KS) : 0.0f;
+    big = fmaxf(big, fabsf(v[h]));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o));
+  // big in [2^e, 2^(e+1)); infinities and NaN stay what they are under any factor
+  const int e = big > 0.0f ? max(-126, min(127, ilogbf(big))) : 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = lane + 64 * h;
+    if (r >= R) continue;
+    if (t16)
+      t16[(size_t)m * R + r] = (_Float16)ldexpf(v[h], -e);
+    else
+      t[(size_t)m * R + r] = live ? v[h] * sc : 0.0f;
+  }
+  if (t16 && lane == 0) ts[m] = ldexpf(sc, e);
+}
+
 // ---------------------------------------------------------------------------
 // Adapters, wide half beside split-K partial sums: one output a lane, R fp32
-// multiply-adds on the fp16 row B[id][n] (16-byte loads).
+// multiply-adds on the fp16 row B[id][n] (16-byte loads, the first four issued
+// with the partials).
 // ---------------------------------------------------------------------------
-template <class Y>
+template <int SMAX, class Y>
 __global__ __launch_bounds__(64) void lora_finish_kernel(const float* __restrict__ part,
                                                          const float* __restrict__ t, Adapters ad,
                                                          Y* __restrict__ y, int M, int N, int S) {
   const size_t mn = (size_t)M * N;
   const size_t i = (size_t)blockIdx.x * 64 + threadIdx.x;
   if (i >= mn) return;
+  Splits<SMAX, 1> p;
+  p.load(part + i, mn, S);
   const int m = (int)(i / N);
   const int n = (int)(i - (size_t)m * N);
   const int id = ad.ids[m];
-  const float v = sum_strided(part + i, mn, S);
   float a = 0.0f;
   if (id >= 0 && id < ad.L) {
     const _Float16* br = reinterpret_cast<const _Float16*>(ad.B) + ((size_t)id * N + n) * ad.R;
     const float* tr = t + (size_t)m * ad.R;
-    for (int r = 0; r < ad.R; r += 8) {
-      float bv[8], tv[8];
-      load8(br + r, bv);
-      load8(tr + r, tv);
+    for (int r0 = 0; r0 < ad.R; r0 += 32) {
+      float bv[4][8], tv[4][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a = __builtin_fmaf(tv[e], bv[e], a);
+      for (int u = 0; u < 4; ++u) {
+        const int r = min(r0 + 8 * u, ad.R - 8);  // past the end: read again, not added
+        load8(br + r, bv[u]);
+        load8(tr + r, tv[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (r0 + 8 * u < ad.R)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a = __builtin_fmaf(tv[u][e], bv[u][e], a);
     }
   }
-  y[i] = (Y)(v + a);
+  y[i] = (Y)(p.sum(mn, S) + a);
 }
 
 // ---------------------------------------------------------------------------
@@ -372,6 +481,7 @@ __global__ __launch_bounds__(kRowThreads) void gradient_rows_kernel(
   }
 }
 
+template <int SMAX>
 __global__ __launch_bounds__(kRowThreads) void gradient_finish_kernel(
     const float* __restrict__ part, const float* __restrict__ rs, uint16_t* __restrict__ dX,
     int M, int K, int S) {
@@ -380,7 +490,9 @@ __global__ __launch_bounds__(kRowThreads) void gradient_finish_kernel(
   const size_t i = ((size_t)blockIdx.x * kRowThreads + threadIdx.x) * 4;
   if (i >= mk) return;
   const float r = rs[i / K];
-  const float4v v = sum_splits4(part + i, mk, S);
+  Splits<SMAX, 4> p;
+  p.load(part + i, mk, S);
+  const float4v v = p.sum(mk, S);
   ushort4v o;
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = float_to_bf16(v[e] * r);
@@ -393,16 +505,20 @@ unsigned blocks(size_t n, int per) { return (unsigned)((n + per - 1) / per); }
 
 hipError_t launch_glu_finish(const float* part, float* h, size_t mn, int S, int act,
                              hipStream_t st) {
-  hipLaunchKernelGGL(glu_finish_kernel, dim3(blocks(mn, 64)), dim3(64), 0, st, part, h, mn, S,
-                     act);
+  by_splits(S, [&](auto n) {
+    hipLaunchKernelGGL(glu_finish_kernel<decltype(n)::value>, dim3(blocks(mn, 64)), dim3(64), 0,
+                       st, part, h, mn, S, act);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_glu_finish_f16(const float* part, uint16_t* H, uint16_t* G, uint16_t* U,
                                  size_t mn, int S, int act, hipStream_t st) {
-  hipLaunchKernelGGL(glu_finish_f16_kernel, dim3(blocks(mn, 4 * kRowThreads)), dim3(kRowThreads),
-                     0, st, part, reinterpret_cast<_Float16*>(H), reinterpret_cast<_Float16*>(G),
-                     reinterpret_cast<_Float16*>(U), mn, S, act);
+  by_splits(S, [&](auto n) {
+    hipLaunchKernelGGL(glu_finish_f16_kernel<decltype(n)::value>, dim3(blocks(mn, 4 * kRowThreads)),
+                       dim3(kRowThreads), 0, st, part, reinterpret_cast<_Float16*>(H),
+                       reinterpret_cast<_Float16*>(G), reinterpret_cast<_Float16*>(U), mn, S, act);
+  });
   return hipGetLastError();
 }
 
@@ -413,31 +529,53 @@ hipError_t launch_lora_shrink(const float* x, const Adapters& ad, float* t, int 
   return hipGetLastError();
 }
 
-hipError_t launch_lora_shrink_f16(const uint16_t* X, const Adapters& ad, float* t, uint16_t* t16,
-                                  float* ts, int M, int K, hipStream_t st) {
+// Shares of K: a chunk or more for every wave, about 1024 workgroups at most.
+int shrink_share(int M, int K) {
+  constexpr int kStep = kShrinkWaves * kShrinkChunk;
+  const int tiles = (M + kShrinkRows - 1) / kShrinkRows;
+  const int s = std::max(1, std::min(512 / tiles, (K + kStep - 1) / kStep));
+  return ((K + s - 1) / s + kStep - 1) / kStep * kStep;
+}
+int shrink_shares(int M, int K) {
+  const int share = shrink_share(M, K);
+  return (K + share - 1) / share;
+}
+
+hipError_t launch_lora_shrink_f16(const uint16_t* X, const Adapters& ad, float* tp, float* t,
+                                  uint16_t* t16, float* ts, int M, int K, hipStream_t st) {
   const _Float16* x = reinterpret_cast<const _Float16*>(X);
-  if (M <= 64 && !t16) {
+  if (!tp) {
     hipLaunchKernelGGL(lora_shrink_kernel<_Float16>, dim3(blocks((size_t)M * ad.R, 4)),
                        dim3(kRowThreads), 0, st, x, ad, t, M, K);
-  } else {
-    hipLaunchKernelGGL(lora_shrink_tile_kernel, dim3(blocks(M, kShrinkRows)),
-                       dim3(kShrinkWaves * kWaveSize), 0, st, x, ad, t,
-                       reinterpret_cast<_Float16*>(t16), ts, M, K);
+    return hipGetLastError();
   }
+  const int share = shrink_share(M, K), KS = shrink_shares(M, K);
+  const int tiles = (M + kShrinkRows - 1) / kShrinkRows;
+  hipLaunchKernelGGL(lora_shrink_tile_kernel, dim3((unsigned)tiles * KS),
+                     dim3(kShrinkWaves * kWaveSize), 0, st, x, ad, tp, M, K, tiles, share);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(lora_rows_kernel, dim3(blocks(M, kRowThreads / kWaveSize)), dim3(kRowThreads),
+                     0, st, tp, ad, t, reinterpret_cast<_Float16*>(t16), ts, M, KS);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_finish(const float* part, const float* t, const Adapters& ad, float* y,
                               int M, int N, int S, hipStream_t st) {
-  hipLaunchKernelGGL(lora_finish_kernel<float>, dim3(blocks((size_t)M * N, 64)), dim3(64), 0, st,
-                     part, t, ad, y, M, N, S);
+  by_splits(S, [&](auto n) {
+    hipLaunchKernelGGL((lora_finish_kernel<decltype(n)::value, float>),
+                       dim3(blocks((size_t)M * N, 64)), dim3(64), 0, st, part, t, ad, y, M, N, S);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_lora_finish_f16(const float* part, const float* t, const Adapters& ad,
                                   uint16_t* Y, int M, int N, int S, hipStream_t st) {
-  hipLaunchKernelGGL(lora_finish_kernel<_Float16>, dim3(blocks((size_t)M * N, 64)), dim3(64), 0,
-                     st, part, t, ad, reinterpret_cast<_Float16*>(Y), M, N, S);
+  by_splits(S, [&](auto n) {
+    hipLaunchKernelGGL((lora_finish_kernel<decltype(n)::value, _Float16>),
+                       dim3(blocks((size_t)M * N, 64)), dim3(64), 0, st, part, t, ad,
+                       reinterpret_cast<_Float16*>(Y), M, N, S);
+  });
   return hipGetLastError();
 }
 
@@ -451,8 +589,11 @@ hipError_t launch_gradient_rows(const uint16_t* dH, const uint16_t* G, const uin
 
 hipError_t launch_gradient_finish(const float* part, const float* rs, uint16_t* dX, int M, int K,
                                   int S, hipStream_t st) {
-  hipLaunchKernelGGL(gradient_finish_kernel, dim3(blocks((size_t)M * K, 4 * kRowThreads)),
-                     dim3(kRowThreads), 0, st, part, rs, dX, M, K, S);
+  by_splits(S, [&](auto n) {
+    hipLaunchKernelGGL(gradient_finish_kernel<decltype(n)::value>,
+                       dim3(blocks((size_t)M * K, 4 * kRowThreads)), dim3(kRowThreads), 0, st, part,
+                       rs, dX, M, K, S);
+  });
   return hipGetLastError();
 }
 
