@@ -316,9 +316,9 @@ int moe_q4_0_layer(const float* x, const float* Wr, const q4_0_block* Wg, const 
  *   decode (q4_0_glu, q4_0_gemv_lora): fp32 activations, 1 <= M <= Q4_GEMV_MAX_M,
  *     any K the GEMV takes, fp32 sums and results;
  *   prompt and gradient (the others): fp16 activations, bf16 gradients, any M;
- *     K % 64 == 0 and N % 64 == 0. Each dequantized weight is rounded to fp16
- *     before its product (as in q4_0_gemm), sums are fp32, results are rounded
- *     once.
+ *     K % 64 == 0 and N % 64 == 0. A dequantized weight is rounded to fp16 before
+ *     its product, as in q4_0_gemm, or, in products of few rows, not rounded;
+ *     sums are fp32, results are rounded once.
  * fp16 and bf16 arrays, fp32 x of q4_0_gemv_lora: 16-byte aligned; Q4_0
  * matrices 2-byte, other fp32 and int32 arrays 4-byte. Every matrix, activation
  * and result array is smaller than 2 GiB. Outputs must not overlap inputs or

@@ -14,7 +14,8 @@ PROBE_LIB = os.path.join(PKG, "libq4probe.so")
 PROBE_SOURCES = ["probe.hip"]
 SOURCES = ["q4moe_api.cpp", "gemv_q4_0.hip", "gemv_mfma_q4_0.hip", "gemv_q8_0.hip",
            "moe_q4_0.hip", "router_moe.hip", "moe_prefill.hip", "gemm_q4_0.hip",
-           "gemv_noalloc.hip", "ffn_decode.hip", "ffn_gemm.hip", "ffn_rows.hip"]
+           "gemv_noalloc.hip", "ffn_decode.hip", "ffn_gemm.hip", "ffn_rows.hip",
+           "ffn_strip.hip"]
 # Per-source extra flags. The matrix-core tiles keep their accumulators in
 # ordinary VGPRs (MFMA "VGPR form"): with accumulation registers the
 # allocator rotated the accumulators between loop iterations (register copies
@@ -23,6 +24,7 @@ EXTRA = {"gemv_mfma_q4_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "moe_q4_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          # With accumulation registers the compiler gave one LDS store of
          # lora_shrink_tile_kernel a wrong offset (row 1 of a tile at row 0).
+         "ffn_strip.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "ffn_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -45,7 +45,6 @@ typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr int BN = 128, BK = 64;
 constexpr int kRole = 256;                 // lanes of one role
-constexpr int kXStages = 3;
 constexpr int kColBytes = BK * 2;          // one column or row of a step in LDS
 constexpr int kBBytes = BN * kColBytes;    // 16 KiB
 constexpr uint32_t kOut = 0x80000000u;
@@ -80,16 +79,24 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Constants of the dequantization. The mask is kept in a vector register, so
-// that masking and setting the exponent is one instruction (which takes at
-// most one constant from elsewhere).
+// Nibbles to scaled halves, two at a time. binary16 0x6400 | v is 1024 + v
+// exactly, and 0x5400 | (v << 4) is 64 + v, so every other nibble needs no
+// shift; (q - 8) is exact, the product is rounded once. The masks are kept in
+// vector registers, so that masking and setting the exponent is one instruction
+// (which takes at most one constant from elsewhere).
 struct Dequant {
-  uint32_t mask = 0x000f000fu;
-  __device__ __forceinline__ Dequant() { asm volatile("" : "+v"(mask)); }
-  __device__ __forceinline__ half2v pair(uint32_t nibbles, half2v d) const {
-    // binary16 0x6400 | v is 1024 + v exactly; (q - 8) is exact, the product is rounded once
+  uint32_t even = 0x000f000fu, odd = 0x00f000f0u;
+  __device__ __forceinline__ Dequant() { asm volatile("" : "+v"(even), "+v"(odd)); }
+  // nibbles at bits 0 and 16, or 4 and 20
+  __device__ __forceinline__ uint32_t low(uint32_t q, half2v d) const {
     const half2v off = {(_Float16)1032.0f, (_Float16)1032.0f};
-    return (__builtin_bit_cast(half2v, (nibbles & mask) | 0x64006400u) - off) * d;
+    return __builtin_bit_cast(
+        uint32_t, (__builtin_bit_cast(half2v, (q & even) | 0x64006400u) - off) * d);
+  }
+  __device__ __forceinline__ uint32_t high(uint32_t q, half2v d) const {
+    const half2v off = {(_Float16)72.0f, (_Float16)72.0f};
+    return __builtin_bit_cast(
+        uint32_t, (__builtin_bit_cast(half2v, (q & odd) | 0x54005400u) - off) * d);
   }
 };
 
@@ -103,63 +110,101 @@ __device__ __forceinline__ void lds_store8(uint8_t* p, uint2 v) {
 }
 
 // ---------------------------------------------------------------- weights
-// Forward: the step's 64 weight rows x 128 columns are 256 units of 4 rows x 8
-// columns, one a producer lane. Lane l of producer wave w: dword c = l % 8 of
-// the column half w / 2 (block c / 4, dword c % 4), rows 4 * rg .. + 3 with
-// rg = l / 8 + 8 * (w % 2). dual: half 0 is the gate, half 1 the up matrix.
+// Two registers of a lane pair 32 (16) lanes apart: afterwards a holds the lower
+// lane's values and b the upper lane's, of register a in the lower lane and of
+// register b in the upper one.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+// Forward: the step's 64 weight rows x 4 blocks are one block a producer lane,
+// two loads (loading units of 4 rows x 8 columns instead, eight loads a lane,
+// cost 75 of 430 us at 2048 x 4096 x 11008). Wave w takes rows 32 * (w % 2) .. of
+// the column half w / 2 (dual: half 0 is the gate, half 1 the up matrix); in the
+// row number of lane l bit 0 is l / 32, bit 1 is l / 16 % 2, the rest l / 2 % 8;
+// its block is l % 2. The four lanes that hold one block column of four
+// consecutive rows exchange dwords by lane swaps (a 4 x 4 transposition), which
+// leaves each with dword 2 * (l / 32) + l / 16 % 2 of all four rows: 4 rows x 8
+// columns.
 template <bool DUAL>
 struct ForwardWeights {
-  static constexpr int kLoads = 8;
   __amdgpu_buffer_rsrc_t r;
   Dequant dq;
   uint32_t vq, vd, pitch;
-  uint32_t st;  // LDS byte offset of column 0 of the unit, before the swizzle
   int n0, chunk, half;
   struct Raw {
-    uint32_t q[4], d[4];
+    uint32_t q[4], d;
   };
   __device__ __forceinline__ void init(const TileArgs& g, int tn, int t) {
     const int w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int l = t & 63;
     const int hw = w >> 1;
-    const int c = l & 7, rg = (l >> 3) + 8 * (w & 1);
-    const int blk = c >> 2, quarter = c & 3;
+    const int blk = l & 1, b4 = (l >> 4) & 1, b5 = l >> 5;
+    const int rg = 8 * (w & 1) + ((l >> 1) & 7);
     pitch = (uint32_t)g.NB * kBlockBytes;
     const uint8_t* base = (DUAL && hw) ? g.W1 : g.W0;
     r = make_rsrc(base, (uint32_t)g.wrows * pitch);
     const int col = DUAL ? 2 * tn + blk : 4 * tn + 2 * hw + blk;  // block column
     // a block column past the matrix reads zeros
-    const uint32_t o = (uint32_t)(4 * rg) * pitch + (uint32_t)col * kBlockBytes;
+    const uint32_t o = (uint32_t)(4 * rg + 2 * b4 + b5) * pitch + (uint32_t)col * kBlockBytes;
     vd = col < g.NB ? o : kOut;
-    vq = col < g.NB ? o + 2 + 4 * quarter : kOut;
-    n0 = (DUAL ? 2 * blk + hw : 2 * hw + blk) * 32 + quarter * 8;
+    vq = col < g.NB ? o + 2 : kOut;
+    n0 = (DUAL ? 2 * blk + hw : 2 * hw + blk) * 32 + (2 * b5 + b4) * 8;
     chunk = rg >> 1;
     half = rg & 1;
   }
-  __device__ __forceinline__ void load(Raw& raw, int ks) const {
+  // all loads go with part 0
+  __device__ __forceinline__ void load(Raw& raw, int ks, int i) const {
+    if (i != 0) return;
     const uint32_t so = (uint32_t)ks * (BK * pitch);
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, vq, so, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      raw.q[i] = __builtin_amdgcn_raw_buffer_load_b32(r, vq, so + i * pitch, 0);
-      raw.d[i] = __builtin_amdgcn_raw_buffer_load_b16(r, vd, so + i * pitch, 0);
-    }
+    for (int j = 0; j < 4; ++j) raw.q[j] = v[j];
+    raw.d = __builtin_amdgcn_raw_buffer_load_b16(r, vd, so, 0);
   }
-  __device__ __forceinline__ void store(const Raw& raw, uint8_t* __restrict__ bs) const {
-    const half2v d01 = __builtin_bit_cast(half2v, (raw.d[0] & 0xffffu) | (raw.d[1] << 16));
-    const half2v d23 = __builtin_bit_cast(half2v, (raw.d[2] & 0xffffu) | (raw.d[3] << 16));
-    // columns 0..3 sit in the low halves of the rows' dwords, 4..7 in the high ones
-    const uint32_t p01[2] = {__builtin_amdgcn_perm(raw.q[1], raw.q[0], 0x05040100u),
-                             __builtin_amdgcn_perm(raw.q[1], raw.q[0], 0x07060302u)};
-    const uint32_t p23[2] = {__builtin_amdgcn_perm(raw.q[3], raw.q[2], 0x05040100u),
-                             __builtin_amdgcn_perm(raw.q[3], raw.q[2], 0x07060302u)};
+  // a unit taken out of its registers: row pairs side by side, columns 0..3 from
+  // the low halves of the rows' dwords, 4..7 from the high ones
+  struct Taken {
+    uint32_t p01[2], p23[2];
+    half2v d01, d23;
+  };
+  __device__ __forceinline__ void take(const Raw& raw, Taken& k) const {
+    uint32_t q0 = raw.q[0], q1 = raw.q[1], q2 = raw.q[2], q3 = raw.q[3];
+    swap32(q0, q2);
+    swap32(q1, q3);
+    swap16(q0, q1);
+    swap16(q2, q3);  // rows 0, 2, 1, 3
+    uint32_t da = raw.d, db = raw.d;
+    swap32(da, db);
+    uint32_t p = (da & 0xffffu) | (db << 16), p2 = p;
+    swap16(p, p2);
+    k.d01 = __builtin_bit_cast(half2v, p);
+    k.d23 = __builtin_bit_cast(half2v, p2);
+    k.p01[0] = __builtin_amdgcn_perm(q2, q0, 0x05040100u);
+    k.p01[1] = __builtin_amdgcn_perm(q2, q0, 0x07060302u);
+    k.p23[0] = __builtin_amdgcn_perm(q3, q1, 0x05040100u);
+    k.p23[1] = __builtin_amdgcn_perm(q3, q1, 0x07060302u);
+  }
+  // columns 2 * part and 2 * part + 1
+  __device__ __forceinline__ void store(const Taken& k, uint8_t* __restrict__ bs, int part) const {
+    const int sh = 8 * (part & 1);
+    const uint32_t a = k.p01[part >> 1] >> sh, b = k.p23[part >> 1] >> sh;
+    uint2 v[2];
+    v[0].x = dq.low(a, k.d01);
+    v[0].y = dq.low(b, k.d23);
+    v[1].x = dq.high(a, k.d01);
+    v[1].y = dq.high(b, k.d23);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int sh = 4 * (c & 3);
-      uint2 v;
-      v.x = __builtin_bit_cast(uint32_t, dq.pair(p01[c >> 2] >> sh, d01));
-      v.y = __builtin_bit_cast(uint32_t, dq.pair(p23[c >> 2] >> sh, d23));
-      const int n = n0 + c;
-      lds_store8(bs + n * kColBytes + ((chunk ^ swz_b(n)) << 4) + half * 8, v);
+    for (int c = 0; c < 2; ++c) {
+      const int n = n0 + 2 * part + c;
+      lds_store8(bs + n * kColBytes + ((chunk ^ swz_b(n)) << 4) + half * 8, v[c]);
     }
   }
 };
@@ -167,7 +212,6 @@ struct ForwardWeights {
 // Gradient: the step's tile is 128 weight rows x 2 blocks, one block a
 // producer lane (row t / 2, block t % 2).
 struct GradientWeights {
-  static constexpr int kLoads = 2;
   __amdgpu_buffer_rsrc_t r0, r1;
   Dequant dq;
   uint32_t vq, vd;
@@ -188,118 +232,154 @@ struct GradientWeights {
     vq = vd + 2;
     nk_mat = g.nk_mat;
   }
-  __device__ __forceinline__ void load(Raw& raw, int ks) const {
+  // all loads go with part 3, when the registers are free
+  __device__ __forceinline__ void load(Raw& raw, int ks, int i) const {
+    if (i != 3) return;
     const bool second = ks >= nk_mat;
     const uint32_t so = (uint32_t)(second ? ks - nk_mat : ks) * (2 * kBlockBytes);
     const __amdgpu_buffer_rsrc_t r = second ? r1 : r0;
     const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, vq, so, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw.q[i] = v[i];
+    for (int j = 0; j < 4; ++j) raw.q[j] = v[j];
     raw.d = __builtin_amdgcn_raw_buffer_load_b16(r, vd, so, 0);
   }
-  __device__ __forceinline__ void store(const Raw& raw, uint8_t* __restrict__ bs) const {
-    const half2v d = __builtin_bit_cast(half2v, (raw.d & 0xffffu) | (raw.d << 16));
+  struct Taken {
+    uint32_t q[4];
+    half2v d;
+  };
+  __device__ __forceinline__ void take(const Raw& raw, Taken& k) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint4 v;
-      v.x = __builtin_bit_cast(uint32_t, dq.pair(raw.q[i], d));
-      v.y = __builtin_bit_cast(uint32_t, dq.pair(raw.q[i] >> 4, d));
-      v.z = __builtin_bit_cast(uint32_t, dq.pair(raw.q[i] >> 8, d));
-      v.w = __builtin_bit_cast(uint32_t, dq.pair(raw.q[i] >> 12, d));
-      *reinterpret_cast<uint4*>(bs + n * kColBytes + (((4 * b + i) ^ swz_b(n)) << 4)) = v;
-    }
+    for (int j = 0; j < 4; ++j) k.q[j] = raw.q[j];
+    k.d = __builtin_bit_cast(half2v, (raw.d & 0xffffu) | (raw.d << 16));
+  }
+  // dword `part` of the block
+  __device__ __forceinline__ void store(const Taken& k, uint8_t* __restrict__ bs, int part) const {
+    const uint32_t q = k.q[part], q8 = q >> 8;
+    uint4 v;
+    v.x = dq.low(q, k.d);
+    v.y = dq.high(q, k.d);
+    v.z = dq.low(q8, k.d);
+    v.w = dq.high(q8, k.d);
+    *reinterpret_cast<uint4*>(bs + n * kColBytes + (((4 * b + part) ^ swz_b(n)) << 4)) = v;
   }
 };
 
 // ---------------------------------------------------------------- left operand
+// A step's left operand through registers: 16-byte loads, 16-byte LDS stores.
+// (LDS-DMA copies of 16 bytes a lane kept the address unit busy for 60 to 80
+// cycles each, 32 of them a step of 256 rows.)
 template <int BM>
-struct LeftCopies {
+struct LeftOperand {
   static constexpr int kInstr = BM * kColBytes / 16 / kRole;
   __amdgpu_buffer_rsrc_t r;
-  uint32_t off[kInstr], wslot;
-  __device__ __forceinline__ void init(const TileArgs& g, int m0, int rows, int t) {
+  uint32_t off[kInstr];
+  int t;
+  struct Raw {
+    uint4 v[kInstr];
+  };
+  __device__ __forceinline__ void init(const TileArgs& g, int m0, int rows, int lane) {
+    t = lane;
     r = make_rsrc(g.X + (size_t)m0 * g.lda, (uint32_t)rows * (uint32_t)g.lda * 2u);
-    wslot = (uint32_t)__builtin_amdgcn_readfirstlane(t >> 6) * (kWaveSize * 16);
 #pragma unroll
     for (int i = 0; i < kInstr; ++i) {
-      const int slot = i * kRole + t;
+      const int slot = i * kRole + t;  // row slot / 8, 16-byte chunk slot % 8
       const int row = slot >> 3;
-      const int c = (slot & 7) ^ swz_x(row);
-      off[i] = row < rows ? ((uint32_t)row * (uint32_t)g.lda + 8u * c) * 2u : kOut;
+      off[i] = row < rows ? ((uint32_t)row * (uint32_t)g.lda + 8u * (slot & 7)) * 2u : kOut;
     }
   }
-  __device__ __forceinline__ void issue(uint8_t* __restrict__ stage, int ks) const {
-#pragma unroll
-    for (int i = 0; i < kInstr; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(stage + wslot + i * kRole * 16),
-                                               16, off[i], (uint32_t)ks * kColBytes, 0, 0);
+  __device__ __forceinline__ void load(Raw& raw, int ks, int i) const {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off[i], (uint32_t)ks * kColBytes, 0);
+    raw.v[i] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  __device__ __forceinline__ void store(const Raw& raw, uint8_t* __restrict__ stage, int i) const {
+    const int slot = i * kRole + t;
+    const int row = slot >> 3;
+    *reinterpret_cast<uint4*>(stage + row * kColBytes + (((slot & 7) ^ swz_x(row)) << 4)) =
+        raw.v[i];
   }
 };
 
-// What the producers do while step ks is multiplied: issue the copies of ks + 2,
-// dequantize ks + 1 from its registers into its LDS tile, load ks + 3 into them.
+// How many steps ahead the producers load, into registers. Few rows leave little
+// to do in a step, so that more of them have to be in flight.
+template <int BM>
+constexpr int kDepth = BM == 64 ? 4 : 2;
+
+// What the producers do while step ks is multiplied: store ks + 1 from its
+// registers into its LDS tiles, dequantized, and load ks + 1 + D into them. Steps
+// past the last repeat it, into registers that are not read.
 template <int BM, class W>
-__device__ __forceinline__ void produce_step(const W& wt, const LeftCopies<BM>& left,
-                                             typename W::Raw& raw, uint8_t* __restrict__ xs,
-                                             uint8_t* __restrict__ b, int& xst, int ks, int ke) {
-  left.issue(xs + xst * (BM * kColBytes), min(ks + 2, ke - 1));
-  xst = xst == kXStages - 1 ? 0 : xst + 1;
-  __builtin_amdgcn_sched_barrier(0);
-  wt.store(raw, b);
-  __builtin_amdgcn_sched_barrier(0);
-  wt.load(raw, min(ks + 3, ke - 1));
-  __builtin_amdgcn_sched_barrier(0);
-  // the left operand of ks + 1 landed; what was issued after it may be in flight
-  constexpr int kAfter = 2 * W::kLoads + LeftCopies<BM>::kInstr;
-  static_assert(kAfter < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(kAfter) & ~0x0f00);
+__device__ __forceinline__ void produce_step(const W& wt, const LeftOperand<BM>& left,
+                                             typename W::Raw& raw,
+                                             typename LeftOperand<BM>::Raw& lraw,
+                                             uint8_t* __restrict__ x, uint8_t* __restrict__ b,
+                                             int next) {
+  typename W::Taken k;
+  wt.take(raw, k);
+  constexpr int kPer = (LeftOperand<BM>::kInstr + 3) / 4;
+#pragma unroll
+  for (int part = 0; part < 4; ++part) {
+    wt.store(k, b, part);
+    wt.load(raw, next, part);
+#pragma unroll
+    for (int i = part * kPer; i < part * kPer + kPer; ++i)
+      if (i < LeftOperand<BM>::kInstr) {
+        left.store(lraw, x, i);
+        left.load(lraw, next, i);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
   lds_barrier();
 }
 
-// The producer waves (lane t of them) over the K steps [kb, ke). Steps past the
-// last repeat it: they land in a stage that is not read.
+// The producer waves (lane t of them) over the K steps [kb, ke).
 template <int BM, Side SIDE>
 __device__ __forceinline__ void produce(const TileArgs& g, uint8_t* __restrict__ xs,
-                                        uint8_t* __restrict__ bs, int m0, int rows, int tn, int kb, int ke, int t) {
+                                        uint8_t* __restrict__ bs, int m0, int rows, int tn, int kb,
+                                        int ke, int t) {
   using W = typename std::conditional<SIDE == kGradient, GradientWeights,
                                       ForwardWeights<SIDE == kDual>>::type;
+  constexpr int D = kDepth<BM>;
   constexpr int kXBytes = BM * kColBytes;
   W wt;
   wt.init(g, tn, t);
-  LeftCopies<BM> left;
+  LeftOperand<BM> left;
   left.init(g, m0, rows, t);
-  typename W::Raw raw[2];
-  wt.load(raw[0], kb);
-  __builtin_amdgcn_sched_barrier(0);
-  left.issue(xs, kb);
-  __builtin_amdgcn_sched_barrier(0);
-  wt.load(raw[1], min(kb + 1, ke - 1));
-  __builtin_amdgcn_sched_barrier(0);
-  left.issue(xs + kXBytes, min(kb + 1, ke - 1));
-  __builtin_amdgcn_sched_barrier(0);
-  wt.store(raw[0], bs);
-  __builtin_amdgcn_sched_barrier(0);
-  wt.load(raw[0], min(kb + 2, ke - 1));
-  __builtin_amdgcn_sched_barrier(0);
-  // left operand of step kb landed; everything issued after it may be in flight
-  constexpr int kAfter = 2 * W::kLoads + LeftCopies<BM>::kInstr;
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(kAfter) & ~0x0f00);
-  lds_barrier();
-  int xst = 2;  // stage of the copies two steps ahead
-  int ks = kb;
-  for (; ks + 2 <= ke; ks += 2) {
-    produce_step<BM>(wt, left, raw[1], xs, bs + kBBytes, xst, ks, ke);
-    produce_step<BM>(wt, left, raw[0], xs, bs, xst, ks + 1, ke);
+  typename W::Raw raw[D];
+  typename LeftOperand<BM>::Raw lraw[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+#pragma unroll
+    for (int part = 0; part < 4; ++part) wt.load(raw[d], min(kb + d, ke - 1), part);
+#pragma unroll
+    for (int i = 0; i < LeftOperand<BM>::kInstr; ++i) left.load(lraw[d], min(kb + d, ke - 1), i);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  if (ks < ke) produce_step<BM>(wt, left, raw[1], xs, bs + kBBytes, xst, ks, ke);
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no copy lands after the workgroup ends
+  produce_step<BM>(wt, left, raw[0], lraw[0], xs, bs, min(kb + D, ke - 1));
+  // unrolled so that registers and LDS tiles are named at compile time
+  static_assert(D % 2 == 0, "the LDS tiles alternate");
+  int ks = kb;
+  for (; ks + D <= ke; ks += D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+      produce_step<BM>(wt, left, raw[(u + 1) % D], lraw[(u + 1) % D],
+                       xs + ((u + 1) & 1) * kXBytes, bs + ((u + 1) & 1) * kBBytes,
+                       min(ks + u + 1 + D, ke - 1));
+  }
+#pragma unroll
+  for (int u = 0; u < D - 1; ++u)
+    if (ks + u < ke)
+      produce_step<BM>(wt, left, raw[(u + 1) % D], lraw[(u + 1) % D],
+                       xs + ((u + 1) & 1) * kXBytes, bs + ((u + 1) & 1) * kBBytes, ke - 1);
 }
 
 template <int BM, Side SIDE>
 __global__ __launch_bounds__(2 * kRole, BM == 64 ? 4 : 2) void ffn_gemm_kernel(TileArgs g) {
   constexpr int kXBytes = BM * kColBytes;
-  __shared__ __attribute__((aligned(1024))) uint8_t xs[kXStages * kXBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t bs[2 * kBBytes];
+  // two steps' left operand and weights; at the end the waves' results
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kXBytes + 2 * kBBytes];
+  uint8_t* xs = lds;
+  uint8_t* bs = lds + 2 * kXBytes;
   const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
   const int tn = L % g.tiles_n;
   const int rest = L / g.tiles_n;
@@ -331,41 +411,86 @@ __global__ __launch_bounds__(2 * kRole, BM == 64 ? 4 : 2) void ffn_gemm_kernel(T
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  lds_barrier();
-  int xst = 0;
-  for (int ks = kb; ks < ke; ++ks) {
-    const uint8_t* x = xs + xst * kXBytes;
-    xst = xst == kXStages - 1 ? 0 : xst + 1;
-    const uint8_t* b = bs + ((ks - kb) & 1) * kBBytes;
+  // A quarter of a step (16 of k) at a time: its operands, then its products.
+  struct Operands {
+    half8 a[MI], b[NJ];
+  };
+  const int ra = wm * WR + (lane & 31), rb = wn * WC + (lane & 31);
+  auto read = [&](Operands& o, const uint8_t* x, const uint8_t* b, int kk) {
+    const int kc = 2 * kk + (lane >> 5);
 #pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      const int kc = 2 * kk + (lane >> 5);
-      half8 af[MI], bf[NJ];
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int r = wm * WR + i * 32 + (lane & 31);
-        af[i] = *reinterpret_cast<const half8*>(x + r * kColBytes + ((kc ^ swz_x(r)) << 4));
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int n = wn * WC + j * 32 + (lane & 31);
-        bf[j] = *reinterpret_cast<const half8*>(b + n * kColBytes + ((kc ^ swz_b(n)) << 4));
-      }
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[i], bf[j], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < MI; ++i) {
+      const int r = ra + 32 * i;
+      o.a[i] = *reinterpret_cast<const half8*>(x + r * kColBytes + ((kc ^ swz_x(r)) << 4));
     }
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // this wave's reads done before the stages are reused
-    lds_barrier();
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int n = rb + 32 * j;
+      o.b[j] = *reinterpret_cast<const half8*>(b + n * kColBytes + ((kc ^ swz_b(n)) << 4));
+    }
+  };
+  auto multiply = [&](const Operands& o) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.b[j], o.a[i], acc[i][j], 0, 0, 0);
+  };
+  // One consumer wave a SIMD: nothing else hides the latency of its LDS reads,
+  // so the reads of a quarter are issued before the products of the one before,
+  // and a step's last products run after the barrier, over the first reads of
+  // the next step. (With the reads of each quarter waited for in turn, a step
+  // took 2500 cycles for 1024 of matrix instructions.)
+  constexpr int Q = BK / 16;
+  lds_barrier();
+  if constexpr (MI * NJ <= 4) {
+    // few products: all of a step's reads at once
+    Operands o[Q];
+    for (int ks = kb; ks < ke; ++ks) {
+      const int cur = (ks - kb) & 1;
+      const uint8_t* x = xs + cur * kXBytes;
+      const uint8_t* b = bs + cur * kBBytes;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) read(o[q], x, b, q);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // this wave's reads done before the stages are reused
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) multiply(o[q]);
+    }
+  } else {
+    Operands o[2];
+    read(o[0], xs, bs, 0);
+    for (int ks = kb; ks < ke; ++ks) {
+      const int cur = (ks - kb) & 1;
+      const uint8_t* x = xs + cur * kXBytes;
+      const uint8_t* b = bs + cur * kBBytes;
+#pragma unroll
+      for (int q = 0; q < Q - 1; ++q) {
+        read(o[(q + 1) & 1], x, b, q + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(o[q & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // this wave's reads done before the stages are reused
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      // past the last step this reads a stage that is not used
+      read(o[0], xs + (cur ^ 1) * kXBytes, bs + (cur ^ 1) * kBBytes, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(o[(Q - 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
-  // A 32 x 32 fp32 result: lane l holds column l % 32; register r holds row
-  // 8 * (r / 4) + 4 * (l / 32) + r % 4.
-  const int mw = m0 + wm * WR;     // first row of the wave
-  const int rw = rows - wm * WR;   // its live rows
-  auto row_of = [&](int i, int r) { return i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); };
+  // The weights are the left operand of the instruction, so a 32 x 32 result has
+  // its rows along the tile's columns: lane l holds row l % 32 of X, register r
+  // column 8 * (r / 4) + 4 * (l / 32) + r % 4. Four registers are four
+  // neighbouring columns.
+  const int mw = m0 + wm * WR;    // first row of the wave
+  const int rw = rows - wm * WR;  // its live rows
+  const int lr = lane & 31, l4 = 4 * (lane >> 5);
 
   if (g.S > 1) {
     const size_t slab = (size_t)g.M * g.ncols;
@@ -373,36 +498,71 @@ __global__ __launch_bounds__(2 * kRole, BM == 64 ? 4 : 2) void ffn_gemm_kernel(T
     for (int j = 0; j < NJ; ++j) {
       const int v = wn * WC + j * 32;  // column of the tile
       const int mat = SIDE == kDual ? (v >> 5) & 1 : 0;
-      const int col = (SIDE == kDual ? tn * 64 + (v >> 6) * 32 : tn * BN + v) + (lane & 31);
-      if (col >= g.ncols) continue;
+      const int col = (SIDE == kDual ? tn * 64 + (v >> 6) * 32 : tn * BN + v) + l4;
+      if (col >= g.ncols) continue;  // 32 columns of a tile are all inside or all outside
       float* dst = g.part + ((size_t)mat * g.S + sp) * slab + col;
 #pragma unroll
       for (int i = 0; i < MI; ++i)
+        if (32 * i + lr < rw)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (row_of(i, r) < rw) dst[(size_t)(mw + row_of(i, r)) * g.ncols] = acc[i][j][r];
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(dst + (size_t)(mw + 32 * i + lr) * g.ncols + 8 * q) =
+                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]);
     }
     return;
   }
 
+  // Results go through the wave's own part of LDS and leave in whole 16-byte
+  // pieces of rows (stored from the registers, two bytes a lane, the 256 x 64
+  // block of three results took 20000 cycles, as long as nine K steps).
+  constexpr int OC = SIDE == kDual ? WC / 2 : WC;  // result columns of the wave
+  constexpr int kPitch = OC * 2 + 16;              // bytes of an LDS row
+  static_assert(4 * WR * kPitch <= 2 * kXBytes + 2 * kBBytes, "results fit the stages");
+  uint8_t* out = lds + wave * (WR * kPitch);
+  const int col0 = SIDE == kDual ? tn * 64 + wn * OC : tn * BN + wn * OC;
+  auto put = [&](int i, int j, const uint2(&v)[4]) {  // 32 rows x 32 columns
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint2*>(out + (32 * i + lr) * kPitch + (32 * j + 8 * q + l4) * 2) = v[q];
+  };
+  auto flush = [&](uint16_t* dst) {
+    constexpr int kPieces = OC / 8;  // 16-byte pieces of a row
+#pragma unroll
+    for (int o = 0; o < WR * kPieces; o += kWaveSize) {
+      const int row = (o + lane) / kPieces, pc = (o + lane) % kPieces;
+      if (row < rw && col0 + 8 * pc < g.ncols)
+        *reinterpret_cast<uint4*>(dst + (size_t)(mw + row) * g.ncols + col0 + 8 * pc) =
+            *reinterpret_cast<const uint4*>(out + row * kPitch + 16 * pc);
+    }
+  };
+  auto pack16 = [](float a, float b, float c, float d) {
+    typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(uint2, half4{(_Float16)a, (_Float16)b, (_Float16)c, (_Float16)d});
+  };
+
   if constexpr (SIDE == kDual) {
 #pragma unroll
-    for (int j = 0; j < NJ; j += 2) {
-      const int col = tn * 64 + (wn * WC / 64 + j / 2) * 32 + (lane & 31);
-      if (col >= g.ncols) continue;
+    for (int what = 0; what < 3; ++what) {  // g and u, then h (acc is formed last)
+      if (what < 2 && !g.G) continue;
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int j = 0; j < NJ; j += 2)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          if (row_of(i, r) >= rw) continue;
-          const size_t o = (size_t)(mw + row_of(i, r)) * g.ncols + col;
-          const float gt = acc[i][j][r], up = acc[i][j + 1][r];
-          g.H[o] = (_Float16)(act_value(gt, g.act) * up);
-          if (g.G) {
-            g.G[o] = (_Float16)gt;
-            g.U[o] = (_Float16)up;
+        for (int i = 0; i < MI; ++i) {
+          uint2 v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float e[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float gt = acc[i][j][4 * q + u], up = acc[i][j + 1][4 * q + u];
+              e[u] = what == 0 ? gt : (what == 1 ? up : act_value<true>(gt, g.act) * up);
+            }
+            v[q] = pack16(e[0], e[1], e[2], e[3]);
           }
+          put(i, j / 2, v);
         }
+      flush(reinterpret_cast<uint16_t*>(what == 0 ? g.G : (what == 1 ? g.U : g.H)));
     }
   } else if constexpr (SIDE == kAdapters) {
     // Wide half of the adapters: for every adapter that occurs in the wave's
@@ -414,59 +574,62 @@ __global__ __launch_bounds__(2 * kRole, BM == 64 ? 4 : 2) void ffn_gemm_kernel(T
     if (id < 0 || id >= g.ad.L) id = -1;
     const unsigned long long any = __ballot(id >= 0);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int col = tn * BN + wn * WC + j * 32 + (lane & 31);
+    for (int i = 0; i < MI; ++i) {
+      const float ts = 32 * i + lr < rw ? g.ts[mw + 32 * i + lr] : 0.0f;
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
+      for (int j = 0; j < NJ; ++j) {
+        const int col = col0 + j * 32 + lr;
         float16v extra;
 #pragma unroll
         for (int r = 0; r < 16; ++r) extra[r] = 0.0f;
         unsigned band = (unsigned)(any >> (32 * i));
-        const int row = i * 32 + (lane & 31);
         while (band) {
           const int cur = __builtin_amdgcn_readlane(id, 32 * i + __builtin_ctz(band));
           const unsigned same = (unsigned)(__ballot(id == cur) >> (32 * i));
           band &= ~same;
-          const bool mine = (same >> (lane & 31)) & 1u;
+          const bool mine = (same >> lr) & 1u;
           const _Float16* bp =
               reinterpret_cast<const _Float16*>(g.ad.B) + ((size_t)cur * g.ncols + col) * R;
-          const _Float16* tp = g.t16 + (size_t)(mw + row) * R;
+          const _Float16* tp = g.t16 + (size_t)(mw + 32 * i + lr) * R;
           for (int k0 = 0; k0 < R; k0 += 16) {
             const int r0 = k0 + 8 * (lane >> 5);
             half8 a = {0, 0, 0, 0, 0, 0, 0, 0}, b = a;
             if (mine && r0 < R) a = *reinterpret_cast<const half8*>(tp + r0);
             if (col < g.ncols && r0 < R) b = *reinterpret_cast<const half8*>(bp + r0);
-            extra = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, extra, 0, 0, 0);
+            extra = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, extra, 0, 0, 0);
           }
         }
+        uint2 v[4];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int m = mw + row_of(i, r);
-          if (row_of(i, r) < rw && col < g.ncols)
-            g.H[(size_t)m * g.ncols + col] =
-                (_Float16)__builtin_fmaf(extra[r], g.ts[m], acc[i][j][r]);
+        for (int q = 0; q < 4; ++q) {
+          float e[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            e[u] = __builtin_fmaf(extra[4 * q + u], ts, acc[i][j][4 * q + u]);
+          v[q] = pack16(e[0], e[1], e[2], e[3]);
         }
+        put(i, j, v);
       }
     }
+    flush(reinterpret_cast<uint16_t*>(g.H));
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int col = tn * BN + wn * WC + j * 32 + (lane & 31);
-      if (col >= g.ncols) continue;
+    for (int i = 0; i < MI; ++i) {
+      const float rs = 32 * i + lr < rw ? g.rs[mw + 32 * i + lr] : 0.0f;
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int j = 0; j < NJ; ++j) {
+        uint2 v[4];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          if (row_of(i, r) >= rw) continue;
-          const int m = mw + row_of(i, r);
-          const float v = acc[i][j][r] * g.rs[m];
-          const uint32_t u = __builtin_bit_cast(uint32_t, v);
-          g.dX[(size_t)m * g.ncols + col] =
-              (u & 0x7fffffffu) > 0x7f800000u
-                  ? (uint16_t)((u >> 16) | 0x40u)
-                  : (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t e[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) e[u] = float_to_bf16(acc[i][j][4 * q + u] * rs);
+          v[q] = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
         }
+        put(i, j, v);
+      }
     }
+    flush(g.dX);
   }
 }
 
@@ -509,8 +672,19 @@ hipError_t launch_tiles(TileArgs& g, const FfnPlan& p, hipStream_t st) {
 
 }  // namespace
 
+// Up to so many rows go through the strips; of those, most use different
+// adapters (requests that decode), and the narrow product is formed row by row.
+constexpr int kFewRows = 64;
+
 FfnPlan plan_glu_gemm(int M, int N, int K) {
   FfnPlan p{};
+  if (M <= kFewRows) {
+    p.strip = true;
+    p.sp = plan_strip(M, N, K, 2, false);
+    p.S = p.sp.S;
+    p.ws_bytes = p.sp.part_bytes;
+    return p;
+  }
   plan_tiles(p, M, (N + 63) / 64, K / BK);
   p.ws_bytes = p.S > 1 ? (size_t)2 * p.S * M * N * sizeof(float) : 0;
   return p;
@@ -519,6 +693,12 @@ FfnPlan plan_glu_gemm(int M, int N, int K) {
 hipError_t launch_glu_gemm(const uint16_t* X, const uint8_t* Wg, const uint8_t* Wu, uint16_t* H,
                            uint16_t* G, uint16_t* U, int M, int N, int K, int act, void* ws,
                            const FfnPlan& p, hipStream_t st) {
+  if (p.strip) {
+    float* part = static_cast<float*>(ws);
+    const hipError_t err = launch_strip(X, Wg, Wu, part, M, N, K, false, p.sp, st);
+    if (err != hipSuccess) return err;
+    return launch_glu_finish_f16(part, H, G, U, (size_t)M * N, p.S, act, st);
+  }
   TileArgs g{};
   g.X = X;
   g.W0 = Wg;
@@ -538,21 +718,23 @@ hipError_t launch_glu_gemm(const uint16_t* X, const uint8_t* Wg, const uint8_t* 
   return launch_glu_finish_f16(g.part, H, G, U, (size_t)M * N, p.S, act, st);
 }
 
-// Up to so many rows most use different adapters (requests that decode), and
-// the narrow product is formed row by row.
-constexpr int kFewRows = 64;
-
 FfnPlan plan_gemm_lora(int M, int N, int K, int R) {
   FfnPlan p{};
-  plan_tiles(p, M, (N + BN - 1) / BN, K / BK);
+  p.strip = M <= kFewRows;
+  if (p.strip) {
+    p.sp = plan_strip(M, N, K, 1, false);
+    p.S = p.sp.S;
+  } else {
+    plan_tiles(p, M, (N + BN - 1) / BN, K / BK);
+  }
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
     at = align256(at + bytes);
     return o;
   };
-  if (M > kFewRows || p.S == 1) p.off_tp = take((size_t)shrink_shares(M, K) * M * R * sizeof(float));
-  if (p.S > 1) {
+  if (!p.strip) p.off_tp = take((size_t)shrink_shares(M, K) * M * R * sizeof(float));
+  if (p.strip || p.S > 1) {
     p.off_part = take((size_t)p.S * M * N * sizeof(float));
     p.off_t = take((size_t)M * R * sizeof(float));
   } else {
@@ -566,12 +748,19 @@ FfnPlan plan_gemm_lora(int M, int N, int K, int R) {
 hipError_t launch_gemm_lora(const uint16_t* X, const uint8_t* B, const Adapters& ad, uint16_t* Y,
                             int M, int N, int K, void* ws, const FfnPlan& p, hipStream_t st) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  float* t = p.S > 1 ? reinterpret_cast<float*>(w + p.off_t) : nullptr;
-  uint16_t* t16 = p.S > 1 ? nullptr : reinterpret_cast<uint16_t*>(w + p.off_t16);
-  float* ts = p.S > 1 ? nullptr : reinterpret_cast<float*>(w + p.off_ts);
-  float* tp = M > kFewRows || p.S == 1 ? reinterpret_cast<float*>(w + p.off_tp) : nullptr;
+  const bool sums = p.strip || p.S > 1;  // partial sums, finished by lora_finish
+  float* part = reinterpret_cast<float*>(w + p.off_part);
+  float* t = sums ? reinterpret_cast<float*>(w + p.off_t) : nullptr;
+  uint16_t* t16 = sums ? nullptr : reinterpret_cast<uint16_t*>(w + p.off_t16);
+  float* ts = sums ? nullptr : reinterpret_cast<float*>(w + p.off_ts);
+  float* tp = p.strip ? nullptr : reinterpret_cast<float*>(w + p.off_tp);
   hipError_t err = launch_lora_shrink_f16(X, ad, tp, t, t16, ts, M, K, st);
   if (err != hipSuccess) return err;
+  if (p.strip) {
+    err = launch_strip(X, B, nullptr, part, M, N, K, false, p.sp, st);
+    if (err != hipSuccess) return err;
+    return launch_lora_finish_f16(part, t, ad, Y, M, N, p.S, st);
+  }
   TileArgs g{};
   g.X = X;
   g.W0 = B;
@@ -580,7 +769,7 @@ hipError_t launch_gemm_lora(const uint16_t* X, const uint8_t* B, const Adapters&
   g.lda = K;
   g.NB = N / kBlockWeights;
   g.wrows = K;
-  g.part = reinterpret_cast<float*>(w + p.off_part);
+  g.part = part;
   g.H = reinterpret_cast<_Float16*>(Y);
   g.t16 = reinterpret_cast<const _Float16*>(t16);
   g.ts = ts;

@@ -10,12 +10,30 @@
 
 namespace q4 {
 
-// ---- decode (fp32, M <= 8) -------------------------------------------------
-// Split-K partial sums of the gate and the up product from one launch of the
-// decode GEMV tiles (grid of both matrices): part[2][S][M][N].
-GemvPlan plan_glu(int M, int N, int K);
+// ---- few rows (ffn_strip.hip) ------------------------------------------------
+// Split-K partial sums part[mats][S][M][N] of X . W0 and, with W1, X . W1, for
+// fp32 X of up to 8 rows or fp16 X of up to 64 (K a multiple of 32).
+struct StripPlan {
+  int DW, strips, steps, S, per;
+  size_t part_bytes;
+};
+StripPlan plan_strip(int M, int N, int K, int mats, bool f32);
+hipError_t launch_strip(const void* X, const uint8_t* W0, const uint8_t* W1, float* part, int M,
+                        int N, int K, bool f32, const StripPlan& p, hipStream_t st);
+
+// ---- decode (fp32, M <= 8; ffn_decode.hip) ----------------------------------
+// Split-K partial sums part[mats][S][M][N] by the strips or by the GEMV tiles.
+struct DecodePlan {
+  bool strip;
+  StripPlan sp;
+  GemvPlan gemv;
+  int S;
+  size_t off_t;     // adapters: fp32 [M][R] behind the partial sums
+  size_t ws_bytes;
+};
+DecodePlan plan_glu(int M, int N, int K);
 hipError_t launch_glu(const float* x, const uint8_t* Wg, const uint8_t* Wu, float* h, int M, int N,
-                      int K, int act, void* ws, const GemvPlan& p, hipStream_t st);
+                      int K, int act, void* ws, const DecodePlan& p, hipStream_t st);
 
 // ---- adapters --------------------------------------------------------------
 struct Adapters {
@@ -26,20 +44,16 @@ struct Adapters {
   int R, L;
 };
 
-// Workspace of q4_0_gemv_lora: the GEMV's partial sums (one slab at least),
-// then t[M][R].
-struct GemvLoraPlan {
-  GemvPlan gemv;
-  size_t off_t, ws_bytes;
-};
-GemvLoraPlan plan_gemv_lora(int M, int N, int K, int R);
+DecodePlan plan_gemv_lora(int M, int N, int K, int R);
 hipError_t launch_gemv_lora(const float* x, const uint8_t* B, const Adapters& ad, float* y, int M,
-                            int N, int K, void* ws, const GemvLoraPlan& p, hipStream_t st);
+                            int N, int K, void* ws, const DecodePlan& p, hipStream_t st);
 
 // ---- prompt and gradient GEMMs (fp16 matrix cores) --------------------------
 // C[M][ncols] (one or two matrices) by tiles of BM x 128, K steps of 64, S
 // splits of the contraction.
 struct FfnPlan {
+  bool strip;       // few rows: by the strips (sp), whose partial sums S counts
+  StripPlan sp;
   int BM;           // tile rows
   int tiles_m, tiles_n;
   int nk;           // K steps of the whole contraction

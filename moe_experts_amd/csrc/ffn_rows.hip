@@ -29,14 +29,6 @@ __device__ __forceinline__ float bf16_to_float(uint16_t b) {
   return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
-// fp32 -> bf16, to nearest, ties to even; a NaN stays one (its high bits with
-// the quiet bit set).
-__device__ __forceinline__ uint16_t float_to_bf16(float f) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40u);
-  return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-}
-
 // ---------------------------------------------------------------------------
 // Sums of split-K partials, in split order. They are bound by the round trip
 // of their loads, so with SMAX > 0 (S <= SMAX) all SMAX loads are issued before
@@ -115,7 +107,7 @@ __global__ __launch_bounds__(64) void glu_finish_kernel(const float* __restrict_
   Splits<SMAX, 1> g, u;
   g.load(part + i, mn, S);
   u.load(part + (size_t)S * mn + i, mn, S);
-  h[i] = act_value(g.sum(mn, S), act) * u.sum(mn, S);
+  h[i] = act_value<false>(g.sum(mn, S), act) * u.sum(mn, S);
 }
 
 template <int SMAX>
@@ -131,7 +123,7 @@ __global__ __launch_bounds__(kRowThreads) void glu_finish_f16_kernel(
   half4 h, gh, uh;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    h[e] = (_Float16)(act_value(g[e], act) * u[e]);
+    h[e] = (_Float16)(act_value<true>(g[e], act) * u[e]);
     gh[e] = (_Float16)g[e];
     uh[e] = (_Float16)u[e];
   }
@@ -409,20 +401,22 @@ __global__ __launch_bounds__(64) void lora_finish_kernel(const float* __restrict
 // binades below them stay normal. rs[m] undoes the factor after the product.
 // Groups of eight values are stored in the order 0 4 1 5 2 6 3 7, the order
 // in which masking a dword of nibbles yields half pairs.
-// One workgroup a row, two passes over it (the second from L2).
+// One workgroup a row. Up to kRowHeld groups of eight a lane (12288 columns) the
+// scaled values are formed once and held in registers; a longer row is gone
+// through twice. Bound by its bytes: 8 B a value read and 4 B written.
 // ---------------------------------------------------------------------------
+constexpr int kRowHeld = 6;
+
+template <int MATS>
 __device__ __forceinline__ void gradient_group(const uint16_t* __restrict__ dH,
                                                const uint16_t* __restrict__ G,
                                                const uint16_t* __restrict__ U, size_t at, int act,
-                                               int mats, float (&dg)[8], float (&du)[8]) {
+                                               float (&dg)[8], float (&du)[8]) {
   typedef uint16_t ushort8 __attribute__((ext_vector_type(8)));
   const ushort8 h = *reinterpret_cast<const ushort8*>(dH + at);
-  if (mats == 1) {
+  if constexpr (MATS == 1) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dg[e] = bf16_to_float(h[e]);
-      du[e] = 0.0f;
-    }
+    for (int e = 0; e < 8; ++e) dg[e] = bf16_to_float(h[e]);
     return;
   }
   const half8 g = *reinterpret_cast<const half8*>(G + at);
@@ -447,20 +441,9 @@ __device__ __forceinline__ void store_group(_Float16* p, const float (&v)[8], fl
   *reinterpret_cast<half8*>(p) = o;
 }
 
-__global__ __launch_bounds__(kRowThreads) void gradient_rows_kernel(
-    const uint16_t* __restrict__ dH, const uint16_t* __restrict__ G,
-    const uint16_t* __restrict__ U, _Float16* __restrict__ a, float* __restrict__ rs, int N,
-    int act, int mats) {
-  __shared__ float wave_big[kRowThreads / kWaveSize];
-  const int m = blockIdx.x;
-  const size_t row = (size_t)m * N;
-  float big = 0.0f;
-  for (int n = threadIdx.x * 8; n < N; n += kRowThreads * 8) {
-    float dg[8], du[8];
-    gradient_group(dH, G, U, row + n, act, mats, dg, du);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(dg[e]), fabsf(du[e])));
-  }
+// The power of two for a row whose largest value is `big`, known to one wave
+// each; the same for all lanes afterwards.
+__device__ __forceinline__ int row_exponent(float big, float* wave_big) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o));
   if ((threadIdx.x & 63) == 0) wave_big[threadIdx.x >> 6] = big;
@@ -469,15 +452,65 @@ __global__ __launch_bounds__(kRowThreads) void gradient_rows_kernel(
   for (int w = 0; w < kRowThreads / kWaveSize; ++w) big = fmaxf(big, wave_big[w]);
   // the factor and its inverse stay normal fp32 numbers; a row with an infinity
   // takes the smallest, so that its finite values stay finite
-  const int e = big > 0.0f ? 13 - max(-113, min(127, ilogbf(big))) : 0;
-  const float s = ldexpf(1.0f, e);
-  if (threadIdx.x == 0) rs[m] = ldexpf(1.0f, -e);
-  _Float16* ar = a + (size_t)m * mats * N;
-  for (int n = threadIdx.x * 8; n < N; n += kRowThreads * 8) {
+  return big > 0.0f ? 13 - max(-113, min(127, ilogbf(big))) : 0;
+}
+
+template <int MATS, int HELD>
+__global__ __launch_bounds__(kRowThreads) void gradient_rows_kernel(
+    const uint16_t* __restrict__ dH, const uint16_t* __restrict__ G,
+    const uint16_t* __restrict__ U, _Float16* __restrict__ a, float* __restrict__ rs, int N,
+    int act) {
+  __shared__ float wave_big[kRowThreads / kWaveSize];
+  constexpr int kStep = kRowThreads * 8;
+  const int m = blockIdx.x;
+  const size_t row = (size_t)m * N;
+  const int n0 = threadIdx.x * 8;
+  _Float16* ar = a + (size_t)m * MATS * N;
+  float big = 0.0f;
+  if constexpr (HELD > 0) {
+    float dg[HELD][8], du[HELD][8];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      if (n0 + i * kStep >= N) break;
+      gradient_group<MATS>(dH, G, U, row + n0 + i * kStep, act, dg[i], du[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      if (n0 + i * kStep >= N) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        big = fmaxf(big, fabsf(dg[i][e]));
+        if constexpr (MATS == 2) big = fmaxf(big, fabsf(du[i][e]));
+      }
+    }
+    const int e = row_exponent(big, wave_big);
+    const float s = ldexpf(1.0f, e);
+    if (threadIdx.x == 0) rs[m] = ldexpf(1.0f, -e);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int n = n0 + i * kStep;
+      if (n >= N) break;
+      store_group(ar + n, dg[i], s);
+      if constexpr (MATS == 2) store_group(ar + N + n, du[i], s);
+    }
+  } else {
     float dg[8], du[8];
-    gradient_group(dH, G, U, row + n, act, mats, dg, du);
-    store_group(ar + n, dg, s);
-    if (mats == 2) store_group(ar + N + n, du, s);
+    for (int n = n0; n < N; n += kStep) {
+      gradient_group<MATS>(dH, G, U, row + n, act, dg, du);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        big = fmaxf(big, fabsf(dg[e]));
+        if constexpr (MATS == 2) big = fmaxf(big, fabsf(du[e]));
+      }
+    }
+    const int e = row_exponent(big, wave_big);
+    const float s = ldexpf(1.0f, e);
+    if (threadIdx.x == 0) rs[m] = ldexpf(1.0f, -e);
+    for (int n = n0; n < N; n += kStep) {
+      gradient_group<MATS>(dH, G, U, row + n, act, dg, du);
+      store_group(ar + n, dg, s);
+      if constexpr (MATS == 2) store_group(ar + N + n, du, s);
+    }
   }
 }
 
@@ -579,12 +612,31 @@ hipError_t launch_lora_finish_f16(const float* part, const float* t, const Adapt
   return hipGetLastError();
 }
 
+template <int MATS>
+hipError_t launch_gradient_rows_t(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
+                                  uint16_t* a, float* rs, int M, int N, int act, hipStream_t st) {
+  const int groups = (N + 8 * kRowThreads - 1) / (8 * kRowThreads);
+  auto go = [&](auto held) {
+    hipLaunchKernelGGL((gradient_rows_kernel<MATS, decltype(held)::value>), dim3((unsigned)M),
+                       dim3(kRowThreads), 0, st, dH, G, U, reinterpret_cast<_Float16*>(a), rs, N,
+                       act);
+  };
+  if (groups <= 1)
+    go(std::integral_constant<int, 1>{});
+  else if (groups <= 2)
+    go(std::integral_constant<int, 2>{});
+  else if (groups <= kRowHeld)
+    go(std::integral_constant<int, kRowHeld>{});
+  else
+    go(std::integral_constant<int, 0>{});
+  return hipGetLastError();
+}
+
 hipError_t launch_gradient_rows(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
                                 uint16_t* a, float* rs, int M, int N, int act, int mats,
                                 hipStream_t st) {
-  hipLaunchKernelGGL(gradient_rows_kernel, dim3((unsigned)M), dim3(kRowThreads), 0, st, dH, G, U,
-                     reinterpret_cast<_Float16*>(a), rs, N, act, mats);
-  return hipGetLastError();
+  return mats == 2 ? launch_gradient_rows_t<2>(dH, G, U, a, rs, M, N, act, st)
+                   : launch_gradient_rows_t<1>(dH, G, U, a, rs, M, N, act, st);
 }
 
 hipError_t launch_gradient_finish(const float* part, const float* rs, uint16_t* dX, int M, int K,

@@ -1,0 +1,453 @@
+// Few rows (up to 64) through one or two Q4_0 matrices of the dense feed-forward
+// operators: split-K partial sums part[mats][S][M][N] in fp32.
+//
+// With few rows the matrices' bytes set the pace, so every wave streams weights
+// from memory straight into registers, dequantizes them there and feeds the
+// matrix cores (v_mfma_f32_16x16x32_f16) without passing them through LDS.
+//
+//   * A wave's step is 32 rows of the matrix by a strip of 128 * DW columns.
+//     Lane l holds, of the 8 rows 8 * (l / 16) .. + 7, DW dwords: the 8 * DW
+//     columns from 8 * DW * (l % 16) on. Those rows are the lane's k values of
+//     the product's right operand, so an 8 x 8 block of nibbles becomes the
+//     operands of 8 products (product c takes column c of every lane): row
+//     pairs are put side by side (v_perm), then a column pair is masked out and
+//     given an exponent, and the offset and the scale are applied in packed
+//     halves.
+//   * Odd nibbles need no shift: 0x6400 | q is 1024 + q, and 0x5400 | (q << 4)
+//     is 64 + q, both exact.
+//   * The lanes of a block share its scales: each loads some of the 8 rows'
+//     scales and hands them over inside the quad.
+//   * The waves of a workgroup take the strip's steps in turn and add their
+//     sums through LDS in wave order; the splits are added by the kernel that
+//     finishes the operator.
+//   * Exact weights: w = (q - 8) * d has up to 14 significant bits. hi =
+//     fp16(w) and lo = w - hi, which fp16 holds exactly (a multiple of d's
+//     last place), take a product each: the weights are not rounded.
+//   * fp32 activations (decode, up to 8 rows): x is scaled by a power of two to
+//     a largest value in [2^13, 2^14) for the row and the workgroup's K range,
+//     and split into hi = fp16(x) and lo = fp16(x - hi); the 16 rows of the left
+//     operand are the 8 his and the 8 los. What is lost is below 2^-22 of the
+//     value (or 2^-38 of the row's largest), under the roundings of an fp32 sum.
+#include <algorithm>
+
+#include "ffn_internal.hpp"
+#include "q4_device.hpp"
+
+namespace q4 {
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;
+constexpr int kStripThreads = kWaves * kWaveSize;
+constexpr int kStepRows = 32;
+
+struct StripArgs {
+  const void* X;       // fp16 [M][K], K % 32 == 0, or fp32 [M][K]
+  const uint8_t* W0;
+  const uint8_t* W1;
+  float* part;
+  int M, K, N, NB;
+  int strips, S, steps, per;  // steps of 32 rows in all, and of one split
+};
+
+template <int DW>
+struct StripWeights {
+  uint32_t q[8][DW];
+  uint32_t d[2 * DW];  // scales this lane loads
+};
+
+// Row pair scales 2p, 2p + 1 of the lane's block, side by side. DW = 1: four
+// lanes share a block, lane i of the quad loaded rows 2i and 2i + 1; DW = 2: two
+// lanes, the even one loaded rows 0..3, the odd one 4..7.
+template <int DW>
+__device__ __forceinline__ void scale_pairs(const StripWeights<DW>& w, half2v (&d)[4]) {
+  static_assert(DW == 1 || DW == 2, "lanes of a quad share blocks");
+  if constexpr (DW == 2) {
+    const int m0 = (int)((w.d[0] & 0xffffu) | (w.d[1] << 16));
+    const int m1 = (int)((w.d[2] & 0xffffu) | (w.d[3] << 16));
+    // quad_perm [0,0,2,2] and [1,1,3,3]
+    d[0] = __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp(m0, 0xa0, 0xf, 0xf, true));
+    d[1] = __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp(m1, 0xa0, 0xf, 0xf, true));
+    d[2] = __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp(m0, 0xf5, 0xf, 0xf, true));
+    d[3] = __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp(m1, 0xf5, 0xf, 0xf, true));
+  } else {
+    const int m = (int)((w.d[0] & 0xffffu) | (w.d[1] << 16));
+    d[0] = __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp(m, 0x00, 0xf, 0xf, true));
+    d[1] = __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp(m, 0x55, 0xf, 0xf, true));
+    d[2] = __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp(m, 0xaa, 0xf, 0xf, true));
+    d[3] = __builtin_bit_cast(half2v, __builtin_amdgcn_mov_dpp(m, 0xff, 0xf, 0xf, true));
+  }
+}
+
+// First row of a step. The last step of a K that is no multiple of 32 reaches
+// back into the one before it, whose rows meet activations of zero there.
+__device__ __forceinline__ int step_start(int step, int K) {
+  return min(step * kStepRows, max(K - kStepRows, 0));
+}
+
+// Where a lane's weights lie.
+template <int DW>
+struct StripSource {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t pitch, vq, vd;  // row 0 of the lane's 8 rows in step 0; its first scale
+  int row;                 // 8 * (l / 16)
+  int drow;                // first of the rows whose scales this lane loads
+  int K;
+  __device__ __forceinline__ void init(const StripArgs& a, const uint8_t* W, int strip, int lane) {
+    constexpr int kLanes = 4 / DW;  // lanes of a block
+    constexpr uint32_t kOut = 0x80000000u;
+    const int cg = lane & 15;
+    const int blk = strip * 4 * DW + cg / kLanes;
+    const int sub = cg % kLanes;
+    K = a.K;
+    pitch = (uint32_t)a.NB * kBlockBytes;
+    r = make_rsrc(W, (uint32_t)a.K * pitch);
+    row = 8 * (lane >> 4);
+    // a block column past the matrix reads zeros
+    vq = blk < a.NB ? (uint32_t)blk * kBlockBytes + 2 + 4 * DW * sub : kOut;
+    vd = blk < a.NB ? (uint32_t)blk * kBlockBytes : kOut;
+    drow = 2 * DW * sub;
+  }
+  __device__ __forceinline__ void load_row(StripWeights<DW>& w, int i, uint32_t o) const {
+    if constexpr (DW == 2) {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, vq + o, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) w.q[i][j] = v[j];
+    } else {
+      w.q[i][0] = __builtin_amdgcn_raw_buffer_load_b32(r, vq + o, 0, 0);
+    }
+  }
+  // Offsets stay in the lane's part of the address, which the range check sees:
+  // with fewer than 32 rows in all, the rows past them read zeros.
+  __device__ __forceinline__ void load(StripWeights<DW>& w, int step) const {
+    constexpr int ND = 2 * DW;
+    const uint32_t o = (uint32_t)(step_start(step, K) + row) * pitch;
+    const uint32_t od = vd + o + (uint32_t)drow * pitch;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+      w.d[i] = __builtin_amdgcn_raw_buffer_load_b16(r, od + i * pitch, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load_row(w, i, o + i * pitch);
+  }
+};
+
+struct StripMasks {
+  // kept in vector registers: masking and setting the exponent is one
+  // instruction, which takes at most one constant from elsewhere
+  uint32_t even = 0x000f000fu, odd = 0x00f000f0u;
+  __device__ __forceinline__ StripMasks() { asm volatile("" : "+v"(even), "+v"(odd)); }
+};
+
+// The products of one step: acc[f][c] += A[f] x column c of the strip.
+template <int RF, int DW>
+__device__ __forceinline__ void strip_products(const StripWeights<DW>& w, const half8 (&A)[RF],
+                                               float4v (&acc)[RF][8 * DW], const StripMasks& mk) {
+  half2v d[4];
+  scale_pairs<DW>(w, d);
+  const half2v off_even = {(_Float16)1032.0f, (_Float16)1032.0f};
+  const half2v off_odd = {(_Float16)72.0f, (_Float16)72.0f};
+#pragma unroll
+  for (int j = 0; j < DW; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        p[i] = __builtin_amdgcn_perm(w.q[2 * i + 1][j], w.q[2 * i][j],
+                                     h ? 0x07060302u : 0x05040100u);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint4v hi, lo;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t b = c >= 2 ? p[i] >> 8 : p[i];
+          half2v v;
+          if (c & 1)
+            v = __builtin_bit_cast(half2v, (b & mk.odd) | 0x54005400u) - off_odd;
+          else
+            v = __builtin_bit_cast(half2v, (b & mk.even) | 0x64006400u) - off_even;
+          const half2v t = v * d[i];
+          hi[i] = __builtin_bit_cast(uint32_t, t);
+          lo[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, d[i], -t));
+        }
+        const int n = 8 * j + 4 * h + c;
+#pragma unroll
+        for (int f = 0; f < RF; ++f) {
+          acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              A[f], __builtin_bit_cast(half8, hi), acc[f][n], 0, 0, 0);
+          acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              A[f], __builtin_bit_cast(half8, lo), acc[f][n], 0, 0, 0);
+        }
+      }
+    }
+}
+
+// LDS: fp32 activations [per][64 lanes][8 halves], then (from the same start)
+// the waves' sums [waves][16][128 * DW].
+template <int DW>
+constexpr int kSumBytes = kWaves * 16 * 128 * DW * 4;
+
+// fp32 activations of the steps [kb, ke) as operands in LDS; inv[m] undoes the
+// row's factor. Wave w takes rows w, w + kWaves .., in groups of 8 values: group g of
+// the row is group g % 4 of step kb + g / 4 and goes to lane 16 * (g % 4) + m
+// (its lo part to m + 8). All loads of four groups a lane are issued together;
+// the values are read again for the second pass, from cache.
+__device__ __forceinline__ void stage_split(const StripArgs& a, int kb, int ke, half8* xa,
+                                            float* inv) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int groups = 4 * (ke - kb);
+  constexpr int kU = 4, kR = 8 / kWaves;
+  __amdgpu_buffer_rsrc_t r[kR];
+#pragma unroll
+  for (int h = 0; h < kR; ++h) {  // rows past the last read zeros
+    const int m = wave + kWaves * h;
+    r[h] = make_rsrc(static_cast<const float*>(a.X) + (size_t)min(m, a.M - 1) * a.K,
+                     m < a.M ? (uint32_t)a.K * 4u : 0u);
+  }
+  auto load = [&](int g0, float(&v)[kR][kU][8]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < kR; ++h)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int g = g0 + 64 * u;
+        const int k = step_start(kb + (g >> 2), a.K) + 8 * (g & 3);
+        const uint32_t o = g < groups ? (uint32_t)k * 4u : 0x80000000u;
+        const auto p = __builtin_amdgcn_raw_buffer_load_b128(r[h], o, 0, 0);
+        const auto q = __builtin_amdgcn_raw_buffer_load_b128(r[h], o + 16, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[h][u][e] = __uint_as_float(p[e]);
+          v[h][u][4 + e] = __uint_as_float(q[e]);
+        }
+      }
+  };
+  float v[kR][kU][8], big[kR] = {};
+  for (int g0 = lane; g0 < groups + lane; g0 += 64 * kU) {
+    load(g0, v);
+#pragma unroll
+    for (int h = 0; h < kR; ++h)
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big[h] = fmaxf(big[h], fabsf(v[h][u][e]));
+  }
+  float s[kR];
+#pragma unroll
+  for (int h = 0; h < kR; ++h) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) big[h] = fmaxf(big[h], __shfl_xor(big[h], o));
+    // the factor and its inverse stay normal; an infinity is not scaled up
+    const int e = big[h] > 0.0f ? 13 - max(-113, min(127, ilogbf(big[h]))) : 0;
+    s[h] = ldexpf(1.0f, e);
+    if (lane == 0) inv[wave + kWaves * h] = ldexpf(1.0f, -e);
+  }
+  for (int g0 = lane; g0 < groups + lane; g0 += 64 * kU) {
+    if (groups > 64 * kU) load(g0, v);  // one round: still there
+#pragma unroll
+    for (int h = 0; h < kR; ++h)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int g = g0 + 64 * u;
+        if (g >= groups) continue;
+        const int step = kb + (g >> 2);
+        const int k = step_start(step, a.K) + 8 * (g & 3);
+        half8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // rows that the step before has taken
+          const float x = k + e >= step * kStepRows ? v[h][u][e] * s[h] : 0.0f;
+          hi[e] = (_Float16)x;
+          lo[e] = (_Float16)(x - (float)hi[e]);
+        }
+        half8* dst = xa + (size_t)(g >> 2) * 64 + 16 * (g & 3) + wave + kWaves * h;
+        dst[0] = hi;
+        dst[8] = lo;
+      }
+  }
+}
+
+template <int RF, int DW, bool F32>
+__global__ __launch_bounds__(kStripThreads) void strip_kernel(StripArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ float inv[8];
+  constexpr int COLS = 128 * DW;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
+  const int strip = L % a.strips;
+  const int rest = L / a.strips;
+  const int s = rest % a.S;
+  const int mat = rest / a.S;
+  const int kb = s * a.per;
+  const int ke = min(a.steps, kb + a.per);
+
+  StripSource<DW> src;
+  src.init(a, mat ? a.W1 : a.W0, strip, lane);
+  constexpr int kAhead = 2;  // steps in flight
+  StripWeights<DW> w[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) src.load(w[u], min(kb + wave + u * kWaves, ke - 1));
+
+  const half8* xa = reinterpret_cast<const half8*>(lds);
+  const _Float16* xr[RF];
+  half8 A[kAhead][RF];
+  auto load_x = [&](half8(&dst)[RF], int step) {
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+      dst[f] = *reinterpret_cast<const half8*>(xr[f] + (size_t)step * kStepRows);
+  };
+  if constexpr (F32) {
+    stage_split(a, kb, ke, reinterpret_cast<half8*>(lds), inv);
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int f = 0; f < RF; ++f)  // rows past the last repeat it, not kept
+      xr[f] = static_cast<const _Float16*>(a.X) +
+              (size_t)min(16 * f + (lane & 15), a.M - 1) * a.K + 8 * (lane >> 4);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load_x(A[u], min(kb + wave + u * kWaves, ke - 1));
+  }
+
+  float4v acc[RF][8 * DW];
+#pragma unroll
+  for (int f = 0; f < RF; ++f)
+#pragma unroll
+    for (int c = 0; c < 8 * DW; ++c) acc[f][c] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+  const StripMasks mk;
+
+  int k = kb + wave;
+  for (; k + (kAhead - 1) * kWaves < ke; k += kAhead * kWaves) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int step = k + u * kWaves;
+      if constexpr (F32) A[u][0] = xa[(size_t)(step - kb) * 64 + lane];
+      strip_products<RF, DW>(w[u], A[u], acc, mk);
+      __builtin_amdgcn_sched_barrier(0);
+      const int next = min(step + kAhead * kWaves, ke - 1);
+      src.load(w[u], next);
+      if constexpr (!F32) load_x(A[u], next);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kAhead - 1; ++u)
+    if (k + u * kWaves < ke) {  // uniform
+      if constexpr (F32) A[u][0] = xa[(size_t)(k + u * kWaves - kb) * 64 + lane];
+      strip_products<RF, DW>(w[u], A[u], acc, mk);
+    }
+
+  // The waves' sums, 16 rows at a time. A 16 x 16 result: lane l holds column
+  // l % 16, here the columns 8 * DW * (l % 16) + c of product c; register e
+  // row 4 * (l / 16) + e.
+  float* red = reinterpret_cast<float*>(lds);
+  float* out = a.part + ((size_t)mat * a.S + s) * a.M * a.N;
+  const int n0 = strip * COLS;
+#pragma unroll
+  for (int f = 0; f < RF; ++f) {
+    __syncthreads();  // the activations, or the sums before, have been read
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float* dst = red + ((size_t)wave * 16 + 4 * (lane >> 4) + e) * COLS + 8 * DW * (lane & 15);
+#pragma unroll
+      for (int c = 0; c < 8 * DW; c += 4)
+        *reinterpret_cast<float4v*>(dst + c) =
+            float4v{acc[f][c][e], acc[f][c + 1][e], acc[f][c + 2][e], acc[f][c + 3][e]};
+    }
+    __syncthreads();
+    constexpr int ROWS = F32 ? 8 : 16;
+    for (int i = threadIdx.x; i < ROWS * COLS; i += kStripThreads) {
+      const int r = i / COLS, c = i % COLS;
+      const int m = 16 * f + r;
+      float v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) {
+        v += red[(q * 16 + r) * COLS + c];
+        if constexpr (F32) v += red[(q * 16 + r + 8) * COLS + c];
+      }
+      if constexpr (F32) v *= inv[r];
+      if (m < a.M && n0 + c < a.N) out[(size_t)m * a.N + n0 + c] = v;
+    }
+  }
+}
+
+template <int RF, int DW, bool F32>
+hipError_t launch_strip_t(const StripArgs& a, int mats, hipStream_t st) {
+  int lds = kSumBytes<DW>;
+  if (F32) lds = std::max(lds, a.per * 1024);
+  hipLaunchKernelGGL((strip_kernel<RF, DW, F32>), dim3(mats * a.S * a.strips),
+                     dim3(kStripThreads), lds, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Strip width: two dwords a lane for decode (rows of 144 bytes, 64 accumulator
+// registers), one for up to 64 rows (128 accumulator registers at 64 rows).
+//
+// Splits: the workgroups, nearly all resident at once, share 256 CUs, so the
+// time goes by the CU with the most work: whole rounds of 256 times the steps of
+// a wave (one more for staging and sums), in units of about 1 us for strips of
+// two dwords, plus the partial sums, written and read again. Measured at 8 rows,
+// two matrices of 4096 x 11008 (86 strips): 2, 3, 4, 5, 6, 7, 8, 9 splits 22.6,
+// 27.2, 22.6, 22.3, 27.5, 27.4, 19.5, 27.9 us.
+StripPlan plan_strip(int M, int N, int K, int mats, bool f32) {
+  StripPlan p{};
+  p.DW = f32 ? 2 : 1;
+  p.strips = (N + 128 * p.DW - 1) / (128 * p.DW);
+  p.steps = (K + kStepRows - 1) / kStepRows;
+  const double unit = f32 ? 1.0 : 0.8;                            // us
+  const double sums = 8.0 * mats * (double)M * N / 4e6;           // us a split
+  double best = 1e30;
+  for (int s = 1; s <= p.steps && s <= 64; ++s) {
+    const int per = (p.steps + s - 1) / s;
+    if ((p.steps + per - 1) / per != s) continue;
+    if (f32 && per > 128) continue;  // 128 KiB of staged activations at most
+    const long long n = (long long)mats * p.strips * s;
+    const double cost =
+        (double)((n + 255) / 256) * ((per + kWaves - 1) / kWaves + 1) * unit + sums * s;
+    if (cost < best) {
+      best = cost;
+      p.per = per;
+      p.S = s;
+    }
+  }
+  if (p.S == 0) {  // a very long K: as few steps as the staging takes
+    p.per = 128;
+    p.S = (p.steps + 127) / 128;
+  }
+  p.part_bytes = (size_t)mats * p.S * M * N * sizeof(float);
+  return p;
+}
+
+hipError_t launch_strip(const void* X, const uint8_t* W0, const uint8_t* W1, float* part, int M,
+                        int N, int K, bool f32, const StripPlan& p, hipStream_t st) {
+  StripArgs a;
+  a.X = X;
+  a.W0 = W0;
+  a.W1 = W1;
+  a.part = part;
+  a.M = M;
+  a.K = K;
+  a.N = N;
+  a.NB = N / kBlockWeights;
+  a.strips = p.strips;
+  a.S = p.S;
+  a.steps = p.steps;
+  a.per = p.per;
+  const int mats = W1 ? 2 : 1;
+  if (f32) return launch_strip_t<1, 2, true>(a, mats, st);
+  switch ((M + 15) / 16) {
+    case 1: return launch_strip_t<1, 1, false>(a, mats, st);
+    case 2: return launch_strip_t<2, 1, false>(a, mats, st);
+    case 3: return launch_strip_t<3, 1, false>(a, mats, st);
+    case 4: return launch_strip_t<4, 1, false>(a, mats, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace q4

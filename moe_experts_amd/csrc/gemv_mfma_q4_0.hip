@@ -35,7 +35,6 @@ struct MfmaArgs {
   float* __restrict__ part;  // [S][M][N]
   int M, N, K, NB;
   int C, Kt, S;
-  const uint8_t* __restrict__ B1;  // the second matrix of a pair launch
 };
 
 // Sum the tile over its row phases and store it. Inside the wave the PW
@@ -44,7 +43,7 @@ struct MfmaArgs {
 // as (p0 + p2) + (p1 + p3), and the corrections are summed in the same order.
 // Each wave then finishes its values (odd columns / 16, minus 8 * corr) into
 // LDS, and the workgroup adds its NW waves in wave order.
-template <int MH, int JW, int NW, bool PAIR>
+template <int MH, int JW, int NW>
 __device__ __forceinline__ void mfma_tile_store(v4f (&acc)[MH][8], float (&corr)[MH],
                                                 float* smem, const MfmaArgs& a, int s, int j0,
                                                 int lane, int wave, int q, int jj) {
@@ -111,7 +110,7 @@ __device__ __forceinline__ void mfma_tile_store(v4f (&acc)[MH][8], float (&corr)
   // Every LDS read of the sum is issued before the first store.
   constexpr int IT = SH::OUT / SH::NT;
   static_assert(IT * SH::NT == SH::OUT, "whole passes over the tile");
-  float* out = (!PAIR && a.S == 1) ? a.y : a.part + (size_t)s * a.M * a.N;
+  float* out = (a.S == 1) ? a.y : a.part + (size_t)s * a.M * a.N;
   const int n0 = j0 * kBlockWeights;
   float sum[IT];
 #pragma unroll
@@ -130,21 +129,12 @@ __device__ __forceinline__ void mfma_tile_store(v4f (&acc)[MH][8], float (&corr)
   }
 }
 
-// PAIR: the grid covers two matrices of one shape (first B, then B1), whose
-// partial sums stand one after the other: part[2][S][M][N], also when S == 1.
-template <int MH, int JW, int NW, bool PAIR>
+template <int MH, int JW, int NW>
 __global__ __launch_bounds__(NW * kWaveSize) void gemv_q4_0_mfma_kernel(MfmaArgs a) {
   extern __shared__ __attribute__((aligned(16))) float smem[];
   const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
   const int c = L % a.C;
-  int s = L / a.C;
-  if constexpr (PAIR) {
-    if (s >= a.S) {
-      s -= a.S;
-      a.B = a.B1;
-      a.part += (size_t)a.S * a.M * a.N;
-    }
-  }
+  const int s = L / a.C;
   const int lane = threadIdx.x % kWaveSize;
   const int wave = threadIdx.x / kWaveSize;
   const int q = lane & 3;
@@ -160,18 +150,14 @@ __global__ __launch_bounds__(NW * kWaveSize) void gemv_q4_0_mfma_kernel(MfmaArgs
   float corr[MH];
   mfma_tile_accumulate<MH, JW, NW>(g, a.x, (uint32_t)(4 * a.M * a.K), xoff, a.M, smem, acc, corr);
 
-  mfma_tile_store<MH, JW, NW, PAIR>(acc, corr, smem, a, s, j0, lane, wave, q, jj);
+  mfma_tile_store<MH, JW, NW>(acc, corr, smem, a, s, j0, lane, wave, q, jj);
 }
 
 template <int MH, int JW, int NW>
 hipError_t launch_mfma_t(const MfmaArgs& a, hipStream_t st) {
   constexpr int lds = mfma_lds_bytes<MH, JW, NW>();
-  if (a.B1)
-    hipLaunchKernelGGL((gemv_q4_0_mfma_kernel<MH, JW, NW, true>), dim3(2 * a.C * a.S),
-                       dim3(NW * kWaveSize), lds, st, a);
-  else
-    hipLaunchKernelGGL((gemv_q4_0_mfma_kernel<MH, JW, NW, false>), dim3(a.C * a.S),
-                       dim3(NW * kWaveSize), lds, st, a);
+  hipLaunchKernelGGL((gemv_q4_0_mfma_kernel<MH, JW, NW>), dim3(a.C * a.S), dim3(NW * kWaveSize),
+                     lds, st, a);
   return hipGetLastError();
 }
 
@@ -198,7 +184,7 @@ uint64_t mfma_offset_span(int Kt, int JW, int NW, uint32_t pitch) {
 // waves in all (two per SIMD; measured: more waves only add partial sums) and
 // at least 64 rows per tile; ties go to more waves, then to fewer splits (less
 // partial-sum traffic).
-bool plan_gemv_mfma(int M, int N, int K, GemvPlan& p, int mats) {
+bool plan_gemv_mfma(int M, int N, int K, GemvPlan& p) {
   if (M < 3 || M > 8) return false;
   const int NB = N / kBlockWeights;
   const uint32_t pitch = (uint32_t)NB * kBlockBytes;
@@ -219,7 +205,7 @@ bool plan_gemv_mfma(int M, int N, int K, GemvPlan& p, int mats) {
         const int S = (K + kt - 1) / kt;
         if (S == last_S) continue;
         last_S = S;
-        const long long n = (long long)mats * C * S;
+        const long long n = (long long)C * S;
         if (n * NW > 2048) break;
         if (S > 1 && kt < 64) break;
         if (mfma_offset_span(kt, JW, NW, pitch) >= (1ull << 31)) continue;
@@ -241,13 +227,12 @@ bool plan_gemv_mfma(int M, int N, int K, GemvPlan& p, int mats) {
   p.Jt = p.JW;
   p.Lr = 0;
   p.P = p.NW * (16 / p.JW);
-  p.ws_bytes = p.S > 1 || mats > 1 ? (size_t)mats * p.S * M * N * sizeof(float) : 0;
+  p.ws_bytes = p.S > 1 ? (size_t)p.S * M * N * sizeof(float) : 0;
   return true;
 }
 
 hipError_t launch_gemv_mfma(const float* x, const uint8_t* B, float* y, int M, int N, int K,
-                            void* ws, const GemvPlan& p, hipStream_t st, bool sum,
-                            const uint8_t* B1) {
+                            void* ws, const GemvPlan& p, hipStream_t st) {
   MfmaArgs a;
   a.x = x;
   a.B = B;
@@ -260,10 +245,9 @@ hipError_t launch_gemv_mfma(const float* x, const uint8_t* B, float* y, int M, i
   a.C = p.C;
   a.Kt = p.Kt;
   a.S = p.S;
-  a.B1 = B1;
   const hipError_t err =
       M > 4 ? launch_mfma_m<2>(a, p.JW, p.NW, st) : launch_mfma_m<1>(a, p.JW, p.NW, st);
-  if (err != hipSuccess || p.S == 1 || !sum) return err;
+  if (err != hipSuccess || p.S == 1) return err;
   return launch_gemv_reduce(a.part, y, M * N, p.S, st);
 }
 

@@ -75,21 +75,20 @@ GemvPlan plan_gemv(int M, int N, int K) {
 }
 
 hipError_t launch_gemv(const float* x, const uint8_t* B, float* y, int M, int N, int K, void* ws,
-                       const GemvPlan& p, hipStream_t st, bool sum) {
-  if (p.mfma) return launch_gemv_mfma(x, B, y, M, N, K, ws, p, st, sum);
-  return launch_vector<Q4_0Format>(x, B, y, M, N, K, ws, p, st, sum);
+                       const GemvPlan& p, hipStream_t st) {
+  if (p.mfma) return launch_gemv_mfma(x, B, y, M, N, K, ws, p, st);
+  return launch_vector<Q4_0Format>(x, B, y, M, N, K, ws, p, st);
 }
 
-GemvPlan plan_gemv_pair(int M, int N, int K) {
-  GemvPlan p{};
-  if (plan_gemv_mfma(M, N, K, p, 2)) return p;
-  return plan_vector<Q4_0Format>(M, N, K, 2);
+GemvPlan plan_gemv_part(int M, int N, int K, int mats) {
+  return plan_vector<Q4_0Format>(M, N, K, mats);
 }
 
-hipError_t launch_gemv_pair(const float* x, const uint8_t* B0, const uint8_t* B1, int M, int N,
-                            int K, void* part, const GemvPlan& p, hipStream_t st) {
-  if (p.mfma) return launch_gemv_mfma(x, B0, nullptr, M, N, K, part, p, st, false, B1);
-  return launch_vector<Q4_0Format, true>(x, B0, nullptr, M, N, K, part, p, st, false, B1);
+hipError_t launch_gemv_part(const float* x, const uint8_t* B, const uint8_t* B1, int M, int N,
+                            int K, float* part, const GemvPlan& p, hipStream_t st) {
+  if (B1) return launch_vector<Q4_0Format, true>(x, B, nullptr, M, N, K, part, p, st, false, B1);
+  // with one split the tiles write y: the slab
+  return launch_vector<Q4_0Format>(x, B, part, M, N, K, part, p, st, false);
 }
 
 }  // namespace q4

@@ -362,7 +362,7 @@ int q4_0_glu(const float* x, const q4_0_block* Wg, const q4_0_block* Wu, float* 
   if (rc != Q4_OK) return rc;
   if (act != Q4_ACT_SILU && act != Q4_ACT_GELU) return Q4_EINVAL;
   if (!aligned(Wu, 2)) return Q4_EALIGN;
-  const q4::GemvPlan p = q4::plan_glu(M, N, K);
+  const q4::DecodePlan p = q4::plan_glu(M, N, K);
   rc = check_ws(ws, ws_bytes, p.ws_bytes);
   if (rc != Q4_OK) return rc;
   return from_hip(q4::launch_glu(x, bytes(Wg), bytes(Wu), h, M, N, K, act, ws, p,
@@ -441,7 +441,7 @@ int q4_0_gemv_lora(const float* x, const q4_0_block* B, const uint16_t* A, const
   if (!aligned16(x, A, Bl) || !aligned(B, 2) || !aligned(ids, 4) || !aligned(scale, 4) ||
       !aligned(y, 4))
     return Q4_EALIGN;
-  const q4::GemvLoraPlan p = q4::plan_gemv_lora(M, N, K, R);
+  const q4::DecodePlan p = q4::plan_gemv_lora(M, N, K, R);
   rc = check_ws(ws, ws_bytes, p.ws_bytes);
   if (rc != Q4_OK) return rc;
   const q4::Adapters ad{A, Bl, ids, scale, R, L};

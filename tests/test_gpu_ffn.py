@@ -51,6 +51,7 @@ def nan_ws(nbytes):
 @pytest.mark.parametrize("M,K,N", [
     (1, 1, 32), (1, 37, 32), (1, 300, 512), (1, 2048, 512), (2, 1000, 544), (3, 64, 32),
     (3, 513, 160), (4, 1024, 256), (5, 777, 96), (8, 2048, 512), (8, 1030, 1056), (7, 1, 64),
+    (3, 31, 32), (4, 33, 288), (3, 262200, 32),
 ])
 def test_glu(M, K, N, act):
     from moe_experts_amd import q4_0_glu, q4_0_glu_workspace_bytes
@@ -193,6 +194,20 @@ def test_gemm_backward(M, N, K):
     assert guards_intact(full, M * K, fill=1232.0) and ws_guards_intact(wfull, need, 0xFF)
 
 
+@pytest.mark.parametrize("N", [2048, 4096, 12288, 12352])
+def test_gradient_rows_of_every_length(N):
+    """Rows that a workgroup holds in one, two or six groups a lane, and longer ones."""
+    from moe_experts_amd import q4_0_gemm_backward, q4_0_glu_backward
+    M, K = 3, 64
+    Wg, Wu = weights(46, K, N), weights(47, K, N)
+    dH = gradient(48, M, N)
+    r = datagen.rng(49)
+    G, U = ((r.standard_normal((M, N)) * 2).astype(np.float16) for _ in range(2))
+    dX = q4_0_glu_backward(dH, to_dev(G), to_dev(U), to_dev(Wg), to_dev(Wu), K)
+    ref.check(host(dX), ref.glu_backward(values(dH), G, U, Wg, Wu, "silu"))
+    ref.check(host(q4_0_gemm_backward(dH, to_dev(Wg), K)), ref.gemm_backward(values(dH), Wg))
+
+
 def test_gradients_of_far_sizes():
     """Rows from 1e-30 to 1e30, and rows of zeros, in one call: each keeps its own precision."""
     from moe_experts_amd import q4_0_gemm_backward
@@ -267,8 +282,10 @@ def test_gemv_lora(M, K, N, R, L, kind):
     got = host(y).reshape(M, N)
     ref.check(got, ref.gemv_lora(x, B, A, Bl, ids, scale))
     assert guards_intact(full, M * N) and ws_guards_intact(wfull, need, 0xFF)
-    if kind == "none":
-        assert np.array_equal(got, host(q4_0_gemv(to_dev(x), to_dev(B), N)))
+    if kind == "none":  # the plain product, whichever tiles form it
+        want, bound = ref.product32(x, B)
+        ref.check(host(q4_0_gemv(to_dev(x), to_dev(B), N)), (want, bound))
+        ref.check(got, (want, bound))
 
 
 @pytest.mark.parametrize("kind", ["mixed", "none", "one", "ragged"])
