@@ -10,9 +10,15 @@
 
 #include <hip/hip_runtime.h>
 
+#include "ffn_internal.hpp"
+#include "q4_device.hpp"
 #include "q4moe.h"
 
 namespace q4 {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 
 // FAST takes the hardware's exp2 and reciprocal (each within about 1 ulp) instead
 // of expf and a division: s is then off by at most about (|v| + 4) * 2^-24 of
@@ -51,6 +57,63 @@ __device__ __forceinline__ uint16_t float_to_bf16(float f) {
   const uint32_t u = __builtin_bit_cast(uint32_t, f);
   if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40u);
   return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+}
+
+// ---------------------------------------------------------------------------
+// Adapters, narrow half, few rows: one wave per (row m, rank index r) runs one
+// dot product of K, eight values a lane and step; the lanes are added by a
+// fixed butterfly. Every adapter row is read once for every row of x that uses
+// it (16-byte loads), so this form is for rows that mostly use different
+// adapters. A row without adapter gets zeros.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4v a = *reinterpret_cast<const float4v*>(p);
+  const float4v b = *reinterpret_cast<const float4v*>(p + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = a[e];
+    v[4 + e] = b[e];
+  }
+}
+__device__ __forceinline__ void load8(const _Float16* p, float (&v)[8]) {
+  const half8 a = *reinterpret_cast<const half8*>(p);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (float)a[e];
+}
+
+template <class X>
+__device__ __forceinline__ void shrink_wave(const X* __restrict__ x, const Adapters& ad,
+                                            float* __restrict__ t, int M, int K, int w) {
+  const int lane = threadIdx.x & 63;
+  const int m = w / ad.R;
+  if (m >= M) return;
+  const int r = w - m * ad.R;
+  const int id = ad.ids[m];
+  float sum = 0.0f;
+  if (id >= 0 && id < ad.L) {
+    const X* xr = x + (size_t)m * K;
+    const _Float16* ar = reinterpret_cast<const _Float16*>(ad.A) + ((size_t)id * ad.R + r) * K;
+    constexpr int kStep = 64 * 8, kUnroll = 4;
+    for (int k0 = lane * 8; k0 < K; k0 += kStep * kUnroll) {
+      float xv[kUnroll][8], av[kUnroll][8];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        // past the end the last group is read again and not added
+        const int k = min(k0 + u * kStep, K - 8);
+        load8(xr + k, xv[u]);
+        load8(ar + k, av[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (k0 + u * kStep < K)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(xv[u][e], av[u][e], sum);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    sum *= ad.scale[id];
+  }
+  if (lane == 0) t[(size_t)m * ad.R + r] = sum;
 }
 
 }  // namespace q4

@@ -39,8 +39,6 @@
 namespace q4 {
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr int BN = 128, BK = 64;
@@ -99,15 +97,6 @@ struct Dequant {
         uint32_t, (__builtin_bit_cast(half2v, (q & odd) | 0x54005400u) - off) * d);
   }
 };
-
-// An 8-byte LDS store that the compiler does not order after the LDS copies in
-// flight (written as an assignment it waited for all of them, though they go to
-// another array). The barrier after it waits for it (lgkmcnt).
-__device__ __forceinline__ void lds_store8(uint8_t* p, uint2 v) {
-  const uint32_t at =
-      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)p;
-  asm volatile("ds_write_b64 %0, %1" ::"v"(at), "v"(__builtin_bit_cast(uint64_t, v)) : "memory");
-}
 
 // ---------------------------------------------------------------- weights
 // Two registers of a lane pair 32 (16) lanes apart: afterwards a holds the lower
@@ -204,7 +193,7 @@ struct ForwardWeights {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int n = n0 + 2 * part + c;
-      lds_store8(bs + n * kColBytes + ((chunk ^ swz_b(n)) << 4) + half * 8, v[c]);
+      *reinterpret_cast<uint2*>(bs + n * kColBytes + ((chunk ^ swz_b(n)) << 4) + half * 8) = v[c];
     }
   }
 };
@@ -374,7 +363,7 @@ __device__ __forceinline__ void produce(const TileArgs& g, uint8_t* __restrict__
 }
 
 template <int BM, Side SIDE>
-__global__ __launch_bounds__(2 * kRole, BM == 64 ? 4 : 2) void ffn_gemm_kernel(TileArgs g) {
+__global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(TileArgs g) {
   constexpr int kXBytes = BM * kColBytes;
   // two steps' left operand and weights; at the end the waves' results
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kXBytes + 2 * kBBytes];
@@ -443,7 +432,7 @@ __global__ __launch_bounds__(2 * kRole, BM == 64 ? 4 : 2) void ffn_gemm_kernel(T
   // took 2500 cycles for 1024 of matrix instructions.)
   constexpr int Q = BK / 16;
   lds_barrier();
-  if constexpr (MI * NJ <= 4) {
+  if constexpr (MI * NJ <= 2) {
     // few products: all of a step's reads at once
     Operands o[Q];
     for (int ks = kb; ks < ke; ++ks) {
@@ -633,22 +622,44 @@ __global__ __launch_bounds__(2 * kRole, BM == 64 ? 4 : 2) void ffn_gemm_kernel(T
   }
 }
 
-// Tiles and splits of C[M][...]: 64-row tiles (56 KB of LDS, two workgroups a
-// CU) up to 128 rows, 256-row tiles above; the contraction is split until the
-// grid has one workgroup for every place on the GPU, in pieces of at least
-// four steps.
-void plan_tiles(FfnPlan& p, int M, int tiles_n, int nk) {
-  p.BM = M <= 128 ? 64 : 256;
-  p.tiles_m = (M + p.BM - 1) / p.BM;
+// Tile height (64, 128 or 256 rows) and splits of the contraction, by the time a
+// CU with the most work takes. n workgroups are k = ceil(n / 256) a CU; a K step
+// costs it, in us (from sweeps of heights and splits at 96 to 2048 rows):
+//   256 rows: 0.68 with few CUs busy, up to 1.05 with all (the clock falls to
+//             1.7 GHz under full load);
+//   128 rows: 0.44 alone, 0.60 each with two on a CU (LDS and registers allow it);
+//    64 rows: 0.40 alone, 0.45 each.
+// A workgroup costs its prologue and results (3, 2 or 1.5 us) besides, splits
+// the partial sums, written and read at 4.5 TB/s, and a kernel that adds them.
+// Full tiles win while they fill the GPU (2048 rows, 4096 x 11008 twice: 624,
+// 430, 398 us with 64, 128, 256 rows), lower ones below (400 rows, 4096 x 4096
+// twice: 67, 44, 52 us; 200 rows of a gradient: 128 rows in 4 splits 23.8 us,
+// 256 rows in 8 splits 28.2).
+void plan_tiles(FfnPlan& p, int M, int tiles_n, int nk, size_t sum_cols) {
+  const int heights[3] = {64, 128, 256};
+  const double start[3] = {1.5, 2.0, 3.0};
+  double best = 1e30;
   p.tiles_n = tiles_n;
   p.nk = nk;
-  const long long tiles = (long long)p.tiles_m * tiles_n;
-  const int places = p.BM == 64 ? 512 : 256;
-  long long s = places / tiles;
-  if (s > nk / 4) s = nk / 4;
-  if (s < 1) s = 1;
-  p.kper = (int)((nk + s - 1) / s);
-  p.S = (nk + p.kper - 1) / p.kper;
+  for (int h = 0; h < 3; ++h)
+    for (int s = 1; s <= 16 && (s == 1 || nk / s >= 2); ++s) {
+      const int kper = (nk + s - 1) / s;
+      if ((nk + kper - 1) / kper != s) continue;
+      const int tiles_m = (M + heights[h] - 1) / heights[h];
+      const double n = (double)tiles_m * tiles_n * s;
+      const double k = (double)(((long long)n + 255) / 256);
+      const double step = h == 2 ? 0.68 + 0.37 * n / (256.0 * k)
+                          : h == 1 ? (k == 1 ? 0.44 : 0.60) : (k == 1 ? 0.40 : 0.45);
+      double cost = k * (kper * step + start[h]);
+      if (s > 1) cost += 4.0 + s * (double)M * (double)sum_cols * 8.0 / 4.5e6;
+      if (cost < best) {
+        best = cost;
+        p.BM = heights[h];
+        p.tiles_m = tiles_m;
+        p.kper = kper;
+        p.S = s;
+      }
+    }
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -663,6 +674,9 @@ hipError_t launch_tiles(TileArgs& g, const FfnPlan& p, hipStream_t st) {
   if (grid > 0x7fffffLL) return hipErrorInvalidValue;  // 2^32 lanes
   if (p.BM == 64)
     hipLaunchKernelGGL((ffn_gemm_kernel<64, SIDE>), dim3((unsigned)grid), dim3(2 * kRole), 0, st,
+                       g);
+  else if (p.BM == 128)
+    hipLaunchKernelGGL((ffn_gemm_kernel<128, SIDE>), dim3((unsigned)grid), dim3(2 * kRole), 0, st,
                        g);
   else
     hipLaunchKernelGGL((ffn_gemm_kernel<256, SIDE>), dim3((unsigned)grid), dim3(2 * kRole), 0,
@@ -685,7 +699,7 @@ FfnPlan plan_glu_gemm(int M, int N, int K) {
     p.ws_bytes = p.sp.part_bytes;
     return p;
   }
-  plan_tiles(p, M, (N + 63) / 64, K / BK);
+  plan_tiles(p, M, (N + 63) / 64, K / BK, (size_t)2 * N);
   p.ws_bytes = p.S > 1 ? (size_t)2 * p.S * M * N * sizeof(float) : 0;
   return p;
 }
@@ -725,7 +739,7 @@ FfnPlan plan_gemm_lora(int M, int N, int K, int R) {
     p.sp = plan_strip(M, N, K, 1, false);
     p.S = p.sp.S;
   } else {
-    plan_tiles(p, M, (N + BN - 1) / BN, K / BK);
+    plan_tiles(p, M, (N + BN - 1) / BN, K / BK, (size_t)N);
   }
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -753,14 +767,14 @@ hipError_t launch_gemm_lora(const uint16_t* X, const uint8_t* B, const Adapters&
   float* t = sums ? reinterpret_cast<float*>(w + p.off_t) : nullptr;
   uint16_t* t16 = sums ? nullptr : reinterpret_cast<uint16_t*>(w + p.off_t16);
   float* ts = sums ? nullptr : reinterpret_cast<float*>(w + p.off_ts);
-  float* tp = p.strip ? nullptr : reinterpret_cast<float*>(w + p.off_tp);
-  hipError_t err = launch_lora_shrink_f16(X, ad, tp, t, t16, ts, M, K, st);
-  if (err != hipSuccess) return err;
   if (p.strip) {
-    err = launch_strip(X, B, nullptr, part, M, N, K, false, p.sp, st);
+    const hipError_t err = launch_strip(X, B, nullptr, part, M, N, K, false, p.sp, st, &ad, t);
     if (err != hipSuccess) return err;
     return launch_lora_finish_f16(part, t, ad, Y, M, N, p.S, st);
   }
+  float* tp = reinterpret_cast<float*>(w + p.off_tp);
+  hipError_t err = launch_lora_shrink(X, ad, tp, t, t16, ts, M, K, st);
+  if (err != hipSuccess) return err;
   TileArgs g{};
   g.X = X;
   g.W0 = B;
@@ -781,7 +795,7 @@ hipError_t launch_gemm_lora(const uint16_t* X, const uint8_t* B, const Adapters&
 
 FfnPlan plan_gradient(int M, int N, int K, int mats) {
   FfnPlan p{};
-  plan_tiles(p, M, (K + BN - 1) / BN, mats * (N / BK));
+  plan_tiles(p, M, (K + BN - 1) / BN, mats * (N / BK), (size_t)K);
   p.off_a = 0;
   size_t at = align256((size_t)M * mats * N * 2);
   p.off_rs = at;

@@ -10,16 +10,27 @@
 
 namespace q4 {
 
+// ---- adapters --------------------------------------------------------------
+struct Adapters {
+  const uint16_t* A;    // fp16 [L][R][K]
+  const uint16_t* B;    // fp16 [L][N][R]
+  const int32_t* ids;   // [M], outside [0, L): no adapter
+  const float* scale;   // [L]
+  int R, L;
+};
+
 // ---- few rows (ffn_strip.hip) ------------------------------------------------
 // Split-K partial sums part[mats][S][M][N] of X . W0 and, with W1, X . W1, for
-// fp32 X of up to 8 rows or fp16 X of up to 64 (K a multiple of 32).
+// fp32 X of up to 8 rows or fp16 X of up to 64 (K a multiple of 32). With ad, the
+// same launch forms the adapters' narrow product t[M][R] (scale included).
 struct StripPlan {
   int DW, strips, steps, S, per;
   size_t part_bytes;
 };
 StripPlan plan_strip(int M, int N, int K, int mats, bool f32);
 hipError_t launch_strip(const void* X, const uint8_t* W0, const uint8_t* W1, float* part, int M,
-                        int N, int K, bool f32, const StripPlan& p, hipStream_t st);
+                        int N, int K, bool f32, const StripPlan& p, hipStream_t st,
+                        const Adapters* ad = nullptr, float* t = nullptr);
 
 // ---- decode (fp32, M <= 8; ffn_decode.hip) ----------------------------------
 // Split-K partial sums part[mats][S][M][N] by the strips or by the GEMV tiles.
@@ -34,15 +45,6 @@ struct DecodePlan {
 DecodePlan plan_glu(int M, int N, int K);
 hipError_t launch_glu(const float* x, const uint8_t* Wg, const uint8_t* Wu, float* h, int M, int N,
                       int K, int act, void* ws, const DecodePlan& p, hipStream_t st);
-
-// ---- adapters --------------------------------------------------------------
-struct Adapters {
-  const uint16_t* A;    // fp16 [L][R][K]
-  const uint16_t* B;    // fp16 [L][N][R]
-  const int32_t* ids;   // [M], outside [0, L): no adapter
-  const float* scale;   // [L]
-  int R, L;
-};
 
 DecodePlan plan_gemv_lora(int M, int N, int K, int R);
 hipError_t launch_gemv_lora(const float* x, const uint8_t* B, const Adapters& ad, float* y, int M,
@@ -89,14 +91,11 @@ hipError_t launch_glu_finish(const float* part, float* h, size_t mn, int S, int 
                              hipStream_t st);
 hipError_t launch_glu_finish_f16(const float* part, uint16_t* H, uint16_t* G, uint16_t* U,
                                  size_t mn, int S, int act, hipStream_t st);
-// t[m][r] = scale[id] * sum_k x[m][k] * A[id][r][k], 0 for a row without adapter.
-hipError_t launch_lora_shrink(const float* x, const Adapters& ad, float* t, int M, int K,
-                              hipStream_t st);
-// Many rows (tp set): tp[shares][M][R] is scratch, the result is t, or, with
-// t16, t16 and ts (FfnPlan). Few rows (tp null): t.
+// t[m][r] = scale[id] * sum_k x[m][k] * A[id][r][k], 0 for a row without adapter,
+// or, with t16, t16 and ts (FfnPlan); tp[shares][M][R] is scratch.
 int shrink_shares(int M, int K);
-hipError_t launch_lora_shrink_f16(const uint16_t* X, const Adapters& ad, float* tp, float* t,
-                                  uint16_t* t16, float* ts, int M, int K, hipStream_t st);
+hipError_t launch_lora_shrink(const uint16_t* X, const Adapters& ad, float* tp, float* t,
+                              uint16_t* t16, float* ts, int M, int K, hipStream_t st);
 // y[m][n] = sum_s part[s][m][n] + sum_r t[m][r] * B[id][n][r]
 hipError_t launch_lora_finish(const float* part, const float* t, const Adapters& ad, float* y,
                               int M, int N, int S, hipStream_t st);

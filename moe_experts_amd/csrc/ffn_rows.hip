@@ -2,7 +2,8 @@
 // after the products with the Q4_0 matrices.
 //
 //   glu_finish       h = act(g) * u from the split-K partial sums of g and u
-//   lora_shrink      t[m] = scale[id] * x[m] . A[id]^T, the adapters' narrow half
+//   lora_shrink      t[m] = scale[id] * x[m] . A[id]^T, the adapters' narrow half (many
+//                    rows; few rows: shrink_wave in the strips' launch)
 //   lora_finish      y = sum of partials + t[m] . B[id]^T, the wide half
 //   gradient_rows    dG = dH * U * act'(G) and dU = dH * act(G), as the fp16
 //                    left operand of the gradient GEMM
@@ -19,9 +20,7 @@
 namespace q4 {
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kRowThreads = 256;
 
@@ -132,71 +131,6 @@ __global__ __launch_bounds__(kRowThreads) void glu_finish_f16_kernel(
     *reinterpret_cast<half4*>(G + i) = gh;
     *reinterpret_cast<half4*>(U + i) = uh;
   }
-}
-
-// ---------------------------------------------------------------------------
-// Adapters, narrow half, few rows: one wave per (row m, rank index r) runs one
-// dot product of K, eight values a lane and step; the lanes are added by a
-// fixed butterfly. Every adapter row is read once for every row of x that uses
-// it (16-byte loads), so this form is for rows that mostly use different
-// adapters. A row without adapter gets zeros.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4v a = *reinterpret_cast<const float4v*>(p);
-  const float4v b = *reinterpret_cast<const float4v*>(p + 4);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = a[e];
-    v[4 + e] = b[e];
-  }
-}
-__device__ __forceinline__ void load8(const _Float16* p, float (&v)[8]) {
-  const half8 a = *reinterpret_cast<const half8*>(p);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = (float)a[e];
-}
-
-template <class X>
-__device__ __forceinline__ void shrink_wave(const X* __restrict__ x, const Adapters& ad,
-                                            float* __restrict__ t, int M, int K, int w) {
-  const int lane = threadIdx.x & 63;
-  const int m = w / ad.R;
-  if (m >= M) return;
-  const int r = w - m * ad.R;
-  const int id = ad.ids[m];
-  float sum = 0.0f;
-  if (id >= 0 && id < ad.L) {
-    const X* xr = x + (size_t)m * K;
-    const _Float16* ar = reinterpret_cast<const _Float16*>(ad.A) + ((size_t)id * ad.R + r) * K;
-    constexpr int kStep = 64 * 8, kUnroll = 4;
-    for (int k0 = lane * 8; k0 < K; k0 += kStep * kUnroll) {
-      float xv[kUnroll][8], av[kUnroll][8];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        // past the end the last group is read again and not added
-        const int k = min(k0 + u * kStep, K - 8);
-        load8(xr + k, xv[u]);
-        load8(ar + k, av[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (k0 + u * kStep < K)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(xv[u][e], av[u][e], sum);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-    sum *= ad.scale[id];
-  }
-  if (lane == 0) t[(size_t)m * ad.R + r] = sum;
-}
-
-template <class X>
-__global__ __launch_bounds__(kRowThreads) void lora_shrink_kernel(const X* __restrict__ x,
-                                                                  Adapters ad,
-                                                                  float* __restrict__ t, int M,
-                                                                  int K) {
-  shrink_wave(x, ad, t, M, K, blockIdx.x * (kRowThreads / kWaveSize) + threadIdx.x / kWaveSize);
 }
 
 // ---------------------------------------------------------------------------
@@ -555,13 +489,6 @@ hipError_t launch_glu_finish_f16(const float* part, uint16_t* H, uint16_t* G, ui
   return hipGetLastError();
 }
 
-hipError_t launch_lora_shrink(const float* x, const Adapters& ad, float* t, int M, int K,
-                              hipStream_t st) {
-  hipLaunchKernelGGL(lora_shrink_kernel<float>, dim3(blocks((size_t)M * ad.R, 4)),
-                     dim3(kRowThreads), 0, st, x, ad, t, M, K);
-  return hipGetLastError();
-}
-
 // Shares of K: a chunk or more for every wave, about 1024 workgroups at most.
 int shrink_share(int M, int K) {
   constexpr int kStep = kShrinkWaves * kShrinkChunk;
@@ -574,18 +501,13 @@ int shrink_shares(int M, int K) {
   return (K + share - 1) / share;
 }
 
-hipError_t launch_lora_shrink_f16(const uint16_t* X, const Adapters& ad, float* tp, float* t,
-                                  uint16_t* t16, float* ts, int M, int K, hipStream_t st) {
-  const _Float16* x = reinterpret_cast<const _Float16*>(X);
-  if (!tp) {
-    hipLaunchKernelGGL(lora_shrink_kernel<_Float16>, dim3(blocks((size_t)M * ad.R, 4)),
-                       dim3(kRowThreads), 0, st, x, ad, t, M, K);
-    return hipGetLastError();
-  }
+hipError_t launch_lora_shrink(const uint16_t* X, const Adapters& ad, float* tp, float* t,
+                              uint16_t* t16, float* ts, int M, int K, hipStream_t st) {
   const int share = shrink_share(M, K), KS = shrink_shares(M, K);
   const int tiles = (M + kShrinkRows - 1) / kShrinkRows;
   hipLaunchKernelGGL(lora_shrink_tile_kernel, dim3((unsigned)tiles * KS),
-                     dim3(kShrinkWaves * kWaveSize), 0, st, x, ad, tp, M, K, tiles, share);
+                     dim3(kShrinkWaves * kWaveSize), 0, st, reinterpret_cast<const _Float16*>(X),
+                     ad, tp, M, K, tiles, share);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(lora_rows_kernel, dim3(blocks(M, kRowThreads / kWaveSize)), dim3(kRowThreads),

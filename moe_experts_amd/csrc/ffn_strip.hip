@@ -29,16 +29,15 @@
 //     operand are the 8 his and the 8 los. What is lost is below 2^-22 of the
 //     value (or 2^-38 of the row's largest), under the roundings of an fp32 sum.
 #include <algorithm>
+#include <type_traits>
 
+#include "ffn_device.hpp"
 #include "ffn_internal.hpp"
 #include "q4_device.hpp"
 
 namespace q4 {
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef float float4v __attribute__((ext_vector_type(4)));
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
@@ -52,6 +51,9 @@ struct StripArgs {
   float* part;
   int M, K, N, NB;
   int strips, S, steps, per;  // steps of 32 rows in all, and of one split
+  int extra;                  // first workgroups: the adapters' narrow product
+  Adapters ad;
+  float* t;
 };
 
 template <int DW>
@@ -278,7 +280,14 @@ __global__ __launch_bounds__(kStripThreads) void strip_kernel(StripArgs a) {
   constexpr int COLS = 128 * DW;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
+  if ((int)blockIdx.x < a.extra) {
+    // Adapters' narrow product, a wave for each (row, rank index): beside the
+    // strips in one launch, whose first workgroups these are.
+    using T = typename std::conditional<F32, float, _Float16>::type;
+    shrink_wave(static_cast<const T*>(a.X), a.ad, a.t, a.M, a.K, (int)blockIdx.x * kWaves + wave);
+    return;
+  }
+  const int L = xcd_logical_tile((int)blockIdx.x - a.extra, (int)gridDim.x - a.extra);
   const int strip = L % a.strips;
   const int rest = L / a.strips;
   const int s = rest % a.S;
@@ -379,7 +388,7 @@ template <int RF, int DW, bool F32>
 hipError_t launch_strip_t(const StripArgs& a, int mats, hipStream_t st) {
   int lds = kSumBytes<DW>;
   if (F32) lds = std::max(lds, a.per * 1024);
-  hipLaunchKernelGGL((strip_kernel<RF, DW, F32>), dim3(mats * a.S * a.strips),
+  hipLaunchKernelGGL((strip_kernel<RF, DW, F32>), dim3(a.extra + mats * a.S * a.strips),
                      dim3(kStripThreads), lds, st, a);
   return hipGetLastError();
 }
@@ -425,8 +434,9 @@ StripPlan plan_strip(int M, int N, int K, int mats, bool f32) {
 }
 
 hipError_t launch_strip(const void* X, const uint8_t* W0, const uint8_t* W1, float* part, int M,
-                        int N, int K, bool f32, const StripPlan& p, hipStream_t st) {
-  StripArgs a;
+                        int N, int K, bool f32, const StripPlan& p, hipStream_t st,
+                        const Adapters* ad, float* t) {
+  StripArgs a{};
   a.X = X;
   a.W0 = W0;
   a.W1 = W1;
@@ -439,6 +449,12 @@ hipError_t launch_strip(const void* X, const uint8_t* W0, const uint8_t* W1, flo
   a.S = p.S;
   a.steps = p.steps;
   a.per = p.per;
+  if (ad) {
+    a.ad = *ad;
+    a.t = t;
+    // a multiple of the XCDs, so that the strips' workgroups keep theirs
+    a.extra = ((M * ad->R + kWaves - 1) / kWaves + kNumXcd - 1) / kNumXcd * kNumXcd;
+  }
   const int mats = W1 ? 2 : 1;
   if (f32) return launch_strip_t<1, 2, true>(a, mats, st);
   switch ((M + 15) / 16) {

@@ -80,15 +80,11 @@ hipError_t launch_gemv(const float* x, const uint8_t* B, float* y, int M, int N,
   return launch_vector<Q4_0Format>(x, B, y, M, N, K, ws, p, st);
 }
 
-GemvPlan plan_gemv_part(int M, int N, int K, int mats) {
-  return plan_vector<Q4_0Format>(M, N, K, mats);
-}
+GemvPlan plan_gemv_pair(int M, int N, int K) { return plan_vector<Q4_0Format>(M, N, K, 2); }
 
-hipError_t launch_gemv_part(const float* x, const uint8_t* B, const uint8_t* B1, int M, int N,
+hipError_t launch_gemv_pair(const float* x, const uint8_t* B, const uint8_t* B1, int M, int N,
                             int K, float* part, const GemvPlan& p, hipStream_t st) {
-  if (B1) return launch_vector<Q4_0Format, true>(x, B, nullptr, M, N, K, part, p, st, false, B1);
-  // with one split the tiles write y: the slab
-  return launch_vector<Q4_0Format>(x, B, part, M, N, K, part, p, st, false);
+  return launch_vector<Q4_0Format, true>(x, B, nullptr, M, N, K, part, p, st, B1);
 }
 
 }  // namespace q4

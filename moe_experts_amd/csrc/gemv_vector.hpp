@@ -188,7 +188,7 @@ GemvPlan plan_vector(int M, int N, int K, int mats = 1) {
 }
 
 template <class Fmt, int M, bool PAIR>
-hipError_t launch_vector_m(const GemvArgs& a, bool staged, bool sum, hipStream_t st) {
+hipError_t launch_vector_m(const GemvArgs& a, bool staged, hipStream_t st) {
   const dim3 grid((PAIR ? 2 : 1) * a.C * a.S);
   constexpr int LPB = Fmt::lanes_per_block(M);
   const int rf = 4 * phase_lds_floats<M, LPB, Fmt>();
@@ -210,16 +210,15 @@ hipError_t launch_vector_m(const GemvArgs& a, bool staged, bool sum, hipStream_t
                        st, a);
   }
   hipError_t err = hipGetLastError();
-  if (err != hipSuccess || a.S == 1 || !sum) return err;
+  if (err != hipSuccess || a.S == 1 || PAIR) return err;
   return launch_gemv_reduce(a.part, a.y, M * a.N, a.S, st);
 }
 
-// Launch a plan of plan_vector<Fmt> (main kernel, then, with sum, the split-K
-// sum). PAIR: B and B1 by a plan for two matrices, no sum.
+// Launch a plan of plan_vector<Fmt> (main kernel, then the split-K sum). PAIR: B
+// and B1 by a plan for two matrices, no sum.
 template <class Fmt, bool PAIR = false>
 hipError_t launch_vector(const float* x, const uint8_t* B, float* y, int M, int N, int K, void* ws,
-                         const GemvPlan& p, hipStream_t st, bool sum = true,
-                         const uint8_t* B1 = nullptr) {
+                         const GemvPlan& p, hipStream_t st, const uint8_t* B1 = nullptr) {
   GemvArgs a;
   a.x = x;
   a.B = B;
@@ -240,17 +239,24 @@ hipError_t launch_vector(const float* x, const uint8_t* B, float* y, int M, int 
   const bool staged = stages_in_lds<Fmt>() && p.Jt == kStagedJt && a.NB % 8 == 0 &&
                       (reinterpret_cast<uintptr_t>(B) & 15) == 0 &&
                       (!PAIR || (reinterpret_cast<uintptr_t>(B1) & 15) == 0);
+  // pairs come with one row or two (more go to the matrix cores)
   switch (M) {
-    case 1: return launch_vector_m<Fmt, 1, PAIR>(a, staged, !PAIR && sum, st);
-    case 2: return launch_vector_m<Fmt, 2, PAIR>(a, staged, !PAIR && sum, st);
-    case 3: return launch_vector_m<Fmt, 3, PAIR>(a, staged, !PAIR && sum, st);
-    case 4: return launch_vector_m<Fmt, 4, PAIR>(a, staged, !PAIR && sum, st);
-    case 5: return launch_vector_m<Fmt, 5, PAIR>(a, staged, !PAIR && sum, st);
-    case 6: return launch_vector_m<Fmt, 6, PAIR>(a, staged, !PAIR && sum, st);
-    case 7: return launch_vector_m<Fmt, 7, PAIR>(a, staged, !PAIR && sum, st);
-    case 8: return launch_vector_m<Fmt, 8, PAIR>(a, staged, !PAIR && sum, st);
-    default: return hipErrorInvalidValue;
+    case 1: return launch_vector_m<Fmt, 1, PAIR>(a, staged, st);
+    case 2: return launch_vector_m<Fmt, 2, PAIR>(a, staged, st);
+    default: break;
   }
+  if constexpr (!PAIR) {
+    switch (M) {
+      case 3: return launch_vector_m<Fmt, 3, false>(a, staged, st);
+      case 4: return launch_vector_m<Fmt, 4, false>(a, staged, st);
+      case 5: return launch_vector_m<Fmt, 5, false>(a, staged, st);
+      case 6: return launch_vector_m<Fmt, 6, false>(a, staged, st);
+      case 7: return launch_vector_m<Fmt, 7, false>(a, staged, st);
+      case 8: return launch_vector_m<Fmt, 8, false>(a, staged, st);
+      default: break;
+    }
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace

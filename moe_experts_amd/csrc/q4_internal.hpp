@@ -27,11 +27,10 @@ struct GemvPlan {
 GemvPlan plan_gemv(int M, int N, int K);
 hipError_t launch_gemv(const float* x, const uint8_t* B, float* y, int M, int N, int K,
                        void* ws, const GemvPlan& p, hipStream_t st);
-// Partial sums only, for kernels that add them up themselves, by the vector
-// tiles (M <= 2 is what they are for): part[S][M][N], or with B1 (a second matrix
-// of the same shape, same launch) part[2][S][M][N]; also when S == 1.
-GemvPlan plan_gemv_part(int M, int N, int K, int mats);
-hipError_t launch_gemv_part(const float* x, const uint8_t* B, const uint8_t* B1, int M, int N,
+// Two matrices of one shape in one launch of the vector tiles (M <= 2 is what
+// they are for): partial sums part[2][S][M][N] only, also when S == 1.
+GemvPlan plan_gemv_pair(int M, int N, int K);
+hipError_t launch_gemv_pair(const float* x, const uint8_t* B, const uint8_t* B1, int M, int N,
                             int K, float* part, const GemvPlan& p, hipStream_t st);
 // matrix-core variant (gemv_mfma_q4_0.hip): false when the shape does not suit it
 bool plan_gemv_mfma(int M, int N, int K, GemvPlan& p);
