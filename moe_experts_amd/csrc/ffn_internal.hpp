@@ -24,7 +24,9 @@ struct Adapters {
 // fp32 X of up to 8 rows or fp16 X of up to 64 (K a multiple of 32). With ad, the
 // same launch forms the adapters' narrow product t[M][R] (scale included).
 struct StripPlan {
-  int DW, strips, steps, S, per;
+  int DW, strips, steps;
+  int base, more;  // splits of a strip: base, the first `more` strips one more
+  int S;           // sums, splits of the most
   size_t part_bytes;
 };
 StripPlan plan_strip(int M, int N, int K, int mats, bool f32);

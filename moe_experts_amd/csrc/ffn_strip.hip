@@ -18,8 +18,8 @@
 //   * The lanes of a block share its scales: each loads some of the 8 rows'
 //     scales and hands them over inside the quad.
 //   * The waves of a workgroup take the strip's steps in turn and add their
-//     sums through LDS in wave order; the splits are added by the kernel that
-//     finishes the operator.
+//     sums through LDS in wave order, each for a quarter of the rows; the splits
+//     are added by the kernel that finishes the operator.
 //   * Exact weights: w = (q - 8) * d has up to 14 significant bits. hi =
 //     fp16(w) and lo = w - hi, which fp16 holds exactly (a multiple of d's
 //     last place), take a product each: the weights are not rounded.
@@ -50,7 +50,10 @@ struct StripArgs {
   const uint8_t* W1;
   float* part;
   int M, K, N, NB;
-  int strips, S, steps, per;  // steps of 32 rows in all, and of one split
+  int T, strips;              // strips of all matrices and of one
+  int base, more;             // splits: base + 1 of the first `more` strips, base of the rest
+  int S, quads;               // sums a strip has room for; rounds of kWaves steps in all
+  int steps;                  // of 32 rows
   int extra;                  // first workgroups: the adapters' narrow product
   Adapters ad;
   float* t;
@@ -152,6 +155,14 @@ __device__ __forceinline__ void strip_products(const StripWeights<DW>& w, const 
   scale_pairs<DW>(w, d);
   const half2v off_even = {(_Float16)1032.0f, (_Float16)1032.0f};
   const half2v off_odd = {(_Float16)72.0f, (_Float16)72.0f};
+  // The lo products of a column follow the hi products of the next: a product's
+  // sum is ready only some 30 cycles after it was issued.
+  half8 low = {};
+  auto add = [&](const half8& W, int n) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+      acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[f], W, acc[f][n], 0, 0, 0);
+  };
 #pragma unroll
   for (int j = 0; j < DW; ++j)
 #pragma unroll
@@ -177,29 +188,54 @@ __device__ __forceinline__ void strip_products(const StripWeights<DW>& w, const 
           lo[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, d[i], -t));
         }
         const int n = 8 * j + 4 * h + c;
-#pragma unroll
-        for (int f = 0; f < RF; ++f) {
-          acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              A[f], __builtin_bit_cast(half8, hi), acc[f][n], 0, 0, 0);
-          acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              A[f], __builtin_bit_cast(half8, lo), acc[f][n], 0, 0, 0);
-        }
+        add(__builtin_bit_cast(half8, hi), n);
+        if (n) add(low, n - 1);
+        low = __builtin_bit_cast(half8, lo);
       }
     }
+  add(low, 8 * DW - 1);
 }
 
 // LDS: fp32 activations [per][64 lanes][8 halves], then (from the same start)
-// the waves' sums [waves][16][128 * DW].
-template <int DW>
-constexpr int kSumBytes = kWaves * 16 * 128 * DW * 4;
+// the waves' sums, up to kSumRows times 16 rows at a time.
+template <int RF>
+constexpr int kSumRows = RF <= 2 ? RF : (RF + 1) / 2;
+template <int RF, int DW>
+constexpr int kSumBytes = kSumRows<RF> * kWaves * (kWaves - 1) * 2 * DW * 1024;
+
+__device__ __forceinline__ half2v to_half2(float a, float b) {
+  typedef float float2v __attribute__((ext_vector_type(2)));
+  return __builtin_convertvector(float2v{a, b}, half2v);
+}
+
+// Largest of a wave, in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+  auto dpp = [](float x, auto ctrl) __attribute__((always_inline)) {
+    return __int_as_float(
+        __builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  // row_ror 8, 4, 2, 1
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x128>()));
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x124>()));
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x122>()));
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x121>()));
+  const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                  false);
+  v = fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
+  const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                  false);
+  return fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+}
 
 // fp32 activations of the steps [kb, ke) as operands in LDS; inv[m] undoes the
 // row's factor. Wave w takes rows w, w + kWaves .., in groups of 8 values: group g of
 // the row is group g % 4 of step kb + g / 4 and goes to lane 16 * (g % 4) + m
-// (its lo part to m + 8). All loads of four groups a lane are issued together;
-// the values are read again for the second pass, from cache.
+// (its lo part to m + 8). All loads of four groups a lane are issued together,
+// then `between` (the first weights: loads return in order, and what this waits
+// for is the activations); more groups are read again for the second pass.
+template <class Between>
 __device__ __forceinline__ void stage_split(const StripArgs& a, int kb, int ke, half8* xa,
-                                            float* inv) {
+                                            float* inv, Between between) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int groups = 4 * (ke - kb);
@@ -229,22 +265,27 @@ __device__ __forceinline__ void stage_split(const StripArgs& a, int kb, int ke, 
       }
   };
   float v[kR][kU][8], big[kR] = {};
-  for (int g0 = lane; g0 < groups + lane; g0 += 64 * kU) {
-    load(g0, v);
+  auto largest = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < kR; ++h)
 #pragma unroll
       for (int u = 0; u < kU; ++u)
 #pragma unroll
         for (int e = 0; e < 8; ++e) big[h] = fmaxf(big[h], fabsf(v[h][u][e]));
+  };
+  load(lane, v);
+  between();
+  largest();
+  for (int g0 = lane + 64 * kU; g0 < groups + lane; g0 += 64 * kU) {
+    load(g0, v);
+    largest();
   }
   float s[kR];
 #pragma unroll
   for (int h = 0; h < kR; ++h) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) big[h] = fmaxf(big[h], __shfl_xor(big[h], o));
-    // the factor and its inverse stay normal; an infinity is not scaled up
-    const int e = big[h] > 0.0f ? 13 - max(-113, min(127, ilogbf(big[h]))) : 0;
+    big[h] = wave_max(big[h]);
+    // the factor and its inverse stay normal
+    const int e = min(14 - __builtin_amdgcn_frexp_expf(big[h]), 126);
     s[h] = ldexpf(1.0f, e);
     if (lane == 0) inv[wave + kWaves * h] = ldexpf(1.0f, -e);
   }
@@ -260,11 +301,14 @@ __device__ __forceinline__ void stage_split(const StripArgs& a, int kb, int ke, 
         const int k = step_start(step, a.K) + 8 * (g & 3);
         half8 hi, lo;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 8; e += 2) {
           // rows that the step before has taken
-          const float x = k + e >= step * kStepRows ? v[h][u][e] * s[h] : 0.0f;
-          hi[e] = (_Float16)x;
-          lo[e] = (_Float16)(x - (float)hi[e]);
+          const float x0 = k + e >= step * kStepRows ? v[h][u][e] : 0.0f;
+          const float x1 = k + e + 1 >= step * kStepRows ? v[h][u][e + 1] : 0.0f;
+          const half2v q = to_half2(x0 * s[h], x1 * s[h]);
+          const half2v r = to_half2(fmaf(x0, s[h], -(float)q[0]), fmaf(x1, s[h], -(float)q[1]));
+          hi[e] = q[0], hi[e + 1] = q[1];
+          lo[e] = r[0], lo[e + 1] = r[1];
         }
         half8* dst = xa + (size_t)(g >> 2) * 64 + 16 * (g & 3) + wave + kWaves * h;
         dst[0] = hi;
@@ -288,19 +332,24 @@ __global__ __launch_bounds__(kStripThreads) void strip_kernel(StripArgs a) {
     return;
   }
   const int L = xcd_logical_tile((int)blockIdx.x - a.extra, (int)gridDim.x - a.extra);
-  const int strip = L % a.strips;
-  const int rest = L / a.strips;
-  const int s = rest % a.S;
-  const int mat = rest / a.S;
-  const int kb = s * a.per;
-  const int ke = min(a.steps, kb + a.per);
+  const int full = a.base * a.T;
+  const int s = L < full ? L / a.T : a.base;
+  const int t = L < full ? L - s * a.T : L - full;
+  const int splits = a.base + (t < a.more);
+  const int mat = t >= a.strips;
+  const int strip = t - mat * a.strips;
+  // rounds of the waves in shares that differ by one at most
+  const int kb = kWaves * (int)((int64_t)s * a.quads / splits);
+  const int ke = min(a.steps, kWaves * (int)((int64_t)(s + 1) * a.quads / splits));
 
   StripSource<DW> src;
   src.init(a, mat ? a.W1 : a.W0, strip, lane);
   constexpr int kAhead = 2;  // steps in flight
   StripWeights<DW> w[kAhead];
+  auto first_weights = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) src.load(w[u], min(kb + wave + u * kWaves, ke - 1));
+    for (int u = 0; u < kAhead; ++u) src.load(w[u], min(kb + wave + u * kWaves, ke - 1));
+  };
 
   const half8* xa = reinterpret_cast<const half8*>(lds);
   const _Float16* xr[RF];
@@ -311,7 +360,7 @@ __global__ __launch_bounds__(kStripThreads) void strip_kernel(StripArgs a) {
       dst[f] = *reinterpret_cast<const half8*>(xr[f] + (size_t)step * kStepRows);
   };
   if constexpr (F32) {
-    stage_split(a, kb, ke, reinterpret_cast<half8*>(lds), inv);
+    stage_split(a, kb, ke, reinterpret_cast<half8*>(lds), inv, first_weights);
     __syncthreads();
   } else {
 #pragma unroll
@@ -320,6 +369,7 @@ __global__ __launch_bounds__(kStripThreads) void strip_kernel(StripArgs a) {
               (size_t)min(16 * f + (lane & 15), a.M - 1) * a.K + 8 * (lane >> 4);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) load_x(A[u], min(kb + wave + u * kWaves, ke - 1));
+    first_weights();
   }
 
   float4v acc[RF][8 * DW];
@@ -350,45 +400,91 @@ __global__ __launch_bounds__(kStripThreads) void strip_kernel(StripArgs a) {
       strip_products<RF, DW>(w[u], A[u], acc, mk);
     }
 
-  // The waves' sums, 16 rows at a time. A 16 x 16 result: lane l holds column
-  // l % 16, here the columns 8 * DW * (l % 16) + c of product c; register e
-  // row 4 * (l / 16) + e.
-  float* red = reinterpret_cast<float*>(lds);
+  // The waves' sums. A 16 x 16 result: lane l holds column l % 16, here the
+  // columns 8 * DW * (l % 16) + c of product c; register e row 4 * (l / 16) + e.
+  // Wave e adds registers e of all waves, in wave order: each leaves the others'
+  // in LDS, [to][from][four columns][lane].
+  constexpr int C4 = 2 * DW, SF = kSumRows<RF>;
+  float4v* red = reinterpret_cast<float4v*>(lds);
+  auto slot = [&](int to, int from, int f, int q) __attribute__((always_inline)) {
+    return ((f * kWaves + to) * (kWaves - 1) + (from < to ? from : from - 1)) * C4 * 64 + q * 64 +
+           lane;
+  };
   float* out = a.part + ((size_t)mat * a.S + s) * a.M * a.N;
-  const int n0 = strip * COLS;
+  const bool clear = splits < a.S && s == 0;  // the last sum of a strip with fewer splits
+  const size_t last = (size_t)(a.S - 1) * a.M * a.N;
+  const float4v zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int f = 0; f < RF; ++f) {
-    __syncthreads();  // the activations, or the sums before, have been read
+  for (int f0 = 0; f0 < RF; f0 += SF) {
+    if (F32 || f0) __syncthreads();  // the activations, or the sums before, have been read
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float* dst = red + ((size_t)wave * 16 + 4 * (lane >> 4) + e) * COLS + 8 * DW * (lane & 15);
+    for (int f = f0; f < f0 + SF && f < RF; ++f)
 #pragma unroll
-      for (int c = 0; c < 8 * DW; c += 4)
-        *reinterpret_cast<float4v*>(dst + c) =
-            float4v{acc[f][c][e], acc[f][c + 1][e], acc[f][c + 2][e], acc[f][c + 3][e]};
-    }
-    __syncthreads();
-    constexpr int ROWS = F32 ? 8 : 16;
-    for (int i = threadIdx.x; i < ROWS * COLS; i += kStripThreads) {
-      const int r = i / COLS, c = i % COLS;
-      const int m = 16 * f + r;
-      float v = 0.0f;
+      for (int e = 0; e < kWaves; ++e) {
+        if (e == wave) continue;  // uniform
 #pragma unroll
-      for (int q = 0; q < kWaves; ++q) {
-        v += red[(q * 16 + r) * COLS + c];
-        if constexpr (F32) v += red[(q * 16 + r + 8) * COLS + c];
+        for (int q = 0; q < C4; ++q)
+          red[slot(e, wave, f - f0, q)] = float4v{acc[f][4 * q][e], acc[f][4 * q + 1][e],
+                                                  acc[f][4 * q + 2][e], acc[f][4 * q + 3][e]};
       }
-      if constexpr (F32) v *= inv[r];
-      if (m < a.M && n0 + c < a.N) out[(size_t)m * a.N + n0 + c] = v;
+    __syncthreads();
+#pragma unroll
+    for (int f = f0; f < f0 + SF && f < RF; ++f) {
+      float4v v[C4];
+#pragma unroll
+      for (int q = 0; q < C4; ++q) {
+        float4v own;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4v r = acc[f][4 * q + i];
+          own[i] = wave < 2 ? (wave == 0 ? r[0] : r[1]) : (wave == 2 ? r[2] : r[3]);
+        }
+        v[q] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int from = 0; from < kWaves; ++from)
+          v[q] += from == wave ? own : red[slot(wave, from, f - f0, q)];
+      }
+      const int n = strip * COLS + 8 * DW * (lane & 15);
+      if constexpr (F32) {
+        // rows 8 .. 15 are the lo parts of 0 .. 7: lanes of the lower half add
+        // the first half of their columns, those of the upper half the second
+#pragma unroll
+        for (int q = 0; q < C4 / 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const auto h = __builtin_amdgcn_permlane32_swap(
+                __float_as_uint(v[q][i]), __float_as_uint(v[q + C4 / 2][i]), false, false);
+            v[q][i] = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+          }
+        const int m = 4 * ((lane >> 4) & 1) + wave;
+        if (m < a.M && n < a.N) {
+          float* dst = out + (size_t)m * a.N + n + (lane >> 5) * 2 * C4;
+#pragma unroll
+          for (int q = 0; q < C4 / 2; ++q) {
+            *reinterpret_cast<float4v*>(dst + 4 * q) = v[q] * inv[m];
+            if (clear) *reinterpret_cast<float4v*>(dst + last + 4 * q) = zero;
+          }
+        }
+      } else {
+        const int m = 16 * f + 4 * (lane >> 4) + wave;
+        if (m < a.M && n < a.N) {
+          float* dst = out + (size_t)m * a.N + n;
+#pragma unroll
+          for (int q = 0; q < C4; ++q) {
+            *reinterpret_cast<float4v*>(dst + 4 * q) = v[q];
+            if (clear) *reinterpret_cast<float4v*>(dst + last + 4 * q) = zero;
+          }
+        }
+      }
     }
   }
 }
 
 template <int RF, int DW, bool F32>
-hipError_t launch_strip_t(const StripArgs& a, int mats, hipStream_t st) {
-  int lds = kSumBytes<DW>;
-  if (F32) lds = std::max(lds, a.per * 1024);
-  hipLaunchKernelGGL((strip_kernel<RF, DW, F32>), dim3(a.extra + mats * a.S * a.strips),
+hipError_t launch_strip_t(const StripArgs& a, hipStream_t st) {
+  int lds = kSumBytes<RF, DW>;
+  if (F32) lds = std::max(lds, (a.quads + a.base - 1) / a.base * kWaves * 1024);
+  hipLaunchKernelGGL((strip_kernel<RF, DW, F32>), dim3(a.extra + a.base * a.T + a.more),
                      dim3(kStripThreads), lds, st, a);
   return hipGetLastError();
 }
@@ -398,37 +494,44 @@ hipError_t launch_strip_t(const StripArgs& a, int mats, hipStream_t st) {
 // Strip width: two dwords a lane for decode (rows of 144 bytes, 64 accumulator
 // registers), one for up to 64 rows (128 accumulator registers at 64 rows).
 //
-// Splits: the workgroups, nearly all resident at once, share 256 CUs, so the
-// time goes by the CU with the most work: whole rounds of 256 times the steps of
-// a wave (one more for staging and sums), in units of about 1 us for strips of
-// two dwords, plus the partial sums, written and read again. Measured at 8 rows,
-// two matrices of 4096 x 11008 (86 strips): 2, 3, 4, 5, 6, 7, 8, 9 splits 22.6,
-// 27.2, 22.6, 22.3, 27.5, 27.4, 19.5, 27.9 us.
+// Splits: any number of workgroups G can be shared out over the strips, some of
+// which then have one split more than the rest; tried are equal splits and one
+// to four workgroups a CU. A CU's time is its share of all rounds of steps (a
+// round: a step of each wave), but at least the longest workgroup's, which alone
+// on a CU takes longer for a round, plus about 2 us a workgroup for staging and
+// sums, plus the partial sums, written and read again. Measured (decode, 8 rows):
+// two matrices of 4096 x 11008 (86 strips) with G = 172, 256, 512, 768, 1024:
+// 24.5, 23.2, 20.9, 22.2, 24.3 us; one of 11008 x 4096 (16 strips) with 128, 192,
+// 256, 512, 768: 17.5, 16.4, 15.0, 16.7, 20.5 us. fp16, 33 rows, two of 4096 x
+// 11008 (172 strips) with 256, 344, 512, 688, 768: 34.4, 29.8, 27.1, 27.7, 28.5.
 StripPlan plan_strip(int M, int N, int K, int mats, bool f32) {
   StripPlan p{};
   p.DW = f32 ? 2 : 1;
   p.strips = (N + 128 * p.DW - 1) / (128 * p.DW);
   p.steps = (K + kStepRows - 1) / kStepRows;
-  const double unit = f32 ? 1.0 : 0.8;                            // us
-  const double sums = 8.0 * mats * (double)M * N / 4e6;           // us a split
+  const int quads = (p.steps + kWaves - 1) / kWaves;
+  const int T = mats * p.strips;
+  // 128 KiB of staged activations at most
+  const int least = f32 ? (quads + 31) / 32 : 1;
+  const double unit[2] = {f32 ? 0.95 : 0.8, f32 ? 0.6 : 0.5};  // us
+  const double sums = 8.0 * mats * (double)M * N / 4e6;  // us a split
   double best = 1e30;
-  for (int s = 1; s <= p.steps && s <= 64; ++s) {
-    const int per = (p.steps + s - 1) / s;
-    if ((p.steps + per - 1) / per != s) continue;
-    if (f32 && per > 128) continue;  // 128 KiB of staged activations at most
-    const long long n = (long long)mats * p.strips * s;
-    const double cost =
-        (double)((n + 255) / 256) * ((per + kWaves - 1) / kWaves + 1) * unit + sums * s;
+  auto consider = [&](long long G) {
+    const int base = (int)(G / T), more = (int)(G % T), S = base + (more > 0);
+    if (base < least || S > quads) return;
+    const double n = (double)((G + 255) / 256);
+    const double longest = unit[0] * ((quads + base - 1) / base);
+    const double shared = unit[1] * n * T * quads / G;
+    const double cost = std::max(longest, shared) + 2.0 * n + sums * S;
     if (cost < best) {
       best = cost;
-      p.per = per;
-      p.S = s;
+      p.base = base;
+      p.more = more;
+      p.S = S;
     }
-  }
-  if (p.S == 0) {  // a very long K: as few steps as the staging takes
-    p.per = 128;
-    p.S = (p.steps + 127) / 128;
-  }
+  };
+  for (int s = least; s <= std::max(least, std::min(quads, 64)); ++s) consider((long long)T * s);
+  for (int r = 1; r <= 4; ++r) consider(256 * r);
   p.part_bytes = (size_t)mats * p.S * M * N * sizeof(float);
   return p;
 }
@@ -446,22 +549,24 @@ hipError_t launch_strip(const void* X, const uint8_t* W0, const uint8_t* W1, flo
   a.N = N;
   a.NB = N / kBlockWeights;
   a.strips = p.strips;
+  a.T = (W1 ? 2 : 1) * p.strips;
+  a.base = p.base;
+  a.more = p.more;
   a.S = p.S;
   a.steps = p.steps;
-  a.per = p.per;
+  a.quads = (p.steps + kWaves - 1) / kWaves;
   if (ad) {
     a.ad = *ad;
     a.t = t;
     // a multiple of the XCDs, so that the strips' workgroups keep theirs
     a.extra = ((M * ad->R + kWaves - 1) / kWaves + kNumXcd - 1) / kNumXcd * kNumXcd;
   }
-  const int mats = W1 ? 2 : 1;
-  if (f32) return launch_strip_t<1, 2, true>(a, mats, st);
+  if (f32) return launch_strip_t<1, 2, true>(a, st);
   switch ((M + 15) / 16) {
-    case 1: return launch_strip_t<1, 1, false>(a, mats, st);
-    case 2: return launch_strip_t<2, 1, false>(a, mats, st);
-    case 3: return launch_strip_t<3, 1, false>(a, mats, st);
-    case 4: return launch_strip_t<4, 1, false>(a, mats, st);
+    case 1: return launch_strip_t<1, 1, false>(a, st);
+    case 2: return launch_strip_t<2, 1, false>(a, st);
+    case 3: return launch_strip_t<3, 1, false>(a, st);
+    case 4: return launch_strip_t<4, 1, false>(a, st);
     default: return hipErrorInvalidValue;
   }
 }
