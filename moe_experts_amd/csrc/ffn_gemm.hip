@@ -5,16 +5,15 @@
 //   gradient  dX = dG . deq(Wg)^T + dU . deq(Wu)^T            one or two matrices
 //
 // Tile BM x 128, K steps of 64, 512 lanes: 4 consumer waves issue only matrix
-// instructions, 4 producer waves fetch the weights, dequantize them into an
-// fp16 LDS tile [column][k] and issue the copies of the left operand, so the
-// VALU work of one role runs beside the matrix work of the other.
+// instructions, 4 producer waves fetch both operands and dequantize the weights
+// into an fp16 LDS tile [column][k], so the VALU work of one role runs beside the
+// matrix work of the other. LDS holds two steps; a barrier a step hands over.
 //
-//   * Left operand: 16-byte LDS-DMA copies, three steps deep, issued two steps
-//     ahead, XOR-swizzled on the source side.
-//   * Weights: a producer lane loads its own share of a step straight into
-//     registers, two steps ahead, and writes the dequantized values into the
-//     double-buffered LDS tile one step ahead. The raw bytes never pass
-//     through LDS.
+//   * Left operand: 16-byte loads into registers, two steps ahead, and 16-byte
+//     LDS stores, XOR-swizzled.
+//   * Weights: a producer lane loads a block of a step straight into registers,
+//     two steps ahead, and writes the dequantized values one step ahead. The raw
+//     bytes never pass through LDS.
 //   * dual: the 128 columns of a tile are 64 columns of the gate and the same
 //     64 of the up matrix, in blocks gate, up, gate, up, so that the wave that
 //     holds a column's gate holds its up value in the same lane and register,
@@ -29,7 +28,17 @@
 //     added in split order by a second kernel), so that the grid fills the GPU.
 //
 // Each dequantized weight (q - 8) * d is rounded to fp16 before its product,
-// as in q4_0_gemm; the sums are fp32.
+// as in q4_0_gemm; the sums are fp32. Rounded weights give g and u an error of
+// about 0.8 of what rounding them to fp16 gives, and h, their product, one 1.54
+// times that of its own rounding. So dual keeps what the rounding took of a
+// quarter of the weights, exactly, and adds its products: 1.42 times, for 467
+// against 410 us at 2048 rows of 4096 x 11008 (half of the weights: 1.29, 539 us;
+// all: 1.00, 703 us).
+//
+// What bounds it: full tiles keep the matrix cores 47 % (forward) to 58 %
+// (gradient) busy at a clock that falls to 1.7 GHz, the power limit's. Deeper
+// prefetch, reads ahead of the products and moving work between the roles left
+// the times as they were.
 #include <type_traits>
 
 #include "ffn_device.hpp"
@@ -48,6 +57,13 @@ constexpr int kBBytes = BN * kColBytes;    // 16 KiB
 constexpr uint32_t kOut = 0x80000000u;
 
 enum Side { kAdapters, kDual, kGradient };
+
+// dual: quarters of a step (16 of k) whose weights' roundings get products of
+// their own, the first and, with two, the third.
+template <Side SIDE>
+constexpr int kRestQuarters = SIDE == kDual ? 1 : 0;
+template <Side SIDE>
+constexpr int kRestBytes = BN * 32 * kRestQuarters<SIDE>;  // of a step, in LDS
 
 struct TileArgs {
   const uint16_t* X;      // left operand [M][lda]
@@ -85,16 +101,24 @@ __device__ __forceinline__ void lds_barrier() {
 struct Dequant {
   uint32_t even = 0x000f000fu, odd = 0x00f000f0u;
   __device__ __forceinline__ Dequant() { asm volatile("" : "+v"(even), "+v"(odd)); }
-  // nibbles at bits 0 and 16, or 4 and 20
-  __device__ __forceinline__ uint32_t low(uint32_t q, half2v d) const {
+  // q - 8 of the nibbles at bits 0 and 16, or 4 and 20
+  __device__ __forceinline__ half2v low_value(uint32_t q) const {
     const half2v off = {(_Float16)1032.0f, (_Float16)1032.0f};
-    return __builtin_bit_cast(
-        uint32_t, (__builtin_bit_cast(half2v, (q & even) | 0x64006400u) - off) * d);
+    return __builtin_bit_cast(half2v, (q & even) | 0x64006400u) - off;
+  }
+  __device__ __forceinline__ half2v high_value(uint32_t q) const {
+    const half2v off = {(_Float16)72.0f, (_Float16)72.0f};
+    return __builtin_bit_cast(half2v, (q & odd) | 0x54005400u) - off;
+  }
+  __device__ __forceinline__ uint32_t low(uint32_t q, half2v d) const {
+    return __builtin_bit_cast(uint32_t, low_value(q) * d);
   }
   __device__ __forceinline__ uint32_t high(uint32_t q, half2v d) const {
-    const half2v off = {(_Float16)72.0f, (_Float16)72.0f};
-    return __builtin_bit_cast(
-        uint32_t, (__builtin_bit_cast(half2v, (q & odd) | 0x54005400u) - off) * d);
+    return __builtin_bit_cast(uint32_t, high_value(q) * d);
+  }
+  // what the rounding of v * d took, exactly
+  static __device__ __forceinline__ uint32_t rest(half2v v, half2v d) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, d, -(v * d)));
   }
 };
 
@@ -114,8 +138,7 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
 }
 
 // Forward: the step's 64 weight rows x 4 blocks are one block a producer lane,
-// two loads (loading units of 4 rows x 8 columns instead, eight loads a lane,
-// cost 75 of 430 us at 2048 x 4096 x 11008). Wave w takes rows 32 * (w % 2) .. of
+// two loads. Wave w takes rows 32 * (w % 2) .. of
 // the column half w / 2 (dual: half 0 is the gate, half 1 the up matrix); in the
 // row number of lane l bit 0 is l / 32, bit 1 is l / 16 % 2, the rest l / 2 % 8;
 // its block is l % 2. The four lanes that hold one block column of four
@@ -128,6 +151,7 @@ struct ForwardWeights {
   Dequant dq;
   uint32_t vq, vd, pitch;
   int n0, chunk, half;
+  int rest_at;  // offset of the rows in a column's roundings, < 0: none are kept
   struct Raw {
     uint32_t q[4], d;
   };
@@ -148,6 +172,8 @@ struct ForwardWeights {
     n0 = (DUAL ? 2 * blk + hw : 2 * hw + blk) * 32 + (2 * b5 + b4) * 8;
     chunk = rg >> 1;
     half = rg & 1;
+    constexpr int LQ = kRestQuarters<kDual>, kEvery = 4 / LQ;
+    rest_at = (rg >> 2) % kEvery == 0 ? (rg >> 2) / kEvery * 32 + (rg & 3) * 8 : -1;
   }
   // all loads go with part 0
   __device__ __forceinline__ void load(Raw& raw, int ks, int i) const {
@@ -194,6 +220,17 @@ struct ForwardWeights {
     for (int c = 0; c < 2; ++c) {
       const int n = n0 + 2 * part + c;
       *reinterpret_cast<uint2*>(bs + n * kColBytes + ((chunk ^ swz_b(n)) << 4) + half * 8) = v[c];
+    }
+    if constexpr (DUAL) {
+      if (rest_at < 0) return;
+      v[0].x = Dequant::rest(dq.low_value(a), k.d01);
+      v[0].y = Dequant::rest(dq.low_value(b), k.d23);
+      v[1].x = Dequant::rest(dq.high_value(a), k.d01);
+      v[1].y = Dequant::rest(dq.high_value(b), k.d23);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<uint2*>(bs + kBBytes + (n0 + 2 * part + c) * (kRestBytes<kDual> / BN) +
+                                  rest_at) = v[c];
     }
   }
 };
@@ -330,6 +367,7 @@ __device__ __forceinline__ void produce(const TileArgs& g, uint8_t* __restrict__
                                       ForwardWeights<SIDE == kDual>>::type;
   constexpr int D = kDepth<BM>;
   constexpr int kXBytes = BM * kColBytes;
+  constexpr int kStage = kBBytes + kRestBytes<SIDE>;
   W wt;
   wt.init(g, tn, t);
   LeftOperand<BM> left;
@@ -352,21 +390,22 @@ __device__ __forceinline__ void produce(const TileArgs& g, uint8_t* __restrict__
 #pragma unroll
     for (int u = 0; u < D; ++u)
       produce_step<BM>(wt, left, raw[(u + 1) % D], lraw[(u + 1) % D],
-                       xs + ((u + 1) & 1) * kXBytes, bs + ((u + 1) & 1) * kBBytes,
+                       xs + ((u + 1) & 1) * kXBytes, bs + ((u + 1) & 1) * kStage,
                        min(ks + u + 1 + D, ke - 1));
   }
 #pragma unroll
   for (int u = 0; u < D - 1; ++u)
     if (ks + u < ke)
       produce_step<BM>(wt, left, raw[(u + 1) % D], lraw[(u + 1) % D],
-                       xs + ((u + 1) & 1) * kXBytes, bs + ((u + 1) & 1) * kBBytes, ke - 1);
+                       xs + ((u + 1) & 1) * kXBytes, bs + ((u + 1) & 1) * kStage, ke - 1);
 }
 
 template <int BM, Side SIDE>
 __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(TileArgs g) {
   constexpr int kXBytes = BM * kColBytes;
+  constexpr int kStage = kBBytes + kRestBytes<SIDE>;
   // two steps' left operand and weights; at the end the waves' results
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kXBytes + 2 * kBBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kXBytes + 2 * kStage];
   uint8_t* xs = lds;
   uint8_t* bs = lds + 2 * kXBytes;
   const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
@@ -401,9 +440,12 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   // A quarter of a step (16 of k) at a time: its operands, then its products.
+  constexpr int LQ = kRestQuarters<SIDE>;
   struct Operands {
-    half8 a[MI], b[NJ];
+    half8 a[MI], b[NJ], rest[LQ ? NJ : 1];
   };
+  // of quarter kk: its place among those with products for the roundings, or -1
+  auto rest_of = [](int kk) { return LQ && kk % (4 / (LQ ? LQ : 1)) == 0 ? kk * LQ / 4 : -1; };
   const int ra = wm * WR + (lane & 31), rb = wn * WC + (lane & 31);
   auto read = [&](Operands& o, const uint8_t* x, const uint8_t* b, int kk) {
     const int kc = 2 * kk + (lane >> 5);
@@ -416,20 +458,28 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
     for (int j = 0; j < NJ; ++j) {
       const int n = rb + 32 * j;
       o.b[j] = *reinterpret_cast<const half8*>(b + n * kColBytes + ((kc ^ swz_b(n)) << 4));
+      if (rest_of(kk) >= 0)
+        o.rest[j] = *reinterpret_cast<const half8*>(b + kBBytes + n * (kRestBytes<SIDE> / BN) +
+                                                    rest_of(kk) * 32 + 16 * (lane >> 5));
     }
   };
-  auto multiply = [&](const Operands& o) {
+  auto multiply = [&](const Operands& o, int kk) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.b[j], o.a[i], acc[i][j], 0, 0, 0);
+    if (rest_of(kk) < 0) return;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.rest[j], o.a[i], acc[i][j], 0, 0, 0);
   };
   // One consumer wave a SIMD: nothing else hides the latency of its LDS reads,
   // so the reads of a quarter are issued before the products of the one before,
   // and a step's last products run after the barrier, over the first reads of
-  // the next step. (With the reads of each quarter waited for in turn, a step
-  // took 2500 cycles for 1024 of matrix instructions.)
+  // the next step.
   constexpr int Q = BK / 16;
   lds_barrier();
   if constexpr (MI * NJ <= 2) {
@@ -438,7 +488,7 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
     for (int ks = kb; ks < ke; ++ks) {
       const int cur = (ks - kb) & 1;
       const uint8_t* x = xs + cur * kXBytes;
-      const uint8_t* b = bs + cur * kBBytes;
+      const uint8_t* b = bs + cur * kStage;
 #pragma unroll
       for (int q = 0; q < Q; ++q) read(o[q], x, b, q);
       __builtin_amdgcn_sched_barrier(0);
@@ -446,7 +496,7 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
       lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int q = 0; q < Q; ++q) multiply(o[q]);
+      for (int q = 0; q < Q; ++q) multiply(o[q], q);
     }
   } else {
     Operands o[2];
@@ -454,21 +504,21 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
     for (int ks = kb; ks < ke; ++ks) {
       const int cur = (ks - kb) & 1;
       const uint8_t* x = xs + cur * kXBytes;
-      const uint8_t* b = bs + cur * kBBytes;
+      const uint8_t* b = bs + cur * kStage;
 #pragma unroll
       for (int q = 0; q < Q - 1; ++q) {
         read(o[(q + 1) & 1], x, b, q + 1);
         __builtin_amdgcn_sched_barrier(0);
-        multiply(o[q & 1]);
+        multiply(o[q & 1], q);
         __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_s_waitcnt(0xc07f);  // this wave's reads done before the stages are reused
       lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
       // past the last step this reads a stage that is not used
-      read(o[0], xs + (cur ^ 1) * kXBytes, bs + (cur ^ 1) * kBBytes, 0);
+      read(o[0], xs + (cur ^ 1) * kXBytes, bs + (cur ^ 1) * kStage, 0);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(o[(Q - 1) & 1]);
+      multiply(o[(Q - 1) & 1], Q - 1);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -507,7 +557,7 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
   // block of three results took 20000 cycles, as long as nine K steps).
   constexpr int OC = SIDE == kDual ? WC / 2 : WC;  // result columns of the wave
   constexpr int kPitch = OC * 2 + 16;              // bytes of an LDS row
-  static_assert(4 * WR * kPitch <= 2 * kXBytes + 2 * kBBytes, "results fit the stages");
+  static_assert(4 * WR * kPitch <= 2 * kXBytes + 2 * kStage, "results fit the stages");
   uint8_t* out = lds + wave * (WR * kPitch);
   const int col0 = SIDE == kDual ? tn * 64 + wn * OC : tn * BN + wn * OC;
   auto put = [&](int i, int j, const uint2(&v)[4]) {  // 32 rows x 32 columns
@@ -631,8 +681,8 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
 //    64 rows: 0.40 alone, 0.45 each.
 // A workgroup costs its prologue and results (3, 2 or 1.5 us) besides, splits
 // the partial sums, written and read at 4.5 TB/s, and a kernel that adds them.
-// Full tiles win while they fill the GPU (2048 rows, 4096 x 11008 twice: 624,
-// 430, 398 us with 64, 128, 256 rows), lower ones below (400 rows, 4096 x 4096
+// Full tiles win while they fill the GPU (2048 rows, 4096 x 11008 twice, without
+// the products for roundings: 624, 430, 398 us with 64, 128, 256 rows), lower ones below (400 rows, 4096 x 4096
 // twice: 67, 44, 52 us; 200 rows of a gradient: 128 rows in 4 splits 23.8 us,
 // 256 rows in 8 splits 28.2).
 void plan_tiles(FfnPlan& p, int M, int tiles_n, int nk, size_t sum_cols) {
