@@ -605,9 +605,9 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
     }
   } else if constexpr (SIDE == kAdapters) {
     // Wide half of the adapters: for every adapter that occurs in the wave's
-    // rows, t16 with the other rows zeroed times B_id^T (R a multiple of 8,
-    // steps of 16, the rest zero). A row meets only its own adapter, so all
-    // adapters share one accumulator, which the row's factor then scales.
+    // rows, t16 times B_id^T (R a multiple of 8, steps of 16, the rest zero), of
+    // which the adapter's own rows keep the result and then scale it: an infinity
+    // or NaN in one adapter stays with the rows that use it.
     const int R = g.ad.R;
     int id = lane < min(WR, rw) ? g.ad.ids[mw + lane] : -1;
     if (id < 0 || id >= g.ad.L) id = -1;
@@ -630,13 +630,18 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
           const _Float16* bp =
               reinterpret_cast<const _Float16*>(g.ad.B) + ((size_t)cur * g.ncols + col) * R;
           const _Float16* tp = g.t16 + (size_t)(mw + 32 * i + lr) * R;
+          float16v own;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) own[r] = 0.0f;
           for (int k0 = 0; k0 < R; k0 += 16) {
             const int r0 = k0 + 8 * (lane >> 5);
             half8 a = {0, 0, 0, 0, 0, 0, 0, 0}, b = a;
             if (mine && r0 < R) a = *reinterpret_cast<const half8*>(tp + r0);
             if (col < g.ncols && r0 < R) b = *reinterpret_cast<const half8*>(bp + r0);
-            extra = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, extra, 0, 0, 0);
+            own = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, own, 0, 0, 0);
           }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) extra[r] = mine ? own[r] : extra[r];
         }
         uint2 v[4];
 #pragma unroll

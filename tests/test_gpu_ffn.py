@@ -346,6 +346,108 @@ def test_unused_adapters_are_not_read():
         assert all(np.array_equal(u, v) and np.isfinite(u).all() for u, v in zip(*outs))
 
 
+@pytest.mark.parametrize("M", [4, 8, 40, 64, 130, 520])
+def test_an_adapter_with_infinities_stays_with_its_rows(M):
+    """Infinities and NaN of one adapter reach the rows that use it, and no others."""
+    from moe_experts_amd import q4_0_gemm_lora, q4_0_gemv_lora
+    K, N, R, L = 256, 192, 24, 3
+    B = weights(64, K, N)
+    A, Bl, scale = adapters(65, L, R, K, N)
+    ids = np.random.default_rng(66).integers(-1, L, M).astype(np.int32)
+    ids[:3] = [0, 1, 2]
+    x = datagen.to_f16(datagen.activations(67, M, K))
+    others = ids != 1
+    for broken in (0, 1, 2):
+        a, b, s = A.copy(), Bl.copy(), scale.copy()
+        if broken == 0:
+            a[1, :, ::7] = np.inf
+        elif broken == 1:
+            b[1, ::5] = np.nan
+        else:
+            s[1] = np.inf
+        calls = [(q4_0_gemm_lora, x)]
+        if M <= 8:
+            calls.append((q4_0_gemv_lora, x.astype(np.float32)))
+        for f, v in calls:
+            right = host(f(to_dev(v), to_dev(B), N, *[to_dev(t) for t in (A, Bl, ids, scale)]))
+            got = host(f(to_dev(v), to_dev(B), N, *[to_dev(t) for t in (a, b, ids, s)]))
+            assert np.array_equal(got[others], right[others])
+            assert not np.isfinite(got[~others]).all()
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 8])
+def test_rows_of_any_size_and_a_row_with_an_infinity(M):
+    """Decode rows from 1e-30 to 1e30 keep their own precision, and a row with an infinity or a
+    NaN leaves the others as they are."""
+    from moe_experts_amd import q4_0_gemv_lora, q4_0_glu
+    K, N, R, L = 520, 96, 8, 2
+    x = datagen.activations(81, M, K) * (10.0 ** np.linspace(-30, 30, M))[:, None]
+    x = x.astype(np.float32)
+    B = weights(82, K, N)
+    A, Bl, scale = adapters(83, L, R, K, N)
+    ids = row_ids("mixed", M, L)
+    ad = [to_dev(v) for v in (A, Bl, ids, scale)]
+    got = host(q4_0_gemv_lora(to_dev(x), to_dev(B), N, *ad))
+    for m in range(M):  # a row by itself: the bound is relative to its own values
+        ref.check(got[m:m + 1], ref.gemv_lora(x[m:m + 1], B, A, Bl, ids[m:m + 1], scale))
+    if M == 1:
+        return
+    Wu = weights(84, K, N)
+    x = datagen.activations(85, M, K)
+    right = host(q4_0_glu(to_dev(x), to_dev(B), to_dev(Wu), N))
+    right_l = host(q4_0_gemv_lora(to_dev(x), to_dev(B), N, *ad))
+    for bad in (np.inf, -np.inf, np.nan):
+        y = x.copy()
+        y[1, 77] = bad
+        got = host(q4_0_glu(to_dev(y), to_dev(B), to_dev(Wu), N))
+        got_l = host(q4_0_gemv_lora(to_dev(y), to_dev(B), N, *ad))
+        keep = np.arange(M) != 1
+        assert np.array_equal(got[keep], right[keep])
+        assert np.array_equal(got_l[keep], right_l[keep])
+        assert not np.isfinite(got_l[1]).any()
+
+
+@pytest.mark.parametrize("shift", [2, 4, 6, 14])
+@pytest.mark.parametrize("M,K,N", [(1, 72, 96), (4, 72, 96), (8, 1000, 544), (5, 40, 288)])
+def test_decode_over_matrices_at_any_even_address(M, K, N, shift):
+    """Q4_0 blocks are 2-byte aligned; rows of an odd number of blocks start in turn at and
+    inside a dword. The bytes before and behind a matrix are not weights."""
+    from moe_experts_amd import q4_0_gemv_lora, q4_0_glu
+    def place(w):
+        flat = np.ascontiguousarray(w).reshape(-1).view(np.uint8)
+        buf = torch.full((flat.size + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        buf[shift:shift + flat.size] = torch.from_numpy(flat.copy()).cuda()
+        return buf[shift:shift + flat.size]
+    x = datagen.activations(86, M, K)
+    Wg, Wu = weights(87, K, N), weights(88, K, N)
+    ref.check(host(q4_0_glu(to_dev(x), place(Wg), place(Wu), N)), ref.glu(x, Wg, Wu, "silu"))
+    A, Bl, scale = adapters(89, 2, 8, K, N)
+    ids = row_ids("mixed", M, 2)
+    got = q4_0_gemv_lora(to_dev(x), place(Wg), N, to_dev(A), to_dev(Bl), to_dev(ids),
+                         to_dev(scale))
+    ref.check(host(got), ref.gemv_lora(x, Wg, A, Bl, ids, scale))
+
+
+@pytest.mark.parametrize("M", [40, 70, 300])
+@pytest.mark.parametrize("shift", [2, 8, 10])
+def test_prompt_and_gradient_over_matrices_at_any_even_address(M, shift):
+    from moe_experts_amd import q4_0_gemm_backward, q4_0_glu_gemm
+    K, N = 192, 320
+    Wg, Wu = weights(90, K, N), weights(91, K, N)
+    bufs = []
+    for w in (Wg, Wu):
+        flat = np.ascontiguousarray(w).reshape(-1).view(np.uint8)
+        buf = torch.full((flat.size + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        buf[shift:shift + flat.size] = torch.from_numpy(flat.copy()).cuda()
+        bufs.append(buf[shift:shift + flat.size])
+    x = datagen.to_f16(datagen.activations(92, M, K))
+    got = q4_0_glu_gemm(to_dev(x), bufs[0], bufs[1], N, save=True)
+    for g, want, what in zip(got, ref.glu_gemm(x, Wg, Wu, "silu"), "HGU"):
+        ref.check(host(g), want, what)
+    dY = gradient(93, M, N)
+    ref.check(host(q4_0_gemm_backward(dY, bufs[0], K)), ref.gemm_backward(values(dY), Wg))
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("M", [3, 40, 300])
 def test_block_with_adapters_and_its_gradient(M):
