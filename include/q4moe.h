@@ -317,13 +317,17 @@ int moe_q4_0_layer(const float* x, const float* Wr, const q4_0_block* Wg, const 
  *     any K the GEMV takes, fp32 sums and results;
  *   prompt and gradient (the others): fp16 activations, bf16 gradients, any M;
  *     K % 64 == 0 and N % 64 == 0. A dequantized weight is rounded to fp16 before
- *     its product, as in q4_0_gemm, or, in products of few rows, not rounded;
- *     sums are fp32, results are rounded once.
+ *     its product, as in q4_0_gemm, or, in products of few rows and for a part of
+ *     the gated block's weights, not rounded; sums are fp32, results are rounded
+ *     once.
+ * Weights (q - 8) * d stay below 65520 in magnitude, the range of fp16. A row with
+ * an infinity or a NaN has results that are not finite, in every column; other
+ * rows are not touched by it.
  * fp16 and bf16 arrays, fp32 x of q4_0_gemv_lora: 16-byte aligned; Q4_0
- * matrices 2-byte, other fp32 and int32 arrays 4-byte. Every matrix, activation
- * and result array is smaller than 2 GiB. Outputs must not overlap inputs or
- * one another. A call fails with Q4_EWORKSPACE when ws is smaller than its
- * *_workspace_bytes.
+ * matrices 2-byte, other fp32 and int32 arrays 4-byte. Every Q4_0 matrix,
+ * activation and result array is smaller than 2 GiB (the adapters' A and Bl may
+ * be larger). Outputs must not overlap inputs or one another. A call fails with
+ * Q4_EWORKSPACE when ws is smaller than its *_workspace_bytes.
  * ------------------------------------------------------------------------- */
 typedef enum q4_act {
   Q4_ACT_SILU = 0, /* z / (1 + exp(-z)) */

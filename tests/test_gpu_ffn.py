@@ -448,6 +448,80 @@ def test_prompt_and_gradient_over_matrices_at_any_even_address(M, shift):
     ref.check(host(q4_0_gemm_backward(dY, bufs[0], K)), ref.gemm_backward(values(dY), Wg))
 
 
+@pytest.mark.parametrize("M", [2, 40, 130])
+def test_adapter_tables_past_four_gigabytes(M):
+    """Rows that use the last adapter of a table whose offsets pass 32 bits."""
+    from moe_experts_amd import q4_0_gemm_lora, q4_0_gemv_lora
+    K, N, R, L = 90112, 64, 128, 190
+    B = weights(94, K, N)
+    A, Bl, scale = adapters(95, 1, R, K, N)
+    table = torch.zeros((L, R, K), dtype=torch.float16, device="cuda")
+    assert table.numel() * 2 > 1 << 32
+    table[L - 1] = to_dev(A)[0]
+    wide = torch.zeros((L, N, R), dtype=torch.float16, device="cuda")
+    wide[L - 1] = to_dev(Bl)[0]
+    factors = torch.zeros(L, dtype=torch.float32, device="cuda")
+    factors[L - 1] = float(scale[0])
+    last = np.where(np.arange(M) % 3 == 1, -1, 0).astype(np.int32)
+    ids = to_dev(np.where(last == 0, L - 1, -1).astype(np.int32))
+    x = datagen.to_f16(datagen.activations(96, M, K))
+    got = q4_0_gemm_lora(to_dev(x), to_dev(B), N, table, wide, ids, factors)
+    ref.check(host(got), ref.gemm_lora(x, B, A, Bl, last, scale))
+    if M <= 8:
+        x = x.astype(np.float32)
+        got = q4_0_gemv_lora(to_dev(x), to_dev(B), N, table, wide, ids, factors)
+        ref.check(host(got), ref.gemv_lora(x, B, A, Bl, last, scale))
+
+
+@pytest.mark.parametrize("M", [1, 5])
+def test_decode_arrays_at_any_dword(M):
+    """x and h of the gated block, and y, are 4-byte aligned."""
+    from moe_experts_amd import q4_0_gemv_lora, q4_0_glu
+    K, N = 333, 160
+    x = datagen.activations(97, M, K)
+    Wg, Wu = weights(98, K, N), weights(99, K, N)
+    at = torch.zeros(M * K + 8, dtype=torch.float32, device="cuda")
+    for o in (1, 2, 3):
+        at[o:o + M * K] = to_dev(x).reshape(-1)
+        h = torch.full((M * N + 8,), 7.0, dtype=torch.float32, device="cuda")
+        q4_0_glu(at[o:o + M * K].view(M, K), to_dev(Wg), to_dev(Wu), N,
+                 h=h[o:o + M * N].view(M, N))
+        ref.check(host(h[o:o + M * N]).reshape(M, N), ref.glu(x, Wg, Wu, "silu"))
+        assert (h[:o] == 7).all() and (h[o + M * N:] == 7).all()
+        A, Bl, scale = adapters(100, 2, 8, 328, N)
+        ids = row_ids("mixed", M, 2)
+        B = weights(101, 328, N)
+        v = datagen.activations(102, M, 328)
+        q4_0_gemv_lora(to_dev(v), to_dev(B), N, to_dev(A), to_dev(Bl), to_dev(ids), to_dev(scale),
+                       y=h[o:o + M * N].view(M, N))
+        ref.check(host(h[o:o + M * N]).reshape(M, N), ref.gemv_lora(v, B, A, Bl, ids, scale))
+
+
+@pytest.mark.parametrize("M", [2, 5, 40, 130])
+def test_weights_of_any_scale(M):
+    """Block scales from the smallest half to ones whose weights reach 65504, beside each other."""
+    from moe_experts_amd import q4_0_gemm_lora, q4_0_glu, q4_0_glu_gemm
+    K, N = 128, 128
+    W = [weights(s, K, N).reshape(K, N // 32, 18).copy() for s in (103, 104)]
+    for i, w in enumerate(W):
+        d = 2.0 ** np.random.default_rng(105 + i).uniform(-24, 12.9, (K, N // 32))
+        w[..., :2] = d.astype(np.float16)[..., None].view(np.uint8)
+    x = datagen.to_f16(datagen.activations(107, M, K) * 2.0 ** -12)
+    if M <= 8:
+        got = q4_0_glu(to_dev(x.astype(np.float32)), to_dev(W[0]), to_dev(W[1]), N)
+        ref.check(host(got), ref.glu(x.astype(np.float32), W[0], W[1], "silu"))
+    else:
+        _, G, U = q4_0_glu_gemm(to_dev(x), to_dev(W[0]), to_dev(W[1]), N, save=True)
+        _, g, u = ref.glu_gemm(x, W[0], W[1], "silu")
+        ref.check(host(G), g, "G")
+        ref.check(host(U), u, "U")
+    A, Bl, scale = adapters(108, 2, 8, K, N)
+    ids = np.full(M, -1, np.int32)
+    got = q4_0_gemm_lora(to_dev(x), to_dev(W[0]), N, to_dev(A), to_dev(Bl), to_dev(ids),
+                         to_dev(scale))
+    ref.check(host(got), ref.gemm_lora(x, W[0], A, Bl, ids, scale))
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("M", [3, 40, 300])
 def test_block_with_adapters_and_its_gradient(M):
