@@ -548,3 +548,22 @@ def test_block_with_adapters_and_its_gradient(M):
     dX = q4_0_glu_backward(dH, G, U, dg, du, K)
     ref.check(host(dH), ref.gemm_backward(values(dY), Wd))
     ref.check(host(dX), ref.glu_backward(values(dH), host(G), host(U), Wg, Wu, "silu"))
+
+
+@pytest.mark.parametrize("M,K,N", [(1930, 64, 4160), (1100, 4352, 64)])
+def test_many_tiles(M, K, N):
+    """More tiles than the GPU takes at once, a last row of tiles with few rows, and columns that
+    are left over for lower tiles."""
+    from moe_experts_amd import q4_0_gemm_backward, q4_0_gemm_lora, q4_0_glu_gemm
+    x = datagen.to_f16(datagen.activations(110, M, K))
+    Wg, Wu = weights(111, K, N), weights(112, K, N)
+    got = q4_0_glu_gemm(to_dev(x), to_dev(Wg), to_dev(Wu), N, save=True)
+    for g, want, what in zip(got, ref.glu_gemm(x, Wg, Wu, "silu"), "HGU"):
+        ref.check(host(g), want, what)
+    dY = gradient(113, M, N)
+    ref.check(host(q4_0_gemm_backward(dY, to_dev(Wg), K)), ref.gemm_backward(values(dY), Wg))
+    A, Bl, scale = adapters(114, 3, 8, K, N)
+    ids = row_ids("ragged", M, 3)
+    got = q4_0_gemm_lora(to_dev(x), to_dev(Wg), N, to_dev(A), to_dev(Bl), to_dev(ids),
+                         to_dev(scale))
+    ref.check(host(got), ref.gemm_lora(x, Wg, A, Bl, ids, scale))
