@@ -143,16 +143,23 @@ _ws_cache: dict = {}
 def workspace(nbytes: int, device) -> torch.Tensor | None:
     if nbytes == 0:
         return None
-    dev = torch.device(device)
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    key = (dev.index, _raw_stream(dev.index))
+    index = torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    return _workspace(nbytes, index, _raw_stream(index))
+
+
+def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    key = (index, stream)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
         with _ws_lock:
             buf = _ws_cache.get(key)
             if buf is None or buf.numel() < nbytes:
-                buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+                buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8,
+                                  device=torch.device("cuda", index))
                 _ws_cache[key] = buf
     return buf
 
@@ -419,13 +426,15 @@ def _run(f, need: int, ws, index: int, *args):
     if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
             return _run(f, need, ws, index, *args)
-    if ws is None:
-        ws = workspace(need, torch.device("cuda", index)) if need else None
-        p, n = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
-    else:
+    stream = _raw_stream(index)
+    p, n = None, 0
+    if ws is not None:
         n = ws.numel()
         p = _ptr(ws, "ws", torch.uint8, n, index)
-    rc = f(*args, p, n, _raw_stream(index))
+    elif need:
+        ws = _workspace(need, index, stream)
+        p, n = ws.data_ptr(), ws.numel()
+    rc = f(*args, p, n, stream)
     if rc != 0:
         raise Q4Error(rc)
 
@@ -475,7 +484,7 @@ def q4_0_glu(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, act: s
     pg = _ptr(Wg, "Wg", torch.uint8, mat, i)
     pu = _ptr(Wu, "Wu", torch.uint8, mat, i)
     if h is None:
-        h = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        h = x.new_empty((M, N), dtype=torch.float32)
     ph = _ptr(h, "h", torch.float32, M * N, i)
     _run(_lib.q4_0_glu, q4_0_glu_workspace_bytes(M, N, K), ws, i, px, pg, pu, ph, M, N, K, a)
     return h
@@ -501,10 +510,10 @@ def q4_0_glu_gemm(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, a
     pg = _ptr(Wg, "Wg", torch.uint8, mat, i)
     pu = _ptr(Wu, "Wu", torch.uint8, mat, i)
     if H is None:
-        H = torch.empty((M, N), dtype=torch.float16, device=X.device)
+        H = X.new_empty((M, N), dtype=torch.float16)
     if save and G is None:
-        G = torch.empty((M, N), dtype=torch.float16, device=X.device)
-        U = torch.empty((M, N), dtype=torch.float16, device=X.device)
+        G = X.new_empty((M, N), dtype=torch.float16)
+        U = X.new_empty((M, N), dtype=torch.float16)
     ph = _ptr(H, "H", torch.float16, M * N, i)
     pG = pU = None
     if G is not None:
@@ -534,7 +543,7 @@ def q4_0_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, Wg: to
     pg = _ptr(Wg, "Wg", torch.uint8, mat, i)
     pu = _ptr(Wu, "Wu", torch.uint8, mat, i)
     if dX is None:
-        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dH.device)
+        dX = dH.new_empty((M, K), dtype=torch.bfloat16)
     px = _ptr(dX, "dX", torch.bfloat16, M * K, i)
     _run(_lib.q4_0_glu_backward, q4_0_glu_backward_workspace_bytes(M, N, K), ws, i, pd, pG, pU, pg,
          pu, px, M, N, K, a)
@@ -552,7 +561,7 @@ def q4_0_gemm_backward(dY: torch.Tensor, B: torch.Tensor, K: int, dX: torch.Tens
     pd = _ptr(dY, "dY", torch.bfloat16, M * N, i)
     pb = _ptr(B, "B", torch.uint8, K * (N // 32) * BLOCK_BYTES, i)
     if dX is None:
-        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dY.device)
+        dX = dY.new_empty((M, K), dtype=torch.bfloat16)
     px = _ptr(dX, "dX", torch.bfloat16, M * K, i)
     _run(_lib.q4_0_gemm_backward, q4_0_gemm_backward_workspace_bytes(M, N, K), ws, i, pd, pb, px,
          M, N, K)
@@ -573,7 +582,7 @@ def _lora(f, need, x, B, N, A, Bl, ids, scale, y, ws, dtype, block, names):
     pi = _ptr(ids, "ids", torch.int32, M, i)
     ps = _ptr(scale, "scale", torch.float32, L, i)
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=x.device)
+        y = x.new_empty((M, N), dtype=dtype)
     py = _ptr(y, names[1], dtype, M * N, i)
     _run(f, need(M, N, K, R), ws, i, px, pb, pA, pB, pi, ps, py, M, N, K, R, L)
     return y
