@@ -605,53 +605,68 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
     }
   } else if constexpr (SIDE == kAdapters) {
     // Wide half of the adapters: for every adapter that occurs in the wave's
-    // rows, t16 times B_id^T (R a multiple of 8, steps of 16, the rest zero), of
-    // which the adapter's own rows keep the result and then scale it: an infinity
-    // or NaN in one adapter stays with the rows that use it.
+    // rows, t16 times B_id^T (R a multiple of 8, steps of 16, the rest zero),
+    // which the adapter's own rows scale and add: an infinity or NaN in one
+    // adapter stays with the rows that use it. The loads of all columns and of kC
+    // steps go out together: with many adapters in a tile most of the time goes
+    // by waiting for them.
+    constexpr int kC = 2;
     const int R = g.ad.R;
+    const int r8 = 8 * (lane >> 5);
     int id = lane < min(WR, rw) ? g.ad.ids[mw + lane] : -1;
     if (id < 0 || id >= g.ad.L) id = -1;
     const unsigned long long any = __ballot(id >= 0);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const float ts = 32 * i + lr < rw ? g.ts[mw + 32 * i + lr] : 0.0f;
+      const int row = min(32 * i + lr, rw - 1);
+      const float ts = g.ts[mw + row];
+      const _Float16* tp = g.t16 + (size_t)(mw + row) * R;
+      unsigned band = (unsigned)(any >> (32 * i));
+      while (band) {
+        const int cur = __builtin_amdgcn_readlane(id, 32 * i + __builtin_ctz(band));
+        const unsigned same = (unsigned)(__ballot(id == cur) >> (32 * i));
+        band &= ~same;
+        const bool mine = (same >> lr) & 1u;
+        const _Float16* bp = reinterpret_cast<const _Float16*>(g.ad.B) +
+                             ((size_t)cur * g.ncols + min(col0, g.ncols - 32) + lr) * R;
+        for (int k0 = 0; k0 < R; k0 += 16 * kC) {
+          half8 a[kC], b[NJ][kC];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int col = col0 + j * 32 + lr;
-        float16v extra;
+          for (int c = 0; c < kC; ++c) {
+            const int at = k0 + 16 * c;
+            if (at >= R) break;  // uniform
+            // past R the left operand is zero and the right one some of the same
+            // adapter's; columns past the matrix are not kept
+            const int r0 = min(at + r8, R - 8);
+            a[c] = *reinterpret_cast<const half8*>(tp + r0);
+            if (at + r8 >= R) a[c] = half8{0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < 16; ++r) extra[r] = 0.0f;
-        unsigned band = (unsigned)(any >> (32 * i));
-        while (band) {
-          const int cur = __builtin_amdgcn_readlane(id, 32 * i + __builtin_ctz(band));
-          const unsigned same = (unsigned)(__ballot(id == cur) >> (32 * i));
-          band &= ~same;
-          const bool mine = (same >> lr) & 1u;
-          const _Float16* bp =
-              reinterpret_cast<const _Float16*>(g.ad.B) + ((size_t)cur * g.ncols + col) * R;
-          const _Float16* tp = g.t16 + (size_t)(mw + 32 * i + lr) * R;
-          float16v own;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) own[r] = 0.0f;
-          for (int k0 = 0; k0 < R; k0 += 16) {
-            const int r0 = k0 + 8 * (lane >> 5);
-            half8 a = {0, 0, 0, 0, 0, 0, 0, 0}, b = a;
-            if (mine && r0 < R) a = *reinterpret_cast<const half8*>(tp + r0);
-            if (col < g.ncols && r0 < R) b = *reinterpret_cast<const half8*>(bp + r0);
-            own = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, own, 0, 0, 0);
+            for (int j = 0; j < NJ; ++j)
+              b[j][c] = *reinterpret_cast<const half8*>(
+                  bp + (uint32_t)((col0 + 32 * j < g.ncols ? 32 * j : 0) * R + r0));
           }
 #pragma unroll
-          for (int r = 0; r < 16; ++r) extra[r] = mine ? own[r] : extra[r];
+          for (int j = 0; j < NJ; ++j) {
+            float16v own;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) own[r] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+              if (k0 + 16 * c < R)
+                own = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[j][c], a[c], own, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              acc[i][j][r] = mine ? __builtin_fmaf(own[r], ts, acc[i][j][r]) : acc[i][j][r];
+          }
         }
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
         uint2 v[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float e[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            e[u] = __builtin_fmaf(extra[4 * q + u], ts, acc[i][j][4 * q + u]);
-          v[q] = pack16(e[0], e[1], e[2], e[3]);
-        }
+        for (int q = 0; q < 4; ++q)
+          v[q] = pack16(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                        acc[i][j][4 * q + 3]);
         put(i, j, v);
       }
     }

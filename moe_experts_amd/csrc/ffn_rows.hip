@@ -135,13 +135,14 @@ __global__ __launch_bounds__(kRowThreads) void glu_finish_f16_kernel(
 
 // ---------------------------------------------------------------------------
 // Adapters, narrow half, many rows, on the matrix cores (fp16 in, fp32 sums).
-// Workgroup (i, c) owns 64 rows of X and one of KS shares of K; its 4 waves
-// take the share's K steps of 16 in turn. For every adapter that occurs in the
-// 64 rows the tile is multiplied with 32 rows of A at a time
+// A workgroup owns 64 rows of X, 32 rank indexes and one of KS shares of K; its
+// 4 waves take the share's K steps of 16 in turn. For every adapter that occurs
+// in the 64 rows the tile is multiplied with the 32 rows of A
 // (v_mfma_f32_32x32x16_f16, both operands read straight from memory, K being
 // contiguous in both) and the rows that use that adapter keep the result. Rows
-// of one prompt stand together, so a tile nearly always holds one or two
-// adapters. Bound by its loads: the shares keep enough of them in flight, and
+// of one prompt stand together, so a tile of long prompts holds one or two
+// adapters, a pass; for many short ones the passes are dealt out to `parts`
+// workgroups, of which those without a pass end at once. Bound by its loads: the shares keep enough of them in flight, and
 // A is read once a tile (2000 rows of 11008 at rank 32 in 7 prompts: 60 us in
 // 16-row tiles and one share, 29 us in eight shares, 27 us in 64-row tiles, 21
 // us with two adapters a pass). The waves'
@@ -151,13 +152,17 @@ constexpr int kShrinkRows = 64, kShrinkWaves = 4, kShrinkRanks = 32, kShrinkChun
 
 __global__ __launch_bounds__(kShrinkWaves * kWaveSize) void lora_shrink_tile_kernel(
     const _Float16* __restrict__ X, Adapters ad, float* __restrict__ tp, int M, int K, int tiles,
-    int share) {
+    int share, int shares, int parts) {
   typedef float float16v __attribute__((ext_vector_type(16)));
   __shared__ float sums[kShrinkWaves][kShrinkRows][kShrinkRanks];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tile = blockIdx.x % tiles;
-  const int c = blockIdx.x / tiles;
+  int rest = blockIdx.x / tiles;
+  const int c = rest % shares;
+  rest /= shares;
+  const int part = rest % parts;               // of the tile's passes
+  const int r0 = rest / parts * kShrinkRanks;  // first rank index
   const int m0 = tile * kShrinkRows;
   const int kb = c * share, ke = min(K, kb + share);  // multiples of a chunk
   const int R = ad.R;
@@ -169,83 +174,86 @@ __global__ __launch_bounds__(kShrinkWaves * kWaveSize) void lora_shrink_tile_ker
 #pragma unroll
   for (int i = 0; i < 2; ++i) xr[i] = X + (size_t)min(m0 + 32 * i + lr, M - 1) * K + kg;
 
-  for (int r0 = 0; r0 < R; r0 += kShrinkRanks) {
-    float16v keep[2];
+  float16v keep[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) keep[i][e] = 0.0f;
-    unsigned long long todo = __ballot(id >= 0);
-    while (todo) {
-      // two adapters a pass, so that a tile across the end of a prompt reads X
-      // once (a lone adapter is taken twice, its second product not kept)
-      const int cur0 = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-      const unsigned long long same0 = __ballot(id == cur0);
-      todo &= ~same0;
-      const bool two = todo != 0;
-      const int cur1 = two ? __builtin_amdgcn_readlane(id, __builtin_ctzll(todo)) : cur0;
-      const unsigned long long same1 = two ? __ballot(id == cur1) : 0;
-      todo &= ~same1;
-      const _Float16* ar[2];
+    for (int e = 0; e < 16; ++e) keep[i][e] = 0.0f;
+  unsigned long long todo = __ballot(id >= 0);
+  // rows whose sums this workgroup writes: part 0 those without adapter too
+  unsigned long long mine = part == 0 ? ~todo : 0;
+  for (int pass = 0; todo; pass = pass + 1 == parts ? 0 : pass + 1) {
+    // two adapters a pass, so that a tile across the end of a prompt reads X
+    // once (a lone adapter is taken twice, its second product not kept)
+    const int cur0 = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    const unsigned long long same0 = __ballot(id == cur0);
+    todo &= ~same0;
+    const bool two = todo != 0;
+    const int cur1 = two ? __builtin_amdgcn_readlane(id, __builtin_ctzll(todo)) : cur0;
+    const unsigned long long same1 = two ? __ballot(id == cur1) : 0;
+    todo &= ~same1;
+    if (pass != part) continue;
+    mine |= same0 | same1;
+    const _Float16* ar[2];
 #pragma unroll
-      for (int f = 0; f < 2; ++f)  // rank indexes past R repeat the last one, not kept
-        ar[f] = reinterpret_cast<const _Float16*>(ad.A) +
-                ((size_t)(f ? cur1 : cur0) * R + min(r0 + lr, R - 1)) * K + kg;
-      float16v acc[2][2];
+    for (int f = 0; f < 2; ++f)  // rank indexes past R repeat the last one, not kept
+      ar[f] = reinterpret_cast<const _Float16*>(ad.A) +
+              ((size_t)(f ? cur1 : cur0) * R + min(r0 + lr, R - 1)) * K + kg;
+    float16v acc[2][2];
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[f][i][e] = 0.0f;
-      for (int k0 = kb + wave * kShrinkChunk; k0 < ke; k0 += kShrinkWaves * kShrinkChunk) {
-        constexpr int kU = kShrinkChunk / 16;
-        half8 xa[kU][2], b[kU][2];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            xa[u][i] = *reinterpret_cast<const half8*>(xr[i] + k0 + 16 * u);
-#pragma unroll
-          for (int f = 0; f < 2; ++f)
-            if (f == 0 || two) b[u][f] = *reinterpret_cast<const half8*>(ar[f] + k0 + 16 * u);
-        }
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          if (f == 0 || two)
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                acc[f][i] =
-                    __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[u][i], b[u][f], acc[f][i], 0, 0, 0);
-      }
-      // a 32 x 32 result: lane l holds column l % 32, register e row
-      // 8 * (e / 4) + 4 * (l / 32) + e % 4
+    for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int row = 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-          keep[i][e] = (same0 >> row) & 1ull
-                           ? acc[0][i][e]
-                           : ((same1 >> row) & 1ull ? acc[1][i][e] : keep[i][e]);
-        }
+        for (int e = 0; e < 16; ++e) acc[f][i][e] = 0.0f;
+    for (int k0 = kb + wave * kShrinkChunk; k0 < ke; k0 += kShrinkWaves * kShrinkChunk) {
+      constexpr int kU = kShrinkChunk / 16;
+      half8 xa[kU][2], b[kU][2];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          xa[u][i] = *reinterpret_cast<const half8*>(xr[i] + k0 + 16 * u);
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          if (f == 0 || two) b[u][f] = *reinterpret_cast<const half8*>(ar[f] + k0 + 16 * u);
+      }
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+        if (f == 0 || two)
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              acc[f][i] =
+                  __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[u][i], b[u][f], acc[f][i], 0, 0, 0);
     }
-    if (r0) __syncthreads();  // the sums of the ranks before have been read
+    // a 32 x 32 result: lane l holds column l % 32, register e row
+    // 8 * (e / 4) + 4 * (l / 32) + e % 4
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        sums[wave][32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)][lr] = keep[i][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < kShrinkRows * kShrinkRanks; i += kShrinkWaves * kWaveSize) {
-      const int row = i / kShrinkRanks, r = i % kShrinkRanks;
-      float v = 0.0f;
+      for (int e = 0; e < 16; ++e) {
+        const int row = 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+        keep[i][e] = (same0 >> row) & 1ull
+                         ? acc[0][i][e]
+                         : ((same1 >> row) & 1ull ? acc[1][i][e] : keep[i][e]);
+      }
+  }
+  if (mine == 0) return;  // the same in every wave
 #pragma unroll
-      for (int w = 0; w < kShrinkWaves; ++w) v += sums[w][row][r];
-      if (m0 + row < M && r0 + r < R) tp[((size_t)c * M + m0 + row) * R + r0 + r] = v;
-    }
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      sums[wave][32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)][lr] = keep[i][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kShrinkRows * kShrinkRanks; i += kShrinkWaves * kWaveSize) {
+    const int row = i / kShrinkRanks, r = i % kShrinkRanks;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kShrinkWaves; ++w) v += sums[w][row][r];
+    if ((mine >> row) & 1ull && m0 + row < M && r0 + r < R)
+      tp[((size_t)c * M + m0 + row) * R + r0 + r] = v;
   }
 }
 
@@ -505,9 +513,11 @@ hipError_t launch_lora_shrink(const uint16_t* X, const Adapters& ad, float* tp, 
                               uint16_t* t16, float* ts, int M, int K, hipStream_t st) {
   const int share = shrink_share(M, K), KS = shrink_shares(M, K);
   const int tiles = (M + kShrinkRows - 1) / kShrinkRows;
-  hipLaunchKernelGGL(lora_shrink_tile_kernel, dim3((unsigned)tiles * KS),
+  const int groups = tiles * KS * ((ad.R + kShrinkRanks - 1) / kShrinkRanks);
+  const int parts = std::max(1, std::min(16, 1024 / groups));
+  hipLaunchKernelGGL(lora_shrink_tile_kernel, dim3((unsigned)groups * parts),
                      dim3(kShrinkWaves * kWaveSize), 0, st, reinterpret_cast<const _Float16*>(X),
-                     ad, tp, M, K, tiles, share);
+                     ad, tp, M, K, tiles, share, KS, parts);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(lora_rows_kernel, dim3(blocks(M, kRowThreads / kWaveSize)), dim3(kRowThreads),
