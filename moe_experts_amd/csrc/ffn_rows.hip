@@ -142,10 +142,12 @@ __global__ __launch_bounds__(kRowThreads) void glu_finish_f16_kernel(
 // contiguous in both) and the rows that use that adapter keep the result. Rows
 // of one prompt stand together, so a tile of long prompts holds one or two
 // adapters, a pass; for many short ones the passes are dealt out to `parts`
-// workgroups, of which those without a pass end at once. Bound by its loads: the shares keep enough of them in flight, and
-// A is read once a tile (2000 rows of 11008 at rank 32 in 7 prompts: 60 us in
-// 16-row tiles and one share, 29 us in eight shares, 27 us in 64-row tiles, 21
-// us with two adapters a pass). The waves'
+// workgroups, of which those without a pass end at once (300 rows of 100 requests,
+// 576 x 2560 at rank 64, with the wide half's loads together: 91.5 -> 39.3 us a
+// call). Bound by its loads: the shares keep enough of them in flight, and A is
+// read once a tile (2000 rows of 11008 at rank 32 in 7 prompts: 60 us in 16-row
+// tiles and one share, 29 us in eight shares, 27 us in 64-row tiles, 21 us with
+// two adapters a pass). The waves'
 // sums are added in wave order, the shares' by lora_rows_kernel.
 // ---------------------------------------------------------------------------
 constexpr int kShrinkRows = 64, kShrinkWaves = 4, kShrinkRanks = 32, kShrinkChunk = 64;
