@@ -35,10 +35,13 @@
 // against 410 us at 2048 rows of 4096 x 11008 (half of the weights: 1.29, 539 us;
 // all: 1.00, 703 us).
 //
-// What bounds it: full tiles keep the matrix cores 47 % (forward) to 58 %
-// (gradient) busy at a clock that falls to 1.7 GHz, the power limit's. Deeper
-// prefetch, reads ahead of the products and moving work between the roles left
-// the times as they were.
+// What bounds it: a step of 256 rows is 1024 cycles of matrix instructions and
+// moves 144 KiB through LDS (1150 cycles); it takes 1750 cycles with all CUs busy,
+// where the power limit holds the clock at 1.75 GHz and the matrix cores are busy
+// 48 % (forward) to 58 % (gradient), 2350 at 2.4 GHz with 160 CUs busy. The
+// consumers' LDS reads are the long chain: raising the producers' wave priority
+// cost 3 to 6 %, raising the consumers' changed nothing, nor did deeper prefetch or
+// moving work between the roles.
 #include <type_traits>
 
 #include "ffn_device.hpp"
