@@ -36,12 +36,12 @@
 // all: 1.00, 703 us).
 //
 // What bounds it: a step of 256 rows is 1024 cycles of matrix instructions and
-// moves 144 KiB through LDS (1150 cycles); it takes 1750 cycles with all CUs busy,
-// where the power limit holds the clock at 1.75 GHz and the matrix cores are busy
-// 48 % (forward) to 58 % (gradient), 2350 at 2.4 GHz with 160 CUs busy. The
-// consumers' LDS reads are the long chain: raising the producers' wave priority
-// cost 3 to 6 %, raising the consumers' changed nothing, nor did deeper prefetch or
-// moving work between the roles.
+// moves 144 KiB through LDS; it takes 1750 cycles with all CUs busy, where the
+// power limit holds the clock at 1.6 to 1.75 GHz, the matrix cores are busy 48 %
+// (forward) to 56 % (gradient) and LDS 45 to 49 %, and 2350 at 2.4 GHz with 160
+// CUs busy. The consumers' chain of LDS reads and products is the long one: raising
+// the producers' wave priority cost 3 to 6 %, raising the consumers' changed
+// nothing, nor did deeper prefetch or moving work between the roles.
 #include <type_traits>
 
 #include "ffn_device.hpp"
