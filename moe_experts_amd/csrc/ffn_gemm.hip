@@ -4,10 +4,14 @@
 //   adapters  Y = X . deq(B) + t . B_id^T                     X fp16 [M][K]
 //   gradient  dX = dG . deq(Wg)^T + dU . deq(Wu)^T            one or two matrices
 //
-// Tile BM x 128, K steps of 64, 512 lanes: 4 consumer waves issue only matrix
-// instructions, 4 producer waves fetch both operands and dequantize the weights
-// into an fp16 LDS tile [column][k], so the VALU work of one role runs beside the
-// matrix work of the other. LDS holds two steps; a barrier a step hands over.
+// Tile BM x 128, K steps of 64. Consumer waves issue the matrix instructions, 4
+// producer waves fetch the weights and dequantize them into an fp16 LDS tile
+// [column][k], so the VALU work of one role runs beside the matrix work of the
+// other. LDS holds two steps; a barrier a step hands over. Up to 128 rows there are
+// 4 consumer waves and the producers copy the left operand too. At 256 rows there
+// are 8, two a SIMD, which copy it themselves: with 4 and 4 waves both roles had
+// 2000 cycles of a step's 2270 to do (777 rows of 5120 x 1536, gradient: 49.5 us;
+// 8 consumers 46.5, and copying 45.6; 2048 rows of 4096 x 4096: 77.3, 75.4, 74.5).
 //
 //   * Left operand: 16-byte loads into registers, two steps ahead, and 16-byte
 //     LDS stores, XOR-swizzled.
@@ -36,12 +40,11 @@
 // all: 1.00, 703 us).
 //
 // What bounds it: a step of 256 rows is 1024 cycles of matrix instructions and
-// moves 144 KiB through LDS; it takes 1750 cycles with all CUs busy, where the
-// power limit holds the clock at 1.6 to 1.75 GHz, the matrix cores are busy 48 %
-// (forward) to 56 % (gradient) and LDS 45 to 49 %, and 2350 at 2.4 GHz with 160
-// CUs busy. The consumers' chain of LDS reads and products is the long one: raising
-// the producers' wave priority cost 3 to 6 %, raising the consumers' changed
-// nothing, nor did deeper prefetch or moving work between the roles.
+// moves 176 KiB through LDS. With all CUs busy the power limit holds the clock at
+// 1.6 to 1.75 GHz, and moving work between the roles gives 2 to 4 %; with 160 CUs
+// busy the clock is 2.4 GHz and the producers' chain is the long one (their
+// weights; consumers wait 500 to 900 of 2700 cycles). Raised wave priorities and
+// deeper prefetch gave nothing.
 #include <type_traits>
 
 #include "ffn_device.hpp"
@@ -293,13 +296,21 @@ struct GradientWeights {
   }
 };
 
+// Consumer waves. Eight, two a SIMD, have time to copy the left operand as well.
+template <int BM>
+constexpr int kConsumers = BM == 256 ? 8 : 4;
+template <int BM>
+constexpr bool kConsumersCopy = BM == 256;
+template <int BM>
+constexpr int kTileThreads = kConsumers<BM> * kWaveSize + kRole;
+
 // ---------------------------------------------------------------- left operand
 // A step's left operand through registers: 16-byte loads, 16-byte LDS stores.
 // (LDS-DMA copies of 16 bytes a lane kept the address unit busy for 60 to 80
 // cycles each, 32 of them a step of 256 rows.)
-template <int BM>
+template <int BM, int LANES>
 struct LeftOperand {
-  static constexpr int kInstr = BM * kColBytes / 16 / kRole;
+  static constexpr int kInstr = BM * kColBytes / 16 / LANES;
   __amdgpu_buffer_rsrc_t r;
   uint32_t off[kInstr];
   int t;
@@ -311,7 +322,7 @@ struct LeftOperand {
     r = make_rsrc(g.X + (size_t)m0 * g.lda, (uint32_t)rows * (uint32_t)g.lda * 2u);
 #pragma unroll
     for (int i = 0; i < kInstr; ++i) {
-      const int slot = i * kRole + t;  // row slot / 8, 16-byte chunk slot % 8
+      const int slot = i * LANES + t;  // row slot / 8, 16-byte chunk slot % 8
       const int row = slot >> 3;
       off[i] = row < rows ? ((uint32_t)row * (uint32_t)g.lda + 8u * (slot & 7)) * 2u : kOut;
     }
@@ -321,7 +332,7 @@ struct LeftOperand {
     raw.v[i] = make_uint4(v[0], v[1], v[2], v[3]);
   }
   __device__ __forceinline__ void store(const Raw& raw, uint8_t* __restrict__ stage, int i) const {
-    const int slot = i * kRole + t;
+    const int slot = i * LANES + t;
     const int row = slot >> 3;
     *reinterpret_cast<uint4*>(stage + row * kColBytes + (((slot & 7) ^ swz_x(row)) << 4)) =
         raw.v[i];
@@ -334,24 +345,26 @@ template <int BM>
 constexpr int kDepth = BM == 64 ? 4 : 2;
 
 // What the producers do while step ks is multiplied: store ks + 1 from its
-// registers into its LDS tiles, dequantized, and load ks + 1 + D into them. Steps
+// registers into its LDS tiles, dequantized, and load ks + 1 + D into them (the left
+// operand where the consumers do not copy it). Steps
 // past the last repeat it, into registers that are not read.
 template <int BM, class W>
-__device__ __forceinline__ void produce_step(const W& wt, const LeftOperand<BM>& left,
+__device__ __forceinline__ void produce_step(const W& wt, const LeftOperand<BM, kRole>& left,
                                              typename W::Raw& raw,
-                                             typename LeftOperand<BM>::Raw& lraw,
+                                             typename LeftOperand<BM, kRole>::Raw& lraw,
                                              uint8_t* __restrict__ x, uint8_t* __restrict__ b,
                                              int next) {
   typename W::Taken k;
   wt.take(raw, k);
-  constexpr int kPer = (LeftOperand<BM>::kInstr + 3) / 4;
+  constexpr int kInstr = kConsumersCopy<BM> ? 0 : LeftOperand<BM, kRole>::kInstr;
+  constexpr int kPer = (kInstr + 3) / 4;
 #pragma unroll
   for (int part = 0; part < 4; ++part) {
     wt.store(k, b, part);
     wt.load(raw, next, part);
 #pragma unroll
     for (int i = part * kPer; i < part * kPer + kPer; ++i)
-      if (i < LeftOperand<BM>::kInstr) {
+      if (i < kInstr) {
         left.store(lraw, x, i);
         left.load(lraw, next, i);
       }
@@ -373,16 +386,17 @@ __device__ __forceinline__ void produce(const TileArgs& g, uint8_t* __restrict__
   constexpr int kStage = kBBytes + kRestBytes<SIDE>;
   W wt;
   wt.init(g, tn, t);
-  LeftOperand<BM> left;
-  left.init(g, m0, rows, t);
+  LeftOperand<BM, kRole> left;
+  if constexpr (!kConsumersCopy<BM>) left.init(g, m0, rows, t);
   typename W::Raw raw[D];
-  typename LeftOperand<BM>::Raw lraw[D];
+  typename LeftOperand<BM, kRole>::Raw lraw[D];
 #pragma unroll
   for (int d = 0; d < D; ++d) {
 #pragma unroll
     for (int part = 0; part < 4; ++part) wt.load(raw[d], min(kb + d, ke - 1), part);
 #pragma unroll
-    for (int i = 0; i < LeftOperand<BM>::kInstr; ++i) left.load(lraw[d], min(kb + d, ke - 1), i);
+    for (int i = 0; i < LeftOperand<BM, kRole>::kInstr; ++i)
+      if constexpr (!kConsumersCopy<BM>) left.load(lraw[d], min(kb + d, ke - 1), i);
     __builtin_amdgcn_sched_barrier(0);
   }
   produce_step<BM>(wt, left, raw[0], lraw[0], xs, bs, min(kb + D, ke - 1));
@@ -404,7 +418,7 @@ __device__ __forceinline__ void produce(const TileArgs& g, uint8_t* __restrict__
 }
 
 template <int BM, Side SIDE>
-__global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(TileArgs g) {
+__global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_kernel(TileArgs g) {
   constexpr int kXBytes = BM * kColBytes;
   constexpr int kStage = kBBytes + kRestBytes<SIDE>;
   // two steps' left operand and weights; at the end the waves' results
@@ -422,8 +436,9 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
   const int ke = min(g.nk, kb + g.kper);  // kb < ke: the plan leaves no split empty
   const int wave = threadIdx.x >> 6;
 
-  if (wave >= 4) {
-    produce<BM, SIDE>(g, xs, bs, m0, rows, tn, kb, ke, (int)threadIdx.x - kRole);
+  constexpr int NC = kConsumers<BM>;
+  if (wave >= NC) {
+    produce<BM, SIDE>(g, xs, bs, m0, rows, tn, kb, ke, (int)threadIdx.x - NC * kWaveSize);
     return;
   }
 
@@ -431,7 +446,7 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
   const int lane = threadIdx.x & 63;
   constexpr int WGR = BM == 256 ? 4 : 2;  // waves along the rows
   constexpr int WR = BM / WGR;            // rows of a wave: 64 or 32
-  constexpr int WC = BN / (4 / WGR);      // columns of a wave: 128 or 64
+  constexpr int WC = BN / (NC / WGR);     // columns of a wave: 64
   constexpr int MI = WR / 32, NJ = WC / 32;
   const int wm = wave % WGR;
   const int wn = wave / WGR;
@@ -479,11 +494,28 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
       for (int j = 0; j < NJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.rest[j], o.a[i], acc[i][j], 0, 0, 0);
   };
-  // One consumer wave a SIMD: nothing else hides the latency of its LDS reads,
-  // so the reads of a quarter are issued before the products of the one before,
-  // and a step's last products run after the barrier, over the first reads of
-  // the next step.
+  // One or two consumer waves a SIMD: little else hides the latency of their LDS
+  // reads, so the reads of a quarter are issued before the products of the one
+  // before, and a step's last products run after the barrier, over the first reads
+  // of the next step.
   constexpr int Q = BK / 16;
+  constexpr bool COPY = kConsumersCopy<BM>;
+  using Left = LeftOperand<BM, NC * kWaveSize>;
+  Left left;
+  typename Left::Raw lraw[2];
+  if constexpr (COPY) {
+    left.init(g, m0, rows, (int)threadIdx.x);
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+#pragma unroll
+      for (int i = 0; i < Left::kInstr; ++i) left.load(lraw[d], min(kb + d, ke - 1), i);
+#pragma unroll
+    for (int i = 0; i < Left::kInstr; ++i) {
+      left.store(lraw[0], xs, i);
+      left.load(lraw[0], min(kb + 2, ke - 1), i);
+    }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  }
   lds_barrier();
   if constexpr (MI * NJ <= 2) {
     // few products: all of a step's reads at once
@@ -504,18 +536,27 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
   } else {
     Operands o[2];
     read(o[0], xs, bs, 0);
-    for (int ks = kb; ks < ke; ++ks) {
+    auto step = [&](int ks, typename Left::Raw& next) __attribute__((always_inline)) {
       const int cur = (ks - kb) & 1;
       const uint8_t* x = xs + cur * kXBytes;
       const uint8_t* b = bs + cur * kStage;
 #pragma unroll
       for (int q = 0; q < Q - 1; ++q) {
         read(o[(q + 1) & 1], x, b, q + 1);
+        if constexpr (COPY) {
+          constexpr int kPer = (Left::kInstr + Q - 2) / (Q - 1);
+#pragma unroll
+          for (int i = q * kPer; i < q * kPer + kPer; ++i)
+            if (i < Left::kInstr) {
+              left.store(next, xs + (cur ^ 1) * kXBytes, i);
+              left.load(next, min(ks + 3, ke - 1), i);
+            }
+        }
         __builtin_amdgcn_sched_barrier(0);
         multiply(o[q & 1], q);
         __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // this wave's reads done before the stages are reused
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // reads and copies done before the stages change roles
       lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
       // past the last step this reads a stage that is not used
@@ -523,6 +564,16 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
       __builtin_amdgcn_sched_barrier(0);
       multiply(o[(Q - 1) & 1], Q - 1);
       __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (COPY) {  // the two sets of registers are named at compile time
+      int ks = kb;
+      for (; ks + 2 <= ke; ks += 2) {
+        step(ks, lraw[1]);
+        step(ks + 1, lraw[0]);
+      }
+      if (ks < ke) step(ks, lraw[1]);
+    } else {
+      for (int ks = kb; ks < ke; ++ks) step(ks, lraw[0]);
     }
   }
 
@@ -560,7 +611,7 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
   // block of three results took 20000 cycles, as long as nine K steps).
   constexpr int OC = SIDE == kDual ? WC / 2 : WC;  // result columns of the wave
   constexpr int kPitch = OC * 2 + 16;              // bytes of an LDS row
-  static_assert(4 * WR * kPitch <= 2 * kXBytes + 2 * kStage, "results fit the stages");
+  static_assert(NC * WR * kPitch <= 2 * kXBytes + 2 * kStage, "results fit the stages");
   uint8_t* out = lds + wave * (WR * kPitch);
   const int col0 = SIDE == kDual ? tn * 64 + wn * OC : tn * BN + wn * OC;
   auto put = [&](int i, int j, const uint2(&v)[4]) {  // 32 rows x 32 columns
@@ -698,7 +749,7 @@ __global__ __launch_bounds__(2 * kRole, BM == 256 ? 2 : 4) void ffn_gemm_kernel(
 // Tile height (64, 128 or 256 rows) and splits of the contraction, by the time a
 // CU with the most work takes. n workgroups are k = ceil(n / 256) a CU; a K step
 // costs it, in us (from sweeps of heights and splits at 96 to 2048 rows):
-//   256 rows: 0.68 with few CUs busy, up to 1.05 with all (the clock falls to
+//   256 rows: 0.63 with few CUs busy, up to 1.02 with all (the clock falls to
 //             1.7 GHz under full load);
 //   128 rows: 0.44 alone, 0.60 each with two on a CU (LDS and registers allow it);
 //    64 rows: 0.40 alone, 0.45 each.
@@ -721,7 +772,7 @@ void plan_tiles(FfnPlan& p, int M, int tiles_n, int nk, size_t sum_cols) {
       const int tiles_m = (M + heights[h] - 1) / heights[h];
       const double n = (double)tiles_m * tiles_n * s;
       const double k = (double)(((long long)n + 255) / 256);
-      const double step = h == 2 ? 0.68 + 0.37 * n / (256.0 * k)
+      const double step = h == 2 ? 0.63 + 0.39 * n / (256.0 * k)
                           : h == 1 ? (k == 1 ? 0.44 : 0.60) : (k == 1 ? 0.40 : 0.45);
       double cost = k * (kper * step + start[h]);
       if (s > 1) cost += 4.0 + s * (double)M * (double)sum_cols * 8.0 / 4.5e6;
@@ -744,15 +795,15 @@ hipError_t launch_tiles(TileArgs& g, const FfnPlan& p, hipStream_t st) {
   g.kper = p.kper;
   g.nk = p.nk;
   const long long grid = (long long)p.tiles_m * p.tiles_n * p.S;
-  if (grid > 0x7fffffLL) return hipErrorInvalidValue;  // 2^32 lanes
+  if (grid > 0x3fffffLL) return hipErrorInvalidValue;  // below 2^32 lanes
   if (p.BM == 64)
-    hipLaunchKernelGGL((ffn_gemm_kernel<64, SIDE>), dim3((unsigned)grid), dim3(2 * kRole), 0, st,
+    hipLaunchKernelGGL((ffn_gemm_kernel<64, SIDE>), dim3((unsigned)grid), dim3(kTileThreads<64>), 0, st,
                        g);
   else if (p.BM == 128)
-    hipLaunchKernelGGL((ffn_gemm_kernel<128, SIDE>), dim3((unsigned)grid), dim3(2 * kRole), 0, st,
+    hipLaunchKernelGGL((ffn_gemm_kernel<128, SIDE>), dim3((unsigned)grid), dim3(kTileThreads<128>), 0, st,
                        g);
   else
-    hipLaunchKernelGGL((ffn_gemm_kernel<256, SIDE>), dim3((unsigned)grid), dim3(2 * kRole), 0,
+    hipLaunchKernelGGL((ffn_gemm_kernel<256, SIDE>), dim3((unsigned)grid), dim3(kTileThreads<256>), 0,
                        st, g);
   return hipGetLastError();
 }
