@@ -45,6 +45,7 @@
 // busy the clock is 2.4 GHz and the producers' chain is the long one (their
 // weights; consumers wait 500 to 900 of 2700 cycles). Raised wave priorities and
 // deeper prefetch gave nothing.
+#include <algorithm>
 #include <type_traits>
 
 #include "ffn_device.hpp"
@@ -747,19 +748,24 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
 }
 
 // Tile height (64, 128 or 256 rows) and splits of the contraction, by the time a
-// CU with the most work takes. n workgroups are k = ceil(n / 256) a CU; a K step
-// costs it, in us (from sweeps of heights and splits at 96 to 2048 rows):
-//   256 rows: 0.63 with few CUs busy, up to 1.02 with all (the clock falls to
-//             1.7 GHz under full load);
-//   128 rows: 0.44 alone, 0.60 each with two on a CU (LDS and registers allow it);
-//    64 rows: 0.40 alone, 0.45 each.
+// CU with the most work takes. n workgroups are k = ceil(n / 256) a CU, a share
+// `load` of what k on every CU would be; `live` is the share of the tiles' rows
+// that exist. A K step costs a workgroup, in us (from sweeps of heights and splits
+// at 100 to 2048 rows; more with more CUs busy, as the clock falls):
+//             gradients, adapters               dual
+//   256 rows  0.39 live + 0.6 load, at least     0.75 + 0.25 load
+//             0.66
+//   128 rows  0.54, or two and more a CU        0.74, 0.45 + 0.2 live load
+//             0.35 + 0.22 live load each
+//    64 rows  0.46, 0.38                        0.60, 0.55
 // A workgroup costs its prologue and results (3, 2 or 1.5 us) besides, splits
 // the partial sums, written and read at 4.5 TB/s, and a kernel that adds them.
-// Full tiles win while they fill the GPU (2048 rows, 4096 x 11008 twice, without
-// the products for roundings: 624, 430, 398 us with 64, 128, 256 rows), lower ones below (400 rows, 4096 x 4096
-// twice: 67, 44, 52 us; 200 rows of a gradient: 128 rows in 4 splits 23.8 us,
-// 256 rows in 8 splits 28.2).
-void plan_tiles(FfnPlan& p, int M, int tiles_n, int nk, size_t sum_cols) {
+// Measured (us): gradient of 150 rows of 11008 x 4096: 256 rows in 2 splits 38.4, 128
+// rows 42.9; of 200 rows of 4096 x 4096: 128 rows in 4 splits 24.6, 256 in 8 28.2;
+// dual, 150 rows of 11008 x 4096: 256 rows in 4 splits 56.3, 128 in 2 75.5; 777 of
+// 5120 x 1536: 51.6 in 2 splits, 59.0 by 128 rows; 2048 of 4096 x 11008, without
+// the products for roundings: 624, 430, 398 with 64, 128, 256 rows.
+void plan_tiles(FfnPlan& p, int M, int tiles_n, int nk, size_t sum_cols, bool dual) {
   const int heights[3] = {64, 128, 256};
   const double start[3] = {1.5, 2.0, 3.0};
   double best = 1e30;
@@ -772,8 +778,16 @@ void plan_tiles(FfnPlan& p, int M, int tiles_n, int nk, size_t sum_cols) {
       const int tiles_m = (M + heights[h] - 1) / heights[h];
       const double n = (double)tiles_m * tiles_n * s;
       const double k = (double)(((long long)n + 255) / 256);
-      const double step = h == 2 ? 0.63 + 0.39 * n / (256.0 * k)
-                          : h == 1 ? (k == 1 ? 0.44 : 0.60) : (k == 1 ? 0.40 : 0.45);
+      const double load = n / (256.0 * k);
+      const double live = (double)M / ((double)tiles_m * heights[h]);
+      double step;
+      if (h == 2)
+        step = dual ? 0.75 + 0.25 * load : std::max(0.66, 0.39 * live + 0.6 * load);
+      else if (h == 1)
+        step = k == 1 ? (dual ? 0.74 : 0.54)
+                      : (dual ? 0.45 + 0.2 * live * load : 0.35 + 0.22 * live * load);
+      else
+        step = k == 1 ? (dual ? 0.60 : 0.46) : (dual ? 0.55 : 0.38);
       double cost = k * (kper * step + start[h]);
       if (s > 1) cost += 4.0 + s * (double)M * (double)sum_cols * 8.0 / 4.5e6;
       if (cost < best) {
@@ -823,7 +837,7 @@ FfnPlan plan_glu_gemm(int M, int N, int K) {
     p.ws_bytes = p.sp.part_bytes;
     return p;
   }
-  plan_tiles(p, M, (N + 63) / 64, K / BK, (size_t)2 * N);
+  plan_tiles(p, M, (N + 63) / 64, K / BK, (size_t)2 * N, true);
   p.ws_bytes = p.S > 1 ? (size_t)2 * p.S * M * N * sizeof(float) : 0;
   return p;
 }
@@ -863,7 +877,7 @@ FfnPlan plan_gemm_lora(int M, int N, int K, int R) {
     p.sp = plan_strip(M, N, K, 1, false);
     p.S = p.sp.S;
   } else {
-    plan_tiles(p, M, (N + BN - 1) / BN, K / BK, (size_t)N);
+    plan_tiles(p, M, (N + BN - 1) / BN, K / BK, (size_t)N, false);
   }
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -919,7 +933,7 @@ hipError_t launch_gemm_lora(const uint16_t* X, const uint8_t* B, const Adapters&
 
 FfnPlan plan_gradient(int M, int N, int K, int mats) {
   FfnPlan p{};
-  plan_tiles(p, M, (K + BN - 1) / BN, mats * (N / BK), (size_t)K);
+  plan_tiles(p, M, (K + BN - 1) / BN, mats * (N / BK), (size_t)K, false);
   p.off_a = 0;
   size_t at = align256((size_t)M * mats * N * 2);
   p.off_rs = at;
