@@ -29,8 +29,9 @@
  *    A *_workspace_bytes() function returns 0 for every shape its entry point
  *    refuses (and for shapes that need no workspace); it never fails otherwise.
  *    Its contents are scratch (no initialisation needed). One workspace serves
- *    one call at a time: calls that overlap in time (for example on two
- *    streams) need separate workspaces.
+ *    one call at a time: calls that overlap in time (on two streams, or
+ *    enqueued by two host threads on one stream, whose kernels may then
+ *    alternate) need separate workspaces.
  *  - Determinism: for the same arguments a call produces bitwise identical
  *    results (fixed reduction order, no floating-point atomics).
  */

@@ -131,13 +131,21 @@ def _dev(t: torch.Tensor, name: str, dtype, numel: int):
     return t.data_ptr()
 
 
-# Workspaces: one scratch buffer per (device, stream), grown on demand. Calls
-# on one stream run in order, so they can share it. A call that is being
-# captured takes memory of its own from the graph's pool instead: graphs that
-# are replayed at the same time must not share scratch memory, and a graph must
-# not depend on a buffer that a later, larger call replaces.
-_ws_lock = threading.Lock()
-_ws_cache: dict = {}
+# Workspaces: one scratch buffer per host thread, device and stream, grown on
+# demand. The calls of one thread on one stream run in order, so they can share
+# it; two threads cannot, even on one stream: a call enqueues several kernels that
+# hand partial sums over, without the interpreter's lock, and another thread's
+# kernels may come between them. A thread's buffers go when it ends; the memory
+# belongs to the stream it was taken on, so kernels still in flight there keep it. A
+# call that is being captured takes memory of its own from the graph's pool
+# instead: graphs that are replayed at the same time must not share scratch memory,
+# and a graph must not depend on a buffer that a later, larger call replaces.
+class _Workspaces(threading.local):
+    def __init__(self):
+        self.buffers: dict = {}  # (device index, stream handle): tensor
+
+
+_workspaces = _Workspaces()
 
 
 def workspace(nbytes: int, device) -> torch.Tensor | None:
@@ -152,15 +160,12 @@ def workspace(nbytes: int, device) -> torch.Tensor | None:
 def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    buffers = _workspaces.buffers
     key = (index, stream)
-    buf = _ws_cache.get(key)
+    buf = buffers.get(key)
     if buf is None or buf.numel() < nbytes:
-        with _ws_lock:
-            buf = _ws_cache.get(key)
-            if buf is None or buf.numel() < nbytes:
-                buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8,
-                                  device=torch.device("cuda", index))
-                _ws_cache[key] = buf
+        buf = buffers[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8,
+                                         device=torch.device("cuda", index))
     return buf
 
 
