@@ -152,12 +152,16 @@ def workspace(nbytes: int, device) -> torch.Tensor | None:
     if nbytes == 0:
         return None
     index = torch.device(device).index
+    if index is not None and index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return workspace(nbytes, device)
     if index is None:
         index = torch.cuda.current_device()
     return _workspace(nbytes, index, _raw_stream(index))
 
 
 def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
+    """`index` is the current device: what is asked is whether its stream is being captured."""
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
     buffers = _workspaces.buffers

@@ -116,3 +116,17 @@ def test_one_thread_keeps_its_buffer(fake):
     grown = binding._workspace(first.numel() + 1, 0, 0)
     assert grown.numel() > first.numel()
     assert binding._workspace(16, 0, 0).data_ptr() == grown.data_ptr()
+
+
+@pytest.mark.parametrize("current,asked", [(0, 1), (1, 0)])
+def test_a_capture_on_another_device_than_the_current_one(fake, current, asked):
+    """Whether a call is captured is asked of the device it runs on."""
+    fake.current = current
+    eager = binding.workspace(4096, torch.device("cuda", asked))
+    assert binding.workspace(4096, torch.device("cuda", asked)) is eager
+    fake.capturing = {asked}
+    captured = binding.workspace(4096, torch.device("cuda", asked))
+    assert captured.data_ptr() != eager.data_ptr() and fake.taken[-1] == (4096, asked)
+    fake.capturing = {current}  # a capture that this call is not part of
+    assert binding.workspace(4096, torch.device("cuda", asked)) is eager
+    assert fake.current == current
