@@ -147,6 +147,20 @@ class _Workspaces(threading.local):
 
 _workspaces = _Workspaces()
 
+# A capture that was not begun through torch (hipStreamBeginCapture) gets ordinary
+# memory, which torch would give to others while the graph still writes to it, and
+# nothing says when that graph ends: such workspaces are kept until the process
+# ends. A caller that minds passes ws.
+_captured: list = []
+
+
+def _of_a_graph_pool(address: int, index: int) -> bool:
+    """Whether torch's allocator has this memory in a pool of its own, as it has a graph's."""
+    for s in torch.cuda.memory_snapshot():
+        if s["device"] == index and s["address"] <= address < s["address"] + s["total_size"]:
+            return tuple(s["segment_pool_id"]) != (0, 0)
+    return False
+
 
 def workspace(nbytes: int, device) -> torch.Tensor | None:
     if nbytes == 0:
@@ -163,7 +177,10 @@ def workspace(nbytes: int, device) -> torch.Tensor | None:
 def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
     """`index` is the current device: what is asked is whether its stream is being captured."""
     if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        if not _of_a_graph_pool(buf.data_ptr(), index):
+            _captured.append(buf)
+        return buf
     buffers = _workspaces.buffers
     key = (index, stream)
     buf = buffers.get(key)

@@ -2,8 +2,10 @@
 the stream lookup and the library's entry point are stand-ins, and the
 interleavings that a GPU would leave to chance are forced with barriers."""
 import ctypes
+import gc
 import threading
 import types
+import weakref
 
 import pytest
 import torch
@@ -36,7 +38,9 @@ class FakeTorch(types.SimpleNamespace):
             def __exit__(self, *exc):
                 fake.current = self.before
 
-        self.cuda = types.SimpleNamespace(device=Device, current_device=lambda: self.current)
+        self.segments = []  # what the allocator reports of its memory
+        self.cuda = types.SimpleNamespace(device=Device, current_device=lambda: self.current,
+                                          memory_snapshot=lambda: self.segments)
 
     @property
     def current(self):
@@ -130,3 +134,34 @@ def test_a_capture_on_another_device_than_the_current_one(fake, current, asked):
     fake.capturing = {current}  # a capture that this call is not part of
     assert binding.workspace(4096, torch.device("cuda", asked)) is eager
     assert fake.current == current
+
+
+@pytest.mark.parametrize("pool,kept", [((1, 0), False), ((0, 7), False), ((0, 0), True),
+                                       (None, True)])
+def test_memory_of_a_captured_call_lives_as_long_as_its_graph(fake, monkeypatch, pool, kept):
+    """A graph's own pool holds the memory of its calls. A capture that was begun otherwise gets
+    ordinary memory, which is free for others as soon as nothing refers to it."""
+    fake.capturing = {0}
+    fake.empty = lambda n, dtype, device: Buffer(n)
+    if pool is not None:
+        fake.segments = [
+            {"device": 0, "address": 1 << 30, "total_size": 1 << 20, "segment_pool_id": (0, 0)},
+            {"device": 1, "address": Buffer.AT, "total_size": 1 << 20, "segment_pool_id": (3, 3)},
+            {"device": 0, "address": Buffer.AT - 512, "total_size": 1 << 20,
+             "segment_pool_id": pool}]
+    gone = weakref.ref(binding._workspace(4096, 0, 0))
+    gc.collect()
+    assert (gone() is not None) == kept
+
+
+class Buffer:
+    AT = 1 << 40
+
+    def __init__(self, n):
+        self.n = n
+
+    def data_ptr(self):
+        return self.AT
+
+    def numel(self):
+        return self.n
