@@ -22,8 +22,11 @@ SOURCES = ["q4moe_api.cpp", "gemv_q4_0.hip", "gemv_mfma_q4_0.hip", "gemv_q8_0.hi
 # on every batch).
 EXTRA = {"gemv_mfma_q4_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "moe_q4_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         # With accumulation registers the compiler gave one LDS store of
-         # lora_shrink_tile_kernel a wrong offset (row 1 of a tile at row 0).
+         # With accumulation registers the compiler (AMD clang 22.0.0, ROCm 7.2.0)
+         # gave one LDS store of lora_shrink_tile_kernel a wrong offset (row 1 of a
+         # tile at row 0: ds_write2_b32 offset0:8 for 32, beside a store from an
+         # accumulation register). ffn_gemm.hip stores accumulators to LDS too.
+         "ffn_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "ffn_strip.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "ffn_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
