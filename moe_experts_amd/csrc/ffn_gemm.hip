@@ -100,6 +100,17 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Hands LDS over at a barrier: this wave's reads and writes of it are done before
+// the barrier. Neither the wait nor the barrier is an access of memory to the
+// compiler, so both orders are stated: none of them may be moved past the wait, in
+// the program (memory clobber) or among the instructions (scheduling barrier).
+__device__ __forceinline__ void lds_hand_over() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  lds_barrier();
+}
+
 // Nibbles to scaled halves, two at a time. binary16 0x6400 | v is 1024 + v
 // exactly, and 0x5400 | (v << 4) is 64 + v, so every other nibble needs no
 // shift; (q - 8) is exact, the product is rounded once. The masks are kept in
@@ -371,8 +382,7 @@ __device__ __forceinline__ void produce_step(const W& wt, const LeftOperand<BM, 
       }
     __builtin_amdgcn_sched_barrier(0);
   }
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-  lds_barrier();
+  lds_hand_over();
 }
 
 // The producer waves (lane t of them) over the K steps [kb, ke).
@@ -515,9 +525,8 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
       left.store(lraw[0], xs, i);
       left.load(lraw[0], min(kb + 2, ke - 1), i);
     }
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
   }
-  lds_barrier();
+  lds_hand_over();
   if constexpr (MI * NJ <= 2) {
     // few products: all of a step's reads at once
     Operands o[Q];
@@ -527,9 +536,7 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
       const uint8_t* b = bs + cur * kStage;
 #pragma unroll
       for (int q = 0; q < Q; ++q) read(o[q], x, b, q);
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // this wave's reads done before the stages are reused
-      lds_barrier();
+      lds_hand_over();  // this wave's reads done before the stages are reused
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int q = 0; q < Q; ++q) multiply(o[q], q);
@@ -557,8 +564,7 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
         multiply(o[q & 1], q);
         __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // reads and copies done before the stages change roles
-      lds_barrier();
+      lds_hand_over();  // reads and copies done before the stages change roles
       __builtin_amdgcn_sched_barrier(0);
       // past the last step this reads a stage that is not used
       read(o[0], xs + (cur ^ 1) * kXBytes, bs + (cur ^ 1) * kStage, 0);
