@@ -61,7 +61,7 @@ constexpr int BN = 128, BK = 64;
 constexpr int kRole = 256;                 // lanes of one role
 constexpr int kColBytes = BK * 2;          // one column or row of a step in LDS
 constexpr int kBBytes = BN * kColBytes;    // 16 KiB
-constexpr uint32_t kOut = 0x80000000u;
+constexpr uint32_t kOut = 0x80000000u;    // past the end of any weight matrix
 
 enum Side { kAdapters, kDual, kGradient };
 
@@ -331,12 +331,17 @@ struct LeftOperand {
   };
   __device__ __forceinline__ void init(const TileArgs& g, int m0, int rows, int lane) {
     t = lane;
-    r = make_rsrc(g.X + (size_t)m0 * g.lda, (uint32_t)rows * (uint32_t)g.lda * 2u);
+    const uint32_t pitch = (uint32_t)g.lda * 2u, bytes = (uint32_t)rows * pitch;
+    r = make_rsrc(g.X + (size_t)m0 * g.lda, bytes);
+    // Rows past the last read zeros, not kept; where 256 rows of a contraction of 2N
+    // pass 2 GiB, kOut is inside, and they repeat the last row. (Repeating it always:
+    // 150 rows of 11008 x 4096 35.3 -> 36.0 us.)
+    const uint32_t dead = bytes <= kOut ? kOut : bytes - pitch;
 #pragma unroll
     for (int i = 0; i < kInstr; ++i) {
       const int slot = i * LANES + t;  // row slot / 8, 16-byte chunk slot % 8
       const int row = slot >> 3;
-      off[i] = row < rows ? ((uint32_t)row * (uint32_t)g.lda + 8u * (slot & 7)) * 2u : kOut;
+      off[i] = (row < rows ? (uint32_t)row * pitch : dead) + 16u * (slot & 7);
     }
   }
   __device__ __forceinline__ void load(Raw& raw, int ks, int i) const {

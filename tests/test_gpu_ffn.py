@@ -567,3 +567,52 @@ def test_many_tiles(M, K, N):
     got = q4_0_gemm_lora(to_dev(x), to_dev(Wg), N, to_dev(A), to_dev(Bl), to_dev(ids),
                          to_dev(scale))
     ref.check(host(got), ref.gemm_lora(x, Wg, A, Bl, ids, scale))
+
+
+def test_gradient_whose_left_operand_passes_two_gigabytes():
+    """Two matrices and millions of columns: the scaled gradients of a tile that lacks rows pass
+    2 GiB. Only a few values of dH are not zero, so that the result is known from a few weights."""
+    from moe_experts_amd import q4_0_glu_backward
+    M, N, K = 50, 12000000, 64  # one tile, whatever its height
+    assert M * 2 * N * 2 > 1 << 31 and M * N * 2 < 1 << 31
+    r = datagen.rng(120)
+    at = r.integers(0, N, (M, 3))  # the columns of each row that carry a gradient
+    at[:, 0] = N - 1 - np.arange(M)
+    dh = (r.standard_normal((M, 3)) * 1e-3).astype(np.float32)
+    g, u = (r.standard_normal((M, 3)).astype(np.float16) for _ in range(2))
+    rows = torch.arange(M, device=dev())[:, None]
+    cols = to_dev(at)
+    dH = torch.zeros((M, N), dtype=torch.bfloat16, device=dev())
+    dH[rows, cols] = to_dev(dh).bfloat16()
+    G, U = (torch.full((M, N), 0.5, dtype=torch.float16, device=dev()) for _ in range(2))
+    G[rows, cols], U[rows, cols] = to_dev(g), to_dev(u)
+    gen = torch.Generator(device="cuda").manual_seed(121)
+    mats = []
+    for _ in range(2):
+        w = torch.randint(0, 256, (K, N // 32, 18), dtype=torch.uint8, device=dev(), generator=gen)
+        d = torch.rand((K, N // 32, 1), device=dev(), generator=gen) * 0.05
+        w[..., :2] = d.half().view(torch.uint8)
+        mats.append(w)
+    dX = host(q4_0_glu_backward(dH, G, U, mats[0], mats[1], K))
+    uniq = np.unique(at)
+    # the weights of the columns in use, as blocks of their own: column c of block c // 32
+    few = []
+    for w in mats:
+        blocks = w[:, to_dev(uniq // 32)].cpu().numpy()
+        few.append(ref.dequant(blocks).reshape(K, uniq.size, 32)[:, np.arange(uniq.size),
+                                                                 uniq % 32])
+    where = np.searchsorted(uniq, at)
+    full = lambda v: values_at(M, uniq.size, where, v)
+    dhv, gv, uv = full(values(dH[rows, cols])), full(g), full(u)
+    a, slope = ref.act(gv, "silu")
+    few_steps = 64 * ref.E32 * (1 + np.abs(gv))
+    want = ref._through([dhv * uv * slope, dhv * a], [np.abs(dhv * uv) * few_steps,
+                                                      np.abs(dhv) * few_steps], few)
+    ref.check(dX, want)
+
+
+def values_at(M, n, where, v):
+    """A matrix of zeros with row m's values v[m] at where[m]."""
+    out = np.zeros((M, n))
+    out[np.arange(M)[:, None], where] = v
+    return out
