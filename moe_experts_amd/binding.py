@@ -420,7 +420,8 @@ def moe_q4_0_prefill(x16: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: 
 # ---------------------------------------------------------------------------
 # Dense feed-forward over frozen Q4_0 weights. These calls take a few
 # microseconds of GPU time at decode, so their host side is kept short: one
-# check per tensor, workspace sizes remembered by shape.
+# check per tensor, workspace sizes remembered by shape. Gradients are calls of
+# their own; torch's autograd sees none of them.
 # ---------------------------------------------------------------------------
 ACTIVATIONS = {"silu": 0, "gelu": 1}
 
@@ -433,12 +434,20 @@ def _act(act: str) -> int:
 
 
 def _ptr(t, name: str, dtype, numel: int, index: int) -> int:
-    """Address of a contiguous tensor of this type and size on device `index`."""
+    """Address of a contiguous tensor of this type and size on device `index`. These calls record
+    nothing for torch's autograd: on a tensor that requires a gradient their results would
+    quietly have none, so that is refused while torch records."""
     if (isinstance(t, torch.Tensor) and t.get_device() == index >= 0 and t.dtype is dtype
-            and t.numel() == numel and t.is_contiguous()):
+            and t.numel() == numel and t.is_contiguous() and not t.requires_grad):
         return t.data_ptr()
-    _dev(t, name, dtype, numel)
-    raise ValueError(f"{name} is on {t.device}, the first argument on device {index}")
+    if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this call does not record: call it "
+                         "under torch.no_grad(), or in the forward or backward of a "
+                         "torch.autograd.Function")
+    p = _dev(t, name, dtype, numel)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the first argument on device {index}")
+    return p
 
 
 def _columns(N: int, block: int):
@@ -555,7 +564,9 @@ def q4_0_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, Wg: to
                       dX: torch.Tensor | None = None,
                       ws: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of q4_0_glu_gemm with respect to X: dX [M, K] bf16 from dH [M, N] bf16 and the
-    G and U that the forward call returned. The weights have no gradient."""
+    G and U that the forward call returned. The weights have no gradient. torch casts what a
+    torch.autograd.Function returns to its input's type: for a float16 X the caller scales the
+    loss, or keeps what is trained in bfloat16 or float32 and casts it before the call."""
     if dH.dim() != 2:
         raise ValueError("dH must be [M, N]")
     M, N = dH.shape

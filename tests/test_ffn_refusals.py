@@ -172,3 +172,47 @@ def test_binding_refuses_what_the_library_cannot_see():
         q4.q4_0_gemv_lora(x, W, N, X, X, torch.zeros(M, dtype=torch.int32), torch.zeros(L))
     with pytest.raises(ValueError, match="device tensor"):
         q4.q4_0_gemm_backward(X.bfloat16(), W, K)
+
+
+def calls_that_want_gradients():
+    """(entry point, its inputs that can require a gradient, the call)."""
+    import moe_experts_amd as q4
+    K, N, M, R, L = 64, 64, 2, 8, 2
+    W = torch.zeros(K * (N // 32) * 18, dtype=torch.uint8)
+    x, X = torch.zeros(M, K), torch.zeros(M, K, dtype=torch.float16)
+    dY, G, U = torch.zeros(M, N).bfloat16(), torch.zeros(M, N).half(), torch.zeros(M, N).half()
+    A, Bl = torch.zeros(L, R, K).half(), torch.zeros(L, N, R).half()
+    ids, s = torch.zeros(M, dtype=torch.int32), torch.zeros(L)
+    return [
+        ("q4_0_glu", (x,), lambda: q4.q4_0_glu(x, W, W, N)),
+        ("q4_0_glu_gemm", (X,), lambda: q4.q4_0_glu_gemm(X, W, W, N)),
+        ("q4_0_glu_backward", (dY, G, U), lambda: q4.q4_0_glu_backward(dY, G, U, W, W, K)),
+        ("q4_0_gemm_backward", (dY,), lambda: q4.q4_0_gemm_backward(dY, W, K)),
+        ("q4_0_gemv_lora", (x, A, Bl, s), lambda: q4.q4_0_gemv_lora(x, W, N, A, Bl, ids, s)),
+        ("q4_0_gemm_lora", (X, A, Bl, s), lambda: q4.q4_0_gemm_lora(X, W, N, A, Bl, ids, s)),
+    ]
+
+
+@pytest.mark.parametrize("which", range(6), ids=lambda i: calls_that_want_gradients()[i][0])
+def test_a_gradient_that_would_be_lost_is_refused(which, monkeypatch):
+    """The calls record nothing for torch's autograd: on inputs that require a gradient their
+    results would quietly have none. (CPU tensors; the check of the device and the library's call
+    are stand-ins.)"""
+    from moe_experts_amd import binding
+    ran = []
+    monkeypatch.setattr(binding, "_dev", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(binding, "_run", lambda *a: ran.append(a))
+    name, inputs, call = calls_that_want_gradients()[which]
+    for t in inputs:
+        t.requires_grad_()
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+        assert not ran
+        # without recording, what a Function's forward runs under too, the call is made
+        for off in (torch.no_grad(), torch.inference_mode()):
+            with off:
+                call()
+            assert ran.pop()
+        t.requires_grad_(False)
+    call()
+    assert ran

@@ -616,3 +616,34 @@ def values_at(M, n, where, v):
     out = np.zeros((M, n))
     out[np.arange(M)[:, None], where] = v
     return out
+
+
+@pytest.mark.parametrize("M", [40, 300])
+def test_block_in_an_autograd_function(M):
+    """The calls as a training program makes them: forward and backward of a
+    torch.autograd.Function, between bfloat16 tensors. Outside one, an input that requires a
+    gradient is refused."""
+    from moe_experts_amd import q4_0_glu_backward, q4_0_glu_gemm
+    K, N = 256, 192
+    Wg, Wu = weights(131, K, N), weights(132, K, N)
+    dg, du = to_dev(Wg), to_dev(Wu)
+
+    class Block(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            H, G, U = q4_0_glu_gemm(x.half(), dg, du, N, save=True)
+            ctx.save_for_backward(G, U)
+            return H.bfloat16()
+
+        @staticmethod
+        def backward(ctx, dh):
+            return q4_0_glu_backward(dh.contiguous(), *ctx.saved_tensors, dg, du, K)
+
+    x = to_dev(datagen.activations(133, M, K) * 0.5).bfloat16().requires_grad_()
+    c = gradient(134, M, N)
+    Block.apply(x).backward(c)
+    _, G, U = q4_0_glu_gemm(x.detach().half(), dg, du, N, save=True)
+    assert torch.equal(x.grad, q4_0_glu_backward(c, G, U, dg, du, K))
+    ref.check(host(x.grad), ref.glu_backward(values(c), host(G), host(U), Wg, Wu, "silu"))
+    with pytest.raises(ValueError, match="requires a gradient"):
+        q4_0_glu_gemm(x.detach().half().requires_grad_(), dg, du, N)
