@@ -317,10 +317,11 @@ int moe_q4_0_layer(const float* x, const float* Wr, const q4_0_block* Wg, const 
  *   decode (q4_0_glu, q4_0_gemv_lora): fp32 activations, 1 <= M <= Q4_GEMV_MAX_M,
  *     any K the GEMV takes, fp32 sums and results;
  *   prompt and gradient (the others): fp16 activations, bf16 gradients, any M;
- *     K % 64 == 0 and N % 64 == 0. A dequantized weight is rounded to fp16 before
- *     its product, as in q4_0_gemm, or, in products of few rows and for a part of
- *     the gated block's weights, not rounded; sums are fp32, results are rounded
- *     once.
+ *     K % 64 == 0 and N % 64 == 0. Sums are fp32, results are rounded once. A
+ *     dequantized weight is rounded to fp16 before its product, as in q4_0_gemm,
+ *     but not in products of up to 64 rows (q4_0_glu_gemm, q4_0_gemm_lora), and
+ *     in q4_0_glu_gemm of more rows the rounding is made good again to three
+ *     quarters at least.
  * Weights (q - 8) * d stay below 65520 in magnitude, the range of fp16. A row with
  * an infinity or a NaN has results that are not finite, in every column; other
  * rows are not touched by it.

@@ -31,16 +31,20 @@
 //   * few rows: the contraction is split over workgroups (fp32 partial sums,
 //     added in split order by a second kernel), so that the grid fills the GPU.
 //
-// Each dequantized weight (q - 8) * d is rounded to fp16 before its product,
+// Each dequantized weight w = (q - 8) * d is rounded to fp16 before its product,
 // as in q4_0_gemm; the sums are fp32. Rounded weights give g and u an error of
-// about 0.8 of what rounding them to fp16 gives, and h, their product, one 1.54
-// times that of its own rounding. So dual keeps what the rounding took of a
-// quarter of the weights, exactly, and adds its products: 1.42 times, for 467
-// against 410 us at 2048 rows of 4096 x 11008 (half of the weights: 1.29, 539 us;
-// all: 1.00, 703 us).
+// about 0.8 of what rounding them to fp16 gives, and h, their product, one 1.5
+// times that of its own rounding. So dual adds the products of what the rounding
+// took, for all weights: w - fp16(w) is at most 4 of d's last places, which an 8-bit
+// float (fp16's exponents, 2 bits of mantissa) holds exactly, and 8-bit products run
+// at twice fp16's rate, 64 of k an instruction. There x is cut to its upper byte, off
+// by less than a quarter and by a tenth on the whole, so that of the roundings at
+// most a quarter is left: 1.006 times. 2048 rows of 4096 x 11008: 503 us, without
+// these products 397, with fp16 ones 800 (1.000 times). The gradients have bf16
+// results, eight times coarser, and round the weights.
 //
-// What bounds it: a step of 256 rows is 1024 cycles of matrix instructions and
-// moves 176 KiB through LDS. With all CUs busy the power limit holds the clock at
+// What bounds it: a step of 256 rows is 1024 cycles of matrix instructions (dual
+// 1536) and moves 176 KiB through LDS (dual 208). With all CUs busy the power limit holds the clock at
 // 1.6 to 1.75 GHz, and moving work between the roles gives 2 to 4 %; with 160 CUs
 // busy the clock is 2.4 GHz and the producers' chain is the long one (their
 // weights; consumers wait 500 to 900 of 2700 cycles). Raised wave priorities and
@@ -56,6 +60,7 @@ namespace q4 {
 namespace {
 
 typedef float float16v __attribute__((ext_vector_type(16)));
+typedef int int8v __attribute__((ext_vector_type(8)));
 
 constexpr int BN = 128, BK = 64;
 constexpr int kRole = 256;                 // lanes of one role
@@ -65,12 +70,11 @@ constexpr uint32_t kOut = 0x80000000u;    // past the end of any weight matrix
 
 enum Side { kAdapters, kDual, kGradient };
 
-// dual: quarters of a step (16 of k) whose weights' roundings get products of
-// their own, the first and, with two, the third.
+// dual: the roundings of a step's weights as 8-bit floats, beside the weights.
 template <Side SIDE>
-constexpr int kRestQuarters = SIDE == kDual ? 1 : 0;
+constexpr bool kRest = SIDE == kDual;
 template <Side SIDE>
-constexpr int kRestBytes = BN * 32 * kRestQuarters<SIDE>;  // of a step, in LDS
+constexpr int kWeightBytes = kBBytes + (kRest<SIDE> ? BN * BK : 0);  // of a step, in LDS
 
 struct TileArgs {
   const uint16_t* X;      // left operand [M][lda]
@@ -93,6 +97,16 @@ struct TileArgs {
 
 __device__ __forceinline__ int swz_x(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int swz_b(int n) { return ((n >> 1) ^ (n >> 5)) & 7; }
+
+// Roundings in LDS: column n's 64 bytes are four pieces of 16, piece 2 * h + p those
+// of quarters 2p and 2p + 1 of the step that lane half h multiplies. Four columns
+// share a line of 256 bytes, in which the pieces are permuted by the column's bits
+// 2, 3, 4 and 6, so that neither the 16 columns of a read nor the 8 of a store meet
+// in a bank.
+__device__ __forceinline__ int rest_piece(int n, int piece) {
+  const int swz = ((n >> 3) & 1) | ((n >> 2) & 1) << 1 | ((n >> 4) & 1) << 2 | ((n >> 6) & 1) << 3;
+  return (n >> 2) * 256 + ((((n & 3) * 4 + piece) ^ swz) << 4);
+}
 
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
@@ -134,11 +148,22 @@ struct Dequant {
   __device__ __forceinline__ uint32_t high(uint32_t q, half2v d) const {
     return __builtin_bit_cast(uint32_t, high_value(q) * d);
   }
-  // what the rounding of v * d took, exactly
-  static __device__ __forceinline__ uint32_t rest(half2v v, half2v d) {
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, d, -(v * d)));
+  // What the rounding of w = v * d took, times 2^8: v * d - w is a whole number of at
+  // most 4 of d's last places, which fp16 holds, and times 2^8 its upper byte alone
+  // does, as an 8-bit float of fp16's exponents (for every d and nibble whose w is
+  // finite).
+  static __device__ __forceinline__ uint32_t rest(half2v v, half2v d, half2v w) {
+    const half2v r = __builtin_elementwise_fma(v, d, -w);
+    const half2v s = {(_Float16)256.0f, (_Float16)256.0f};
+    return __builtin_bit_cast(uint32_t, r * s);
   }
 };
+
+// The upper bytes of four halves: truncated to two bits of mantissa, as 8-bit floats
+// of the same exponents.
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07050301u);
+}
 
 // ---------------------------------------------------------------- weights
 // Two registers of a lane pair 32 (16) lanes apart: afterwards a holds the lower
@@ -169,7 +194,7 @@ struct ForwardWeights {
   Dequant dq;
   uint32_t vq, vd, pitch;
   int n0, chunk, half;
-  int rest_at;  // offset of the rows in a column's roundings, < 0: none are kept
+  int rest_at;  // place of the roundings in column n0
   struct Raw {
     uint32_t q[4], d;
   };
@@ -190,8 +215,8 @@ struct ForwardWeights {
     n0 = (DUAL ? 2 * blk + hw : 2 * hw + blk) * 32 + (2 * b5 + b4) * 8;
     chunk = rg >> 1;
     half = rg & 1;
-    constexpr int LQ = kRestQuarters<kDual>, kEvery = 4 / LQ;
-    rest_at = (rg >> 2) % kEvery == 0 ? (rg >> 2) / kEvery * 32 + (rg & 3) * 8 : -1;
+    // row 4 * rg is k = 16 * (rg / 4) + 4 * (rg % 4)
+    rest_at = rest_piece(n0, (rg & 2) + (rg >> 3)) + 8 * ((rg >> 2) & 1) + 4 * (rg & 1);
   }
   // all loads go with part 0
   __device__ __forceinline__ void load(Raw& raw, int ks, int i) const {
@@ -229,27 +254,20 @@ struct ForwardWeights {
   __device__ __forceinline__ void store(const Taken& k, uint8_t* __restrict__ bs, int part) const {
     const int sh = 8 * (part & 1);
     const uint32_t a = k.p01[part >> 1] >> sh, b = k.p23[part >> 1] >> sh;
-    uint2 v[2];
-    v[0].x = dq.low(a, k.d01);
-    v[0].y = dq.low(b, k.d23);
-    v[1].x = dq.high(a, k.d01);
-    v[1].y = dq.high(b, k.d23);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int n = n0 + 2 * part + c;
-      *reinterpret_cast<uint2*>(bs + n * kColBytes + ((chunk ^ swz_b(n)) << 4) + half * 8) = v[c];
-    }
-    if constexpr (DUAL) {
-      if (rest_at < 0) return;
-      v[0].x = Dequant::rest(dq.low_value(a), k.d01);
-      v[0].y = Dequant::rest(dq.low_value(b), k.d23);
-      v[1].x = Dequant::rest(dq.high_value(a), k.d01);
-      v[1].y = Dequant::rest(dq.high_value(b), k.d23);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        *reinterpret_cast<uint2*>(bs + kBBytes + (n0 + 2 * part + c) * (kRestBytes<kDual> / BN) +
-                                  rest_at) = v[c];
-    }
+    store_column(bs, 2 * part, dq.low_value(a), dq.low_value(b), k);
+    store_column(bs, 2 * part + 1, dq.high_value(a), dq.high_value(b), k);
+  }
+  __device__ __forceinline__ void store_column(uint8_t* __restrict__ bs, int c, half2v v01,
+                                               half2v v23, const Taken& k) const {
+    const int n = n0 + c;
+    const half2v w01 = v01 * k.d01, w23 = v23 * k.d23;
+    *reinterpret_cast<uint2*>(bs + n * kColBytes + ((chunk ^ swz_b(n)) << 4) + half * 8) =
+        make_uint2(__builtin_bit_cast(uint32_t, w01), __builtin_bit_cast(uint32_t, w23));
+    if constexpr (DUAL)
+      // rest_piece(n0 + c, ..): n0 is a multiple of 8
+      *reinterpret_cast<uint32_t*>(bs + kBBytes + (c >> 2) * 256 +
+                                   (rest_at ^ (((c & 3) * 4 ^ (c >> 2) * 2) << 4))) =
+          upper_bytes(Dequant::rest(v01, k.d01, w01), Dequant::rest(v23, k.d23, w23));
   }
 };
 
@@ -399,7 +417,7 @@ __device__ __forceinline__ void produce(const TileArgs& g, uint8_t* __restrict__
                                       ForwardWeights<SIDE == kDual>>::type;
   constexpr int D = kDepth<BM>;
   constexpr int kXBytes = BM * kColBytes;
-  constexpr int kStage = kBBytes + kRestBytes<SIDE>;
+  constexpr int kStage = kWeightBytes<SIDE>;
   W wt;
   wt.init(g, tn, t);
   LeftOperand<BM, kRole> left;
@@ -436,7 +454,7 @@ __device__ __forceinline__ void produce(const TileArgs& g, uint8_t* __restrict__
 template <int BM, Side SIDE>
 __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_kernel(TileArgs g) {
   constexpr int kXBytes = BM * kColBytes;
-  constexpr int kStage = kBBytes + kRestBytes<SIDE>;
+  constexpr int kStage = kWeightBytes<SIDE>;
   // two steps' left operand and weights; at the end the waves' results
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kXBytes + 2 * kStage];
   uint8_t* xs = lds;
@@ -474,41 +492,62 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   // A quarter of a step (16 of k) at a time: its operands, then its products.
-  constexpr int LQ = kRestQuarters<SIDE>;
+  constexpr bool REST = kRest<SIDE>;
   struct Operands {
-    half8 a[MI], b[NJ], rest[LQ ? NJ : 1];
+    half8 a[MI], b[NJ];
   };
-  // of quarter kk: its place among those with products for the roundings, or -1
-  auto rest_of = [](int kk) { return LQ && kk % (4 / (LQ ? LQ : 1)) == 0 ? kk * LQ / 4 : -1; };
   const int ra = wm * WR + (lane & 31), rb = wn * WC + (lane & 31);
+  // A lane's place in the stages in quarter 0; quarter kk is 2 * kk chunks on, before
+  // the swizzle, the next 32 rows swizzled alike, the next 32 columns by one more.
+  int xo = ra * kColBytes + (((lane >> 5) ^ swz_x(ra)) << 4);
+  int bo = rb * kColBytes + (((lane >> 5) ^ swz_b(rb)) << 4);
   auto read = [&](Operands& o, const uint8_t* x, const uint8_t* b, int kk) {
-    const int kc = 2 * kk + (lane >> 5);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int r = ra + 32 * i;
-      o.a[i] = *reinterpret_cast<const half8*>(x + r * kColBytes + ((kc ^ swz_x(r)) << 4));
-    }
+    for (int i = 0; i < MI; ++i)
+      o.a[i] = *reinterpret_cast<const half8*>(x + (xo ^ (kk << 5)) + 32 * i * kColBytes);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int n = rb + 32 * j;
-      o.b[j] = *reinterpret_cast<const half8*>(b + n * kColBytes + ((kc ^ swz_b(n)) << 4));
-      if (rest_of(kk) >= 0)
-        o.rest[j] = *reinterpret_cast<const half8*>(b + kBBytes + n * (kRestBytes<SIDE> / BN) +
-                                                    rest_of(kk) * 32 + 16 * (lane >> 5));
-    }
+    for (int j = 0; j < NJ; ++j)
+      o.b[j] =
+          *reinterpret_cast<const half8*>(b + (bo ^ (kk << 5) ^ (j << 4)) + 32 * j * kColBytes);
   };
-  auto multiply = [&](const Operands& o, int kk) {
+  auto multiply = [&](const Operands& o) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.b[j], o.a[i], acc[i][j], 0, 0, 0);
-    if (rest_of(kk) < 0) return;
+  };
+  // The roundings' products, a whole step's (64 of k) at once in 8-bit floats. The
+  // lane's 32 values of k are those of its four quarters, on both sides.
+  struct Rest {
+    int8v b[REST ? NJ : 1], a[REST ? MI : 1];
+  };
+  int ro = kBBytes + rest_piece(rb, 2 * (lane >> 5));
+  auto read_rest = [&](Rest& t, const uint8_t* b) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)  // 32 columns on are 8 lines
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint4 v = *reinterpret_cast<const uint4*>(b + (ro ^ (p << 4)) + 32 * BK * j);
+        t.b[j][4 * p] = v.x, t.b[j][4 * p + 1] = v.y, t.b[j][4 * p + 2] = v.z,
+                  t.b[j][4 * p + 3] = v.w;
+      }
+  };
+  auto take_rest = [&](Rest& t, const Operands& o, int q) {  // the left operand of quarter q
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const uint4 v = __builtin_bit_cast(uint4, o.a[i]);
+      t.a[i][2 * q] = upper_bytes(v.x, v.y);
+      t.a[i][2 * q + 1] = upper_bytes(v.z, v.w);
+    }
+  };
+  auto multiply_rest = [&](const Rest& t) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o.rest[j], o.a[i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < NJ; ++j)  // scales 2^-8 and 1, formats 5 exponent bits and 2 more
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            t.b[j], t.a[i], acc[i][j], 1, 1, 0, 0x77777777, 0, 0x7f7f7f7f);
   };
   // One or two consumer waves a SIMD: little else hides the latency of their LDS
   // reads, so the reads of a quarter are issued before the products of the one
@@ -518,17 +557,18 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
   constexpr bool COPY = kConsumersCopy<BM>;
   using Left = LeftOperand<BM, NC * kWaveSize>;
   Left left;
-  typename Left::Raw lraw[2];
+  constexpr int SETS = REST ? 1 : 2;  // steps of it in flight: registers are short beside roundings
+  typename Left::Raw lraw[SETS];
   if constexpr (COPY) {
     left.init(g, m0, rows, (int)threadIdx.x);
 #pragma unroll
-    for (int d = 0; d < 2; ++d)
+    for (int d = 0; d < SETS; ++d)
 #pragma unroll
       for (int i = 0; i < Left::kInstr; ++i) left.load(lraw[d], min(kb + d, ke - 1), i);
 #pragma unroll
     for (int i = 0; i < Left::kInstr; ++i) {
       left.store(lraw[0], xs, i);
-      left.load(lraw[0], min(kb + 2, ke - 1), i);
+      left.load(lraw[0], min(kb + SETS, ke - 1), i);
     }
   }
   lds_hand_over();
@@ -541,10 +581,16 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
       const uint8_t* b = bs + cur * kStage;
 #pragma unroll
       for (int q = 0; q < Q; ++q) read(o[q], x, b, q);
+      Rest rest;
+      if constexpr (REST) read_rest(rest, b);
       lds_hand_over();  // this wave's reads done before the stages are reused
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int q = 0; q < Q; ++q) multiply(o[q], q);
+      for (int q = 0; q < Q; ++q) {
+        if constexpr (REST) take_rest(rest, o[q], q);
+        multiply(o[q]);
+      }
+      if constexpr (REST) multiply_rest(rest);
     }
   } else {
     Operands o[2];
@@ -553,6 +599,9 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
       const int cur = (ks - kb) & 1;
       const uint8_t* x = xs + cur * kXBytes;
       const uint8_t* b = bs + cur * kStage;
+      // beside roundings formed anew in each step: kept, the quarters' addresses take 12 registers
+      if constexpr (REST) asm volatile("" : "+v"(xo), "+v"(bo), "+v"(ro));
+      Rest rest;
 #pragma unroll
       for (int q = 0; q < Q - 1; ++q) {
         read(o[(q + 1) & 1], x, b, q + 1);
@@ -562,11 +611,19 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
           for (int i = q * kPer; i < q * kPer + kPer; ++i)
             if (i < Left::kInstr) {
               left.store(next, xs + (cur ^ 1) * kXBytes, i);
-              left.load(next, min(ks + 3, ke - 1), i);
+              left.load(next, min(ks + 1 + SETS, ke - 1), i);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        multiply(o[q & 1], q);
+        if constexpr (REST) take_rest(rest, o[q & 1], q);
+        multiply(o[q & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (REST) {  // the roundings' products are the step's last
+        read_rest(rest, b);
+        __builtin_amdgcn_sched_barrier(0);
+        take_rest(rest, o[(Q - 1) & 1], Q - 1);
+        multiply(o[(Q - 1) & 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
       lds_hand_over();  // reads and copies done before the stages change roles
@@ -574,10 +631,13 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
       // past the last step this reads a stage that is not used
       read(o[0], xs + (cur ^ 1) * kXBytes, bs + (cur ^ 1) * kStage, 0);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(o[(Q - 1) & 1], Q - 1);
+      if constexpr (REST)
+        multiply_rest(rest);
+      else
+        multiply(o[(Q - 1) & 1]);
       __builtin_amdgcn_sched_barrier(0);
     };
-    if constexpr (COPY) {  // the two sets of registers are named at compile time
+    if constexpr (COPY && SETS == 2) {  // the sets of registers are named at compile time
       int ks = kb;
       for (; ks + 2 <= ke; ks += 2) {
         step(ks, lraw[1]);

@@ -1,0 +1,74 @@
+"""How exactly the dense feed-forward forms its products (ffn_precision.py)."""
+import numpy as np
+import pytest
+import torch
+
+from moe_experts_amd import datagen
+from tests import ffn_precision as fp
+from tests import ffn_ref as ref
+from tests.gpu_util import to_dev
+from tests.test_gpu_ffn import adapters, host, row_ids, weights
+
+pytestmark = pytest.mark.gpu
+
+# few rows (1 to 4 groups of 16, exact weights) and tiles
+FEW = (1, 16, 17, 33, 49, 64)
+MANY = (65, 100, 150, 300, 777)
+
+
+@pytest.mark.parametrize("K,N", [(64, 64), (576, 192), (1088, 320)])
+@pytest.mark.parametrize("M", FEW + MANY)
+def test_gated_block_differences(M, K, N):
+    """Weights that differ by less than fp16 holds of them."""
+    from moe_experts_amd import q4_0_glu_gemm
+    Wg, Wu = fp.near_rows(1, K, N), fp.near_rows(2, K, N)
+    for at in (0, 37):
+        x = fp.differences(M, K, at)
+        _, G, U = q4_0_glu_gemm(to_dev(x), to_dev(Wg), to_dev(Wu), N, save=True)
+        assert np.array_equal(host(G), fp.exact_differences(x, Wg))
+        assert np.array_equal(host(U), fp.exact_differences(x, Wu))
+
+
+@pytest.mark.parametrize("K,N", [(576, 192), (4096, 256), (1088, 1088)])
+@pytest.mark.parametrize("M", FEW + MANY)
+def test_gated_block_norms(M, K, N):
+    from moe_experts_amd import q4_0_glu_gemm
+    x = datagen.to_f16(datagen.activations(3, M, K))
+    Wg, Wu = weights(4, K, N), weights(5, K, N)
+    left = 0.0 if M <= 64 else fp.LEFT
+    H, G, U = (host(t) for t in q4_0_glu_gemm(to_dev(x), to_dev(Wg), to_dev(Wu), N, save=True))
+    g, eg = fp.norm_bound(x, Wg, left, True)
+    u, eu = fp.norm_bound(x, Wu, left, True)
+    fp.check_norm(G, g, eg, "g")
+    fp.check_norm(U, u, eu, "u")
+    # h: its own rounding, and the errors of the unrounded g and u through the product, element
+    # by element of the size the norms give them
+    a, slope = ref.act(g, "silu")
+    h = a * u
+    per = lambda x_, B: fp.norm_bound(x_, B, left, False)[1] / np.sqrt(g.size)
+    through = np.sqrt(np.square(slope * u).sum() * per(x, Wg) ** 2
+                      + np.square(a).sum() * per(x, Wu) ** 2)
+    fp.check_norm(H, h, np.hypot(np.linalg.norm(h - fp.rounded16(h)), 2 * through), "h")
+
+
+@pytest.mark.parametrize("M", [3, 5, 8])
+def test_decode_differences_and_norms(M):
+    """fp32 rows over exact weights."""
+    from moe_experts_amd import q4_0_gemv_lora, q4_0_glu
+    K, N, R, L = 1000, 288, 8, 2
+    Wg, Wu = fp.near_rows(6, K, N), fp.near_rows(7, K, N)
+    A, Bl, scale = adapters(8, L, R, K, N)
+    none = to_dev(np.full(M, -1, np.int32))
+    ad = [to_dev(A), to_dev(Bl), none, to_dev(scale)]
+    for at in range(0, K, 97):
+        x = fp.differences(M, K, at).astype(np.float32)
+        y = host(q4_0_gemv_lora(to_dev(x), to_dev(Wg), N, *ad))
+        g, u = fp.exact_differences(x, Wg), fp.exact_differences(x, Wu)
+        assert np.array_equal(y, g)
+        h = host(q4_0_glu(to_dev(x), to_dev(Wg), to_dev(Wu), N))
+        want = ref.act(g, "silu")[0] * u
+        assert (np.abs(h - want) <= 16 * ref.E32 * np.abs(want)).all()
+    x = datagen.activations(9, M, K)
+    B = weights(10, K, N)
+    y = host(q4_0_gemv_lora(to_dev(x), to_dev(B), N, *ad))
+    fp.check_norm(y, *fp.norm_bound(x, B, 0.0, False))
