@@ -391,6 +391,22 @@ int q4_0_gemm_lora(const uint16_t* X, const q4_0_block* B, const uint16_t* A, co
                    const int32_t* ids, const float* scale, uint16_t* Y, int M, int N, int K,
                    int R, int L, void* ws, size_t ws_bytes, void* stream);
 
+/* Which kernel serves a shape of the prompt and gradient forms (for inspection and
+ * tests; host arithmetic only). form: whose call; M, N, K: as in it.
+ *   rows    rows of a GEMM tile (64, 128 or 256), 0 for the strips of few rows
+ *   splits  workgroups that share the contraction of a tile, 1 for none
+ *   steps   K steps of a split (64 of the contraction, strips 32; of a gradient of two
+ *           matrices, both), the last split's may be fewer
+ * Fails as the call does for M, N and K; Q4_EINVAL for another form or a null
+ * pointer. */
+typedef enum q4_ffn_form {
+  Q4_FFN_GLU_GEMM = 0,
+  Q4_FFN_GLU_BACKWARD = 1,
+  Q4_FFN_GEMM_BACKWARD = 2,
+  Q4_FFN_GEMM_LORA = 3
+} q4_ffn_form;
+int q4_0_ffn_plan(int form, int M, int N, int K, int* rows, int* splits, int* steps);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,7 @@ _EXPORTS = ("q4_0_gemv", "q8_0_gemv", "q8_0_gemv_workspace_bytes", "q4_0_gemm", 
             "q4_0_glu_backward_workspace_bytes", "q4_0_gemm_backward",
             "q4_0_gemm_backward_workspace_bytes", "q4_0_gemv_lora",
             "q4_0_gemv_lora_workspace_bytes", "q4_0_gemm_lora", "q4_0_gemm_lora_workspace_bytes",
+            "q4_0_ffn_plan",
             "Q4Error")
 
 

@@ -87,6 +87,9 @@ for _f in (_lib.q4_0_gemv_lora, _lib.q4_0_gemm_lora):
     _f.restype = _I
     _f.argtypes = [_P] * 7 + [_I] * 5 + [_P, _Z, _P]
 
+_lib.q4_0_ffn_plan.restype = _I
+_lib.q4_0_ffn_plan.argtypes = [_I] * 4 + [ctypes.POINTER(_I)] * 3
+
 BLOCK_BYTES = 18
 Q8_BLOCK_BYTES = 34
 
@@ -502,6 +505,22 @@ def q4_0_gemv_lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
 @functools.lru_cache(maxsize=1024)
 def q4_0_gemm_lora_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
     return int(_lib.q4_0_gemm_lora_workspace_bytes(M, N, K, R))
+
+
+#: Calls whose kernel q4_0_ffn_plan tells.
+FFN_FORMS = {"q4_0_glu_gemm": 0, "q4_0_glu_backward": 1, "q4_0_gemm_backward": 2,
+             "q4_0_gemm_lora": 3}
+
+
+def q4_0_ffn_plan(form: str, M: int, N: int, K: int):
+    """(rows of a GEMM tile, or 0 for the strips of few rows; splits of the contraction; K steps
+    of a split) by which the call `form` serves a shape."""
+    if form not in FFN_FORMS:
+        raise ValueError(f"form must be one of {sorted(FFN_FORMS)} (got {form!r})")
+    rows, splits, steps = _I(), _I(), _I()
+    _check(_lib.q4_0_ffn_plan(FFN_FORMS[form], M, N, K, ctypes.byref(rows), ctypes.byref(splits),
+                              ctypes.byref(steps)))
+    return rows.value, splits.value, steps.value
 
 
 def q4_0_glu(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, N: int, act: str = "silu",

@@ -470,4 +470,22 @@ int q4_0_gemm_lora(const uint16_t* X, const q4_0_block* B, const uint16_t* A, co
                                        static_cast<hipStream_t>(stream)));
 }
 
+int q4_0_ffn_plan(int form, int M, int N, int K, int* rows, int* splits, int* steps) {
+  if (!rows || !splits || !steps) return Q4_EINVAL;
+  if (form < Q4_FFN_GLU_GEMM || form > Q4_FFN_GEMM_LORA) return Q4_EINVAL;
+  const int rc = check_ffn_shape(M, N, K);
+  if (rc != Q4_OK) return rc;
+  q4::FfnPlan p;
+  if (form == Q4_FFN_GLU_GEMM)
+    p = q4::plan_glu_gemm(M, N, K);
+  else if (form == Q4_FFN_GEMM_LORA)
+    p = q4::plan_gemm_lora(M, N, K, 8);  // no rank changes it
+  else
+    p = q4::plan_gradient(M, N, K, form == Q4_FFN_GLU_BACKWARD ? 2 : 1);
+  *rows = p.strip ? 0 : p.BM;
+  *splits = p.S;
+  *steps = p.strip ? (p.sp.steps + p.S - 1) / p.S : p.kper;
+  return Q4_OK;
+}
+
 }  // extern "C"

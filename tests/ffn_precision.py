@@ -69,3 +69,26 @@ def exact_differences(x, B):
     y = x.astype(np.float64) @ ref.dequant(B)
     assert (rounded16(y) == y).all()
     return y
+
+
+def _bf16(v):
+    """v rounded to bf16, to nearest, ties to even."""
+    u = np.ascontiguousarray(v, dtype=np.float32).view(np.uint32).astype(np.uint64)
+    u = (u + 0x7fff + ((u >> 16) & 1)) & 0xffff0000
+    return u.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def gradient_bound(rows, mats):
+    """How far (2-norm) sum_i rows[i] . mats[i]^T may be from its value, as a gradient: the rows
+    scaled together to 2^13..2^14 and rounded to fp16, the weights rounded to fp16, the result to
+    bf16. The parts are known exactly and do not depend on one another; their squares add up to
+    within a few hundredths (of M * K products of them)."""
+    big = np.max([np.abs(r).max(1) for r in rows], axis=0)
+    scale = 2.0 ** (13 - np.floor(np.log2(np.where(big > 0, big, 1.0))))[:, None]
+    value = sum(r @ w.T for r, w in zip(rows, mats))
+    weights = sum(r @ (w - rounded16(w)).T for r, w in zip(rows, mats))
+    operand = sum((r - rounded16(r * scale) / scale) @ w.T for r, w in zip(rows, mats))
+    terms = sum(w.shape[1] for w in mats)
+    parts = [np.linalg.norm(v) for v in (value - _bf16(value), weights, operand)]
+    parts.append(2 * np.sqrt(terms) * ref.E32 * np.linalg.norm(value))
+    return value, 1.05 * float(np.sqrt(np.sum(np.square(parts))))

@@ -80,3 +80,32 @@ def test_every_rounding_is_held_by_an_eight_bit_float():
         rest = (exact[fine] - w[fine].astype(np.float64)) * 256
         held = (rest.astype(np.float16).view(np.uint16) & 0xff00).view(np.float16)
         assert (held.astype(np.float64) == rest).all()
+
+
+@pytest.mark.parametrize("plant,right", [("none", True), ("half operand", True),
+                                         ("weights cut", False), ("operand cut", False),
+                                         ("columns of the other", False), ("matrices swapped", False)])
+def test_gradient_norms(plant, right):
+    """Gradients through two matrices, against what may be rounded on the way."""
+    r = datagen.rng(4)
+    rows = [r.standard_normal((M, N)) * np.exp(r.standard_normal((M, 1))) for _ in range(2)]
+    mats = [ref.dequant(datagen.q4_0_random(s, K, N)) for s in (5, 6)]
+    value, bound = fp.gradient_bound(rows, mats)
+    cut = lambda v: (v.astype(np.float16).view(np.uint16) & 0xfff0).view(np.float16).astype(float)
+    got = [v.copy() for v in rows], [fp.rounded16(m) for m in mats]
+    if plant == "half operand":
+        got[0][:] = [fp.rounded16(v) for v in rows]
+    elif plant == "weights cut":
+        got[1][:] = [cut(m) for m in mats]
+    elif plant == "operand cut":
+        got[0][:] = [cut(v) for v in rows]
+    elif plant == "columns of the other":
+        got[0][1][:, 64:] = rows[0][:, 64:]
+    elif plant == "matrices swapped":
+        got[1].reverse()
+    dx = fp._bf16(sum(a @ w.T for a, w in zip(*got)))
+    if right:
+        fp.check_norm(dx, value, bound)
+    else:
+        with pytest.raises(AssertionError, match="of the bound"):
+            fp.check_norm(dx, value, bound)

@@ -216,3 +216,29 @@ def test_a_gradient_that_would_be_lost_is_refused(which, monkeypatch):
         t.requires_grad_(False)
     call()
     assert ran
+
+
+def test_plan_over_extreme_shapes(lib):
+    """The plan of a shape fails as its call does, and else names a kernel."""
+    i, ptr = ctypes.c_int, ctypes.POINTER(ctypes.c_int)
+    lib.q4_0_ffn_plan.argtypes = [i] * 4 + [ptr] * 3
+    rows, splits, steps = (i(7) for _ in range(3))
+    refs = [ctypes.byref(v) for v in (rows, splits, steps)]
+    for form in (-1, 4):
+        assert lib.q4_0_ffn_plan(form, 65, 64, 64, *refs) == EINVAL
+    for at in range(3):
+        assert lib.q4_0_ffn_plan(0, 65, 64, 64, *refs[:at], None, *refs[at + 1:]) == EINVAL
+    assert (rows.value, splits.value, steps.value) == (7, 7, 7)
+    names = ("q4_0_glu_gemm", "q4_0_glu_backward", "q4_0_gemm_backward", "q4_0_gemm_lora")
+    vals = (-1, 0, 1, 64, 65, 96, 4096, 65536, (1 << 31) - 64, (1 << 31) - 1)
+    for form, name in enumerate(names):
+        for M in vals:
+            for N in vals:
+                for K in vals:
+                    rc = lib.q4_0_ffn_plan(form, M, N, K, *refs)
+                    s = [M, N, K] + list(VALID[name][1][3:])
+                    if rc == 0:
+                        assert rows.value in (0, 64, 128, 256) and splits.value >= 1
+                        assert steps.value >= 1
+                    else:  # the call's own check, which comes before anything is enqueued
+                        assert call(lib, name, sizes=s) == rc
