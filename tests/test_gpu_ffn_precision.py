@@ -72,3 +72,50 @@ def test_decode_differences_and_norms(M):
     B = weights(10, K, N)
     y = host(q4_0_gemv_lora(to_dev(x), to_dev(B), N, *ad))
     fp.check_norm(y, *fp.norm_bound(x, B, 0.0, False))
+
+
+@pytest.mark.parametrize("M", FEW)
+def test_projection_of_few_rows(M):
+    """fp16 rows over exact weights, without and with adapters."""
+    from moe_experts_amd import q4_0_gemm_lora
+    K, N, R, L = 1088, 320, 16, 3
+    A, Bl, scale = adapters(11, L, R, K, N)
+    ad = [to_dev(A), to_dev(Bl)]
+    none, s = to_dev(np.full(M, -1, np.int32)), to_dev(scale)
+    B = fp.near_rows(12, K, N)
+    for at in range(0, K, 113):
+        x = fp.differences(M, K, at)
+        y = host(q4_0_gemm_lora(to_dev(x), to_dev(B), N, *ad, none, s))
+        assert np.array_equal(y, fp.exact_differences(x, B))
+    x, B = datagen.to_f16(datagen.activations(13, M, K)), weights(14, K, N)
+    y = host(q4_0_gemm_lora(to_dev(x), to_dev(B), N, *ad, none, s))
+    fp.check_norm(y, *fp.norm_bound(x, B, 0.0, True))
+    # with adapters: two more fp32 sums, of K and of R terms
+    ids = row_ids("mixed", M, L)
+    y = host(q4_0_gemm_lora(to_dev(x), to_dev(B), N, *ad, to_dev(ids), s))
+    value = x.astype(np.float64) @ ref.dequant(B) + ref.adapters(x, A, Bl, ids, scale, False)[0]
+    own = np.linalg.norm(value - fp.rounded16(value))
+    sums = 2 * (np.sqrt(K) + np.sqrt(R)) * ref.E32 * np.linalg.norm(value) * 2
+    fp.check_norm(y, value, np.hypot(own, sums))
+
+
+@pytest.mark.parametrize("K", [1, 5, 8, 31, 33, 40])
+@pytest.mark.parametrize("M", [2, 3, 8])
+def test_decode_of_short_rows_reads_none_of_the_next(M, K):
+    """Rows shorter than a step of 32: an infinity at the start of each other row, which stands
+    right behind, does not reach them."""
+    from moe_experts_amd import q4_0_gemv_lora, q4_0_glu
+    N = 96
+    Wg, Wu = weights(15, K, N), weights(16, K, N)
+    x = datagen.activations(17, M, K)
+    bad = x.copy()
+    bad[1::2, 0] = np.inf
+    calls = [lambda v: q4_0_glu(to_dev(v), to_dev(Wg), to_dev(Wu), N)]
+    if K % 8 == 0:
+        A, Bl, scale = adapters(18, 2, 8, K, N)
+        rest = [to_dev(t) for t in (A, Bl, row_ids("mixed", M, 2), scale)]
+        calls.append(lambda v: q4_0_gemv_lora(to_dev(v), to_dev(Wg), N, *rest))
+    for call in calls:
+        right, got = host(call(x)), host(call(bad))
+        assert np.array_equal(got[0::2], right[0::2])
+        assert not np.isfinite(got[1::2]).any()
