@@ -836,9 +836,11 @@ __global__ __launch_bounds__(kTileThreads<BM>, BM == 256 ? 3 : 4) void ffn_gemm_
 // the partial sums, written and read at 4.5 TB/s, and a kernel that adds them.
 // Measured (us): gradient of 150 rows of 11008 x 4096: 256 rows in 2 splits 38.4, 128
 // rows 42.9; of 200 rows of 4096 x 4096: 128 rows in 4 splits 24.6, 256 in 8 28.2;
-// dual, 150 rows of 11008 x 4096: 256 rows in 4 splits 56.3, 128 in 2 75.5; 777 of
-// 5120 x 1536: 51.6 in 2 splits, 59.0 by 128 rows; 2048 of 4096 x 11008, without
-// the products for roundings: 624, 430, 398 with 64, 128, 256 rows.
+// dual, 150 rows of 11008 x 4096: 256 rows in 4 splits 61.7, 128 in 2 77.4; 777 of
+// 5120 x 1536: 256 in 2 splits 56.7, 128 in 3 55.8; 2048 of 4096 x 11008: 801, 543, 497
+// with 64, 128, 256 rows. (The model's dual steps are from before the roundings had
+// products of their own; over 60 shapes of 70 to 2048 rows with them the plan takes the
+// fastest of 30 heights and splits or one within 7 %, at 300 rows within 11 %.)
 void plan_tiles(FfnPlan& p, int M, int tiles_n, int nk, size_t sum_cols, bool dual) {
   const int heights[3] = {64, 128, 256};
   const double start[3] = {1.5, 2.0, 3.0};
