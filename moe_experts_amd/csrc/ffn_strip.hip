@@ -117,9 +117,13 @@ struct StripSource {
     pitch = (uint32_t)a.NB * kBlockBytes;
     r = make_rsrc(W, (uint32_t)a.K * pitch);
     row = 8 * (lane >> 4);
-    // a block column past the matrix reads zeros
-    vq = blk < a.NB ? (uint32_t)blk * kBlockBytes + 2 + 4 * DW * sub : kOut;
-    vd = blk < a.NB ? (uint32_t)blk * kBlockBytes : kOut;
+    // A block column past the matrix reads zeros, and so do 8 rows past a matrix of
+    // fewer than 32, from kOut on: with row 0 those offsets stay below 2^32, 31 rows of
+    // the widest matrix would not.
+    const bool out = blk >= a.NB || row >= a.K;
+    if (out) row = 0;
+    vq = out ? kOut : (uint32_t)blk * kBlockBytes + 2 + 4 * DW * sub;
+    vd = out ? kOut : (uint32_t)blk * kBlockBytes;
     drow = 2 * DW * sub;
   }
   __device__ __forceinline__ void load_row(StripWeights<DW>& w, int i, uint32_t o) const {
@@ -131,8 +135,8 @@ struct StripSource {
       w.q[i][0] = __builtin_amdgcn_raw_buffer_load_b32(r, vq + o, 0, 0);
     }
   }
-  // Offsets stay in the lane's part of the address, which the range check sees:
-  // with fewer than 32 rows in all, the rows past them read zeros.
+  // Offsets stay in the lane's part of the address, which the range check sees: of
+  // a group of 8 rows that ends past the matrix, the rows past it read zeros.
   __device__ __forceinline__ void load(StripWeights<DW>& w, int step) const {
     constexpr int ND = 2 * DW;
     const uint32_t o = (uint32_t)(step_start(step, K) + row) * pitch;

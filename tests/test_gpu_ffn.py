@@ -647,3 +647,30 @@ def test_block_in_an_autograd_function(M):
     ref.check(host(x.grad), ref.glu_backward(values(c), host(G), host(U), Wg, Wu, "silu"))
     with pytest.raises(ValueError, match="requires a gradient"):
         q4_0_glu_gemm(x.detach().half().requires_grad_(), dg, du, N)
+
+
+@pytest.mark.parametrize("K,M", [(8, 1), (16, 2)])
+def test_projection_of_the_widest_matrices(K, M):
+    """A matrix of nearly 2 GiB with fewer rows than a strip's step of 32: the offsets of the rows
+    that it lacks pass 32 bits. Every byte that is not a scale reads as NaN in a scale's place."""
+    from moe_experts_amd import q4_0_gemv_lora
+    nb = min(((1 << 31) - 1) // (18 * K), ((1 << 31) - 1) // (128 * M))
+    N, P = 32 * nb, 64
+    assert K > 8 or 24 * nb * 18 > 1 << 32
+    r = datagen.rng(140)
+    d = r.uniform(0.01, 0.02, (K, P)).astype(np.float16)
+    some = np.full((K, P, 18), 0xFF, np.uint8)
+    some[..., :2] = d[..., None].view(np.uint8)
+    of = torch.arange(nb, device=dev()) % P
+    B = to_dev(some)[:, of].contiguous()
+    x = datagen.activations(141, M, K)
+    A = torch.zeros((1, 8, K), dtype=torch.float16, device=dev())
+    Bl = torch.zeros((1, N, 8), dtype=torch.float16, device=dev())
+    ids = torch.full((M,), -1, dtype=torch.int32, device=dev())
+    y = q4_0_gemv_lora(to_dev(x), B, N, A, Bl, ids, torch.ones(1, device=dev()))
+    want, bound = ref.product32(x, some)  # weights 15 - 8 = 7 times d, block by block
+    want, bound = (to_dev(v.reshape(M, P, 32)[:, :, 0]) for v in (want, bound))
+    for m in range(M):
+        got = y[m].view(nb, 32)
+        off = (got.double() - want[m][of][:, None]).abs()
+        assert bool((off <= bound[m][of][:, None]).all()), (m, float(got.sum()))
