@@ -7,7 +7,8 @@ matrix cores), the on-device router
 shared experts); over frozen dense Q4_0 weights the gated block ``q4_0_glu`` /
 ``q4_0_glu_gemm`` with its gradient ``q4_0_glu_backward``, the projection with the
 low-rank adapters of many requests ``q4_0_gemv_lora`` / ``q4_0_gemm_lora`` and the
-gradient of a projection ``q4_0_gemm_backward``; and their workspace-size helpers. They are loaded from ``libq4moe.so`` on first use; there is no CPU
+gradient of a projection ``q4_0_gemm_backward`` (``q4_0_ffn_plan`` tells which kernel
+serves a shape of them); and their workspace-size helpers. They are loaded from ``libq4moe.so`` on first use; there is no CPU
 fallback. ``moe_experts_amd.datagen`` (seeded synthetic inputs) does not need
 the library.
 """

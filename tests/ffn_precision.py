@@ -41,13 +41,14 @@ def check_norm(got, value, bound, what=""):
     assert off <= bound, f"{what}: off by {off:.4g}, {off / bound:.3g} of the bound"
 
 
-def near_rows(seed, K, N):
+def near_rows(seed, K, N, place=-18):
     """A Q4_0 matrix whose rows have the same nibbles and, column block by column block, scales
-    that differ by a few last places."""
+    that differ by a few last places, of 2^place (-24 to 2: the normal scales of fp16 whose
+    weights it holds)."""
     r = np.random.default_rng(seed)
     nb = N // 32
     q = r.integers(0, 256, (1, nb, 16), dtype=np.uint8)
-    d = (r.integers(1100, 1900, (1, nb)) + r.integers(0, 7, (K, nb))) * 2.0 ** -18
+    d = (r.integers(1100, 1900, (1, nb)) + r.integers(0, 7, (K, nb))) * 2.0 ** place
     B = np.empty((K, nb, 18), dtype=np.uint8)
     B[..., 2:] = q
     B[..., :2] = d.astype(np.float16)[..., None].view(np.uint8)

@@ -55,9 +55,10 @@ def test_norms(plant):
             fp.check_norm(got, value, bound)
 
 
+@pytest.mark.parametrize("place", [-24, -18, 2])
 @pytest.mark.parametrize("plant", RIGHT + WRONG)
-def test_differences(plant):
-    x, B = fp.differences(M, K), fp.near_rows(3, K, N)
+def test_differences(plant, place):
+    x, B = fp.differences(M, K), fp.near_rows(3, K, N, place)
     got = fp.rounded16(product(x, B, plant))
     assert (got == fp.exact_differences(x, B)).all() == (plant in RIGHT)
 

@@ -29,6 +29,19 @@ def test_gated_block_differences(M, K, N):
         assert np.array_equal(host(U), fp.exact_differences(x, Wu))
 
 
+@pytest.mark.parametrize("place", [-24, -21, -14, -6, 2])
+@pytest.mark.parametrize("M", (16, 100, 150, 777))
+def test_gated_block_differences_at_every_scale(M, place):
+    """Scales from the smallest normal ones of fp16 to those whose weights are its largest."""
+    from moe_experts_amd import q4_0_glu_gemm
+    K, N = 576, 192
+    Wg, Wu = fp.near_rows(1, K, N, place), fp.near_rows(2, K, N, -18)
+    x = fp.differences(M, K)
+    _, G, U = q4_0_glu_gemm(to_dev(x), to_dev(Wg), to_dev(Wu), N, save=True)
+    assert np.array_equal(host(G), fp.exact_differences(x, Wg))
+    assert np.array_equal(host(U), fp.exact_differences(x, Wu))
+
+
 @pytest.mark.parametrize("K,N", [(576, 192), (4096, 256), (1088, 1088)])
 @pytest.mark.parametrize("M", FEW + MANY)
 def test_gated_block_norms(M, K, N):
