@@ -47,10 +47,10 @@
 // eight times coarser, and round the weights.
 //
 // What bounds it: a step of 256 rows is 1024 cycles of matrix instructions (dual
-// 1536) and moves 176 KiB through LDS (dual 208). With all CUs busy the power limit holds the clock at
-// 1.6 to 1.75 GHz, and moving work between the roles gives 2 to 4 %; with 160 CUs
-// busy the clock is 2.4 GHz and the producers' chain is the long one (their
-// weights; consumers wait 500 to 900 of 2700 cycles). Raised wave priorities and
+// 1536) and moves 176 KiB through LDS (dual 216). With all CUs busy the power limit
+// holds the clock at 1.6 to 1.75 GHz, and moving work between the roles gives 2 to
+// 4 %; with 160 CUs busy the clock is 2.4 GHz and the producers' chain is the long one
+// (their weights; consumers wait 500 to 900 of 2700 cycles). Raised wave priorities and
 // deeper prefetch gave nothing.
 #include <algorithm>
 #include <type_traits>

@@ -10,6 +10,7 @@ import weakref
 import pytest
 import torch
 
+import tests.built  # noqa: F401  (binding loads the library)
 from moe_experts_amd import binding
 
 WAIT = 20  # seconds until a barrier gives up

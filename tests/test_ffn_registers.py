@@ -13,6 +13,7 @@ import subprocess
 import numpy as np
 import pytest
 
+import tests.built  # noqa: F401
 from tests import ffn_ref as ref
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -25,9 +26,6 @@ def said_of_objects(tmp_path, *command):
     """What a tool prints of each gfx950 object in the library."""
     if not os.path.exists(command[0]):
         pytest.skip(f"{command[0]} is not installed")
-    if not os.path.exists(LIB):
-        from moe_experts_amd import build
-        build.build()
     data = open(LIB, "rb").read()
     starts = [m.start() for m in re.finditer(b"\x7fELF\x02\x01\x01\x40", data)]  # AMDGPU's
     for a, b in zip(starts, starts[1:] + [len(data)]):

@@ -5,6 +5,7 @@ and that is asked of the plan."""
 import numpy as np
 import pytest
 
+import tests.built  # noqa: F401  (the plan is the library's)
 from moe_experts_amd import datagen, q4_0_ffn_plan
 from tests import ffn_precision as fp
 from tests import ffn_ref as ref
