@@ -407,6 +407,83 @@ typedef enum q4_ffn_form {
 } q4_ffn_form;
 int q4_0_ffn_plan(int form, int M, int N, int K, int* rows, int* splits, int* steps);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit rows: int8 q[R][C] with one fp32 scale s[R] a row, the value of an element
+ * being q * s. One format for three uses: activations that a product takes in 8 bits
+ * (a scale for each token), weights stored in 8 bits (a scale for each output channel),
+ * and activations kept in 8 bits from a forward pass for the gradients: the rows that
+ * i8_gemm multiplied are the ones that i8_gemm_backward_weight reads again.
+ * (The 2000-line engine article, §2.2, weighs 8-bit against 4-bit weights; here both
+ * operands have 8 bits, so that the integer matrix cores multiply them.)
+ *
+ * Weights are W[N][K], one row for each output channel, as a linear layer stores them:
+ *   Y[M x N] = X[M x K] . W[N x K]^T.
+ * K % 16 == 0, 16 <= K <= Q4_I8_MAX_K, N % 8 == 0, any M >= 1 (i8_gemv: M <=
+ * Q4_GEMV_MAX_M); i8_quantize and i8_dequantize take any K >= 1. An operand pads what
+ * falls short with zeros when it is stored. Any int8 may stand in a row, -128 too.
+ * Sums of products of int8 are whole numbers and exact (K <= Q4_I8_MAX_K keeps them
+ * below 2^31). A scale may be of either sign, zero, an infinity or a NaN; a row whose
+ * scale is a NaN makes every result that it takes part in a NaN.
+ * Arrays of int8, fp16 and bf16, and results of i8_gemm and i8_gemv, are 16-byte
+ * aligned (the arrays of i8_quantize and i8_dequantize: to their own type), other fp32
+ * arrays 4-byte; every array is smaller than 2 GiB. Outputs must not overlap inputs
+ * or one another.
+ * ------------------------------------------------------------------------- */
+typedef enum q4_type {
+  Q4_TYPE_F32 = 0,
+  Q4_TYPE_F16 = 1,
+  Q4_TYPE_BF16 = 2
+} q4_type;
+#define Q4_I8_MAX_K 131056 /* K * 128 * 128 < 2^31 */
+
+/* Rows of X (fp32, fp16 or bf16 [M][K]) to int8:
+ *   scale[m] = max_k |X[m][k]| / 127, rounded to fp32
+ *   Q[m][k]  = X[m][k] / scale[m], the real quotient rounded to the nearest whole number,
+ *              ties to the even one, and held within -127 .. 127
+ * A row of zeros (or one whose scale rounds to zero) has scale 0 and zeros. A row that
+ * holds an infinity or a NaN has a NaN for its scale, and zeros. */
+int i8_quantize(const void* X, int type, int8_t* Q, float* scale, int M, int K, void* stream);
+
+/* X[m][k] = Q[m][k] * scale[m], rounded once to fp32 and once more to fp16 or bf16. */
+int i8_dequantize(const int8_t* Q, const float* scale, void* X, int type, int M, int K,
+                  void* stream);
+
+/* Decode: y[m][n] = s[m] * sw[n] * sum_k q[m][k] * W[n][k] for fp32 rows x, where q and s
+ * are what i8_quantize makes of x; the call quantizes them itself.
+ *   x fp32 [M][K]     W int8 [N][K], sw fp32 [N]     y fp32 [M][N] */
+size_t i8_gemv_workspace_bytes(int M, int N, int K);
+int i8_gemv(const float* x, const int8_t* W, const float* sw, float* y, int M, int N, int K,
+            void* ws, size_t ws_bytes, void* stream);
+
+/* Any number of rows: Y[m][n] = sx[m] * sw[n] * sum_k X[m][k] * W[n][k].
+ *   X int8 [M][K], sx fp32 [M]     W int8 [N][K], sw fp32 [N]
+ *   Y fp32, fp16 or bf16 [M][N] by `type`, formed in fp32 and rounded once */
+size_t i8_gemm_workspace_bytes(int M, int N, int K);
+int i8_gemm(const int8_t* X, const float* sx, const int8_t* W, const float* sw, void* Y, int type,
+            int M, int N, int K, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the product with respect to its left operand's values:
+ *   dX[m][k] = sum_n dY[m][n] * sw[n] * W[n][k]
+ *   dY bf16 [M][N]     dX bf16 [M][K]
+ * (quantizing passes it on unchanged). The products dY * sw of a row are scaled together
+ * by a power of two to the range of fp16 and rounded to it, and the sum, in fp32, is scaled
+ * back, so gradients need no loss scale. A row of dY with an infinity or a NaN has results
+ * that are not finite, in every column; other rows are not touched by it. */
+size_t i8_gemm_backward_workspace_bytes(int M, int N, int K);
+int i8_gemm_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint16_t* dX, int M,
+                     int N, int K, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the product with respect to the weights' values, from the 8-bit rows of the
+ * forward pass:
+ *   dW[n][k] = sum_m dY[m][n] * sx[m] * X[m][k]
+ *   dY bf16 [M][N]     X int8 [M][K], sx fp32 [M]     dW bf16 [N][K], overwritten
+ * The products dY * sx of a column of dY are scaled and rounded as i8_gemm_backward does
+ * those of a row. A column of dY with an infinity or a NaN has a row of dW that is not
+ * finite; a token whose scale is a NaN leaves nothing finite. */
+size_t i8_gemm_backward_weight_workspace_bytes(int M, int N, int K);
+int i8_gemm_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx, uint16_t* dW,
+                            int M, int N, int K, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,7 +8,9 @@ shared experts); over frozen dense Q4_0 weights the gated block ``q4_0_glu`` /
 ``q4_0_glu_gemm`` with its gradient ``q4_0_glu_backward``, the projection with the
 low-rank adapters of many requests ``q4_0_gemv_lora`` / ``q4_0_gemm_lora`` and the
 gradient of a projection ``q4_0_gemm_backward`` (``q4_0_ffn_plan`` tells which kernel
-serves a shape of them); and their workspace-size helpers. They are loaded from ``libq4moe.so`` on first use; there is no CPU
+serves a shape of them); over rows of int8 with a scale each ``i8_quantize`` /
+``i8_dequantize``, the products ``i8_gemv`` / ``i8_gemm`` and their gradients
+``i8_gemm_backward`` / ``i8_gemm_backward_weight``, which read the same rows; and their workspace-size helpers. They are loaded from ``libq4moe.so`` on first use; there is no CPU
 fallback. ``moe_experts_amd.datagen`` (seeded synthetic inputs) does not need
 the library.
 """
@@ -23,6 +25,9 @@ _EXPORTS = ("q4_0_gemv", "q8_0_gemv", "q8_0_gemv_workspace_bytes", "q4_0_gemm", 
             "q4_0_gemm_backward_workspace_bytes", "q4_0_gemv_lora",
             "q4_0_gemv_lora_workspace_bytes", "q4_0_gemm_lora", "q4_0_gemm_lora_workspace_bytes",
             "q4_0_ffn_plan",
+            "i8_quantize", "i8_dequantize", "i8_gemv", "i8_gemv_workspace_bytes", "i8_gemm",
+            "i8_gemm_workspace_bytes", "i8_gemm_backward", "i8_gemm_backward_workspace_bytes",
+            "i8_gemm_backward_weight", "i8_gemm_backward_weight_workspace_bytes",
             "Q4Error")
 
 

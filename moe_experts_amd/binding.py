@@ -90,6 +90,19 @@ for _f in (_lib.q4_0_gemv_lora, _lib.q4_0_gemm_lora):
 _lib.q4_0_ffn_plan.restype = _I
 _lib.q4_0_ffn_plan.argtypes = [_I] * 4 + [ctypes.POINTER(_I)] * 3
 
+for _name, _ptrs in (("i8_gemv", 4), ("i8_gemm", 5), ("i8_gemm_backward", 4),
+                     ("i8_gemm_backward_weight", 4)):
+    _f = getattr(_lib, _name + "_workspace_bytes")
+    _f.restype = _Z
+    _f.argtypes = [_I] * 3
+    _f = getattr(_lib, _name)
+    _f.restype = _I
+    _f.argtypes = [_P] * _ptrs + [_I] * (4 if _name == "i8_gemm" else 3) + [_P, _Z, _P]
+_lib.i8_quantize.restype = _I
+_lib.i8_quantize.argtypes = [_P, _I, _P, _P, _I, _I, _P]
+_lib.i8_dequantize.restype = _I
+_lib.i8_dequantize.argtypes = [_P, _P, _P, _I, _I, _I, _P]
+
 BLOCK_BYTES = 18
 Q8_BLOCK_BYTES = 34
 
@@ -660,3 +673,180 @@ def q4_0_gemm_lora(X: torch.Tensor, B: torch.Tensor, N: int, A: torch.Tensor, Bl
     """q4_0_gemv_lora for any number of rows, X and Y fp16; K and N multiples of 64."""
     return _lora(_lib.q4_0_gemm_lora, q4_0_gemm_lora_workspace_bytes, X, B, N, A, Bl, ids, scale,
                  Y, ws, torch.float16, 64, ("X", "Y"))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit rows: int8 with one fp32 scale a row, as operands of products and as
+# activations kept for the gradients. As above, gradients are calls of their own.
+# ---------------------------------------------------------------------------
+#: Types of activations and results.
+I8_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _type(dtype, name: str) -> int:
+    a = I8_TYPES.get(dtype)
+    if a is None:
+        raise TypeError(f"{name} must be one of {[str(d) for d in I8_TYPES]} (got {dtype})")
+    return a
+
+
+def _call(f, index: int, *args):
+    """Call f(*args, stream) on device `index`, which need not be the current one."""
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _call(f, index, *args)
+    rc = f(*args, _raw_stream(index))
+    if rc != 0:
+        raise Q4Error(rc)
+
+
+@functools.lru_cache(maxsize=1024)
+def i8_gemv_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.i8_gemv_workspace_bytes(M, N, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def i8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.i8_gemm_workspace_bytes(M, N, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def i8_gemm_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.i8_gemm_backward_workspace_bytes(M, N, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def i8_gemm_backward_weight_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.i8_gemm_backward_weight_workspace_bytes(M, N, K))
+
+
+def i8_quantize(X: torch.Tensor, Q: torch.Tensor | None = None,
+                scale: torch.Tensor | None = None):
+    """Rows of X [M, K] (float32, float16 or bfloat16) as int8 and one fp32 scale each:
+    (Q [M, K], scale [M]) with scale = max|x| / 127 and Q the whole number nearest to x / scale
+    (ties to even). Any K. Activations for i8_gemm and for the gradients, or weights [N, K]."""
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    M, K = X.shape
+    a = _type(X.dtype, "X's dtype")
+    i = X.get_device()
+    px = _ptr(X, "X", X.dtype, M * K, i)
+    if Q is None:
+        Q = X.new_empty((M, K), dtype=torch.int8)
+    if scale is None:
+        scale = X.new_empty((M,), dtype=torch.float32)
+    pq = _ptr(Q, "Q", torch.int8, M * K, i)
+    ps = _ptr(scale, "scale", torch.float32, M, i)
+    _call(_lib.i8_quantize, i, px, a, pq, ps, M, K)
+    return Q, scale
+
+
+def i8_dequantize(Q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.float32,
+                  X: torch.Tensor | None = None) -> torch.Tensor:
+    """The values Q * scale of int8 rows [M, K], as float32, float16 or bfloat16 (of X, if it
+    is given)."""
+    if Q.dim() != 2:
+        raise ValueError("Q must be [M, K]")
+    M, K = Q.shape
+    if X is not None:
+        dtype = X.dtype
+    a = _type(dtype, "dtype")
+    i = Q.get_device()
+    pq = _ptr(Q, "Q", torch.int8, M * K, i)
+    ps = _ptr(scale, "scale", torch.float32, M, i)
+    if X is None:
+        X = Q.new_empty((M, K), dtype=dtype)
+    px = _ptr(X, "X", dtype, M * K, i)
+    _call(_lib.i8_dequantize, i, pq, ps, px, a, M, K)
+    return X
+
+
+def _rows_columns(W: torch.Tensor, name: str, K: int) -> int:
+    if W.dim() != 2 or W.shape[1] != K:
+        raise ValueError(f"{name} must be [N, K] with K = {K}")
+    return W.shape[0]
+
+
+def i8_gemv(x: torch.Tensor, W: torch.Tensor, sw: torch.Tensor, y: torch.Tensor | None = None,
+            ws: torch.Tensor | None = None) -> torch.Tensor:
+    """y[M, N] = x . (W * sw)^T for x [M, K] fp32, M <= 8, each row of it quantized to int8 as by
+    i8_quantize, and weights W int8 [N, K] with a scale for each row. K a multiple of 16, N of 8."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    N = _rows_columns(W, "W", K)
+    i = x.get_device()
+    px = _ptr(x, "x", torch.float32, M * K, i)
+    pw = _ptr(W, "W", torch.int8, N * K, i)
+    ps = _ptr(sw, "sw", torch.float32, N, i)
+    if y is None:
+        y = x.new_empty((M, N), dtype=torch.float32)
+    py = _ptr(y, "y", torch.float32, M * N, i)
+    _run(_lib.i8_gemv, i8_gemv_workspace_bytes(M, N, K), ws, i, px, pw, ps, py, M, N, K)
+    return y
+
+
+def i8_gemm(X: torch.Tensor, sx: torch.Tensor, W: torch.Tensor, sw: torch.Tensor,
+            dtype: torch.dtype = torch.float16, Y: torch.Tensor | None = None,
+            ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Y[M, N] = (X * sx) . (W * sw)^T for int8 rows X [M, K] and W [N, K] with a scale for each
+    row, any M; Y float32, float16 or bfloat16 (dtype, or that of Y). K a multiple of 16, N of 8."""
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    M, K = X.shape
+    N = _rows_columns(W, "W", K)
+    if Y is not None:
+        dtype = Y.dtype
+    a = _type(dtype, "dtype")
+    i = X.get_device()
+    px = _ptr(X, "X", torch.int8, M * K, i)
+    psx = _ptr(sx, "sx", torch.float32, M, i)
+    pw = _ptr(W, "W", torch.int8, N * K, i)
+    psw = _ptr(sw, "sw", torch.float32, N, i)
+    if Y is None:
+        Y = X.new_empty((M, N), dtype=dtype)
+    py = _ptr(Y, "Y", dtype, M * N, i)
+    _run(_lib.i8_gemm, i8_gemm_workspace_bytes(M, N, K), ws, i, px, psx, pw, psw, py, a, M, N, K)
+    return Y
+
+
+def i8_gemm_backward(dY: torch.Tensor, W: torch.Tensor, sw: torch.Tensor,
+                     dX: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of i8_gemm with respect to the values of X: dX [M, K] bf16 = dY . (W * sw) from
+    dY [M, N] bf16. Quantizing passes it on unchanged."""
+    if dY.dim() != 2 or W.dim() != 2:
+        raise ValueError("dY must be [M, N] and W [N, K]")
+    M, N = dY.shape
+    K = W.shape[1]
+    i = dY.get_device()
+    pd = _ptr(dY, "dY", torch.bfloat16, M * N, i)
+    pw = _ptr(W, "W", torch.int8, N * K, i)
+    ps = _ptr(sw, "sw", torch.float32, N, i)
+    if dX is None:
+        dX = dY.new_empty((M, K), dtype=torch.bfloat16)
+    px = _ptr(dX, "dX", torch.bfloat16, M * K, i)
+    _run(_lib.i8_gemm_backward, i8_gemm_backward_workspace_bytes(M, N, K), ws, i, pd, pw, ps, px,
+         M, N, K)
+    return dX
+
+
+def i8_gemm_backward_weight(dY: torch.Tensor, X: torch.Tensor, sx: torch.Tensor,
+                            dW: torch.Tensor | None = None,
+                            ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of i8_gemm with respect to the values of W, from the int8 rows that the forward
+    pass multiplied: dW [N, K] bf16 = dY^T . (X * sx) from dY [M, N] bf16."""
+    if dY.dim() != 2 or X.dim() != 2 or X.shape[0] != dY.shape[0]:
+        raise ValueError("dY must be [M, N] and X [M, K]")
+    M, N = dY.shape
+    K = X.shape[1]
+    i = dY.get_device()
+    pd = _ptr(dY, "dY", torch.bfloat16, M * N, i)
+    px = _ptr(X, "X", torch.int8, M * K, i)
+    ps = _ptr(sx, "sx", torch.float32, M, i)
+    if dW is None:
+        dW = dY.new_empty((N, K), dtype=torch.bfloat16)
+    pg = _ptr(dW, "dW", torch.bfloat16, N * K, i)
+    _run(_lib.i8_gemm_backward_weight, i8_gemm_backward_weight_workspace_bytes(M, N, K), ws, i,
+         pd, px, ps, pg, M, N, K)
+    return dW

@@ -1,0 +1,322 @@
+// Gradients of the 8-bit product:
+//   input    dX[m][k] = sum_n (dY[m][n] * sw[n]) * W[n][k]
+//   weights  dW[n][k] = sum_m (dY[m][n] * sx[m]) * X[m][k]
+// Both are C[i][j] = rs[i] * sum_c A[i][c] * B[c][j] with A fp16 (the bracket, scaled; written
+// by a row kernel, for the weights transposed) and B the int8 operand as it stands in memory,
+// its rows along the contraction: one kernel on the fp16 matrix cores with fp32 sums. Every
+// int8 is an fp16 number, so only A is rounded.
+//
+// B's step is copied into LDS as bytes; ds_read_b64_tr_b8 gives a lane eight values of one
+// column, that is of the contraction, which become halves in ten instructions: with the
+// sign bit turned, a byte behind 0x64 is the half 1024 + 128 + q.
+#include <algorithm>
+
+#include "i8_device.hpp"
+#include "i8_internal.hpp"
+#include "i8_tile.hpp"
+
+namespace q4 {
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float16v __attribute__((ext_vector_type(16)));
+
+constexpr int BK = kStepBytes / 2;  // of the contraction in a step
+
+struct GradArgs {
+  const uint16_t* A;  // fp16 [rows][ld]
+  const int8_t* B;    // [depth][cols]
+  const float* rs;
+  uint16_t* out;      // bf16 [rows][cols]
+  int rows, cols, depth, ld;
+  int tiles_m, tiles_n, nk, S, kper;
+  float* part;
+};
+
+// Where 16-byte chunk c of row k stands: eight rows of one chunk, which 16 lanes read at once,
+// and their right neighbours, which the next 16 read, meet no bank twice.
+template <int BN>
+__device__ __forceinline__ int swz_byte(int k) {
+  return BN == 256 ? 2 * (k & 7) : 2 * ((k >> 1) & 3);
+}
+
+template <int BN, int THREADS>
+struct ByteCopy {
+  static constexpr int kChunks = BN / 16;
+  static constexpr int kInstr = BK * kChunks / THREADS;
+  static_assert(THREADS / kChunks % 8 == 0, "one swizzle a lane");
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t off, pitch;
+  __device__ __forceinline__ void init(const GradArgs& g, int j0, int t) {
+    pitch = (uint32_t)g.cols;
+    // rows past the last are past the end: zeros; columns past the last are not kept
+    r = make_rsrc(g.B + j0, (uint32_t)g.depth * pitch - (uint32_t)j0);
+    const int k = t / kChunks;
+    off = (uint32_t)k * pitch + 16u * (uint32_t)((t % kChunks) ^ swz_byte<BN>(k));
+  }
+  __device__ __forceinline__ void issue(uint8_t* stage, int ks, int wave) const {
+    const uint32_t so = (uint32_t)ks * BK * pitch;
+#pragma unroll
+    for (int i = 0; i < kInstr; ++i)
+      copy16(r, stage + (i * THREADS + wave * kWaveSize) * 16,
+             off + (uint32_t)(i * (THREADS / kChunks)) * pitch, so);
+  }
+};
+
+__device__ __forceinline__ half8 to_halves(int2v q) {
+  uint32_t h[4];
+  const half2v off = {(_Float16)1152.0f, (_Float16)1152.0f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = (uint32_t)q[i] ^ 0x80808080u;
+    h[2 * i] = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
+    h[2 * i + 1] = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, h[i]) - off);
+  return __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
+}
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs g) {
+  constexpr int kThreads = WM * WN * kWaveSize;
+  constexpr int WR = BM / WM, WC = BN / WN;
+  constexpr int MI = WR / 32, NJ = WC / 32;
+  constexpr int kA = BM * kStepBytes, kB = BK * BN;
+  constexpr int kPitch = WC * 2 + 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[kA + kB];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[kA + kB];
+  const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
+  const int tiles = g.tiles_m * g.tiles_n;
+  const int sp = L / tiles;
+  int tm, tn;
+  tile_of(L - sp * tiles, g.tiles_m, g.tiles_n, tm, tn);
+  const int i0 = tm * BM, j0 = tn * BN;
+  const int rows = min(BM, g.rows - i0);
+  const int kb = sp * g.kper, ke = min(g.nk, kb + g.kper);
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+
+  RowCopy<BM, kThreads> ca;
+  ByteCopy<BN, kThreads> cb;
+  ca.init(g.A + (size_t)i0 * g.ld, rows, (uint32_t)g.ld * 2u, t);
+  cb.init(g, j0, t);
+  auto issue = [&](uint8_t* stage, int ks) __attribute__((always_inline)) {
+    const int k = min(ks, ke - 1);
+    ca.issue(stage, k, kStepBytes, wave);  // ld is whole steps
+    cb.issue(stage + kA, k, wave);
+  };
+
+  float16v acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  struct Operands {
+    half8 a[MI];
+    int2v b[NJ];
+  };
+  const int ra = wm * WR + (lane & 31);
+  const int ao = ra * kStepBytes + (((lane >> 5) ^ swz_row(ra)) << 4);
+  // The 16 lanes of a group read eight rows of 16 columns; lane l gets column l % 32 of the
+  // wave's 32, rows 8 * (l / 32) .. of the quarter's 16.
+  const int kr = 8 * (lane >> 5) + ((lane & 15) >> 1);
+  const int bo = kA + kr * BN + 8 * (lane & 1);
+  const int bc = (wn * WC / 16 + ((lane >> 4) & 1)) ^ swz_byte<BN>(kr);
+  auto read = [&](Operands& o, const uint8_t* stage, int q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      o.a[i] = *reinterpret_cast<const half8*>(stage + (ao ^ (q << 5)) + 32 * i * kStepBytes);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      o.b[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (__attribute__((address_space(3))) int2v*)(stage + bo + q * 16 * BN +
+                                                     ((bc ^ (2 * j)) << 4)));
+  };
+  auto multiply = [&](const Operands& o) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const half8 b = to_halves(o.b[j]);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, o.a[i], acc[i][j], 0, 0, 0);
+    }
+  };
+  Operands o[2];
+  auto step = [&](uint8_t* cur, uint8_t* next, int ks) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      read(o[(q + 1) & 1], cur, q + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(o[q & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    tile_hand_over();
+    read(o[0], next, 0);
+    issue(cur, ks + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(o[1]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  issue(s0, kb);
+  issue(s1, kb + 1);
+  tile_hand_over();
+  read(o[0], s0, 0);
+  int ks = kb;
+  for (; ks + 2 <= ke; ks += 2) {
+    step(s0, s1, ks);
+    step(s1, s0, ks + 1);
+  }
+  if (ks < ke) step(s0, s1, ks);
+  tile_hand_over();
+
+  // Lane l holds row l % 32 of A, register r column 8 * (r / 4) + 4 * (l / 32) + r % 4.
+  const int iw = i0 + wm * WR, rlive = rows - wm * WR;
+  const int jw = j0 + wn * WC;
+  const int lr = lane & 31, l4 = 4 * (lane >> 5);
+  if (g.S > 1) {
+    float* dst = g.part + (size_t)sp * g.rows * g.cols;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      if (32 * i + lr < rlive)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = jw + 32 * j + 8 * q + l4;
+            if (n < g.cols)
+              *reinterpret_cast<float4*>(dst + (size_t)(iw + 32 * i + lr) * g.cols + n) =
+                  make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                              acc[i][j][4 * q + 3]);
+          }
+    return;
+  }
+  static_assert((WM * WN + 1) / 2 * 32 * kPitch <= kA + kB, "half of the waves in either stage");
+  uint8_t* res = (wave & 1 ? s1 : s0) + (wave >> 1) * (32 * kPitch);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const float s = g.rs[min(iw + 32 * i + lr, g.rows - 1)];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e[u] = i8_to_bf16(acc[i][j][4 * q + u] * s);
+        *reinterpret_cast<uint2*>(res + lr * kPitch + (32 * j + 8 * q + l4) * 2) =
+            make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+      }
+    constexpr int kPieces = WC / 8;
+#pragma unroll
+    for (int p0 = 0; p0 < 32 * kPieces; p0 += kWaveSize) {
+      const int r = (p0 + lane) / kPieces, pc = (p0 + lane) % kPieces;
+      const int n = jw + 8 * pc;
+      if (32 * i + r < rlive && n < g.cols)
+        *reinterpret_cast<uint4*>(g.out + (size_t)(iw + 32 * i + r) * g.cols + n) =
+            *reinterpret_cast<const uint4*>(res + r * kPitch + 16 * pc);
+    }
+  }
+}
+
+template <int BM, int BN, int WM, int WN>
+void launch_tile(const GradArgs& g, hipStream_t st) {
+  hipLaunchKernelGGL((i8_gradient_kernel<BM, BN, WM, WN>),
+                     dim3((unsigned)(g.tiles_m * g.tiles_n * g.S)), dim3(WM * WN * kWaveSize), 0,
+                     st, g);
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// rows x cols results over a contraction of `depth`; chunks of `big` for the transposition
+I8Plan plan_gradient(int rows, int cols, int depth, int chunks) {
+  I8Plan p{};
+  p.ld = (depth + BK - 1) / BK * BK;
+  p.nk = p.ld / BK;
+  p.BN = 256;
+  p.BM = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  if ((long long)((rows + 255) / 256) * ((cols + 255) / 256) >= 256) p.BM = 256;
+  p.tiles_m = (rows + p.BM - 1) / p.BM;
+  p.tiles_n = (cols + p.BN - 1) / p.BN;
+  int s = 1;
+  while (p.tiles_m * p.tiles_n * s * 2 <= 320 && p.nk / (2 * s) >= 4) s *= 2;
+  p.kper = (p.nk + s - 1) / s;
+  p.S = (p.nk + p.kper - 1) / p.kper;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at = align256(at + bytes);
+    return o;
+  };
+  p.off_a = take((size_t)rows * p.ld * 2);
+  p.off_rs = take((size_t)rows * sizeof(float));
+  p.off_max = take((size_t)chunks * rows * sizeof(uint32_t));
+  p.off_part = take(p.S > 1 ? (size_t)p.S * rows * cols * sizeof(float) : 0);
+  p.ws_bytes = at;
+  return p;
+}
+
+hipError_t launch_tiles(const int8_t* B, uint16_t* out, int rows, int cols, int depth, uint8_t* w,
+                        const I8Plan& p, hipStream_t st) {
+  if ((long long)p.tiles_m * p.tiles_n * p.S > 0x3fffffLL) return hipErrorInvalidValue;
+  GradArgs g{reinterpret_cast<const uint16_t*>(w + p.off_a),
+             B,
+             reinterpret_cast<const float*>(w + p.off_rs),
+             out,
+             rows,
+             cols,
+             depth,
+             p.ld,
+             p.tiles_m,
+             p.tiles_n,
+             p.nk,
+             p.S,
+             p.kper,
+             reinterpret_cast<float*>(w + p.off_part)};
+  if (p.BM == 32)
+    launch_tile<32, 256, 1, 4>(g, st);
+  else if (p.BM == 64)
+    launch_tile<64, 256, 1, 4>(g, st);
+  else if (p.BM == 128)
+    launch_tile<128, 256, 2, 4>(g, st);
+  else
+    launch_tile<256, 256, 2, 4>(g, st);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || p.S == 1) return err;
+  return launch_i8_gradient_finish(g.part, g.rs, out, rows, cols, p.S, st);
+}
+
+}  // namespace
+
+I8Plan plan_i8_backward(int M, int N, int K) { return plan_gradient(M, K, N, 0); }
+
+hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint16_t* dX,
+                              int M, int N, int K, void* ws, const I8Plan& p, hipStream_t st) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const hipError_t err =
+      launch_i8_gradient_rows(dY, sw, reinterpret_cast<uint16_t*>(w + p.off_a),
+                              reinterpret_cast<float*>(w + p.off_rs), M, N, p.ld, st);
+  if (err != hipSuccess) return err;
+  return launch_tiles(W, dX, M, K, N, w, p, st);
+}
+
+I8Plan plan_i8_backward_weight(int M, int N, int K) {
+  return plan_gradient(N, K, M, i8_max_chunks(M));
+}
+
+hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx,
+                                     uint16_t* dW, int M, int N, int K, void* ws, const I8Plan& p,
+                                     hipStream_t st) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const hipError_t err = launch_i8_gradient_columns(
+      dY, sx, reinterpret_cast<uint16_t*>(w + p.off_a), reinterpret_cast<float*>(w + p.off_rs),
+      reinterpret_cast<uint32_t*>(w + p.off_max), M, N, p.ld, st);
+  if (err != hipSuccess) return err;
+  return launch_tiles(X, dW, N, K, M, w, p, st);
+}
+
+}  // namespace q4

@@ -1,0 +1,78 @@
+// Plans and launchers of the 8-bit operators: rows of int8 with one fp32 scale
+// each, their products and the gradients of those products.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "q4moe.h"
+
+namespace q4 {
+
+// ---- rows (i8_rows.hip) ------------------------------------------------------
+hipError_t launch_i8_quantize(const void* X, int type, int8_t* Q, float* scale, int M, int K,
+                              hipStream_t st);
+hipError_t launch_i8_dequantize(const int8_t* Q, const float* scale, void* X, int type, int M,
+                                int K, hipStream_t st);
+
+// ---- few rows (i8_strip.hip) -------------------------------------------------
+// Y = X . W^T for X of up to kI8FewRows rows, scaled and rounded.
+constexpr int kI8FewRows = 64;
+hipError_t launch_i8_strip(const int8_t* X, const float* sx, const int8_t* W, const float* sw,
+                           void* Y, int type, int M, int N, int K, hipStream_t st);
+struct I8GemvPlan {
+  bool fused;      // the rows are quantized by every workgroup, not by a launch of their own
+  size_t off_s;    // else: int8 [M][K], then fp32 [M]
+  size_t ws_bytes;
+};
+I8GemvPlan plan_i8_gemv(int M, int N, int K);
+hipError_t launch_i8_gemv(const float* x, const int8_t* W, const float* sw, float* y, int M, int N,
+                          int K, void* ws, const I8GemvPlan& p, hipStream_t st);
+
+// ---- many rows (i8_gemm.hip, i8_gradient.hip) ---------------------------------
+// Result [rows][cols] by tiles of BM x BN, K steps of 128 bytes of the left operand, S splits of
+// the contraction (32-bit partial sums [S][rows][cols] in ws).
+struct I8Plan {
+  bool strip;      // i8_gemm: few rows
+  int BM, BN;
+  int tiles_m, tiles_n;
+  int nk;          // K steps of the whole contraction
+  int S, kper;     // splits, K steps of one
+  size_t off_a;    // gradients: the left operand, fp16 [rows][ld]
+  size_t off_rs;   // gradients: fp32 [rows], what a row of the product is multiplied by
+  size_t off_max;  // weight gradient: uint32 [chunks of M][N]
+  size_t off_part;
+  int ld;          // gradients: values of a row of the left operand
+  size_t ws_bytes;
+};
+
+I8Plan plan_i8_gemm(int M, int N, int K);
+hipError_t launch_i8_gemm(const int8_t* X, const float* sx, const int8_t* W, const float* sw,
+                          void* Y, int type, int M, int N, int K, void* ws, const I8Plan& p,
+                          hipStream_t st);
+
+I8Plan plan_i8_backward(int M, int N, int K);
+hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint16_t* dX,
+                              int M, int N, int K, void* ws, const I8Plan& p, hipStream_t st);
+
+I8Plan plan_i8_backward_weight(int M, int N, int K);
+hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx,
+                                     uint16_t* dW, int M, int N, int K, void* ws, const I8Plan& p,
+                                     hipStream_t st);
+
+// ---- left operands of the gradients, sums of splits (i8_rows.hip) --------------
+// a[m][n] = fp16(dY[m][n] * sw[n] * 2^e), n < ld (zero past N), rs[m] = 2^-e
+hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs,
+                                   int M, int N, int ld, hipStream_t st);
+// a[n][m] = fp16(dY[m][n] * sx[m] * 2^e), m < ld (zero past M), rs[n] = 2^-e; big: scratch,
+// the largest magnitudes of a column in each of i8_max_chunks(M) chunks of the rows
+int i8_max_chunks(int M);
+hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint16_t* a, float* rs,
+                                      uint32_t* big, int M, int N, int ld, hipStream_t st);
+hipError_t launch_i8_finish(const int32_t* part, const float* sx, const float* sw, void* Y,
+                            int type, int M, int N, int S, hipStream_t st);
+hipError_t launch_i8_gradient_finish(const float* part, const float* rs, uint16_t* out, int rows,
+                                     int cols, int S, hipStream_t st);
+
+}  // namespace q4

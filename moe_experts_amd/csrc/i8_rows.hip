@@ -1,0 +1,453 @@
+// Row kernels of the 8-bit operators: what stands before and after their products.
+//
+//   quantize          rows of activations or weights to int8 and one scale each
+//   dequantize        and back
+//   gradient_rows     dY * sw as the fp16 left operand of the input's gradient
+//   gradient_columns  dY * sx, transposed, as that of the weights' gradient
+//   finish            results from the split sums of a product
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "i8_device.hpp"
+#include "i8_internal.hpp"
+
+namespace q4 {
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxGrid = 1 << 20;  // workgroups; each takes every kMaxGrid-th row after its own
+
+int row_grid(long long n) { return (int)std::min<long long>(n, kMaxGrid); }
+
+// Eight values from p, of which the first n exist (n >= 8: all); the rest are zero. p is
+// aligned to one value.
+template <int TYPE>
+__device__ __forceinline__ void load_values(const typename Val<TYPE>::T* __restrict__ p, int n,
+                                            float (&x)[8]) {
+  typename Val<TYPE>::T v[8] = {};
+  if (n >= 8) {
+    __builtin_memcpy(v, p, sizeof(v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) v[e] = p[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = Val<TYPE>::get(v[e]);
+}
+
+__device__ __forceinline__ void store_int8(int8_t* __restrict__ p, int n, const uint32_t (&q)[2]) {
+  if (n >= 8) {
+    __builtin_memcpy(p, q, 8);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e] = (int8_t)(q[e >> 2] >> (8 * (e & 3)));
+  }
+}
+
+// One workgroup a row. V pieces of eight values a lane stay in registers between the
+// search for the largest and the rounding; LOOP reads longer rows twice.
+template <int TYPE, int THREADS, int V, bool LOOP>
+__global__ __launch_bounds__(THREADS) void i8_quantize_kernel(
+    const typename Val<TYPE>::T* __restrict__ X, int8_t* __restrict__ Q,
+    float* __restrict__ scale, int M, int K) {
+  __shared__ uint32_t at[THREADS / kWaveSize];
+  for (int m = blockIdx.x; m < M; m += gridDim.x) {
+    const typename Val<TYPE>::T* xr = X + (size_t)m * K;
+    int8_t* qr = Q + (size_t)m * K;
+    float x[V][8];
+    uint32_t big = 0;
+    for (int k0 = 0; k0 < K; k0 += THREADS * 8 * V) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int k = k0 + (v * THREADS + (int)threadIdx.x) * 8;
+        load_values<TYPE>(xr + min(k, K), K - k, x[v]);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = max(big, magnitude(x[v][e]));
+      if (!LOOP) break;
+    }
+    const RowScale rs = row_scale(workgroup_max<THREADS>(big, at));
+    if (threadIdx.x == 0) scale[m] = rs.s;
+    for (int k0 = 0; k0 < K; k0 += THREADS * 8 * V) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int k = k0 + (v * THREADS + (int)threadIdx.x) * 8;
+        if (LOOP) load_values<TYPE>(xr + min(k, K), K - k, x[v]);
+        if (k < K) {
+          uint32_t q[2];
+          to_int8<8>(x[v], rs, q);
+          store_int8(qr + k, K - k, q);
+        }
+      }
+      if (!LOOP) break;
+    }
+    if (THREADS > kWaveSize) __syncthreads();  // `at` is read before the next row writes it
+  }
+}
+
+// Eight values a lane, a workgroup a piece of a row.
+template <int TYPE, int THREADS>
+__global__ __launch_bounds__(THREADS) void i8_dequantize_kernel(
+    const int8_t* __restrict__ Q, const float* __restrict__ scale,
+    typename Val<TYPE>::T* __restrict__ X, int M, int K, int pieces) {
+  for (long long i = blockIdx.x; i < (long long)M * pieces; i += gridDim.x) {
+    const int m = (int)(i / pieces);
+    const int k = ((int)(i % pieces) * THREADS + (int)threadIdx.x) * 8;
+    if (k >= K) continue;
+    const float s = scale[m];
+    const int8_t* qr = Q + (size_t)m * K + k;
+    typename Val<TYPE>::T* xr = X + (size_t)m * K + k;
+    int8_t q[8] = {};
+    if (K - k >= 8) {
+      __builtin_memcpy(q, qr, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k + e < K) q[e] = qr[e];
+    }
+    typename Val<TYPE>::T v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = Val<TYPE>::put((float)q[e] * s);
+    if (K - k >= 8) {
+      __builtin_memcpy(xr, v, sizeof(v));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k + e < K) xr[e] = v[e];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Left operands of the gradients. A product dY * scale is rounded to fp16 once: 2^-12 of
+// itself, where bf16 would take 2^-9, as much as the result's own rounding. Gradients lie
+// far below fp16's range, so the values that one sum adds are scaled together by a power
+// of two (exact) that takes the largest of them to 2^13..2^14; the sum is scaled back.
+// ---------------------------------------------------------------------------
+struct PowerOfTwo {
+  float up, down;
+};
+__device__ __forceinline__ PowerOfTwo to_fp16_range(uint32_t big) {
+  // zeros, infinities and NaN stay as they are
+  const bool plain = big == 0 || big >= 0x7f800000u;
+  const int e = plain ? 0 : min(126, 13 + 127 - (int)(big >> 23));
+  PowerOfTwo p;
+  p.up = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+  p.down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+  return p;
+}
+
+__device__ __forceinline__ void load_products(const uint16_t* __restrict__ p,
+                                              const float* __restrict__ s, float (&x)[8]) {
+  uint16_t v[8];
+  __builtin_memcpy(v, __builtin_assume_aligned(p, 16), 16);
+  float sv[8];
+  __builtin_memcpy(sv, s, 32);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = Val<Q4_TYPE_BF16>::get(v[e]) * sv[e];
+}
+
+// One workgroup a row of dY; N and ld are multiples of 8.
+template <int THREADS, int V, bool LOOP>
+__global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
+    const uint16_t* __restrict__ dY, const float* __restrict__ sw, _Float16* __restrict__ a,
+    float* __restrict__ rs, int M, int N, int ld) {
+  __shared__ uint32_t at[THREADS / kWaveSize];
+  for (int m = blockIdx.x; m < M; m += gridDim.x) {
+    const uint16_t* yr = dY + (size_t)m * N;
+    _Float16* ar = a + (size_t)m * ld;
+    float x[V][8];
+    uint32_t big = 0;
+    for (int n0 = 0; n0 < N; n0 += THREADS * 8 * V) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int n = n0 + (v * THREADS + (int)threadIdx.x) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[v][e] = 0.0f;
+        if (n < N) load_products(yr + n, sw + n, x[v]);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = max(big, magnitude(x[v][e]));
+      if (!LOOP) break;
+    }
+    const PowerOfTwo p = to_fp16_range(workgroup_max<THREADS>(big, at));
+    if (threadIdx.x == 0) rs[m] = p.down;
+    for (int n0 = 0; n0 < ld; n0 += THREADS * 8 * V) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int n = n0 + (v * THREADS + (int)threadIdx.x) * 8;
+        if (n >= ld) continue;
+        if (LOOP) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[v][e] = 0.0f;
+          if (n < N) load_products(yr + n, sw + n, x[v]);
+        }
+        half8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = (_Float16)(x[v][e] * p.up);
+        *reinterpret_cast<half8*>(ar + n) = h;
+      }
+      if (!LOOP) break;
+    }
+    if (THREADS > kWaveSize) __syncthreads();
+  }
+}
+
+// Largest |dY * sx| of 64 columns in a chunk of the rows. Every workgroup of the second kernel
+// reads all chunks' values of its columns, so there are at most kMaxChunks.
+constexpr int kCols = 64, kColLanes = kCols / 8, kRowLanes = kRowThreads / kColLanes;
+constexpr int kChunkRows = 256, kMaxChunks = 64;
+
+int max_rows(int M) {  // of a chunk
+  const int least = (M + kMaxChunks - 1) / kMaxChunks;
+  return std::max(kChunkRows, (least + kRowLanes - 1) / kRowLanes * kRowLanes);
+}
+
+__global__ __launch_bounds__(kRowThreads) void i8_column_max_kernel(
+    const uint16_t* __restrict__ dY, const float* __restrict__ sx, uint32_t* __restrict__ big,
+    int M, int N, int tiles_n, int chunk_rows) {
+  __shared__ uint32_t at[kRowLanes][kCols];
+  const int c8 = (int)threadIdx.x % kColLanes, r = (int)threadIdx.x / kColLanes;
+  const int n = ((int)blockIdx.x % tiles_n) * kCols + c8 * 8;
+  const int chunk = (int)blockIdx.x / tiles_n;
+  uint32_t b[8] = {};
+  if (n < N) {
+    const int m1 = (int)min((long long)M, (long long)(chunk + 1) * chunk_rows);
+#pragma unroll 8
+    for (int m = chunk * chunk_rows + r; m < m1; m += kRowLanes) {
+      uint16_t v[8];
+      __builtin_memcpy(v, __builtin_assume_aligned(dY + (size_t)m * N + n, 16), 16);
+      const float s = sx[m];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e] = max(b[e], magnitude(Val<Q4_TYPE_BF16>::get(v[e]) * s));
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) at[r][c8 * 8 + e] = b[e];
+  __syncthreads();
+  if (threadIdx.x < kCols) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < kRowLanes; ++i) v = max(v, at[i][threadIdx.x]);
+    const int col = ((int)blockIdx.x % tiles_n) * kCols + (int)threadIdx.x;
+    if (col < N) big[(size_t)chunk * N + col] = v;
+  }
+}
+
+// 64 columns by a chunk of rows of dY, transposed through LDS 64 rows at a time.
+__global__ __launch_bounds__(kRowThreads) void i8_gradient_columns_kernel(
+    const uint16_t* __restrict__ dY, const float* __restrict__ sx,
+    const uint32_t* __restrict__ big, _Float16* __restrict__ a, float* __restrict__ rs, int M,
+    int N, int ld, int tiles_n, int chunks) {
+  constexpr int kPitch = 64 + 8;  // halves of a row of the transposed tile
+  __shared__ __attribute__((aligned(16))) _Float16 tile[kCols * kPitch];
+  __shared__ float up[kCols];
+  const int n0 = ((int)blockIdx.x % tiles_n) * kCols;
+  const int chunk = (int)blockIdx.x / tiles_n;
+  if (threadIdx.x < kCols) {
+    const int n = n0 + (int)threadIdx.x;
+    uint32_t v = 0;
+    if (n < N)
+      for (int c = 0; c < chunks; ++c) v = max(v, big[(size_t)c * N + n]);
+    const PowerOfTwo p = to_fp16_range(v);
+    up[threadIdx.x] = p.up;
+    if (n < N && chunk == 0) rs[n] = p.down;
+  }
+  __syncthreads();
+  const int c8 = (int)threadIdx.x % kColLanes, r = (int)threadIdx.x / kColLanes;
+  const int n = n0 + c8 * 8;
+  float u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = up[c8 * 8 + e];
+  const int m1 = min(ld, (chunk + 1) * kChunkRows);  // ld is a multiple of 64
+  for (int m0 = chunk * kChunkRows; m0 < m1; m0 += 64) {
+#pragma unroll
+    for (int i = 0; i < 64 / kRowLanes; ++i) {
+      const int mr = i * kRowLanes + r, m = m0 + mr;
+      uint16_t v[8] = {};
+      float s = 0.0f;
+      if (m < M && n < N) {
+        __builtin_memcpy(v, __builtin_assume_aligned(dY + (size_t)m * N + n, 16), 16);
+        s = sx[m];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        tile[(c8 * 8 + e) * kPitch + mr] =
+            (_Float16)(Val<Q4_TYPE_BF16>::get(v[e]) * s * u[e]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCols * 8 / kRowThreads; ++i) {
+      const int piece = i * kRowThreads + (int)threadIdx.x;
+      const int col = piece >> 3, p8 = piece & 7;
+      if (n0 + col < N)
+        *reinterpret_cast<half8*>(a + (size_t)(n0 + col) * ld + m0 + p8 * 8) =
+            *reinterpret_cast<const half8*>(tile + col * kPitch + p8 * 8);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums of splits, in split order, four results a lane. Eight loads at a time are issued
+// before the first addition; those past the last split repeat it and are not added.
+// ---------------------------------------------------------------------------
+template <class V>
+__device__ __forceinline__ V sum_splits(const V* __restrict__ p, size_t stride, int S) {
+  V sum{};
+  for (int s0 = 0; s0 < S; s0 += 8) {
+    V t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = p[(size_t)min(s0 + i, S - 1) * stride];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s0 + i < S) sum += t[i];
+  }
+  return sum;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kRowThreads) void i8_finish_kernel(
+    const int32_t* __restrict__ part, const float* __restrict__ sx, const float* __restrict__ sw,
+    typename Val<TYPE>::T* __restrict__ Y, size_t mn, int N, int S) {
+  const size_t i = ((size_t)blockIdx.x * kRowThreads + threadIdx.x) * 4;
+  if (i >= mn) return;
+  const int m = (int)(i / N), n = (int)(i - (size_t)m * N);
+  const int4v v = sum_splits(reinterpret_cast<const int4v*>(part + i), mn / 4, S);
+  const float s = sx[m];
+  typename Val<TYPE>::T y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = Val<TYPE>::put((float)v[e] * s * sw[n + e]);
+  __builtin_memcpy(__builtin_assume_aligned(Y + i, sizeof(y)), y, sizeof(y));
+}
+
+__global__ __launch_bounds__(kRowThreads) void i8_gradient_finish_kernel(
+    const float* __restrict__ part, const float* __restrict__ rs, uint16_t* __restrict__ out,
+    size_t mn, int cols, int S) {
+  const size_t i = ((size_t)blockIdx.x * kRowThreads + threadIdx.x) * 4;
+  if (i >= mn) return;
+  const float4v v = sum_splits(reinterpret_cast<const float4v*>(part + i), mn / 4, S);
+  const float s = rs[i / cols];
+  uint16_t y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = (uint16_t)i8_to_bf16(v[e] * s);
+  __builtin_memcpy(__builtin_assume_aligned(out + i, 8), y, 8);
+}
+
+template <int TYPE, int THREADS, int V, bool LOOP>
+void quantize(const void* X, int8_t* Q, float* scale, int M, int K, hipStream_t st) {
+  hipLaunchKernelGGL((i8_quantize_kernel<TYPE, THREADS, V, LOOP>), dim3(row_grid(M)),
+                     dim3(THREADS), 0, st, static_cast<const typename Val<TYPE>::T*>(X), Q, scale,
+                     M, K);
+}
+
+template <int THREADS, int V, bool LOOP>
+void gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs, int M, int N,
+                   int ld, hipStream_t st) {
+  hipLaunchKernelGGL((i8_gradient_rows_kernel<THREADS, V, LOOP>), dim3(row_grid(M)),
+                     dim3(THREADS), 0, st, dY, sw, reinterpret_cast<_Float16*>(a), rs, M, N, ld);
+}
+
+}  // namespace
+
+hipError_t launch_i8_quantize(const void* X, int type, int8_t* Q, float* scale, int M, int K,
+                              hipStream_t st) {
+  i8_by_type(type, [&](auto t) {
+    constexpr int TYPE = decltype(t)::value;
+    if (K <= 512)
+      quantize<TYPE, 64, 1, false>(X, Q, scale, M, K, st);
+    else if (K <= 2048)
+      quantize<TYPE, 256, 1, false>(X, Q, scale, M, K, st);
+    else if (K <= 4096)
+      quantize<TYPE, 256, 2, false>(X, Q, scale, M, K, st);
+    else if (K <= 8192)
+      quantize<TYPE, 256, 4, false>(X, Q, scale, M, K, st);
+    else if (K <= 16384)
+      quantize<TYPE, 256, 8, false>(X, Q, scale, M, K, st);
+    else
+      quantize<TYPE, 256, 4, true>(X, Q, scale, M, K, st);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_dequantize(const int8_t* Q, const float* scale, void* X, int type, int M,
+                                int K, hipStream_t st) {
+  i8_by_type(type, [&](auto t) {
+    constexpr int TYPE = decltype(t)::value;
+    typedef typename Val<TYPE>::T T;
+    if (K <= 512) {
+      hipLaunchKernelGGL((i8_dequantize_kernel<TYPE, 64>), dim3(row_grid(M)), dim3(64), 0, st, Q,
+                         scale, static_cast<T*>(X), M, K, 1);
+    } else {
+      const int pieces = (K - 1) / (kRowThreads * 8) + 1;
+      hipLaunchKernelGGL((i8_dequantize_kernel<TYPE, kRowThreads>),
+                         dim3(row_grid((long long)M * pieces)), dim3(kRowThreads), 0, st, Q, scale,
+                         static_cast<T*>(X), M, K, pieces);
+    }
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs,
+                                   int M, int N, int ld, hipStream_t st) {
+  if (ld <= 512)
+    gradient_rows<64, 1, false>(dY, sw, a, rs, M, N, ld, st);
+  else if (ld <= 2048)
+    gradient_rows<256, 1, false>(dY, sw, a, rs, M, N, ld, st);
+  else if (ld <= 4096)
+    gradient_rows<256, 2, false>(dY, sw, a, rs, M, N, ld, st);
+  else if (ld <= 8192)
+    gradient_rows<256, 4, false>(dY, sw, a, rs, M, N, ld, st);
+  else if (ld <= 16384)
+    gradient_rows<256, 8, false>(dY, sw, a, rs, M, N, ld, st);
+  else
+    gradient_rows<256, 4, true>(dY, sw, a, rs, M, N, ld, st);
+  return hipGetLastError();
+}
+
+int i8_max_chunks(int M) { return (M + max_rows(M) - 1) / max_rows(M); }
+
+hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint16_t* a, float* rs,
+                                      uint32_t* big, int M, int N, int ld, hipStream_t st) {
+  const int tiles_n = (N + kCols - 1) / kCols, maxima = i8_max_chunks(M);
+  const long long grid = (long long)tiles_n * ((M + kChunkRows - 1) / kChunkRows);
+  if (grid > 0xffffffLL) return hipErrorInvalidValue;  // below 2^32 lanes
+  hipLaunchKernelGGL(i8_column_max_kernel, dim3((unsigned)(tiles_n * maxima)), dim3(kRowThreads), 0,
+                     st, dY, sx, big, M, N, tiles_n, max_rows(M));
+  hipLaunchKernelGGL(i8_gradient_columns_kernel, dim3((unsigned)grid), dim3(kRowThreads), 0, st,
+                     dY, sx, big, reinterpret_cast<_Float16*>(a), rs, M, N, ld, tiles_n, maxima);
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_finish(const int32_t* part, const float* sx, const float* sw, void* Y,
+                            int type, int M, int N, int S, hipStream_t st) {
+  const size_t mn = (size_t)M * N;
+  const unsigned grid = (unsigned)((mn / 4 + kRowThreads - 1) / kRowThreads);
+  i8_by_type(type, [&](auto t) {
+    constexpr int TYPE = decltype(t)::value;
+    hipLaunchKernelGGL((i8_finish_kernel<TYPE>), dim3(grid), dim3(kRowThreads), 0, st, part, sx, sw,
+                       static_cast<typename Val<TYPE>::T*>(Y), mn, N, S);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_gradient_finish(const float* part, const float* rs, uint16_t* out, int rows,
+                                     int cols, int S, hipStream_t st) {
+  const size_t mn = (size_t)rows * cols;
+  const unsigned grid = (unsigned)((mn / 4 + kRowThreads - 1) / kRowThreads);
+  hipLaunchKernelGGL(i8_gradient_finish_kernel, dim3(grid), dim3(kRowThreads), 0, st, part, rs, out,
+                     mn, cols, S);
+  return hipGetLastError();
+}
+
+}  // namespace q4

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "ffn_internal.hpp"
+#include "i8_internal.hpp"
 #include "q4_internal.hpp"
 
 namespace {
@@ -137,6 +138,45 @@ int check_gemv_lora_shape(int M, int N, int K, int R) {
 int check_gemm_lora_shape(int M, int N, int K, int R) {
   const int rc = check_ffn_shape(M, N, K);
   return rc != Q4_OK ? rc : check_rank(R);
+}
+
+// 8-bit rows.
+int type_bytes(int type) {
+  return type == Q4_TYPE_F32 ? 4 : type == Q4_TYPE_F16 || type == Q4_TYPE_BF16 ? 2 : 0;
+}
+
+int check_i8_rows(const void* X, int type, const int8_t* Q, const float* scale, int M, int K) {
+  const int size = type_bytes(type);
+  if (!X || !Q || !scale || M <= 0 || K <= 0 || size == 0) return Q4_EINVAL;
+  if ((long long)M * K > kMaxBytes / size || (long long)M * 4 > kMaxBytes) return Q4_ETOOBIG;
+  if (!aligned(X, size) || !aligned(scale, 4)) return Q4_EALIGN;
+  return Q4_OK;
+}
+
+// Products and gradients: M x K rows, N x K rows, M x N results or gradients of `size` bytes a
+// value.
+int check_i8_shape(int M, int N, int K, int size) {
+  if (M <= 0 || N <= 0 || K <= 0) return Q4_EINVAL;
+  if (K % 16 != 0 || N % 8 != 0 || K > Q4_I8_MAX_K) return Q4_ESHAPE;
+  if ((long long)N * K > kMaxBytes || (long long)M * K > kMaxBytes ||
+      (long long)M * N > kMaxBytes / size || (long long)M * 4 > kMaxBytes ||
+      (long long)N * 4 > kMaxBytes)
+    return Q4_ETOOBIG;
+  return Q4_OK;
+}
+
+int check_i8_gemv_shape(int M, int N, int K) {
+  const int rc = check_i8_shape(M, N, K, 4);
+  if (rc != Q4_OK) return rc;
+  if (M > Q4_GEMV_MAX_M) return Q4_ESHAPE;
+  return (long long)M * K * 4 > kMaxBytes ? Q4_ETOOBIG : Q4_OK;
+}
+
+// dX is M x K, dW N x K, both bf16
+int check_i8_gradient_shape(int M, int N, int K, int rows) {
+  const int rc = check_i8_shape(M, N, K, 2);
+  if (rc != Q4_OK) return rc;
+  return (long long)rows * K * 2 > kMaxBytes ? Q4_ETOOBIG : Q4_OK;
 }
 
 // 16-byte alignment of every array given (NULL is aligned)
@@ -486,6 +526,95 @@ int q4_0_ffn_plan(int form, int M, int N, int K, int* rows, int* splits, int* st
   *splits = p.S;
   *steps = p.strip ? (p.sp.steps + p.S - 1) / p.S : p.kper;
   return Q4_OK;
+}
+
+int i8_quantize(const void* X, int type, int8_t* Q, float* scale, int M, int K, void* stream) {
+  const int rc = check_i8_rows(X, type, Q, scale, M, K);
+  if (rc != Q4_OK) return rc;
+  return from_hip(
+      q4::launch_i8_quantize(X, type, Q, scale, M, K, static_cast<hipStream_t>(stream)));
+}
+
+int i8_dequantize(const int8_t* Q, const float* scale, void* X, int type, int M, int K,
+                  void* stream) {
+  const int rc = check_i8_rows(X, type, Q, scale, M, K);
+  if (rc != Q4_OK) return rc;
+  return from_hip(
+      q4::launch_i8_dequantize(Q, scale, X, type, M, K, static_cast<hipStream_t>(stream)));
+}
+
+size_t i8_gemv_workspace_bytes(int M, int N, int K) {
+  if (check_i8_gemv_shape(M, N, K) != Q4_OK) return 0;
+  return q4::plan_i8_gemv(M, N, K).ws_bytes;
+}
+
+int i8_gemv(const float* x, const int8_t* W, const float* sw, float* y, int M, int N, int K,
+            void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !W || !sw || !y) return Q4_EINVAL;
+  int rc = check_i8_gemv_shape(M, N, K);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(W, y) || !aligned(x, 4) || !aligned(sw, 4)) return Q4_EALIGN;
+  const q4::I8GemvPlan p = q4::plan_i8_gemv(M, N, K);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  return from_hip(
+      q4::launch_i8_gemv(x, W, sw, y, M, N, K, ws, p, static_cast<hipStream_t>(stream)));
+}
+
+// Of the widest result: a workspace serves every type.
+size_t i8_gemm_workspace_bytes(int M, int N, int K) {
+  if (check_i8_shape(M, N, K, 2) != Q4_OK) return 0;
+  return q4::plan_i8_gemm(M, N, K).ws_bytes;
+}
+
+int i8_gemm(const int8_t* X, const float* sx, const int8_t* W, const float* sw, void* Y, int type,
+            int M, int N, int K, void* ws, size_t ws_bytes, void* stream) {
+  const int size = type_bytes(type);
+  if (!X || !sx || !W || !sw || !Y || size == 0) return Q4_EINVAL;
+  int rc = check_i8_shape(M, N, K, size);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(X, W, Y) || !aligned(sx, 4) || !aligned(sw, 4)) return Q4_EALIGN;
+  const q4::I8Plan p = q4::plan_i8_gemm(M, N, K);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  return from_hip(q4::launch_i8_gemm(X, sx, W, sw, Y, type, M, N, K, ws, p,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+size_t i8_gemm_backward_workspace_bytes(int M, int N, int K) {
+  if (check_i8_gradient_shape(M, N, K, M) != Q4_OK) return 0;
+  return q4::plan_i8_backward(M, N, K).ws_bytes;
+}
+
+int i8_gemm_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint16_t* dX, int M,
+                     int N, int K, void* ws, size_t ws_bytes, void* stream) {
+  if (!dY || !W || !sw || !dX) return Q4_EINVAL;
+  int rc = check_i8_gradient_shape(M, N, K, M);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(dY, W, dX) || !aligned(sw, 4)) return Q4_EALIGN;
+  const q4::I8Plan p = q4::plan_i8_backward(M, N, K);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  return from_hip(q4::launch_i8_backward(dY, W, sw, dX, M, N, K, ws, p,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+size_t i8_gemm_backward_weight_workspace_bytes(int M, int N, int K) {
+  if (check_i8_gradient_shape(M, N, K, N) != Q4_OK) return 0;
+  return q4::plan_i8_backward_weight(M, N, K).ws_bytes;
+}
+
+int i8_gemm_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx, uint16_t* dW,
+                            int M, int N, int K, void* ws, size_t ws_bytes, void* stream) {
+  if (!dY || !X || !sx || !dW) return Q4_EINVAL;
+  int rc = check_i8_gradient_shape(M, N, K, N);
+  if (rc != Q4_OK) return rc;
+  if (!aligned16(dY, X, dW) || !aligned(sx, 4)) return Q4_EALIGN;
+  const q4::I8Plan p = q4::plan_i8_backward_weight(M, N, K);
+  rc = check_ws(ws, ws_bytes, p.ws_bytes);
+  if (rc != Q4_OK) return rc;
+  return from_hip(q4::launch_i8_backward_weight(dY, X, sx, dW, M, N, K, ws, p,
+                                                static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
