@@ -82,7 +82,7 @@ __device__ __forceinline__ void quantize_to_lds(const StripArgs& g, uint8_t* __r
 
 // G groups of 16 rows of X, A of 16 rows of W.
 template <int G, int A, int TYPE, bool FUSED>
-__global__ __launch_bounds__(kStripThreads, 2) void i8_strip_kernel(StripArgs g) {
+__global__ __launch_bounds__(kStripThreads, 2) void i8_few_rows_kernel(StripArgs g) {
   constexpr int U = 8 / A;  // loads of W of one piece: 8 KiB a wave
   // xq: rows of K rounded up to 64, and 16 bytes more, of which K % 16 == 0 and M * K <= kFusedValues
   constexpr int kXq = FUSED ? kFusedValues + Q4_GEMV_MAX_M * (64 + 16) : 16;
@@ -187,7 +187,7 @@ hipError_t launch(StripArgs g, hipStream_t st) {
   g.blocks = (g.N + 16 * A - 1) / (16 * A);
   // two dimensions: one of the widest matrices' workgroups would pass 2^32 lanes
   const int x = std::min(g.blocks, 1 << 20);
-  hipLaunchKernelGGL((i8_strip_kernel<G, A, TYPE, FUSED>), dim3(x, (g.blocks + x - 1) / x),
+  hipLaunchKernelGGL((i8_few_rows_kernel<G, A, TYPE, FUSED>), dim3(x, (g.blocks + x - 1) / x),
                      dim3(kStripThreads), 0, st, g);
   return hipGetLastError();
 }
