@@ -484,6 +484,19 @@ size_t i8_gemm_backward_weight_workspace_bytes(int M, int N, int K);
 int i8_gemm_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx, uint16_t* dW,
                             int M, int N, int K, void* ws, size_t ws_bytes, void* stream);
 
+/* Which kernel serves a shape of them (for inspection and tests; host arithmetic only).
+ * form: whose call; M, N, K: as in it.
+ *   rows, cols  of a tile of the result; rows is 0 for the kernel of few rows
+ *   splits      workgroups that share the contraction of a tile, 1 for none
+ *   steps       K steps of a split (128 of i8_gemm's contraction, 64 of a gradient's)
+ * Fails as the call does for M, N and K; Q4_EINVAL for another form or a null pointer. */
+typedef enum q4_i8_form {
+  Q4_I8_GEMM = 0,
+  Q4_I8_GEMM_BACKWARD = 1,
+  Q4_I8_GEMM_BACKWARD_WEIGHT = 2
+} q4_i8_form;
+int i8_gemm_plan(int form, int M, int N, int K, int* rows, int* cols, int* splits, int* steps);
+
 #ifdef __cplusplus
 }
 #endif

@@ -98,6 +98,8 @@ for _name, _ptrs in (("i8_gemv", 4), ("i8_gemm", 5), ("i8_gemm_backward", 4),
     _f = getattr(_lib, _name)
     _f.restype = _I
     _f.argtypes = [_P] * _ptrs + [_I] * (4 if _name == "i8_gemm" else 3) + [_P, _Z, _P]
+_lib.i8_gemm_plan.restype = _I
+_lib.i8_gemm_plan.argtypes = [_I] * 4 + [ctypes.POINTER(_I)] * 4
 _lib.i8_quantize.restype = _I
 _lib.i8_quantize.argtypes = [_P, _I, _P, _P, _I, _I, _P]
 _lib.i8_dequantize.restype = _I
@@ -718,6 +720,20 @@ def i8_gemm_backward_workspace_bytes(M: int, N: int, K: int) -> int:
 @functools.lru_cache(maxsize=1024)
 def i8_gemm_backward_weight_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(_lib.i8_gemm_backward_weight_workspace_bytes(M, N, K))
+
+
+#: Calls whose kernel i8_gemm_plan tells.
+I8_FORMS = {"i8_gemm": 0, "i8_gemm_backward": 1, "i8_gemm_backward_weight": 2}
+
+
+def i8_gemm_plan(form: str, M: int, N: int, K: int):
+    """(rows of a tile of the result, or 0 for the kernel of few rows; its columns; splits of the
+    contraction; K steps of a split) by which the call `form` serves a shape."""
+    if form not in I8_FORMS:
+        raise ValueError(f"form must be one of {sorted(I8_FORMS)} (got {form!r})")
+    v = [_I() for _ in range(4)]
+    _check(_lib.i8_gemm_plan(I8_FORMS[form], M, N, K, *[ctypes.byref(i) for i in v]))
+    return tuple(i.value for i in v)
 
 
 def i8_quantize(X: torch.Tensor, Q: torch.Tensor | None = None,

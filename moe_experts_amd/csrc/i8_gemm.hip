@@ -22,17 +22,21 @@ struct GemmArgs {
 };
 
 // WM x WN waves over a tile of BM rows of X and BN rows of W.
-template <int BM, int BN, int WM, int WN, int TYPE>
+template <int BM, int BN, int WM, int WN, int KB, int NS, bool WHOLE, int TYPE>
 __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) {
   constexpr int kThreads = WM * WN * kWaveSize;
   constexpr int WR = BM / WM, WC = BN / WN;  // of a wave
   constexpr int MI = WR / 32, NJ = WC / 32;
-  constexpr int kX = BM * kStepBytes, kW = BN * kStepBytes;
+  constexpr int kX = BM * KB, kW = BN * KB, kStage = kX + kW;
   constexpr int kPitch = WC * 4 + 16;  // bytes of 32 rows of results in LDS, wave by wave
-  static_assert(WM * WN * 32 * kPitch <= 2 * (kX + kW), "results fit the stages");
-  // Two steps, apart, so that the compiler can tell a copy into one from a read of the other.
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[kX + kW];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[kX + kW];
+  // The steps' stages are apart, so that the compiler can tell a copy into one from a read of
+  // another.
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage], s1[kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t s2[NS > 2 ? kStage : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t s3[NS > 3 ? kStage : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t s4[NS > 4 ? kStage : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t s5[NS > 5 ? kStage : 16];
+  uint8_t* const st[6] = {s0, s1, s2, s3, s4, s5};
   const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
   const int tiles = g.tiles_m * g.tiles_n;
   const int sp = L / tiles;
@@ -45,14 +49,15 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave % WM, wn = wave / WM;
 
-  RowCopy<BM, kThreads> cx;
-  RowCopy<BN, kThreads> cw;
+  RowCopy<BM, kThreads, KB> cx;
+  RowCopy<BN, kThreads, KB> cw;
+  constexpr int kCopies = cx.kInstr + cw.kInstr;  // of a wave in a step
   cx.init(g.X + (size_t)m0 * g.K, rows, (uint32_t)g.K, t);
   cw.init(g.W + (size_t)n0 * g.K, cols, (uint32_t)g.K, t);
-  // steps past the last repeat it, into a stage that is not read
+  // steps past the last copy zeros, without an access of memory, and are not read
   auto issue = [&](uint8_t* stage, int ks) __attribute__((always_inline)) {
     const int k = min(ks, ke - 1);
-    const int left = g.K - k * kStepBytes;
+    const int left = ks < ke ? g.K - k * KB : 0;
     cx.issue(stage, k, left, wave);
     cw.issue(stage + kX, k, left, wave);
   };
@@ -69,15 +74,15 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
   };
   const int rx = wm * WR + (lane & 31), rw = wn * WC + (lane & 31);
   // chunk 2 * q + lane / 32 of a row in quarter q; 32 rows on the swizzle is the same
-  const int xo = rx * kStepBytes + (((lane >> 5) ^ swz_row(rx)) << 4);
-  const int wo = kX + rw * kStepBytes + (((lane >> 5) ^ swz_row(rw)) << 4);
+  const int xo = rx * KB + (((lane >> 5) ^ swz_row<KB>(rx)) << 4);
+  const int wo = kX + rw * KB + (((lane >> 5) ^ swz_row<KB>(rw)) << 4);
   auto read = [&](Operands& o, const uint8_t* stage, int q) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
-      o.x[i] = *reinterpret_cast<const int4v*>(stage + (xo ^ (q << 5)) + 32 * i * kStepBytes);
+      o.x[i] = *reinterpret_cast<const int4v*>(stage + (xo ^ (q << 5)) + 32 * i * KB);
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-      o.w[j] = *reinterpret_cast<const int4v*>(stage + (wo ^ (q << 5)) + 32 * j * kStepBytes);
+      o.w[j] = *reinterpret_cast<const int4v*>(stage + (wo ^ (q << 5)) + 32 * j * KB);
   };
   auto multiply = [&](const Operands& o) __attribute__((always_inline)) {
 #pragma unroll
@@ -86,35 +91,52 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
       for (int j = 0; j < NJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[j], o.x[i], acc[i][j], 0, 0, 0);
   };
-  // The reads of a quarter are issued before the products of the one before; a step's last
-  // products run over the first reads of the next step and the copies of the one after.
-  Operands o[2];
-  auto step = [&](uint8_t* cur, uint8_t* next, int ks) __attribute__((always_inline)) {
+  // The reads of 32 bytes of a step are issued before the products of the 32 before; a step's
+  // last products run over the first reads of the next step and the copies into the stage
+  // that this step leaves.
+  constexpr int Q = KB / 32;
+  Operands o[WHOLE ? 2 * Q : 2];
+  auto step = [&](uint8_t* cur, uint8_t* next, int ks, int half) __attribute__((always_inline)) {
+    if constexpr (WHOLE) {
+      tile_hand_over<kCopies*(NS - 2)>();
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      read(o[(q + 1) & 1], cur, q + 1);
+      for (int q = 0; q < Q; ++q) read(o[Q * (1 - half) + q], next, q);
+      issue(cur, ks + NS);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(o[q & 1]);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) multiply(o[Q * half + q]);
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q - 1; ++q) {
+        read(o[(q + 1) & 1], cur, q + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(o[q & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      tile_hand_over<kCopies*(NS - 2)>();
+      read(o[0], next, 0);
+      issue(cur, ks + NS);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(o[1]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    tile_hand_over();
-    read(o[0], next, 0);
-    issue(cur, ks + 2);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(o[1]);
-    __builtin_amdgcn_sched_barrier(0);
   };
-  issue(s0, kb);
-  issue(s1, kb + 1);
-  tile_hand_over();
-  read(o[0], s0, 0);
+#pragma unroll
+  for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
+  tile_hand_over<kCopies*(NS - 1)>();
+#pragma unroll
+  for (int q = 0; q < (WHOLE ? Q : 1); ++q) read(o[q], s0, q);
+  // stages and operand sets alternate at compile time
+  constexpr int U = WHOLE && NS % 2 ? 2 * NS : NS;
   int ks = kb;
-  for (; ks + 2 <= ke; ks += 2) {
-    step(s0, s1, ks);
-    step(s1, s0, ks + 1);
-  }
-  if (ks < ke) step(s0, s1, ks);
-  tile_hand_over();  // the last copies have landed before results go where they went
+  for (; ks + U <= ke; ks += U)
+#pragma unroll
+    for (int u = 0; u < U; ++u) step(st[u % NS], st[(u + 1) % NS], ks + u, u & 1);
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (ks + u < ke) step(st[u % NS], st[(u + 1) % NS], ks + u, u & 1);
+  tile_hand_over<0>();  // the last copies have landed before results go where they went
 
   // A 32 x 32 result has rows of W along its registers: lane l holds row l % 32 of X, register
   // r column 8 * (r / 4) + 4 * (l / 32) + r % 4.
@@ -140,8 +162,13 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
   }
   // Results pass through the wave's own part of LDS, 32 rows at a time, and leave in 16-byte
   // pieces.
-  static_assert(WM * WN / 2 * 32 * kPitch <= kX + kW, "half of the waves in either stage");
-  uint8_t* out = (wave & 1 ? s1 : s0) + (wave >> 1) * (32 * kPitch);
+  constexpr int kFit = kStage / (32 * kPitch);  // waves whose results fit a stage
+  static_assert(kFit * NS >= WM * WN, "results fit the stages");
+  uint8_t* out = s0;
+#pragma unroll
+  for (int u = 1; u < NS; ++u)
+    if (wave / kFit == u) out = st[u];
+  out += wave % kFit * (32 * kPitch);
   typedef typename Val<TYPE>::T T;
   constexpr int kPer = 16 / sizeof(T);         // values of a piece
   constexpr int kPieces = WC / kPer;           // of a row
@@ -180,10 +207,10 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
   }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int KB, int NS, bool WHOLE>
 void launch_tile(const GemmArgs& g, int type, hipStream_t st) {
   i8_by_type(type, [&](auto t) {
-    hipLaunchKernelGGL((i8_gemm_kernel<BM, BN, WM, WN, decltype(t)::value>),
+    hipLaunchKernelGGL((i8_gemm_kernel<BM, BN, WM, WN, KB, NS, WHOLE, decltype(t)::value>),
                        dim3((unsigned)(g.tiles_m * g.tiles_n * g.S)), dim3(WM * WN * kWaveSize), 0,
                        st, g);
   });
@@ -191,19 +218,21 @@ void launch_tile(const GemmArgs& g, int type, hipStream_t st) {
 
 }  // namespace
 
+// Tiles, measured (us a call, bf16 results): 2048 rows of 4096 x 11008: 256 x 192 95, 128 x 256
+// 104, 128 x 128 121; of 4096 x 4096: 46, 39, 45; 777 of 4096 x 4096: 35, 30, 21, and 64 x 128
+// 23; of 5120 x 1536: 64 x 128 17.7, 128 x 128 22 (in 3 splits 20.8), 64 x 64 20; 130 of
+// 4096 x 4096: 12.4, 15, 9.5.
+constexpr I8Tile kTiles[] = {{256, 192, 0.90, 0.90, 0.50},
+                             {128, 256, 0.70, 0.70, 0.30},
+                             {128, 128, 0.46, 0.46, 0.14},
+                             {64, 128, 0.35, 0.27, 0.04},
+                             {64, 64, 0.20, 0.19, 0.02}};
+
 I8Plan plan_i8_gemm(int M, int N, int K) {
   I8Plan p{};
   p.strip = M <= kI8FewRows;
   if (p.strip) return p;
-  p.nk = (K + kStepBytes - 1) / kStepBytes;
-  p.BM = p.BN = 128;
-  if (M > 1024 && N >= 4096) p.BM = p.BN = 256;
-  p.tiles_m = (M + p.BM - 1) / p.BM;
-  p.tiles_n = (N + p.BN - 1) / p.BN;
-  int s = 1;
-  while (p.tiles_m * p.tiles_n * s * 2 <= 320 && p.nk / (2 * s) >= 4) s *= 2;
-  p.kper = (p.nk + s - 1) / s;
-  p.S = (p.nk + p.kper - 1) / p.kper;
+  plan_i8_tiles(p, kTiles, M, N, (K + 127) / 128);
   if (p.S > 1) p.ws_bytes = (size_t)p.S * M * N * sizeof(int32_t);
   return p;
 }
@@ -212,13 +241,16 @@ hipError_t launch_i8_gemm(const int8_t* X, const float* sx, const int8_t* W, con
                           void* Y, int type, int M, int N, int K, void* ws, const I8Plan& p,
                           hipStream_t st) {
   if (p.strip) return launch_i8_strip(X, sx, W, sw, Y, type, M, N, K, st);
-  GemmArgs g{X, sx, W, sw, Y, M, N, K, p.tiles_m, p.tiles_n, p.nk, p.S, p.kper,
-             static_cast<int32_t*>(ws)};
+  const GemmArgs g{X, sx, W, sw, Y, M, N, K, p.tiles_m, p.tiles_n, p.nk, p.S, p.kper,
+                   static_cast<int32_t*>(ws)};
   if ((long long)p.tiles_m * p.tiles_n * p.S > 0x3fffffLL) return hipErrorInvalidValue;
-  if (p.BM == 256)
-    launch_tile<256, 256, 2, 4>(g, type, st);
-  else
-    launch_tile<128, 128, 2, 2>(g, type, st);
+  switch (p.tile) {
+    case 0: launch_tile<256, 192, 4, 2, 128, 2, false>(g, type, st); break;
+    case 1: launch_tile<128, 256, 2, 4, 128, 3, false>(g, type, st); break;
+    case 2: launch_tile<128, 128, 2, 4, 128, 4, false>(g, type, st); break;
+    case 3: launch_tile<64, 128, 2, 4, 128, 3, true>(g, type, st); break;
+    default: launch_tile<64, 64, 2, 2, 128, 4, true>(g, type, st);
+  }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;
   return launch_i8_finish(g.part, sx, sw, Y, type, M, N, p.S, st);

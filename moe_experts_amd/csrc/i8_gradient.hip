@@ -22,7 +22,7 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 
-constexpr int BK = kStepBytes / 2;  // of the contraction in a step
+constexpr int kStepBytes = 128, BK = kStepBytes / 2;  // of a row of A in a step
 
 struct GradArgs {
   const uint16_t* A;  // fp16 [rows][ld]
@@ -55,12 +55,12 @@ struct ByteCopy {
     const int k = t / kChunks;
     off = (uint32_t)k * pitch + 16u * (uint32_t)((t % kChunks) ^ swz_byte<BN>(k));
   }
-  __device__ __forceinline__ void issue(uint8_t* stage, int ks, int wave) const {
+  __device__ __forceinline__ void issue(uint8_t* stage, int ks, bool live, int wave) const {
     const uint32_t so = (uint32_t)ks * BK * pitch;
 #pragma unroll
     for (int i = 0; i < kInstr; ++i)
       copy16(r, stage + (i * THREADS + wave * kWaveSize) * 16,
-             off + (uint32_t)(i * (THREADS / kChunks)) * pitch, so);
+             live ? off + (uint32_t)(i * (THREADS / kChunks)) * pitch : kPastEnd, so);
   }
 };
 
@@ -79,15 +79,19 @@ __device__ __forceinline__ half8 to_halves(int2v q) {
   return __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int NS, bool WHOLE>
 __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs g) {
   constexpr int kThreads = WM * WN * kWaveSize;
   constexpr int WR = BM / WM, WC = BN / WN;
   constexpr int MI = WR / 32, NJ = WC / 32;
-  constexpr int kA = BM * kStepBytes, kB = BK * BN;
+  constexpr int kA = BM * kStepBytes, kB = BK * BN, kStage = kA + kB;
   constexpr int kPitch = WC * 2 + 16;
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[kA + kB];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[kA + kB];
+  // The steps' stages are apart, so that the compiler can tell a copy into one from a read of
+  // another.
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage], s1[kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t s2[NS > 2 ? kStage : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t s3[NS > 3 ? kStage : 16];
+  uint8_t* const st[4] = {s0, s1, s2, s3};
   const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
   const int tiles = g.tiles_m * g.tiles_n;
   const int sp = L / tiles;
@@ -100,14 +104,16 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave % WM, wn = wave / WM;
 
-  RowCopy<BM, kThreads> ca;
+  RowCopy<BM, kThreads, kStepBytes> ca;
   ByteCopy<BN, kThreads> cb;
   ca.init(g.A + (size_t)i0 * g.ld, rows, (uint32_t)g.ld * 2u, t);
   cb.init(g, j0, t);
+  constexpr int kCopies = ca.kInstr + cb.kInstr;  // of a wave in a step
+  // steps past the last copy zeros, without an access of memory, and are not read
   auto issue = [&](uint8_t* stage, int ks) __attribute__((always_inline)) {
     const int k = min(ks, ke - 1);
-    ca.issue(stage, k, kStepBytes, wave);  // ld is whole steps
-    cb.issue(stage + kA, k, wave);
+    ca.issue(stage, k, ks < ke ? kStepBytes : 0, wave);  // ld is whole steps
+    cb.issue(stage + kA, k, ks < ke, wave);
   };
 
   float16v acc[MI][NJ];
@@ -122,12 +128,13 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
     int2v b[NJ];
   };
   const int ra = wm * WR + (lane & 31);
-  const int ao = ra * kStepBytes + (((lane >> 5) ^ swz_row(ra)) << 4);
+  const int ao = ra * kStepBytes + (((lane >> 5) ^ swz_row<kStepBytes>(ra)) << 4);
   // The 16 lanes of a group read eight rows of 16 columns; lane l gets column l % 32 of the
   // wave's 32, rows 8 * (l / 32) .. of the quarter's 16.
   const int kr = 8 * (lane >> 5) + ((lane & 15) >> 1);
   const int bo = kA + kr * BN + 8 * (lane & 1);
-  const int bc = (wn * WC / 16 + ((lane >> 4) & 1)) ^ swz_byte<BN>(kr);
+  const int bc = wn * (WC / 16) + ((lane >> 4) & 1);
+  const int bs = swz_byte<BN>(kr);
   auto read = [&](Operands& o, const uint8_t* stage, int q) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -136,7 +143,7 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
     for (int j = 0; j < NJ; ++j)
       o.b[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
           (__attribute__((address_space(3))) int2v*)(stage + bo + q * 16 * BN +
-                                                     ((bc ^ (2 * j)) << 4)));
+                                                     (((bc + 2 * j) ^ bs) << 4)));
   };
   auto multiply = [&](const Operands& o) __attribute__((always_inline)) {
 #pragma unroll
@@ -147,33 +154,49 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, o.a[i], acc[i][j], 0, 0, 0);
     }
   };
-  Operands o[2];
-  auto step = [&](uint8_t* cur, uint8_t* next, int ks) __attribute__((always_inline)) {
+  constexpr int Q = BK / 16;
+  Operands o[WHOLE ? 2 * Q : 2];
+  auto step = [&](uint8_t* cur, uint8_t* next, int ks, int half) __attribute__((always_inline)) {
+    if constexpr (WHOLE) {
+      tile_hand_over<kCopies*(NS - 2)>();
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      read(o[(q + 1) & 1], cur, q + 1);
+      for (int q = 0; q < Q; ++q) read(o[Q * (1 - half) + q], next, q);
+      issue(cur, ks + NS);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(o[q & 1]);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) multiply(o[Q * half + q]);
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q - 1; ++q) {
+        read(o[(q + 1) & 1], cur, q + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(o[q & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      tile_hand_over<kCopies*(NS - 2)>();
+      read(o[0], next, 0);
+      issue(cur, ks + NS);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(o[1]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    tile_hand_over();
-    read(o[0], next, 0);
-    issue(cur, ks + 2);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(o[1]);
-    __builtin_amdgcn_sched_barrier(0);
   };
-  issue(s0, kb);
-  issue(s1, kb + 1);
-  tile_hand_over();
-  read(o[0], s0, 0);
+#pragma unroll
+  for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
+  tile_hand_over<kCopies*(NS - 1)>();
+#pragma unroll
+  for (int q = 0; q < (WHOLE ? Q : 1); ++q) read(o[q], s0, q);
+  // stages and operand sets alternate at compile time
+  constexpr int U = WHOLE && NS % 2 ? 2 * NS : NS;
   int ks = kb;
-  for (; ks + 2 <= ke; ks += 2) {
-    step(s0, s1, ks);
-    step(s1, s0, ks + 1);
-  }
-  if (ks < ke) step(s0, s1, ks);
-  tile_hand_over();
+  for (; ks + U <= ke; ks += U)
+#pragma unroll
+    for (int u = 0; u < U; ++u) step(st[u % NS], st[(u + 1) % NS], ks + u, u & 1);
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (ks + u < ke) step(st[u % NS], st[(u + 1) % NS], ks + u, u & 1);
+  tile_hand_over<0>();  // the last copies have landed before results go where they went
 
   // Lane l holds row l % 32 of A, register r column 8 * (r / 4) + 4 * (l / 32) + r % 4.
   const int iw = i0 + wm * WR, rlive = rows - wm * WR;
@@ -196,8 +219,13 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
           }
     return;
   }
-  static_assert((WM * WN + 1) / 2 * 32 * kPitch <= kA + kB, "half of the waves in either stage");
-  uint8_t* res = (wave & 1 ? s1 : s0) + (wave >> 1) * (32 * kPitch);
+  constexpr int kFit = kStage / (32 * kPitch);  // waves whose results fit a stage
+  static_assert(kFit * NS >= WM * WN, "results fit the stages");
+  uint8_t* res = s0;
+#pragma unroll
+  for (int u = 1; u < NS; ++u)
+    if (wave / kFit == u) res = st[u];
+  res += wave % kFit * (32 * kPitch);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const float s = g.rs[min(iw + 32 * i + lr, g.rows - 1)];
@@ -223,29 +251,31 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
   }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int NS, bool WHOLE>
 void launch_tile(const GradArgs& g, hipStream_t st) {
-  hipLaunchKernelGGL((i8_gradient_kernel<BM, BN, WM, WN>),
+  hipLaunchKernelGGL((i8_gradient_kernel<BM, BN, WM, WN, NS, WHOLE>),
                      dim3((unsigned)(g.tiles_m * g.tiles_n * g.S)), dim3(WM * WN * kWaveSize), 0,
                      st, g);
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
+// Tiles, measured (us, the product alone): 11008 x 4096 results over 2048: 128 x 256 190,
+// 128 x 128 197; 2048 x 4096 over 11008: 181, 192; 1536 x 5120 over 777: 26.2, 24.6; 150 x 11008
+// over 4096: 128 x 128 34, 64 x 128 36, 32 x 128 27; 130 x 4096 over 4096: 19.4 and 18.5 and
+// 16.6 in 3, 2 and 3 splits; 16 x 11008 over 1999: 32 x 128 in 2 splits 10.0. Of 256 x 256
+// no more than of 128 x 256: 192 and 181 (in 2 splits). Two stages do better than more where
+// two workgroups fit a CU by that: 128 x 256 in 3 stages 219 instead of 190.
+constexpr I8Tile kTiles[] = {{128, 256, 0.80, 0.72, 0.25},
+                             {128, 128, 0.30, 0.28, 0.27},
+                             {64, 128, 0.26, 0.20, 0.12},
+                             {32, 128, 0.18, 0.10, 0.09}};
+
 // rows x cols results over a contraction of `depth`; chunks of `big` for the transposition
 I8Plan plan_gradient(int rows, int cols, int depth, int chunks) {
   I8Plan p{};
   p.ld = (depth + BK - 1) / BK * BK;
-  p.nk = p.ld / BK;
-  p.BN = 256;
-  p.BM = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  if ((long long)((rows + 255) / 256) * ((cols + 255) / 256) >= 256) p.BM = 256;
-  p.tiles_m = (rows + p.BM - 1) / p.BM;
-  p.tiles_n = (cols + p.BN - 1) / p.BN;
-  int s = 1;
-  while (p.tiles_m * p.tiles_n * s * 2 <= 320 && p.nk / (2 * s) >= 4) s *= 2;
-  p.kper = (p.nk + s - 1) / s;
-  p.S = (p.nk + p.kper - 1) / p.kper;
+  plan_i8_tiles(p, kTiles, rows, cols, p.ld / BK);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -277,14 +307,12 @@ hipError_t launch_tiles(const int8_t* B, uint16_t* out, int rows, int cols, int 
              p.S,
              p.kper,
              reinterpret_cast<float*>(w + p.off_part)};
-  if (p.BM == 32)
-    launch_tile<32, 256, 1, 4>(g, st);
-  else if (p.BM == 64)
-    launch_tile<64, 256, 1, 4>(g, st);
-  else if (p.BM == 128)
-    launch_tile<128, 256, 2, 4>(g, st);
-  else
-    launch_tile<256, 256, 2, 4>(g, st);
+  switch (p.tile) {
+    case 0: launch_tile<128, 256, 2, 4, 2, false>(g, st); break;
+    case 1: launch_tile<128, 128, 2, 4, 2, false>(g, st); break;
+    case 2: launch_tile<64, 128, 2, 4, 4, true>(g, st); break;
+    default: launch_tile<32, 128, 1, 4, 4, true>(g, st);
+  }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;
   return launch_i8_gradient_finish(g.part, g.rs, out, rows, cols, p.S, st);
@@ -305,7 +333,7 @@ hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* 
 }
 
 I8Plan plan_i8_backward_weight(int M, int N, int K) {
-  return plan_gradient(N, K, M, i8_max_chunks(M));
+  return plan_gradient(N, K, M, i8_max_chunks(M, N));
 }
 
 hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx,

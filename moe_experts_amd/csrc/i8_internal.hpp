@@ -35,6 +35,7 @@ hipError_t launch_i8_gemv(const float* x, const int8_t* W, const float* sw, floa
 // the contraction (32-bit partial sums [S][rows][cols] in ws).
 struct I8Plan {
   bool strip;      // i8_gemm: few rows
+  int tile;        // of those compiled
   int BM, BN;
   int tiles_m, tiles_n;
   int nk;          // K steps of the whole contraction
@@ -46,6 +47,48 @@ struct I8Plan {
   int ld;          // gradients: values of a row of the left operand
   size_t ws_bytes;
 };
+
+// What a tile costs. A CU that has n of them to do takes n * (each + busy * load) us a K step,
+// load being the share of what n on every CU would be (the clock falls as more of the GPU is
+// busy), or `alone` with one. They come from sweeps of tiles and splits.
+struct I8Tile {
+  int BM, BN;
+  double alone, each, busy;
+};
+// The tile and the number of splits by the time a CU with the most work takes: its steps, 3 us
+// and 0.8 a tile for the start and the results; splits cost the partial sums, written and read
+// at 4.5 TB/s, and a kernel that adds them.
+template <int COUNT>
+void plan_i8_tiles(I8Plan& p, const I8Tile (&tiles)[COUNT], int rows, int cols, int nk) {
+  double best = 1e30;
+  p.nk = nk;
+  for (int t = 0; t < COUNT; ++t) {
+    const int tm = (rows + tiles[t].BM - 1) / tiles[t].BM;
+    const int tn = (cols + tiles[t].BN - 1) / tiles[t].BN;
+    for (int s = 1; s <= 32 && (s == 1 || nk / s >= 2); ++s) {
+      const int kper = (nk + s - 1) / s;
+      if ((nk + kper - 1) / kper != s) continue;
+      const double count = (double)tm * tn * s;
+      if (s > 1 && count > 4096) continue;
+      const double n = (double)(((long long)count + 255) / 256);
+      const double load = count / (256.0 * n);
+      const double step =
+          n == 1 ? tiles[t].alone + tiles[t].busy * load : n * (tiles[t].each + tiles[t].busy * load);
+      double cost = kper * step + 3.0 + 0.8 * n;
+      if (s > 1) cost += 4.0 + s * (double)rows * cols * 8.0 / 4.5e6;
+      if (cost < best) {
+        best = cost;
+        p.tile = t;
+        p.BM = tiles[t].BM;
+        p.BN = tiles[t].BN;
+        p.tiles_m = tm;
+        p.tiles_n = tn;
+        p.S = s;
+        p.kper = kper;
+      }
+    }
+  }
+}
 
 I8Plan plan_i8_gemm(int M, int N, int K);
 hipError_t launch_i8_gemm(const int8_t* X, const float* sx, const int8_t* W, const float* sw,
@@ -66,8 +109,8 @@ hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const 
 hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs,
                                    int M, int N, int ld, hipStream_t st);
 // a[n][m] = fp16(dY[m][n] * sx[m] * 2^e), m < ld (zero past M), rs[n] = 2^-e; big: scratch,
-// the largest magnitudes of a column in each of i8_max_chunks(M) chunks of the rows
-int i8_max_chunks(int M);
+// the largest magnitudes of a column in each of i8_max_chunks(M, N) chunks of the rows
+int i8_max_chunks(int M, int N);
 hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint16_t* a, float* rs,
                                       uint32_t* big, int M, int N, int ld, hipStream_t st);
 hipError_t launch_i8_finish(const int32_t* part, const float* sx, const float* sw, void* Y,

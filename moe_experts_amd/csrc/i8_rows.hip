@@ -19,39 +19,38 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kRowThreads = 256;
+constexpr int kFewRows = 256;       // rows by wider workgroups: no more than one a CU
 constexpr int kMaxGrid = 1 << 20;  // workgroups; each takes every kMaxGrid-th row after its own
 
 int row_grid(long long n) { return (int)std::min<long long>(n, kMaxGrid); }
 
-// Eight values from p, of which the first n exist (n >= 8: all); the rest are zero. p is
-// aligned to one value.
+// Eight values as they stand in memory (aligned to one value). Kept so, 16-bit types take half
+// the registers.
 template <int TYPE>
-__device__ __forceinline__ void load_values(const typename Val<TYPE>::T* __restrict__ p, int n,
-                                            float (&x)[8]) {
-  typename Val<TYPE>::T v[8] = {};
-  if (n >= 8) {
-    __builtin_memcpy(v, p, sizeof(v));
-  } else {
+struct Piece {
+  typedef typename Val<TYPE>::T T;
+  static constexpr int kWords = sizeof(T) * 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* __restrict__ p) { __builtin_memcpy(w, p, sizeof(w)); }
+  // Keeps the compiler from holding the values converted from one use to the next.
+  __device__ __forceinline__ void fresh() {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) v[e] = p[e];
+    for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = Val<TYPE>::get(v[e]);
-}
-
-__device__ __forceinline__ void store_int8(int8_t* __restrict__ p, int n, const uint32_t (&q)[2]) {
-  if (n >= 8) {
-    __builtin_memcpy(p, q, 8);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) p[e] = (int8_t)(q[e >> 2] >> (8 * (e & 3)));
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(T) == 4)
+      return __builtin_bit_cast(float, w[e]);
+    else if constexpr (TYPE == Q4_TYPE_BF16)
+      return __builtin_bit_cast(float, e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    else
+      return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[e / 2] >> (16 * (e & 1))));
   }
-}
+};
 
-// One workgroup a row. V pieces of eight values a lane stay in registers between the
-// search for the largest and the rounding; LOOP reads longer rows twice.
+// One workgroup a row of at least eight values. V pieces of eight a lane stay in registers
+// between the search for the largest and the rounding; LOOP reads longer rows twice. A piece
+// that would end behind the row is moved to end with it: some values are then done twice,
+// alike. Lanes behind the row repeat its last piece and store nothing.
 template <int TYPE, int THREADS, int V, bool LOOP>
 __global__ __launch_bounds__(THREADS) void i8_quantize_kernel(
     const typename Val<TYPE>::T* __restrict__ X, int8_t* __restrict__ Q,
@@ -60,14 +59,12 @@ __global__ __launch_bounds__(THREADS) void i8_quantize_kernel(
   for (int m = blockIdx.x; m < M; m += gridDim.x) {
     const typename Val<TYPE>::T* xr = X + (size_t)m * K;
     int8_t* qr = Q + (size_t)m * K;
-    float x[V][8];
+    Piece<TYPE> x[V];
     uint32_t big = 0;
     for (int k0 = 0; k0 < K; k0 += THREADS * 8 * V) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int k = k0 + (v * THREADS + (int)threadIdx.x) * 8;
-        load_values<TYPE>(xr + min(k, K), K - k, x[v]);
-      }
+      for (int v = 0; v < V; ++v)
+        x[v].load(xr + min(k0 + (v * THREADS + (int)threadIdx.x) * 8, K - 8));
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -80,11 +77,15 @@ __global__ __launch_bounds__(THREADS) void i8_quantize_kernel(
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int k = k0 + (v * THREADS + (int)threadIdx.x) * 8;
-        if (LOOP) load_values<TYPE>(xr + min(k, K), K - k, x[v]);
+        if (LOOP) x[v].load(xr + min(k, K - 8));
+        x[v].fresh();
         if (k < K) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = x[v][e];
           uint32_t q[2];
-          to_int8<8>(x[v], rs, q);
-          store_int8(qr + k, K - k, q);
+          to_int8<8>(f, rs, q);
+          __builtin_memcpy(qr + min(k, K - 8), q, 8);
         }
       }
       if (!LOOP) break;
@@ -93,7 +94,32 @@ __global__ __launch_bounds__(THREADS) void i8_quantize_kernel(
   }
 }
 
-// Eight values a lane, a workgroup a piece of a row.
+// Rows of fewer than eight values, one a lane.
+template <int TYPE>
+__global__ __launch_bounds__(kRowThreads) void i8_quantize_short_kernel(
+    const typename Val<TYPE>::T* __restrict__ X, int8_t* __restrict__ Q,
+    float* __restrict__ scale, int M, int K) {
+  for (long long m = (long long)blockIdx.x * kRowThreads + threadIdx.x; m < M;
+       m += (long long)gridDim.x * kRowThreads) {
+    float x[8];
+    uint32_t big = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = e < K ? Val<TYPE>::get(X[(size_t)m * K + min(e, K - 1)]) : 0.0f;
+      big = max(big, magnitude(x[e]));
+    }
+    const RowScale rs = row_scale(big);
+    scale[m] = rs.s;
+    uint32_t q[2];
+    to_int8<8>(x, rs, q);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < K) Q[(size_t)m * K + e] = (int8_t)(q[e >> 2] >> (8 * (e & 3)));
+  }
+}
+
+// Eight values a lane, a workgroup a piece of a row of at least eight; the last eight of a row
+// as in i8_quantize_kernel.
 template <int TYPE, int THREADS>
 __global__ __launch_bounds__(THREADS) void i8_dequantize_kernel(
     const int8_t* __restrict__ Q, const float* __restrict__ scale,
@@ -102,28 +128,25 @@ __global__ __launch_bounds__(THREADS) void i8_dequantize_kernel(
     const int m = (int)(i / pieces);
     const int k = ((int)(i % pieces) * THREADS + (int)threadIdx.x) * 8;
     if (k >= K) continue;
+    const size_t at = (size_t)m * K + min(k, K - 8);
     const float s = scale[m];
-    const int8_t* qr = Q + (size_t)m * K + k;
-    typename Val<TYPE>::T* xr = X + (size_t)m * K + k;
-    int8_t q[8] = {};
-    if (K - k >= 8) {
-      __builtin_memcpy(q, qr, 8);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e < K) q[e] = qr[e];
-    }
+    int8_t q[8];
+    __builtin_memcpy(q, Q + at, 8);
     typename Val<TYPE>::T v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = Val<TYPE>::put((float)q[e] * s);
-    if (K - k >= 8) {
-      __builtin_memcpy(xr, v, sizeof(v));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e < K) xr[e] = v[e];
-    }
+    __builtin_memcpy(X + at, v, sizeof(v));
   }
+}
+
+// Rows of fewer than eight values, a value a lane.
+template <int TYPE>
+__global__ __launch_bounds__(kRowThreads) void i8_dequantize_short_kernel(
+    const int8_t* __restrict__ Q, const float* __restrict__ scale,
+    typename Val<TYPE>::T* __restrict__ X, long long n, int K) {
+  for (long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kRowThreads)
+    X[i] = Val<TYPE>::put((float)Q[i] * scale[i / K]);
 }
 
 // ---------------------------------------------------------------------------
@@ -145,16 +168,6 @@ __device__ __forceinline__ PowerOfTwo to_fp16_range(uint32_t big) {
   return p;
 }
 
-__device__ __forceinline__ void load_products(const uint16_t* __restrict__ p,
-                                              const float* __restrict__ s, float (&x)[8]) {
-  uint16_t v[8];
-  __builtin_memcpy(v, __builtin_assume_aligned(p, 16), 16);
-  float sv[8];
-  __builtin_memcpy(sv, s, 32);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = Val<Q4_TYPE_BF16>::get(v[e]) * sv[e];
-}
-
 // One workgroup a row of dY; N and ld are multiples of 8.
 template <int THREADS, int V, bool LOOP>
 __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
@@ -165,15 +178,25 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
     const uint16_t* yr = dY + (size_t)m * N;
     _Float16* ar = a + (size_t)m * ld;
     float x[V][8];
-    uint32_t big = 0;
-    for (int n0 = 0; n0 < N; n0 += THREADS * 8 * V) {
+    // products of the pieces from n0 on, zeros behind the row
+    auto load = [&](int n0) {
+      Piece<Q4_TYPE_BF16> y[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int n = n0 + (v * THREADS + (int)threadIdx.x) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[v][e] = 0.0f;
-        if (n < N) load_products(yr + n, sw + n, x[v]);
+        const int n = min(n0 + (v * THREADS + (int)threadIdx.x) * 8, N - 8);
+        y[v].load(yr + n);
+        __builtin_memcpy(x[v], sw + n, 32);
       }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool in = n0 + (v * THREADS + (int)threadIdx.x) * 8 < N;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[v][e] = in ? y[v][e] * x[v][e] : 0.0f;
+      }
+    };
+    uint32_t big = 0;
+    for (int n0 = 0; n0 < N; n0 += THREADS * 8 * V) {
+      load(n0);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -183,15 +206,11 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
     const PowerOfTwo p = to_fp16_range(workgroup_max<THREADS>(big, at));
     if (threadIdx.x == 0) rs[m] = p.down;
     for (int n0 = 0; n0 < ld; n0 += THREADS * 8 * V) {
+      if (LOOP) load(n0);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int n = n0 + (v * THREADS + (int)threadIdx.x) * 8;
         if (n >= ld) continue;
-        if (LOOP) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[v][e] = 0.0f;
-          if (n < N) load_products(yr + n, sw + n, x[v]);
-        }
         half8 h;
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = (_Float16)(x[v][e] * p.up);
@@ -200,6 +219,71 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
       if (!LOOP) break;
     }
     if (THREADS > kWaveSize) __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dY * sx by columns, up to kOnceRows rows: one workgroup holds eight columns of all rows in
+// registers, so that dY is read once for the search and the rounding. A lane has P pairs of
+// neighbouring rows; a pair's values of a column are one dword of the result, and 64 lanes
+// store 256 bytes of a column together. The 16 bytes of a row share their line with those of
+// seven other workgroups, which run on the same XCD.
+// ---------------------------------------------------------------------------
+constexpr int kOnceRows = 8192, kOnceCols = 2048;
+bool columns_once(int M, int N) { return M <= kOnceRows && N <= kOnceCols; }
+
+template <int THREADS, int P>
+__global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
+    const uint16_t* __restrict__ dY, const float* __restrict__ sx, _Float16* __restrict__ a,
+    float* __restrict__ rs, int M, int N, int ld) {
+  constexpr int kWaves = THREADS / kWaveSize;
+  __shared__ uint32_t at[kWaves][8];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int n = xcd_logical_tile(blockIdx.x, gridDim.x) * 8;
+  Piece<Q4_TYPE_BF16> v[P][2];
+  float s[P][2];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = 2 * (p * THREADS + t) + h;
+      v[p][h].load(dY + (size_t)min(m, M - 1) * N + n);
+      s[p][h] = sx[min(m, M - 1)];
+    }
+  // rows past the last are zeros, whatever the one that was read in their place holds
+  auto value = [&](int p, int h, int e) {
+    return 2 * (p * THREADS + t) + h < M ? v[p][h][e] * s[p][h] : 0.0f;
+  };
+  uint32_t big[8] = {};
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) big[e] = max(big[e], magnitude(value(p, h, e)));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int o = 1; o < kWaveSize; o <<= 1)
+      big[e] = max(big[e], (uint32_t)__shfl_xor((int)big[e], o));
+    if (lane == e) at[wave][e] = big[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint32_t b = at[0][e];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) b = max(b, at[w][e]);
+    const PowerOfTwo f = to_fp16_range(b);
+    if (t == e) rs[n + e] = f.down;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+      const int m = 2 * (p * THREADS + t);  // ld is even
+      if (m < ld)
+        *reinterpret_cast<half2v*>(a + (size_t)(n + e) * ld + m) =
+            half2v{(_Float16)(value(p, 0, e) * f.up), (_Float16)(value(p, 1, e) * f.up)};
+    }
   }
 }
 
@@ -244,55 +328,68 @@ __global__ __launch_bounds__(kRowThreads) void i8_column_max_kernel(
   }
 }
 
-// 64 columns by a chunk of rows of dY, transposed through LDS 64 rows at a time.
+// 64 columns by kChunkRows rows of dY, all read at once, then transposed through LDS 128 rows at
+// a time: two neighbouring rows of a column are a dword, and 64 lanes store 256 bytes of a
+// column.
 __global__ __launch_bounds__(kRowThreads) void i8_gradient_columns_kernel(
     const uint16_t* __restrict__ dY, const float* __restrict__ sx,
     const uint32_t* __restrict__ big, _Float16* __restrict__ a, float* __restrict__ rs, int M,
     int N, int ld, int tiles_n, int chunks) {
-  constexpr int kPitch = 64 + 8;  // halves of a row of the transposed tile
-  __shared__ __attribute__((aligned(16))) _Float16 tile[kCols * kPitch];
+  constexpr int kPairs = kChunkRows / 2 / kRowLanes;  // of a lane
+  constexpr int kPitch = 64 + 1;  // dwords of a column: eight columns on are eight banks on
+  __shared__ uint32_t tile[kCols * kPitch];
   __shared__ float up[kCols];
   const int n0 = ((int)blockIdx.x % tiles_n) * kCols;
-  const int chunk = (int)blockIdx.x / tiles_n;
+  const int m0 = (int)blockIdx.x / tiles_n * kChunkRows;
+  const int c8 = (int)threadIdx.x % kColLanes, r = (int)threadIdx.x / kColLanes;
+  const int n = min(n0 + c8 * 8, N - 8);  // columns past the last are not stored
+  Piece<Q4_TYPE_BF16> v[kPairs][2];
+  float s[kPairs][2];
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = min(m0 + 2 * (p * kRowLanes + r) + h, M - 1);
+      v[p][h].load(dY + (size_t)m * N + n);
+      s[p][h] = sx[m];
+    }
   if (threadIdx.x < kCols) {
-    const int n = n0 + (int)threadIdx.x;
-    uint32_t v = 0;
-    if (n < N)
-      for (int c = 0; c < chunks; ++c) v = max(v, big[(size_t)c * N + n]);
-    const PowerOfTwo p = to_fp16_range(v);
-    up[threadIdx.x] = p.up;
-    if (n < N && chunk == 0) rs[n] = p.down;
+    const int col = n0 + (int)threadIdx.x;
+    uint32_t b = 0;
+    if (col < N)
+      for (int c = 0; c < chunks; ++c) b = max(b, big[(size_t)c * N + col]);
+    const PowerOfTwo f = to_fp16_range(b);
+    up[threadIdx.x] = f.up;
+    if (col < N && m0 == 0) rs[col] = f.down;
   }
   __syncthreads();
-  const int c8 = (int)threadIdx.x % kColLanes, r = (int)threadIdx.x / kColLanes;
-  const int n = n0 + c8 * 8;
   float u[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) u[e] = up[c8 * 8 + e];
-  const int m1 = min(ld, (chunk + 1) * kChunkRows);  // ld is a multiple of 64
-  for (int m0 = chunk * kChunkRows; m0 < m1; m0 += 64) {
 #pragma unroll
-    for (int i = 0; i < 64 / kRowLanes; ++i) {
-      const int mr = i * kRowLanes + r, m = m0 + mr;
-      uint16_t v[8] = {};
-      float s = 0.0f;
-      if (m < M && n < N) {
-        __builtin_memcpy(v, __builtin_assume_aligned(dY + (size_t)m * N + n, 16), 16);
-        s = sx[m];
+  for (int p = 0; p < kPairs; p += 2) {
+    const int mt = m0 + 2 * p * kRowLanes;  // first of the 128 rows
+    if (mt >= ld) break;                    // uniform
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+        half2v h;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          h[j] = m0 + 2 * ((p + i) * kRowLanes + r) + j < M
+                     ? (_Float16)(v[p + i][j][e] * s[p + i][j] * u[e])
+                     : (_Float16)0.0f;
+        tile[(c8 * 8 + e) * kPitch + i * kRowLanes + r] = __builtin_bit_cast(uint32_t, h);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        tile[(c8 * 8 + e) * kPitch + mr] =
-            (_Float16)(Val<Q4_TYPE_BF16>::get(v[e]) * s * u[e]);
-    }
     __syncthreads();
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-    for (int i = 0; i < kCols * 8 / kRowThreads; ++i) {
-      const int piece = i * kRowThreads + (int)threadIdx.x;
-      const int col = piece >> 3, p8 = piece & 7;
-      if (n0 + col < N)
-        *reinterpret_cast<half8*>(a + (size_t)(n0 + col) * ld + m0 + p8 * 8) =
-            *reinterpret_cast<const half8*>(tile + col * kPitch + p8 * 8);
+    for (int i = 0; i < kCols; i += kRowThreads / kWaveSize) {
+      const int col = i + wave, m = mt + 2 * lane;  // ld is even
+      if (n0 + col < N && m < ld)
+        *reinterpret_cast<uint32_t*>(a + (size_t)(n0 + col) * ld + m) = tile[col * kPitch + lane];
     }
     __syncthreads();
   }
@@ -364,14 +461,25 @@ hipError_t launch_i8_quantize(const void* X, int type, int8_t* Q, float* scale, 
                               hipStream_t st) {
   i8_by_type(type, [&](auto t) {
     constexpr int TYPE = decltype(t)::value;
-    if (K <= 512)
+    if (K < 8)
+      hipLaunchKernelGGL((i8_quantize_short_kernel<TYPE>),
+                         dim3(row_grid(((long long)M + kRowThreads - 1) / kRowThreads)),
+                         dim3(kRowThreads), 0, st, static_cast<const typename Val<TYPE>::T*>(X), Q,
+                         scale, M, K);
+    else if (K <= 512)
       quantize<TYPE, 64, 1, false>(X, Q, scale, M, K, st);
     else if (K <= 2048)
       quantize<TYPE, 256, 1, false>(X, Q, scale, M, K, st);
+    else if (M <= kFewRows && K <= 8192)
+      quantize<TYPE, 1024, 1, false>(X, Q, scale, M, K, st);
+    else if (M <= kFewRows && K <= 16384)
+      quantize<TYPE, 1024, 2, false>(X, Q, scale, M, K, st);
     else if (K <= 4096)
       quantize<TYPE, 256, 2, false>(X, Q, scale, M, K, st);
     else if (K <= 8192)
       quantize<TYPE, 256, 4, false>(X, Q, scale, M, K, st);
+    else if (K <= 12288)
+      quantize<TYPE, 256, 6, false>(X, Q, scale, M, K, st);
     else if (K <= 16384)
       quantize<TYPE, 256, 8, false>(X, Q, scale, M, K, st);
     else
@@ -385,7 +493,12 @@ hipError_t launch_i8_dequantize(const int8_t* Q, const float* scale, void* X, in
   i8_by_type(type, [&](auto t) {
     constexpr int TYPE = decltype(t)::value;
     typedef typename Val<TYPE>::T T;
-    if (K <= 512) {
+    if (K < 8) {
+      const long long n = (long long)M * K;
+      hipLaunchKernelGGL((i8_dequantize_short_kernel<TYPE>),
+                         dim3(row_grid((n + kRowThreads - 1) / kRowThreads)), dim3(kRowThreads), 0,
+                         st, Q, scale, static_cast<T*>(X), n, K);
+    } else if (K <= 512) {
       hipLaunchKernelGGL((i8_dequantize_kernel<TYPE, 64>), dim3(row_grid(M)), dim3(64), 0, st, Q,
                          scale, static_cast<T*>(X), M, K, 1);
     } else {
@@ -408,6 +521,8 @@ hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t
     gradient_rows<256, 2, false>(dY, sw, a, rs, M, N, ld, st);
   else if (ld <= 8192)
     gradient_rows<256, 4, false>(dY, sw, a, rs, M, N, ld, st);
+  else if (ld <= 12288)
+    gradient_rows<256, 6, false>(dY, sw, a, rs, M, N, ld, st);
   else if (ld <= 16384)
     gradient_rows<256, 8, false>(dY, sw, a, rs, M, N, ld, st);
   else
@@ -415,11 +530,36 @@ hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t
   return hipGetLastError();
 }
 
-int i8_max_chunks(int M) { return (M + max_rows(M) - 1) / max_rows(M); }
+int i8_max_chunks(int M, int N) {
+  return columns_once(M, N) ? 0 : (M + max_rows(M) - 1) / max_rows(M);
+}
 
 hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint16_t* a, float* rs,
                                       uint32_t* big, int M, int N, int ld, hipStream_t st) {
-  const int tiles_n = (N + kCols - 1) / kCols, maxima = i8_max_chunks(M);
+  if (columns_once(M, N)) {
+    auto go = [&](auto threads, auto pairs) {
+      constexpr int T = decltype(threads)::value;
+      hipLaunchKernelGGL((i8_gradient_columns_once_kernel<T, decltype(pairs)::value>),
+                         dim3((unsigned)(N / 8)), dim3(T), 0, st, dY, sx,
+                         reinterpret_cast<_Float16*>(a), rs, M, N, ld);
+    };
+    typedef std::integral_constant<int, 1> One;
+    typedef std::integral_constant<int, 1024> Widest;
+    if (ld <= 128)
+      go(std::integral_constant<int, 64>{}, One{});
+    else if (ld <= 512)
+      go(std::integral_constant<int, 256>{}, One{});
+    else if (ld <= 1024)
+      go(std::integral_constant<int, 512>{}, One{});
+    else if (ld <= 2048)
+      go(Widest{}, One{});
+    else if (ld <= 4096)
+      go(Widest{}, std::integral_constant<int, 2>{});
+    else
+      go(Widest{}, std::integral_constant<int, 4>{});
+    return hipGetLastError();
+  }
+  const int tiles_n = (N + kCols - 1) / kCols, maxima = i8_max_chunks(M, N);
   const long long grid = (long long)tiles_n * ((M + kChunkRows - 1) / kChunkRows);
   if (grid > 0xffffffLL) return hipErrorInvalidValue;  // below 2^32 lanes
   hipLaunchKernelGGL(i8_column_max_kernel, dim3((unsigned)(tiles_n * maxima)), dim3(kRowThreads), 0,

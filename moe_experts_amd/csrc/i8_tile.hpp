@@ -13,34 +13,39 @@
 namespace q4 {
 
 constexpr uint32_t kPastEnd = 0x80000000u;  // offset past the end of any array
-constexpr int kStepBytes = 128;             // of a row of the left operand in a K step
 
-__device__ __forceinline__ int swz_row(int r) { return (r >> 1) & 7; }
+// KB bytes of a row in a step (64 or 128): where the row's 16-byte chunks are turned by.
+template <int KB>
+__device__ __forceinline__ int swz_row(int r) {
+  return KB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
 
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off,
                                        uint32_t so) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 16, off, so, 0, 0);
 }
 
-// The copies of ROWS rows of 128 bytes by THREADS lanes.
-template <int ROWS, int THREADS>
+// The copies of ROWS rows of KB bytes by THREADS lanes.
+template <int ROWS, int THREADS, int KB>
 struct RowCopy {
-  static constexpr int kInstr = ROWS * 8 / THREADS;
-  static_assert(ROWS * 8 % THREADS == 0 && THREADS % 128 == 0, "whole copies, one swizzle a lane");
+  static constexpr int kChunks = KB / 16;
+  static constexpr int kInstr = ROWS * kChunks / THREADS;
+  static_assert(ROWS * kChunks % THREADS == 0 && THREADS / kChunks % 16 == 0,
+                "whole copies, one swizzle a lane");
   __amdgpu_buffer_rsrc_t r;
   uint32_t off[kInstr];
   int chunk;  // 16 * (the lane's chunk in a step)
   // `rows` (at least one) rows of `pitch` bytes from `base`; rows past them repeat the last
   __device__ __forceinline__ void init(const void* base, int rows, uint32_t pitch, int t) {
     r = make_rsrc(base, (uint32_t)rows * pitch);
-    chunk = 16 * ((t & 7) ^ swz_row(t >> 3));
+    chunk = 16 * ((t % kChunks) ^ swz_row<KB>(t / kChunks));
 #pragma unroll
     for (int i = 0; i < kInstr; ++i)
-      off[i] = (uint32_t)min((i * THREADS + t) >> 3, rows - 1) * pitch + (uint32_t)chunk;
+      off[i] = (uint32_t)min((i * THREADS + t) / kChunks, rows - 1) * pitch + (uint32_t)chunk;
   }
   // Step ks into `stage`; bytes past `left` of the step (the row's end) become zeros.
   __device__ __forceinline__ void issue(uint8_t* stage, int ks, int left, int wave) const {
-    const uint32_t so = (uint32_t)ks * kStepBytes;
+    const uint32_t so = (uint32_t)ks * KB;
     const bool live = chunk < left;
 #pragma unroll
     for (int i = 0; i < kInstr; ++i)
@@ -48,12 +53,15 @@ struct RowCopy {
   }
 };
 
-// Hands LDS over at a barrier: this wave's reads of it are done and its copies into it have
-// landed.
+// Hands LDS over at a barrier: this wave's reads of it are done, and of its copies into it all
+// but the last COPIES have landed.
+template <int COPIES>
 __device__ __forceinline__ void tile_hand_over() {
+  static_assert(COPIES < 64, "vmcnt");
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  // vmcnt(COPIES) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0x0070 | (COPIES & 15) | (COPIES >> 4) << 14);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");

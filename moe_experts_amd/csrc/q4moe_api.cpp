@@ -617,4 +617,21 @@ int i8_gemm_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx
                                                 static_cast<hipStream_t>(stream)));
 }
 
+int i8_gemm_plan(int form, int M, int N, int K, int* rows, int* cols, int* splits, int* steps) {
+  if (!rows || !cols || !splits || !steps) return Q4_EINVAL;
+  if (form < Q4_I8_GEMM || form > Q4_I8_GEMM_BACKWARD_WEIGHT) return Q4_EINVAL;
+  const int rc = form == Q4_I8_GEMM
+                     ? check_i8_shape(M, N, K, 2)
+                     : check_i8_gradient_shape(M, N, K, form == Q4_I8_GEMM_BACKWARD ? M : N);
+  if (rc != Q4_OK) return rc;
+  const q4::I8Plan p = form == Q4_I8_GEMM            ? q4::plan_i8_gemm(M, N, K)
+                       : form == Q4_I8_GEMM_BACKWARD ? q4::plan_i8_backward(M, N, K)
+                                                     : q4::plan_i8_backward_weight(M, N, K);
+  *rows = p.strip ? 0 : p.BM;
+  *cols = p.strip ? 0 : p.BN;
+  *splits = p.strip ? 1 : p.S;
+  *steps = p.strip ? (K + 127) / 128 : p.kper;
+  return Q4_OK;
+}
+
 }  // extern "C"
