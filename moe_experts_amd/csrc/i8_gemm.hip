@@ -221,12 +221,14 @@ void launch_tile(const GemmArgs& g, int type, hipStream_t st) {
 // Tiles, measured (us a call, bf16 results): 2048 rows of 4096 x 11008: 256 x 192 95, 128 x 256
 // 104, 128 x 128 121; of 4096 x 4096: 46, 39, 45; 777 of 4096 x 4096: 35, 30, 21, and 64 x 128
 // 23; of 5120 x 1536: 64 x 128 17.7, 128 x 128 22 (in 3 splits 20.8), 64 x 64 20; 130 of
-// 4096 x 4096: 12.4, 15, 9.5.
+// 4096 x 4096: 12.4, 15, 9.5; 33 of 4096 x 11008: 64 x 64 13.9, 32 x 128 15.5; 20 of 4096 x 4096:
+// 32 x 64 8.0.
 constexpr I8Tile kTiles[] = {{256, 192, 0.90, 0.90, 0.50},
                              {128, 256, 0.70, 0.70, 0.30},
                              {128, 128, 0.46, 0.46, 0.14},
                              {64, 128, 0.35, 0.27, 0.04},
-                             {64, 64, 0.20, 0.19, 0.02}};
+                             {64, 64, 0.20, 0.19, 0.02},
+                             {32, 64, 0.13, 0.11, 0.04}};
 
 I8Plan plan_i8_gemm(int M, int N, int K) {
   I8Plan p{};
@@ -249,7 +251,8 @@ hipError_t launch_i8_gemm(const int8_t* X, const float* sx, const int8_t* W, con
     case 1: launch_tile<128, 256, 2, 4, 128, 3, false>(g, type, st); break;
     case 2: launch_tile<128, 128, 2, 4, 128, 4, false>(g, type, st); break;
     case 3: launch_tile<64, 128, 2, 4, 128, 3, true>(g, type, st); break;
-    default: launch_tile<64, 64, 2, 2, 128, 4, true>(g, type, st);
+    case 4: launch_tile<64, 64, 2, 2, 128, 4, true>(g, type, st); break;
+    default: launch_tile<32, 64, 1, 2, 128, 4, true>(g, type, st);
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;

@@ -18,7 +18,7 @@ hipError_t launch_i8_dequantize(const int8_t* Q, const float* scale, void* X, in
 
 // ---- few rows (i8_strip.hip) -------------------------------------------------
 // Y = X . W^T for X of up to kI8FewRows rows, scaled and rounded.
-constexpr int kI8FewRows = 64;
+constexpr int kI8FewRows = 16;
 hipError_t launch_i8_strip(const int8_t* X, const float* sx, const int8_t* W, const float* sw,
                            void* Y, int type, int M, int N, int K, hipStream_t st);
 struct I8GemvPlan {
