@@ -1,25 +1,32 @@
 // 8-bit product of few rows: Y = (X . W^T) * sx * sw for up to 16 rows of X, and the
 // decode form that takes fp32 rows and quantizes them itself.
 //
-// A workgroup owns 16 rows of W (columns of Y) and its four waves share out the
-// contraction. v_mfma_i32_16x16x64_i8 takes 16 bytes of one row in a lane for both operands,
-// so the weights go from memory straight into its registers, 64 bytes of each of 16 rows a
-// load, and nothing but the sums passes through LDS: they are whole numbers, so the order in
-// which the waves' are added does not matter.
+// A workgroup owns 16 rows of W (columns of Y) and its four waves share out the contraction.
+// A wave copies 128 bytes of each of the 16 rows a step, memory -> LDS, several steps ahead,
+// into a part of LDS of its own: nothing is waited for but its own copies. It multiplies them
+// by v_mfma_i32_16x16x64_i8. The waves' sums meet in LDS; they are whole numbers, so their
+// order does not matter.
 //
-// Bound by the weights' way from memory, 16 MB in FIG1 us and 45 MB in FIG2
+// Bound by the weights' way from memory. With the weights loaded straight into the matrix
+// instruction's registers (16 rows of 64 bytes a load): 8 rows of 11008 x 4096 12.1 us, by
+// copies (8 rows of 128 bytes each) 10.2, 4.4 TB/s; a row of 4096 x 4096 4.9 and 4.6.
+//
+// fp32 rows of up to kFusedValues values in all are quantized by every workgroup for itself
+// while its first weights are on their way: a row of 4096 for 4096 x 4096 6.5 us, against
+// 4.7 and 3.2 for a launch that quantizes and the time between the two. With more values it
+// takes longer than that launch (4 rows of 4096: 11.0 against 8.9).
 #include <algorithm>
 
 #include "i8_device.hpp"
 #include "i8_internal.hpp"
+#include "i8_tile.hpp"
 
 namespace q4 {
 namespace {
 
 constexpr int kWaves = 4;
 constexpr int kStripThreads = kWaves * kWaveSize;
-constexpr uint32_t kOut = 0x80000000u;  // past the end of any array
-constexpr int kFusedValues = 16384;     // of x, in the LDS of a workgroup that quantizes them
+constexpr int kFusedValues = 8192;  // of x, where every workgroup quantizes them for itself
 constexpr int kFusedPieces = kFusedValues / 8 / kStripThreads;
 
 struct StripArgs {
@@ -32,6 +39,17 @@ struct StripArgs {
   int M, N, K;
   int blocks;
 };
+
+// A barrier for LDS alone: copies from memory stay in flight over it.
+__device__ __forceinline__ void lds_only_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 // Fused: all of x in registers, the largest of each row by LDS, int8 into xq, rows `pitch`
 // bytes apart.
@@ -50,7 +68,7 @@ struct FusedRows {
     const int t = threadIdx.x;
     const int total = g.M * g.K / 8;
     if (t < Q4_GEMV_MAX_M) big[t] = 0;
-    __syncthreads();
+    lds_only_barrier();
 #pragma unroll
     for (int i = 0; i < kFusedPieces; ++i) {
       const int p = i * kStripThreads + t;
@@ -69,7 +87,7 @@ struct FusedRows {
         atomicMax(&big[row], b);
       }
     }
-    __syncthreads();
+    lds_only_barrier();
 #pragma unroll
     for (int i = 0; i < kFusedPieces; ++i) {
       const int p = i * kStripThreads + t;
@@ -82,76 +100,107 @@ struct FusedRows {
         if (p * 8 == row * g.K) sx[row] = rs.s;
       }
     }
-    __syncthreads();
+    lds_only_barrier();
   }
 };
 
-template <int TYPE, bool FUSED>
+// XROWS: rows of X that a wave copies, 8 or 16; 0 for the fused form.
+template <int TYPE, int XROWS, int NS>
 __global__ __launch_bounds__(kStripThreads) void i8_few_rows_kernel(StripArgs g) {
-  constexpr int U = 4;  // loads of a piece; two pieces are in flight
-  // rows of K rounded up to 64, and 16 bytes more; K % 16 == 0 and M * K <= kFusedValues
-  constexpr int kXq = FUSED ? kFusedValues + Q4_GEMV_MAX_M * (64 + 16) : 16;
+  constexpr bool FUSED = XROWS == 0;
+  constexpr int kCopies = 2 + XROWS / 8;           // of a step, eight rows each
+  constexpr int kStage = kCopies * 1024;           // of a wave
+  // rows of K rounded up to 128, and 16 bytes more; K % 16 == 0 and M * K <= kFusedValues
+  constexpr int kXq = FUSED ? kFusedValues + Q4_GEMV_MAX_M * (128 + 16) : 16;
   __shared__ __attribute__((aligned(16))) uint8_t xq[kXq];
   __shared__ uint32_t big[Q4_GEMV_MAX_M];
   __shared__ float sxq[Q4_GEMV_MAX_M];
   __shared__ __attribute__((aligned(16))) int4v sums[kWaves][kWaveSize];
+  // The steps' stages are apart, so that the compiler can tell a copy into one from a read of
+  // another; in each every wave has its own part.
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[kWaves * kStage], s1[kWaves * kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t s2[NS > 2 ? kWaves * kStage : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t s3[NS > 3 ? kWaves * kStage : 16];
+  uint8_t* const st[4] = {s0, s1, s2, s3};
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int block = (int)(blockIdx.y * gridDim.x + blockIdx.x);
   if (block >= g.blocks) return;  // the whole workgroup, before any barrier
   const int n0 = block * 16;
   const int K = g.K;
-  const int nk = (K + 63) / 64, per = (nk + kWaves - 1) / kWaves;
+  const int nk = (K + 127) / 128, per = (nk + kWaves - 1) / kWaves;
   const int kb = min(nk, wave * per), ke = min(nk, kb + per);
   const __amdgpu_buffer_rsrc_t rw =
       make_rsrc(g.W + (size_t)n0 * K, (uint32_t)min(16, g.N - n0) * (uint32_t)K);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(g.X, FUSED ? 0u : (uint32_t)g.M * (uint32_t)K);
-  const int kl = 16 * (lane >> 4);
-  const uint32_t row = (uint32_t)(lane & 15) * (uint32_t)K + (uint32_t)kl;
-  const int pitch = nk * 64 + 16;
+  const int pitch = nk * 128 + 16;
 
+  // Copies: eight lanes a row of 128 bytes, chunks turned by the row as in the tiles.
+  const int cr = lane >> 3, chunk = 16 * ((lane & 7) ^ swz_row<128>(cr));
+  const int chunk8 = 16 * ((lane & 7) ^ swz_row<128>(cr + 8));
+  const uint32_t at = (uint32_t)cr * (uint32_t)K + (uint32_t)chunk;
+  const uint32_t at8 = (uint32_t)(cr + 8) * (uint32_t)K + (uint32_t)chunk8;
+  // steps of another wave, values past the row and rows past the last read zeros, without an
+  // access of memory
+  auto issue = [&](uint8_t* stage, int s) __attribute__((always_inline)) {
+    uint8_t* mine = stage + wave * kStage;
+    const uint32_t so = (uint32_t)min(s, nk - 1) * 128u;
+    const int left = s < ke ? K - s * 128 : 0;
+    const uint32_t o = chunk < left ? at : kPastEnd, o8 = chunk8 < left ? at8 : kPastEnd;
+    if constexpr (XROWS >= 8) copy16(rx, mine + 2048, o, so);
+    if constexpr (XROWS >= 16) copy16(rx, mine + 3072, o8, so);
+    copy16(rw, mine, o, so);
+    copy16(rw, mine + 1024, o8, so);
+  };
   // x first: loads return in order, and the weights are many
   FusedRows rows;
   if constexpr (FUSED) rows.load(g);
-  struct Piece {
-    int4v w[U], x[FUSED ? 1 : U];
-  };
-  auto load = [&](Piece& p, int s0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int s = s0 + u;
-      // steps of another wave, values past the row and rows past the last read zeros
-      const uint32_t o = s < ke && s * 64 + kl < K ? row : kOut;
-      const uint32_t so = (uint32_t)min(s, nk - 1) * 64u;
-      if constexpr (!FUSED)
-        p.x[u] =
-            __builtin_bit_cast(int4v, __builtin_amdgcn_raw_buffer_load_b128(rx, o, so, 0));
-      p.w[u] = __builtin_bit_cast(int4v, __builtin_amdgcn_raw_buffer_load_b128(rw, o, so, 0));
-    }
-  };
-  int4v acc = int4v{0, 0, 0, 0};
-  const int token = FUSED ? min(lane & 15, g.M - 1) : 0;  // rows past the last are not kept
-  auto multiply = [&](const Piece& p, int s0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      int4v x;
-      if constexpr (FUSED)
-        x = *reinterpret_cast<const int4v*>(xq + token * pitch + min(s0 + u, nk - 1) * 64 + kl);
-      else
-        x = p.x[u];
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(p.w[u], x, acc, 0, 0, 0);
-    }
-  };
-  Piece p[2];
-  load(p[0], kb);
-  load(p[1], kb + U);
+  for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
   if constexpr (FUSED) rows.quantize(g, xq, pitch, big, sxq);
-  for (int s = kb; s < ke; s += 2 * U) {
-    multiply(p[0], s);
-    load(p[0], s + 2 * U);
-    multiply(p[1], s + U);
-    load(p[1], s + 3 * U);
-  }
+
+  int4v acc = int4v{0, 0, 0, 0};
+  const int r = lane & 15, c = lane >> 4;
+  const int wo = r * 128 + ((c ^ swz_row<128>(r)) << 4);
+  // rows of X past the last are not kept: they repeat others
+  const int xr = FUSED ? min(r, g.M - 1) : r % (XROWS ? XROWS : 1);
+  const int xo = FUSED ? xr * pitch + 16 * c : 2048 + xr * 128 + ((c ^ swz_row<128>(xr)) << 4);
+  auto step = [&](uint8_t* stage, int s) __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    // this wave's copies of the step have landed: vmcnt(kCopies * (NS - 1))
+    constexpr int kLeft = kCopies * (NS - 1);
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (kLeft & 15) | (kLeft >> 4) << 14);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* mine = stage + wave * kStage;
+    int4v w[2], x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[h] = *reinterpret_cast<const int4v*>(mine + (wo ^ (h << 6)));
+      if constexpr (FUSED)
+        x[h] = *reinterpret_cast<const int4v*>(xq + xo + s * 128 + h * 64);
+      else
+        x[h] = *reinterpret_cast<const int4v*>(mine + (xo ^ (h << 6)));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h], x[h], acc, 0, 0, 0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is copied over
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    issue(stage, s + NS);
+  };
+  int s = kb;
+  for (; s + NS <= ke; s += NS)
+#pragma unroll
+    for (int u = 0; u < NS; ++u) step(st[u], s + u);
+#pragma unroll
+  for (int u = 0; u < NS - 1; ++u)
+    if (s + u < ke) step(st[u], s + u);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no copy lands after the workgroup ends
   sums[wave][lane] = acc;
   __syncthreads();
   // lane l of a 16 x 16 result holds row l % 16 of X and four neighbouring columns
@@ -160,20 +209,20 @@ __global__ __launch_bounds__(kStripThreads) void i8_few_rows_kernel(StripArgs g)
   int4v v = sums[0][lane];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) v += sums[w][lane];
-  const float s = FUSED ? sxq[m] : g.sx[m];
+  const float sm = FUSED ? sxq[m] : g.sx[m];
   typename Val<TYPE>::T y[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = Val<TYPE>::put((float)v[e] * s * g.sw[n + e]);
+  for (int e = 0; e < 4; ++e) y[e] = Val<TYPE>::put((float)v[e] * sm * g.sw[n + e]);
   typename Val<TYPE>::T* dst = static_cast<typename Val<TYPE>::T*>(g.Y) + (size_t)m * g.N + n;
   __builtin_memcpy(__builtin_assume_aligned(dst, sizeof(y)), y, sizeof(y));
 }
 
-template <int TYPE, bool FUSED>
+template <int TYPE, int XROWS, int NS>
 hipError_t launch(StripArgs g, hipStream_t st) {
   g.blocks = (g.N + 15) / 16;
   // two dimensions: one of the widest matrices' workgroups would pass 2^32 lanes
   const int x = std::min(g.blocks, 1 << 20);
-  hipLaunchKernelGGL((i8_few_rows_kernel<TYPE, FUSED>), dim3(x, (g.blocks + x - 1) / x),
+  hipLaunchKernelGGL((i8_few_rows_kernel<TYPE, XROWS, NS>), dim3(x, (g.blocks + x - 1) / x),
                      dim3(kStripThreads), 0, st, g);
   return hipGetLastError();
 }
@@ -186,7 +235,12 @@ hipError_t launch_i8_strip(const int8_t* X, const float* sx, const int8_t* W, co
                            void* Y, int type, int M, int N, int K, hipStream_t st) {
   const StripArgs g{X, nullptr, sx, W, sw, Y, M, N, K, 0};
   hipError_t err = hipSuccess;
-  i8_by_type(type, [&](auto t) { err = launch<decltype(t)::value, false>(g, st); });
+  i8_by_type(type, [&](auto t) {
+    if (M <= 8)
+      err = launch<decltype(t)::value, 8, 4>(g, st);
+    else
+      err = launch<decltype(t)::value, 16, 3>(g, st);
+  });
   return err;
 }
 
@@ -204,7 +258,7 @@ hipError_t launch_i8_gemv(const float* x, const int8_t* W, const float* sw, floa
                           int K, void* ws, const I8GemvPlan& p, hipStream_t st) {
   if (p.fused) {
     const StripArgs g{nullptr, x, nullptr, W, sw, y, M, N, K, 0};
-    return launch<Q4_TYPE_F32, true>(g, st);
+    return launch<Q4_TYPE_F32, 0, 3>(g, st);
   }
   int8_t* q = static_cast<int8_t*>(ws);
   float* s = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.off_s);
