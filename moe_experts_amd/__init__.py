@@ -34,7 +34,8 @@ _EXPORTS = ("q4_0_gemv", "q8_0_gemv", "q8_0_gemv_workspace_bytes", "q4_0_gemm", 
 def __getattr__(name):
     if name in _EXPORTS:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found without this call from now on
+        return value
     raise AttributeError(name)
 
 

@@ -749,10 +749,14 @@ def i8_quantize(X: torch.Tensor, Q: torch.Tensor | None = None,
     px = _ptr(X, "X", X.dtype, M * K, i)
     if Q is None:
         Q = X.new_empty((M, K), dtype=torch.int8)
+        pq = Q.data_ptr()
+    else:
+        pq = _ptr(Q, "Q", torch.int8, M * K, i)
     if scale is None:
         scale = X.new_empty((M,), dtype=torch.float32)
-    pq = _ptr(Q, "Q", torch.int8, M * K, i)
-    ps = _ptr(scale, "scale", torch.float32, M, i)
+        ps = scale.data_ptr()
+    else:
+        ps = _ptr(scale, "scale", torch.float32, M, i)
     _call(_lib.i8_quantize, i, px, a, pq, ps, M, K)
     return Q, scale
 
@@ -772,7 +776,9 @@ def i8_dequantize(Q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = tor
     ps = _ptr(scale, "scale", torch.float32, M, i)
     if X is None:
         X = Q.new_empty((M, K), dtype=dtype)
-    px = _ptr(X, "X", dtype, M * K, i)
+        px = X.data_ptr()
+    else:
+        px = _ptr(X, "X", dtype, M * K, i)
     _call(_lib.i8_dequantize, i, pq, ps, px, a, M, K)
     return X
 
@@ -797,7 +803,9 @@ def i8_gemv(x: torch.Tensor, W: torch.Tensor, sw: torch.Tensor, y: torch.Tensor 
     ps = _ptr(sw, "sw", torch.float32, N, i)
     if y is None:
         y = x.new_empty((M, N), dtype=torch.float32)
-    py = _ptr(y, "y", torch.float32, M * N, i)
+        py = y.data_ptr()
+    else:
+        py = _ptr(y, "y", torch.float32, M * N, i)
     _run(_lib.i8_gemv, i8_gemv_workspace_bytes(M, N, K), ws, i, px, pw, ps, py, M, N, K)
     return y
 
@@ -821,7 +829,9 @@ def i8_gemm(X: torch.Tensor, sx: torch.Tensor, W: torch.Tensor, sw: torch.Tensor
     psw = _ptr(sw, "sw", torch.float32, N, i)
     if Y is None:
         Y = X.new_empty((M, N), dtype=dtype)
-    py = _ptr(Y, "Y", dtype, M * N, i)
+        py = Y.data_ptr()
+    else:
+        py = _ptr(Y, "Y", dtype, M * N, i)
     _run(_lib.i8_gemm, i8_gemm_workspace_bytes(M, N, K), ws, i, px, psx, pw, psw, py, a, M, N, K)
     return Y
 
@@ -841,7 +851,9 @@ def i8_gemm_backward(dY: torch.Tensor, W: torch.Tensor, sw: torch.Tensor,
     ps = _ptr(sw, "sw", torch.float32, N, i)
     if dX is None:
         dX = dY.new_empty((M, K), dtype=torch.bfloat16)
-    px = _ptr(dX, "dX", torch.bfloat16, M * K, i)
+        px = dX.data_ptr()
+    else:
+        px = _ptr(dX, "dX", torch.bfloat16, M * K, i)
     _run(_lib.i8_gemm_backward, i8_gemm_backward_workspace_bytes(M, N, K), ws, i, pd, pw, ps, px,
          M, N, K)
     return dX
@@ -862,7 +874,9 @@ def i8_gemm_backward_weight(dY: torch.Tensor, X: torch.Tensor, sx: torch.Tensor,
     ps = _ptr(sx, "sx", torch.float32, M, i)
     if dW is None:
         dW = dY.new_empty((N, K), dtype=torch.bfloat16)
-    pg = _ptr(dW, "dW", torch.bfloat16, N * K, i)
+        pg = dW.data_ptr()
+    else:
+        pg = _ptr(dW, "dW", torch.bfloat16, N * K, i)
     _run(_lib.i8_gemm_backward_weight, i8_gemm_backward_weight_workspace_bytes(M, N, K), ws, i,
          pd, px, ps, pg, M, N, K)
     return dW

@@ -34,7 +34,7 @@ def lib():
 #: name: pointers' alignments in order, sizes (M, N, K) of a valid call that needs a workspace
 VALID = {
     "i8_gemv": ((4, 16, 4, 16), (8, 64, 11008)),
-    "i8_gemm": ((16, 4, 16, 4, 16), (130, 64, 4096)),
+    "i8_gemm": ((16, 4, 16, 4, 16), (130, 64, 65536)),
     "i8_gemm_backward": ((16, 16, 4, 16), (40, 128, 64)),
     "i8_gemm_backward_weight": ((16, 16, 4, 16), (40, 128, 64)),
 }
@@ -131,6 +131,33 @@ def test_workspace_sizes_over_extreme_shapes(lib, name):
                 bad = bad or N * K >= 1 << 31 or M * K >= 1 << 31 or 2 * M * N >= 1 << 31
                 if bad or (name == "i8_gemv" and M > 8):
                     assert got == 0, (M, N, K)
+
+
+def test_plan_over_extreme_shapes(lib):
+    """The plan of a shape fails as its call does, and else names a kernel."""
+    i, ptr = ctypes.c_int, ctypes.POINTER(ctypes.c_int)
+    lib.i8_gemm_plan.argtypes = [i] * 4 + [ptr] * 4
+    out = [i(7) for _ in range(4)]
+    refs = [ctypes.byref(v) for v in out]
+    for form in (-1, 3):
+        assert lib.i8_gemm_plan(form, 65, 64, 64, *refs) == EINVAL
+    for at in range(4):
+        assert lib.i8_gemm_plan(0, 65, 64, 64, *refs[:at], None, *refs[at + 1:]) == EINVAL
+    assert [v.value for v in out] == [7] * 4
+    vals = (-1, 0, 1, 8, 16, 17, 64, 72, 4096, 65536, MAX_K, MAX_K + 16, (1 << 27) - 8, (1 << 31) - 1)
+    for form, name in enumerate(("i8_gemm", "i8_gemm_backward", "i8_gemm_backward_weight")):
+        for M in vals:
+            for N in vals:
+                for K in vals:
+                    rc = lib.i8_gemm_plan(form, M, N, K, *refs)
+                    if rc != 0:  # the call's own check, which comes before anything is enqueued
+                        assert call(lib, name, sizes=(M, N, K)) == rc
+                        continue
+                    rows, cols, splits, steps = (v.value for v in out)
+                    assert splits >= 1 and steps >= 1 and (rows == 0) == (cols == 0)
+                    depth = K if form == 0 else 2 * (N if form == 1 else M)
+                    total = (depth + 127) // 128
+                    assert (splits - 1) * steps < total <= splits * steps  # none is empty
 
 
 def test_rows(lib):
