@@ -1,6 +1,24 @@
-// 8-bit product of many rows: Y = (X . W^T) * sx * sw, X int8 [M][K], W int8 [N][K], on the
-// integer matrix cores (v_mfma_i32_32x32x32_i8). The sums are whole numbers and exact, so
+// 8-bit product of more than 16 rows: Y = (X . W^T) * sx * sw, X int8 [M][K], W int8 [N][K], on
+// the integer matrix cores (v_mfma_i32_32x32x32_i8). The sums are whole numbers and exact, so
 // splits of the contraction change nothing.
+//
+// Tiles of BM rows of X and BN rows of W, K steps of 128 bytes. Both operands have their
+// contraction contiguous, so a step is copied memory -> LDS as it stands, NS steps in LDS, and a
+// lane's 16 bytes of a row are what the matrix instruction takes. One barrier a step.
+//   * Large tiles leave the least to move: per 1 KiB of operands that a wave reads from LDS,
+//     64 x 96 results give 1.2 products of 32 x 32 x 32, 64 x 64 one, 32 x 32 half of one.
+//     256 x 192 is the largest whose accumulators leave room for two sets of operands
+//     (256 x 384, one pass of 232 tiles over the CUs: 95 us too, registers spilled).
+//   * Small tiles (WHOLE) read all of the next step's operands before they multiply this
+//     step's: with 64 to 128 cycles of products a quarter, reading one quarter ahead left
+//     them waiting for LDS (130 rows of 4096 x 4096 by 64 x 64: 11.3 -> 9.5 us).
+//
+// What bounds it: 2048 rows of 4096 x 11008 take 95 us, 1.95 POP/s. With all CUs busy the power
+// limit holds the clock at 1.5 to 1.7 GHz, at which the matrix cores are busy three quarters
+// of a tile's time: without LDS reads it takes 85 us, without copies 83, with neither 72. A
+// deeper ring of stages, registers in place of LDS-DMA, raised priorities and freer scheduling
+// all came out within 3 %. Where few tiles leave the clock at 2.4 GHz, 777 rows of 5120 x 1536,
+// a step of 64 x 128 takes 850 cycles, of which LDS is busy 700 (64 KiB read, 24 KiB written).
 #include <algorithm>
 
 #include "i8_device.hpp"
@@ -22,21 +40,19 @@ struct GemmArgs {
 };
 
 // WM x WN waves over a tile of BM rows of X and BN rows of W.
-template <int BM, int BN, int WM, int WN, int KB, int NS, bool WHOLE, int TYPE>
+template <int BM, int BN, int WM, int WN, int NS, bool WHOLE, int TYPE>
 __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) {
   constexpr int kThreads = WM * WN * kWaveSize;
   constexpr int WR = BM / WM, WC = BN / WN;  // of a wave
   constexpr int MI = WR / 32, NJ = WC / 32;
-  constexpr int kX = BM * KB, kW = BN * KB, kStage = kX + kW;
+  constexpr int kX = BM * kStepBytes, kW = BN * kStepBytes, kStage = kX + kW;
   constexpr int kPitch = WC * 4 + 16;  // bytes of 32 rows of results in LDS, wave by wave
   // The steps' stages are apart, so that the compiler can tell a copy into one from a read of
   // another.
   __shared__ __attribute__((aligned(1024))) uint8_t s0[kStage], s1[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t s2[NS > 2 ? kStage : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t s3[NS > 3 ? kStage : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t s4[NS > 4 ? kStage : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t s5[NS > 5 ? kStage : 16];
-  uint8_t* const st[6] = {s0, s1, s2, s3, s4, s5};
+  uint8_t* const st[4] = {s0, s1, s2, s3};
   const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
   const int tiles = g.tiles_m * g.tiles_n;
   const int sp = L / tiles;
@@ -49,15 +65,15 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave % WM, wn = wave / WM;
 
-  RowCopy<BM, kThreads, KB> cx;
-  RowCopy<BN, kThreads, KB> cw;
+  RowCopy<BM, kThreads> cx;
+  RowCopy<BN, kThreads> cw;
   constexpr int kCopies = cx.kInstr + cw.kInstr;  // of a wave in a step
   cx.init(g.X + (size_t)m0 * g.K, rows, (uint32_t)g.K, t);
   cw.init(g.W + (size_t)n0 * g.K, cols, (uint32_t)g.K, t);
   // steps past the last copy zeros, without an access of memory, and are not read
   auto issue = [&](uint8_t* stage, int ks) __attribute__((always_inline)) {
     const int k = min(ks, ke - 1);
-    const int left = ks < ke ? g.K - k * KB : 0;
+    const int left = ks < ke ? g.K - k * kStepBytes : 0;
     cx.issue(stage, k, left, wave);
     cw.issue(stage + kX, k, left, wave);
   };
@@ -74,15 +90,15 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
   };
   const int rx = wm * WR + (lane & 31), rw = wn * WC + (lane & 31);
   // chunk 2 * q + lane / 32 of a row in quarter q; 32 rows on the swizzle is the same
-  const int xo = rx * KB + (((lane >> 5) ^ swz_row<KB>(rx)) << 4);
-  const int wo = kX + rw * KB + (((lane >> 5) ^ swz_row<KB>(rw)) << 4);
+  const int xo = rx * kStepBytes + (((lane >> 5) ^ swz_row(rx)) << 4);
+  const int wo = kX + rw * kStepBytes + (((lane >> 5) ^ swz_row(rw)) << 4);
   auto read = [&](Operands& o, const uint8_t* stage, int q) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
-      o.x[i] = *reinterpret_cast<const int4v*>(stage + (xo ^ (q << 5)) + 32 * i * KB);
+      o.x[i] = *reinterpret_cast<const int4v*>(stage + (xo ^ (q << 5)) + 32 * i * kStepBytes);
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-      o.w[j] = *reinterpret_cast<const int4v*>(stage + (wo ^ (q << 5)) + 32 * j * KB);
+      o.w[j] = *reinterpret_cast<const int4v*>(stage + (wo ^ (q << 5)) + 32 * j * kStepBytes);
   };
   auto multiply = [&](const Operands& o) __attribute__((always_inline)) {
 #pragma unroll
@@ -94,7 +110,7 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
   // The reads of 32 bytes of a step are issued before the products of the 32 before; a step's
   // last products run over the first reads of the next step and the copies into the stage
   // that this step leaves.
-  constexpr int Q = KB / 32;
+  constexpr int Q = kStepBytes / 32;
   Operands o[WHOLE ? 2 * Q : 2];
   auto step = [&](uint8_t* cur, uint8_t* next, int ks, int half) __attribute__((always_inline)) {
     if constexpr (WHOLE) {
@@ -207,10 +223,10 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gemm_kernel(GemmArgs g) 
   }
 }
 
-template <int BM, int BN, int WM, int WN, int KB, int NS, bool WHOLE>
+template <int BM, int BN, int WM, int WN, int NS, bool WHOLE>
 void launch_tile(const GemmArgs& g, int type, hipStream_t st) {
   i8_by_type(type, [&](auto t) {
-    hipLaunchKernelGGL((i8_gemm_kernel<BM, BN, WM, WN, KB, NS, WHOLE, decltype(t)::value>),
+    hipLaunchKernelGGL((i8_gemm_kernel<BM, BN, WM, WN, NS, WHOLE, decltype(t)::value>),
                        dim3((unsigned)(g.tiles_m * g.tiles_n * g.S)), dim3(WM * WN * kWaveSize), 0,
                        st, g);
   });
@@ -234,7 +250,7 @@ I8Plan plan_i8_gemm(int M, int N, int K) {
   I8Plan p{};
   p.strip = M <= kI8FewRows;
   if (p.strip) return p;
-  plan_i8_tiles(p, kTiles, M, N, (K + 127) / 128);
+  plan_i8_tiles(p, kTiles, M, N, (K + kStepBytes - 1) / kStepBytes);
   if (p.S > 1) p.ws_bytes = (size_t)p.S * M * N * sizeof(int32_t);
   return p;
 }
@@ -247,12 +263,12 @@ hipError_t launch_i8_gemm(const int8_t* X, const float* sx, const int8_t* W, con
                    static_cast<int32_t*>(ws)};
   if ((long long)p.tiles_m * p.tiles_n * p.S > 0x3fffffLL) return hipErrorInvalidValue;
   switch (p.tile) {
-    case 0: launch_tile<256, 192, 4, 2, 128, 2, false>(g, type, st); break;
-    case 1: launch_tile<128, 256, 2, 4, 128, 3, false>(g, type, st); break;
-    case 2: launch_tile<128, 128, 2, 4, 128, 4, false>(g, type, st); break;
-    case 3: launch_tile<64, 128, 2, 4, 128, 3, true>(g, type, st); break;
-    case 4: launch_tile<64, 64, 2, 2, 128, 4, true>(g, type, st); break;
-    default: launch_tile<32, 64, 1, 2, 128, 4, true>(g, type, st);
+    case 0: launch_tile<256, 192, 4, 2, 2, false>(g, type, st); break;
+    case 1: launch_tile<128, 256, 2, 4, 3, false>(g, type, st); break;
+    case 2: launch_tile<128, 128, 2, 4, 4, false>(g, type, st); break;
+    case 3: launch_tile<64, 128, 2, 4, 3, true>(g, type, st); break;
+    case 4: launch_tile<64, 64, 2, 2, 4, true>(g, type, st); break;
+    default: launch_tile<32, 64, 1, 2, 4, true>(g, type, st);
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;

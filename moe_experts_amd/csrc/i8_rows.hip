@@ -5,6 +5,12 @@
 //   gradient_rows     dY * sw as the fp16 left operand of the input's gradient
 //   gradient_columns  dY * sx, transposed, as that of the weights' gradient
 //   finish            results from the split sums of a product
+//
+// All are bound by memory where they are large: 2048 x 11008 bf16 is quantized in 14.2 us and
+// restored in 13.3, 4.8 and 5.1 TB/s of the 67.6 MB that each moves (a large copy reaches 5.1).
+// One pass over the data: a row stays in registers between the search for its largest value
+// and the rounding, as it stands in memory (converted first, quantizing took 21.3 us, for
+// want of waves a CU). Few rows take wider workgroups (8 rows of 11008 fp32: 5.0 -> 3.8 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

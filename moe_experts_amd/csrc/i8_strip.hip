@@ -136,8 +136,8 @@ __global__ __launch_bounds__(kStripThreads) void i8_few_rows_kernel(StripArgs g)
   const int pitch = nk * 128 + 16;
 
   // Copies: eight lanes a row of 128 bytes, chunks turned by the row as in the tiles.
-  const int cr = lane >> 3, chunk = 16 * ((lane & 7) ^ swz_row<128>(cr));
-  const int chunk8 = 16 * ((lane & 7) ^ swz_row<128>(cr + 8));
+  const int cr = lane >> 3, chunk = 16 * ((lane & 7) ^ swz_row(cr));
+  const int chunk8 = 16 * ((lane & 7) ^ swz_row(cr + 8));
   const uint32_t at = (uint32_t)cr * (uint32_t)K + (uint32_t)chunk;
   const uint32_t at8 = (uint32_t)(cr + 8) * (uint32_t)K + (uint32_t)chunk8;
   // steps of another wave, values past the row and rows past the last read zeros, without an
@@ -161,10 +161,10 @@ __global__ __launch_bounds__(kStripThreads) void i8_few_rows_kernel(StripArgs g)
 
   int4v acc = int4v{0, 0, 0, 0};
   const int r = lane & 15, c = lane >> 4;
-  const int wo = r * 128 + ((c ^ swz_row<128>(r)) << 4);
+  const int wo = r * 128 + ((c ^ swz_row(r)) << 4);
   // rows of X past the last are not kept: they repeat others
   const int xr = FUSED ? min(r, g.M - 1) : r % (XROWS ? XROWS : 1);
-  const int xo = FUSED ? xr * pitch + 16 * c : 2048 + xr * 128 + ((c ^ swz_row<128>(xr)) << 4);
+  const int xo = FUSED ? xr * pitch + 16 * c : 2048 + xr * 128 + ((c ^ swz_row(xr)) << 4);
   auto step = [&](uint8_t* stage, int s) __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);

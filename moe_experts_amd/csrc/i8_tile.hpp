@@ -13,22 +13,20 @@
 namespace q4 {
 
 constexpr uint32_t kPastEnd = 0x80000000u;  // offset past the end of any array
+constexpr int kStepBytes = 128;             // of a row of the left operand in a step
 
-// KB bytes of a row in a step (64 or 128): where the row's 16-byte chunks are turned by.
-template <int KB>
-__device__ __forceinline__ int swz_row(int r) {
-  return KB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
-}
+// What the chunks of a row are turned by.
+__device__ __forceinline__ int swz_row(int r) { return (r >> 1) & 7; }
 
 __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off,
                                        uint32_t so) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 16, off, so, 0, 0);
 }
 
-// The copies of ROWS rows of KB bytes by THREADS lanes.
-template <int ROWS, int THREADS, int KB>
+// The copies of ROWS rows of a step by THREADS lanes.
+template <int ROWS, int THREADS>
 struct RowCopy {
-  static constexpr int kChunks = KB / 16;
+  static constexpr int kChunks = kStepBytes / 16;
   static constexpr int kInstr = ROWS * kChunks / THREADS;
   static_assert(ROWS * kChunks % THREADS == 0 && THREADS / kChunks % 16 == 0,
                 "whole copies, one swizzle a lane");
@@ -38,14 +36,14 @@ struct RowCopy {
   // `rows` (at least one) rows of `pitch` bytes from `base`; rows past them repeat the last
   __device__ __forceinline__ void init(const void* base, int rows, uint32_t pitch, int t) {
     r = make_rsrc(base, (uint32_t)rows * pitch);
-    chunk = 16 * ((t % kChunks) ^ swz_row<KB>(t / kChunks));
+    chunk = 16 * ((t % kChunks) ^ swz_row(t / kChunks));
 #pragma unroll
     for (int i = 0; i < kInstr; ++i)
       off[i] = (uint32_t)min((i * THREADS + t) / kChunks, rows - 1) * pitch + (uint32_t)chunk;
   }
   // Step ks into `stage`; bytes past `left` of the step (the row's end) become zeros.
   __device__ __forceinline__ void issue(uint8_t* stage, int ks, int left, int wave) const {
-    const uint32_t so = (uint32_t)ks * KB;
+    const uint32_t so = (uint32_t)ks * kStepBytes;
     const bool live = chunk < left;
 #pragma unroll
     for (int i = 0; i < kInstr; ++i)

@@ -144,6 +144,17 @@ def test_dequantize(M, K, kind):
     assert torch.equal(i8_dequantize(to_dev(q), to_dev(s), dtype=TYPES[kind]).cpu(), want)
 
 
+def test_broken_rows_stay_broken():
+    """What i8_quantize makes of a row with an infinity or a NaN comes back as NaN, and its
+    neighbours come back whole."""
+    from moe_experts_amd import i8_dequantize, i8_quantize
+    for K in (5, 300, 5000):
+        x = to_dev(datagen.activations(23, 4, K))
+        x[1, 0], x[2, K - 1] = float("inf"), float("nan")
+        back = i8_dequantize(*i8_quantize(x), dtype=torch.bfloat16)
+        assert torch.isnan(back[1:3].float()).all() and torch.isfinite(back[0::3].float()).all()
+
+
 # ------------------------------------------------------------------ products
 #: few rows in every grouping, tiles of every height, ragged ends, with and without splits
 GEMM_SHAPES = [(1, 16, 8), (1, 4096, 256), (5, 80, 24), (8, 11008, 72), (16, 1040, 136),
