@@ -74,9 +74,10 @@ _Static_assert(sizeof(q8_0_block) == 34, "q8_0_block must be 34 bytes");
 typedef enum q4_status {
   Q4_OK = 0,
   Q4_EINVAL = -1,      /* null pointer or non-positive dimension */
-  Q4_ESHAPE = -2,      /* N/H/I not a multiple of 32, or M/T/topk/E out of range */
+  Q4_ESHAPE = -2,      /* N/H/I not a multiple of 32, or M/T/topk/E out of range (products of
+                          8-bit rows: K no multiple of 16, N of 8, or K out of range) */
   Q4_EALIGN = -3,      /* pointer misaligned (blocks 2 B, fp32/fp16 arrays 4 B, router x and
-                          Wr 16 B, ws 256 B) */
+                          Wr 16 B, operands of 8-bit products 16 B, ws 256 B) */
   Q4_EWORKSPACE = -4,  /* workspace missing or smaller than required */
   Q4_EHIP = -5,        /* the HIP runtime reported an error at launch */
   Q4_ETOOBIG = -6      /* a size exceeds the limits of the implementation */

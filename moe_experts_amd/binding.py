@@ -683,6 +683,7 @@ def q4_0_gemm_lora(X: torch.Tensor, B: torch.Tensor, N: int, A: torch.Tensor, Bl
 # ---------------------------------------------------------------------------
 #: Types of activations and results.
 I8_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_TOO_BIG = -6  # Q4_ETOOBIG
 
 
 def _type(dtype, name: str) -> int:
@@ -690,6 +691,13 @@ def _type(dtype, name: str) -> int:
     if a is None:
         raise TypeError(f"{name} must be one of {[str(d) for d in I8_TYPES]} (got {dtype})")
     return a
+
+
+def _ints(*sizes):
+    """Refuse sizes that are no C ints: the call would lose their upper bits and pass for another
+    shape."""
+    if max(sizes) > 0x7fffffff:
+        raise Q4Error(_TOO_BIG)
 
 
 def _call(f, index: int, *args):
@@ -704,21 +712,25 @@ def _call(f, index: int, *args):
 
 @functools.lru_cache(maxsize=1024)
 def i8_gemv_workspace_bytes(M: int, N: int, K: int) -> int:
+    _ints(M, N, K)
     return int(_lib.i8_gemv_workspace_bytes(M, N, K))
 
 
 @functools.lru_cache(maxsize=1024)
 def i8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    _ints(M, N, K)
     return int(_lib.i8_gemm_workspace_bytes(M, N, K))
 
 
 @functools.lru_cache(maxsize=1024)
 def i8_gemm_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    _ints(M, N, K)
     return int(_lib.i8_gemm_backward_workspace_bytes(M, N, K))
 
 
 @functools.lru_cache(maxsize=1024)
 def i8_gemm_backward_weight_workspace_bytes(M: int, N: int, K: int) -> int:
+    _ints(M, N, K)
     return int(_lib.i8_gemm_backward_weight_workspace_bytes(M, N, K))
 
 
@@ -731,6 +743,7 @@ def i8_gemm_plan(form: str, M: int, N: int, K: int):
     contraction; K steps of a split) by which the call `form` serves a shape."""
     if form not in I8_FORMS:
         raise ValueError(f"form must be one of {sorted(I8_FORMS)} (got {form!r})")
+    _ints(M, N, K)
     v = [_I() for _ in range(4)]
     _check(_lib.i8_gemm_plan(I8_FORMS[form], M, N, K, *[ctypes.byref(i) for i in v]))
     return tuple(i.value for i in v)
@@ -744,6 +757,7 @@ def i8_quantize(X: torch.Tensor, Q: torch.Tensor | None = None,
     if X.dim() != 2:
         raise ValueError("X must be [M, K]")
     M, K = X.shape
+    _ints(M, K)
     a = _type(X.dtype, "X's dtype")
     i = X.get_device()
     px = _ptr(X, "X", X.dtype, M * K, i)
@@ -768,6 +782,7 @@ def i8_dequantize(Q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = tor
     if Q.dim() != 2:
         raise ValueError("Q must be [M, K]")
     M, K = Q.shape
+    _ints(M, K)
     if X is not None:
         dtype = X.dtype
     a = _type(dtype, "dtype")
@@ -797,6 +812,7 @@ def i8_gemv(x: torch.Tensor, W: torch.Tensor, sw: torch.Tensor, y: torch.Tensor 
         raise ValueError("x must be [M, K]")
     M, K = x.shape
     N = _rows_columns(W, "W", K)
+    need = i8_gemv_workspace_bytes(M, N, K)
     i = x.get_device()
     px = _ptr(x, "x", torch.float32, M * K, i)
     pw = _ptr(W, "W", torch.int8, N * K, i)
@@ -806,7 +822,7 @@ def i8_gemv(x: torch.Tensor, W: torch.Tensor, sw: torch.Tensor, y: torch.Tensor 
         py = y.data_ptr()
     else:
         py = _ptr(y, "y", torch.float32, M * N, i)
-    _run(_lib.i8_gemv, i8_gemv_workspace_bytes(M, N, K), ws, i, px, pw, ps, py, M, N, K)
+    _run(_lib.i8_gemv, need, ws, i, px, pw, ps, py, M, N, K)
     return y
 
 
@@ -819,6 +835,7 @@ def i8_gemm(X: torch.Tensor, sx: torch.Tensor, W: torch.Tensor, sw: torch.Tensor
         raise ValueError("X must be [M, K]")
     M, K = X.shape
     N = _rows_columns(W, "W", K)
+    need = i8_gemm_workspace_bytes(M, N, K)
     if Y is not None:
         dtype = Y.dtype
     a = _type(dtype, "dtype")
@@ -832,7 +849,7 @@ def i8_gemm(X: torch.Tensor, sx: torch.Tensor, W: torch.Tensor, sw: torch.Tensor
         py = Y.data_ptr()
     else:
         py = _ptr(Y, "Y", dtype, M * N, i)
-    _run(_lib.i8_gemm, i8_gemm_workspace_bytes(M, N, K), ws, i, px, psx, pw, psw, py, a, M, N, K)
+    _run(_lib.i8_gemm, need, ws, i, px, psx, pw, psw, py, a, M, N, K)
     return Y
 
 
@@ -845,6 +862,7 @@ def i8_gemm_backward(dY: torch.Tensor, W: torch.Tensor, sw: torch.Tensor,
         raise ValueError("dY must be [M, N] and W [N, K]")
     M, N = dY.shape
     K = W.shape[1]
+    need = i8_gemm_backward_workspace_bytes(M, N, K)
     i = dY.get_device()
     pd = _ptr(dY, "dY", torch.bfloat16, M * N, i)
     pw = _ptr(W, "W", torch.int8, N * K, i)
@@ -854,8 +872,7 @@ def i8_gemm_backward(dY: torch.Tensor, W: torch.Tensor, sw: torch.Tensor,
         px = dX.data_ptr()
     else:
         px = _ptr(dX, "dX", torch.bfloat16, M * K, i)
-    _run(_lib.i8_gemm_backward, i8_gemm_backward_workspace_bytes(M, N, K), ws, i, pd, pw, ps, px,
-         M, N, K)
+    _run(_lib.i8_gemm_backward, need, ws, i, pd, pw, ps, px, M, N, K)
     return dX
 
 
@@ -868,6 +885,7 @@ def i8_gemm_backward_weight(dY: torch.Tensor, X: torch.Tensor, sx: torch.Tensor,
         raise ValueError("dY must be [M, N] and X [M, K]")
     M, N = dY.shape
     K = X.shape[1]
+    need = i8_gemm_backward_weight_workspace_bytes(M, N, K)
     i = dY.get_device()
     pd = _ptr(dY, "dY", torch.bfloat16, M * N, i)
     px = _ptr(X, "X", torch.int8, M * K, i)
@@ -877,6 +895,5 @@ def i8_gemm_backward_weight(dY: torch.Tensor, X: torch.Tensor, sx: torch.Tensor,
         pg = dW.data_ptr()
     else:
         pg = _ptr(dW, "dW", torch.bfloat16, N * K, i)
-    _run(_lib.i8_gemm_backward_weight, i8_gemm_backward_weight_workspace_bytes(M, N, K), ws, i,
-         pd, px, ps, pg, M, N, K)
+    _run(_lib.i8_gemm_backward_weight, need, ws, i, pd, px, ps, pg, M, N, K)
     return dW

@@ -195,10 +195,12 @@ const char* q4_strerror(int status) {
   switch (status) {
     case Q4_OK: return "success";
     case Q4_EINVAL: return "invalid argument: null pointer or non-positive dimension";
-    case Q4_ESHAPE: return "unsupported shape: N/H/I must be multiples of 32, M/T/topk/E within limits";
+    case Q4_ESHAPE:
+      return "unsupported shape: N/H/I must be multiples of 32, M/T/topk/E within limits (products "
+             "of 8-bit rows: K a multiple of 16, N of 8, within limits)";
     case Q4_EALIGN:
       return "misaligned pointer (blocks 2 B, fp32/fp16 arrays 4 B, router x and Wr 16 B, "
-             "workspace 256 B)";
+             "operands of 8-bit products 16 B, workspace 256 B)";
     case Q4_EWORKSPACE: return "workspace missing or too small";
     case Q4_EHIP: return "HIP runtime error at launch";
     case Q4_ETOOBIG: return "size exceeds implementation limits";
@@ -561,7 +563,7 @@ int i8_gemv(const float* x, const int8_t* W, const float* sw, float* y, int M, i
       q4::launch_i8_gemv(x, W, sw, y, M, N, K, ws, p, static_cast<hipStream_t>(stream)));
 }
 
-// Of the widest result: a workspace serves every type.
+// One size for all types of the result, also of a shape that fp32 results make too big.
 size_t i8_gemm_workspace_bytes(int M, int N, int K) {
   if (check_i8_shape(M, N, K, 2) != Q4_OK) return 0;
   return q4::plan_i8_gemm(M, N, K).ws_bytes;

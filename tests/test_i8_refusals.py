@@ -243,3 +243,53 @@ def test_a_gradient_that_would_be_lost_is_refused(monkeypatch):
             t.requires_grad_(False)
         call_()
         assert ran.pop()
+
+
+WIDE = (1 << 32) + 64  # loses its upper bits where a C int is taken
+
+
+@pytest.mark.parametrize("at", range(3))
+@pytest.mark.parametrize("name", VALID)
+def test_sizes_that_are_no_c_ints(name, at):
+    """Not the shape that their lower 32 bits would be."""
+    import tests.built  # noqa: F401  (binding loads the library)
+    from moe_experts_amd import binding
+    sizes = [64, 64, 64]
+    sizes[at] = WIDE
+    with pytest.raises(binding.Q4Error) as e:
+        getattr(binding, name + "_workspace_bytes")(*sizes)
+    assert e.value.status == EBIG
+    if name in binding.I8_FORMS:
+        with pytest.raises(binding.Q4Error) as e:
+            binding.i8_gemm_plan(name, *sizes)
+        assert e.value.status == EBIG
+
+
+def test_tensors_whose_sizes_are_no_c_ints():
+    """Tensors without memory: the sizes are refused first."""
+    import tests.built  # noqa: F401
+    from moe_experts_amd import binding as b
+
+    def t(rows, cols, dtype):
+        return torch.empty((rows, cols) if cols else (rows,), dtype=dtype, device="meta")
+
+    i8, f32, f16, bf16 = torch.int8, torch.float32, torch.float16, torch.bfloat16
+    for m, k in ((WIDE, 1), (1, WIDE)):
+        with pytest.raises(b.Q4Error) as e:
+            b.i8_quantize(t(m, k, f16))
+        assert e.value.status == EBIG
+        with pytest.raises(b.Q4Error) as e:
+            b.i8_dequantize(t(m, k, i8), t(m, 0, f32))
+        assert e.value.status == EBIG
+    for at in range(3):
+        s = [1, 8, 16]
+        s[at] = WIDE
+        M, N, K = s
+        sx, sw = t(M, 0, f32), t(N, 0, f32)
+        for call in (lambda: b.i8_gemv(t(M, K, f32), t(N, K, i8), sw),
+                     lambda: b.i8_gemm(t(M, K, i8), sx, t(N, K, i8), sw),
+                     lambda: b.i8_gemm_backward(t(M, N, bf16), t(N, K, i8), sw),
+                     lambda: b.i8_gemm_backward_weight(t(M, N, bf16), t(M, K, i8), sx)):
+            with pytest.raises(b.Q4Error) as e:
+                call()
+            assert e.value.status == EBIG
