@@ -14,6 +14,9 @@ namespace q4 {
 
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 typedef int int16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 
@@ -150,6 +153,88 @@ __device__ __forceinline__ uint32_t workgroup_max(uint32_t v, uint32_t* at) {
     for (int w = 1; w < THREADS / kWaveSize; ++w) v = max(v, at[w]);
   }
   return v;
+}
+
+// The largest of a wave's values of eight columns, dealt out to the lanes while they are
+// reduced: with lanes a multiple of STRIDE apart holding values of the same columns, lanes
+// below 8 * STRIDE end with a column each in v[0], the one that is returned.
+template <int STRIDE>
+__device__ __forceinline__ int wave_max_of_eight(uint32_t (&v)[8]) {
+  const int lane = threadIdx.x & 63;
+  int e = 0;
+#pragma unroll
+  for (int half = 4, o = STRIDE; half > 0; half >>= 1, o <<= 1) {
+    const bool up = lane & o;
+    e += up ? half : 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const uint32_t keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
+      v[i] = max(keep, (uint32_t)__shfl_xor((int)send, o));
+    }
+  }
+#pragma unroll
+  for (int o = 8 * STRIDE; o < kWaveSize; o <<= 1)
+    v[0] = max(v[0], (uint32_t)__shfl_xor((int)v[0], o));
+  return e;
+}
+
+// Eight values as they stand in memory (aligned to one value). Kept so, 16-bit types take half
+// the registers.
+template <int TYPE>
+struct Piece {
+  typedef typename Val<TYPE>::T T;
+  static constexpr int kWords = sizeof(T) * 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* __restrict__ p) { __builtin_memcpy(w, p, sizeof(w)); }
+  // Keeps the compiler from holding the values converted from one use to the next.
+  __device__ __forceinline__ void fresh() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(T) == 4)
+      return __builtin_bit_cast(float, w[e]);
+    else if constexpr (TYPE == Q4_TYPE_BF16)
+      return __builtin_bit_cast(float, e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    else
+      return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[e / 2] >> (16 * (e & 1))));
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Left operands of the gradients. A product dY * scale is rounded to fp16 once: 2^-12 of
+// itself, where bf16 would take 2^-9, as much as the result's own rounding. Gradients lie
+// far below fp16's range, so the values that one sum adds are scaled together by a power
+// of two (exact) that takes the largest of them to 2^13..2^14; the sum is scaled back.
+// ---------------------------------------------------------------------------
+struct PowerOfTwo {
+  float up, down;
+};
+__device__ __forceinline__ PowerOfTwo to_fp16_range(uint32_t big) {
+  // zeros, infinities and NaN stay as they are
+  const bool plain = big == 0 || big >= 0x7f800000u;
+  const int e = plain ? 0 : min(126, 13 + 127 - (int)(big >> 23));
+  PowerOfTwo p;
+  p.up = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
+  p.down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+  return p;
+}
+
+// Eight int8 as halves, exactly: with the sign bit turned, a byte behind 0x64 is the half
+// 1024 + 128 + q.
+__device__ __forceinline__ half8 to_halves(int2v q) {
+  uint32_t h[4];
+  const half2v off = {(_Float16)1152.0f, (_Float16)1152.0f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = (uint32_t)q[i] ^ 0x80808080u;
+    h[2 * i] = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
+    h[2 * i + 1] = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, h[i]) - off);
+  return __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
 }
 
 }  // namespace q4

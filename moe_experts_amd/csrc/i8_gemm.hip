@@ -249,7 +249,11 @@ constexpr I8Tile kTiles[] = {{256, 192, 0.90, 0.90, 0.50},
 I8Plan plan_i8_gemm(int M, int N, int K) {
   I8Plan p{};
   p.strip = M <= kI8FewRows;
-  if (p.strip) return p;
+  if (p.strip) {
+    p.S = 1;
+    p.kper = (K + 127) / 128;
+    return p;
+  }
   plan_i8_tiles(p, kTiles, M, N, (K + kStepBytes - 1) / kStepBytes);
   if (p.S > 1) p.ws_bytes = (size_t)p.S * M * N * sizeof(int32_t);
   return p;

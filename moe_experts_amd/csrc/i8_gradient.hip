@@ -24,8 +24,6 @@
 namespace q4 {
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr int BK = kStepBytes / 2;  // of the contraction in a step
@@ -69,21 +67,6 @@ struct ByteCopy {
              live ? off + (uint32_t)(i * (THREADS / kChunks)) * pitch : kPastEnd, so);
   }
 };
-
-__device__ __forceinline__ half8 to_halves(int2v q) {
-  uint32_t h[4];
-  const half2v off = {(_Float16)1152.0f, (_Float16)1152.0f};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t u = (uint32_t)q[i] ^ 0x80808080u;
-    h[2 * i] = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
-    h[2 * i + 1] = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, h[i]) - off);
-  return __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
-}
 
 template <int BM, int BN, int WM, int WN, int NS, bool WHOLE>
 __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs g) {
@@ -339,6 +322,8 @@ hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* 
 }
 
 I8Plan plan_i8_backward_weight(int M, int N, int K) {
+  I8Plan p{};
+  if (plan_i8_few_channels(p, M, N, K)) return p;
   return plan_gradient(N, K, M, i8_max_chunks(M, N));
 }
 
@@ -346,6 +331,8 @@ hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const 
                                      uint16_t* dW, int M, int N, int K, void* ws, const I8Plan& p,
                                      hipStream_t st) {
   uint8_t* w = static_cast<uint8_t*>(ws);
+  if (p.strip)
+    return launch_i8_few_channels(dY, X, sx, dW, M, N, K, reinterpret_cast<float*>(w), p, st);
   const hipError_t err = launch_i8_gradient_columns(
       dY, sx, reinterpret_cast<uint16_t*>(w + p.off_a), reinterpret_cast<float*>(w + p.off_rs),
       reinterpret_cast<uint32_t*>(w + p.off_max), M, N, p.ld, st);

@@ -34,7 +34,7 @@ hipError_t launch_i8_gemv(const float* x, const int8_t* W, const float* sw, floa
 // Result [rows][cols] by tiles of BM x BN, K steps of 128 bytes of the left operand, S splits of
 // the contraction (32-bit partial sums [S][rows][cols] in ws).
 struct I8Plan {
-  bool strip;      // i8_gemm: few rows
+  bool strip;      // few rows of the result, by a kernel of their own (BM is 0)
   int tile;        // of those compiled
   int BM, BN;
   int tiles_m, tiles_n;
@@ -104,6 +104,13 @@ hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const 
                                      uint16_t* dW, int M, int N, int K, void* ws, const I8Plan& p,
                                      hipStream_t st);
 
+// ---- few output channels (i8_channels.hip) --------------------------------------
+// Plans the weights' gradient of up to 16 output channels; false: by tiles.
+bool plan_i8_few_channels(I8Plan& p, int M, int N, int K);
+hipError_t launch_i8_few_channels(const uint16_t* dY, const int8_t* X, const float* sx,
+                                  uint16_t* dW, int M, int N, int K, float* part, const I8Plan& p,
+                                  hipStream_t st);
+
 // ---- left operands of the gradients, sums of splits (i8_rows.hip) --------------
 // a[m][n] = fp16(dY[m][n] * sw[n] * 2^e), n < ld (zero past N), rs[m] = 2^-e
 hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs,
@@ -115,6 +122,7 @@ hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint1
                                       uint32_t* big, int M, int N, int ld, hipStream_t st);
 hipError_t launch_i8_finish(const int32_t* part, const float* sx, const float* sw, void* Y,
                             int type, int M, int N, int S, hipStream_t st);
+// rs may be null: sums as they are
 hipError_t launch_i8_gradient_finish(const float* part, const float* rs, uint16_t* out, int rows,
                                      int cols, int S, hipStream_t st);
 

@@ -21,37 +21,12 @@
 namespace q4 {
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kRowThreads = 256;
 constexpr int kFewRows = 256;       // rows by wider workgroups: no more than one a CU
 constexpr int kMaxGrid = 1 << 20;  // workgroups; each takes every kMaxGrid-th row after its own
 
 int row_grid(long long n) { return (int)std::min<long long>(n, kMaxGrid); }
-
-// Eight values as they stand in memory (aligned to one value). Kept so, 16-bit types take half
-// the registers.
-template <int TYPE>
-struct Piece {
-  typedef typename Val<TYPE>::T T;
-  static constexpr int kWords = sizeof(T) * 2;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void load(const T* __restrict__ p) { __builtin_memcpy(w, p, sizeof(w)); }
-  // Keeps the compiler from holding the values converted from one use to the next.
-  __device__ __forceinline__ void fresh() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
-  }
-  __device__ __forceinline__ float operator[](int e) const {
-    if constexpr (sizeof(T) == 4)
-      return __builtin_bit_cast(float, w[e]);
-    else if constexpr (TYPE == Q4_TYPE_BF16)
-      return __builtin_bit_cast(float, e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-    else
-      return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[e / 2] >> (16 * (e & 1))));
-  }
-};
 
 // One workgroup a row of at least eight values. V pieces of eight a lane stay in registers
 // between the search for the largest and the rounding; LOOP reads longer rows twice. A piece
@@ -155,25 +130,6 @@ __global__ __launch_bounds__(kRowThreads) void i8_dequantize_short_kernel(
     X[i] = Val<TYPE>::put((float)Q[i] * scale[i / K]);
 }
 
-// ---------------------------------------------------------------------------
-// Left operands of the gradients. A product dY * scale is rounded to fp16 once: 2^-12 of
-// itself, where bf16 would take 2^-9, as much as the result's own rounding. Gradients lie
-// far below fp16's range, so the values that one sum adds are scaled together by a power
-// of two (exact) that takes the largest of them to 2^13..2^14; the sum is scaled back.
-// ---------------------------------------------------------------------------
-struct PowerOfTwo {
-  float up, down;
-};
-__device__ __forceinline__ PowerOfTwo to_fp16_range(uint32_t big) {
-  // zeros, infinities and NaN stay as they are
-  const bool plain = big == 0 || big >= 0x7f800000u;
-  const int e = plain ? 0 : min(126, 13 + 127 - (int)(big >> 23));
-  PowerOfTwo p;
-  p.up = __builtin_bit_cast(float, (uint32_t)(127 + e) << 23);
-  p.down = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
-  return p;
-}
-
 // One workgroup a row of dY; N and ld are multiples of 8.
 template <int THREADS, int V, bool LOOP>
 __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
@@ -270,21 +226,8 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 8; ++e) big[e] = max(big[e], magnitude(value(p, h, e)));
-  // The eight columns are dealt out to the lanes of each eight while they are reduced: ten
-  // exchanges instead of 48. Lane l ends with column e = l's bits 0, 1, 2 from the highest.
-#pragma unroll
-  for (int o = 1, half = 4; o < 8; o <<= 1, half >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const uint32_t keep = up ? big[i + half] : big[i], send = up ? big[i] : big[i + half];
-      big[i] = max(keep, (uint32_t)__shfl_xor((int)send, o));
-    }
-  }
-#pragma unroll
-  for (int o = 8; o < kWaveSize; o <<= 1)
-    big[0] = max(big[0], (uint32_t)__shfl_xor((int)big[0], o));
-  if (lane < 8) at[wave][(lane & 1) * 4 + (lane & 2) + (lane >> 2)] = big[0];
+  const int e = wave_max_of_eight<1>(big);
+  if (lane < 8) at[wave][e] = big[0];
   __syncthreads();
   if (t < kWaveSize) {  // wave 0: lane l column l % 8 of every eighth wave
     uint32_t b = 0;
@@ -305,7 +248,6 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
     const float up = factor[e];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      typedef _Float16 half2v __attribute__((ext_vector_type(2)));
       const int m = 2 * (p * THREADS + t);  // ld is even
       if (m < ld)
         *reinterpret_cast<half2v*>(a + (size_t)(n + e) * ld + m) =
@@ -401,8 +343,7 @@ __global__ __launch_bounds__(kRowThreads) void i8_gradient_columns_kernel(
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-        half2v h;
+          half2v h;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           h[j] = m0 + 2 * ((p + i) * kRowLanes + r) + j < M
@@ -461,7 +402,7 @@ __global__ __launch_bounds__(kRowThreads) void i8_gradient_finish_kernel(
   const size_t i = ((size_t)blockIdx.x * kRowThreads + threadIdx.x) * 4;
   if (i >= mn) return;
   const float4v v = sum_splits(reinterpret_cast<const float4v*>(part + i), mn / 4, S);
-  const float s = rs[i / cols];
+  const float s = rs ? rs[i / cols] : 1.0f;
   uint16_t y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = (uint16_t)i8_to_bf16(v[e] * s);

@@ -40,17 +40,6 @@ struct StripArgs {
   int blocks;
 };
 
-// A barrier for LDS alone: copies from memory stay in flight over it.
-__device__ __forceinline__ void lds_only_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 // Fused: all of x in registers, the largest of each row by LDS, int8 into xq, rows `pitch`
 // bytes apart.
 struct FusedRows {

@@ -629,10 +629,10 @@ int i8_gemm_plan(int form, int M, int N, int K, int* rows, int* cols, int* split
   const q4::I8Plan p = form == Q4_I8_GEMM            ? q4::plan_i8_gemm(M, N, K)
                        : form == Q4_I8_GEMM_BACKWARD ? q4::plan_i8_backward(M, N, K)
                                                      : q4::plan_i8_backward_weight(M, N, K);
-  *rows = p.strip ? 0 : p.BM;
-  *cols = p.strip ? 0 : p.BN;
-  *splits = p.strip ? 1 : p.S;
-  *steps = p.strip ? (K + 127) / 128 : p.kper;
+  *rows = p.BM;
+  *cols = p.BN;
+  *splits = p.S;
+  *steps = p.kper;
   return Q4_OK;
 }
 

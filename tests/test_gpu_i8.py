@@ -332,6 +332,63 @@ def test_backward_weight_of_many_tokens():
     ref.check_norm(got, want[0])
 
 
+#: lengths around a pair, a step, what a wave, a lane and a workgroup take, and splits
+FEW_TOKENS = [1, 2, 31, 32, 33, 255, 257, 511, 512, 513, 1023, 1025, 1999, 2047, 2048, 2049, 4095,
+              4096, 4097, 6001, 32769]
+
+
+@pytest.mark.parametrize("N", [8, 16])
+@pytest.mark.parametrize("M", FEW_TOKENS)
+def test_backward_weight_of_few_channels(M, N):
+    from moe_experts_amd import (i8_gemm_backward_weight,
+                                 i8_gemm_backward_weight_workspace_bytes)
+    K = (16, 48, 64, 80, 208)[M % 5]
+    dY, X, sx = gradient(90, M, N), int8(91, M, K, low=-128), scales(92, M)
+    full, dW = guarded(N * K, torch.bfloat16, fill=7.0)
+    need = i8_gemm_backward_weight_workspace_bytes(M, N, K)
+    wfull, ws = guarded_ws(need, fill=0xFF)
+    i8_gemm_backward_weight(dY, to_dev(X), to_dev(sx), dW=dW.view(N, K), ws=ws)
+    want = ref.backward_weight(host(dY), X, sx)
+    ref.check(host(dW.view(N, K)), want)
+    ref.check_norm(host(dW.view(N, K)), want[0])
+    assert guards_intact(full, N * K, fill=7.0) and ws_guards_intact(wfull, need, fill=0xFF)
+
+
+@pytest.mark.parametrize("N", [8, 16])
+@pytest.mark.parametrize("M", [70, 9000])
+def test_few_channels_of_far_sizes(M, N):
+    """Channels of any size beside one another; tokens whose size falls by 2^40 on the way, so that
+    splits scale by powers of their own; a channel of zeros."""
+    from moe_experts_amd import i8_gemm_backward_weight
+    K = 80
+    r = datagen.rng(93)
+    X, sx = int8(94, M, K), scales(95, M)
+    size = 2.0 ** np.linspace(-60, 90, N)
+    size[5] = 0
+    fall = 2.0 ** np.linspace(0, -40, M)[:, None]
+    dY = typed(r.standard_normal((M, N)) * size * fall, "bf16")
+    got = host(i8_gemm_backward_weight(dY, to_dev(X), to_dev(sx)))
+    ref.check(got, ref.backward_weight(host(dY), X, sx))
+    assert not got[5].any()
+
+
+@pytest.mark.parametrize("N", [8, 16])
+@pytest.mark.parametrize("M", [70, 9000])
+def test_few_broken_channels_stay_alone(M, N):
+    from moe_experts_amd import i8_gemm_backward_weight
+    K = 272
+    dY, X, sx = gradient(96, M, N), to_dev(int8(97, M, K)), scales(98, M)
+    was = i8_gemm_backward_weight(dY, X, to_dev(sx))
+    broken = dY.clone()
+    broken[3, 6], broken[M - 1, 1] = float("inf"), float("nan")
+    got = i8_gemm_backward_weight(broken, X, to_dev(sx))
+    keep = [n for n in range(N) if n not in (1, 6)]
+    assert not torch.isfinite(got[[1, 6]].float()).any()
+    assert torch.equal(got[keep], was[keep])
+    sx[M - 2] = np.nan
+    assert torch.isnan(i8_gemm_backward_weight(dY, X, to_dev(sx)).float()).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(7, 24, 48), (64, 1032, 272), (150, 2048, 512), (300, 520, 4112),
                                    (4200, 136, 4112)])
 def test_gradients_pick_single_values(M, N, K):

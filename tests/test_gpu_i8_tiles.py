@@ -1,4 +1,5 @@
-"""Every tile of the 8-bit products and gradients by i8_gemm_plan: with and without splits, odd
+"""Every tile of the 8-bit products and gradients by i8_gemm_plan, and the kernel of few output
+channels: with and without splits, odd
 and even numbers of K steps, fewer steps than stages, half-full last tiles. Products exactly;
 gradients exactly where one term makes a value, and by their norm where all do."""
 import numpy as np
@@ -36,7 +37,10 @@ WEIGHT = [(17, 16, 8), (65, 16, 8), (130, 16, 8), (200, 16, 8), (257, 16, 8), (1
           (2050, 16, 1000), (2500, 16, 520), (3100, 16, 1544),
           (17, 144, 8200), (65, 144, 8200), (130, 144, 8200), (200, 144, 8200), (257, 144, 8200),
           (2050, 16, 1544), (2050, 16, 3080), (4200, 16, 2056),
-          (17, 32784, 8), (65, 11008, 264), (130, 272, 11008), (200, 272, 11008), (257, 400, 8200)]
+          (17, 32784, 8), (65, 11008, 264), (130, 272, 11008), (200, 272, 11008), (257, 400, 8200),
+          (64, 16, 24), (65, 16, 24), (400, 16, 24), (1700, 16, 24), (2500, 16, 24), (17, 32784, 24),
+          (4097, 144, 8), (4200, 144, 8), (2048, 4096, 16), (2049, 4096, 16), (9000, 1040, 16),
+          (40000, 80, 16), (40000, 80, 8), (140000, 16, 8), (66000, 144, 16)]
 SHAPES = {"i8_gemm": GEMM, "i8_gemm_backward": BACKWARD, "i8_gemm_backward_weight": WEIGHT}
 
 
@@ -49,8 +53,9 @@ def plan(form, M, K, N):
 def test_the_shapes_reach_every_tile(form):
     got = {(r, c, s > 1, steps % 2) for r, c, s, steps in (plan(form, *m) for m in SHAPES[form])}
     tiles = {(r, c) for r, c, _, _ in got}
-    want = {"i8_gemm": {(32, 64), (64, 64), (64, 128), (128, 128), (128, 256), (256, 192)}}.get(
-        form, {(32, 128), (64, 128), (128, 128), (128, 256)})
+    gradient = {(32, 128), (64, 128), (128, 128), (128, 256)}
+    want = {"i8_gemm": {(32, 64), (64, 64), (64, 128), (128, 128), (128, 256), (256, 192)},
+            "i8_gemm_backward": gradient, "i8_gemm_backward_weight": gradient | {(0, 0)}}[form]
     assert tiles == want
     for tile in tiles:
         for split in (False, True):
