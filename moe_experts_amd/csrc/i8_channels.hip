@@ -71,13 +71,14 @@ __global__ __launch_bounds__(kThreads) void i8_few_channels_kernel(ChannelArgs g
   float s[P][2];
 #pragma unroll
   for (int p = 0; p < P; ++p)
-    if (2 * p * kLanes < left)  // uniform
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int m = m0 + min(2 * (p * kLanes + pair) + h, left - 1);
-        v[p][h].load(g.dY + (size_t)m * N + 8 * half);
-        s[p][h] = g.sx[m];
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int m = m0 + min(2 * (p * kLanes + pair) + h, left - 1);
+      v[p][h].load(g.dY + (size_t)m * N + 8 * half);
+      s[p][h] = g.sx[m];
+    }
+  asm volatile("" ::: "memory");  // the copies below stay below
+  __builtin_amdgcn_sched_barrier(0);
 
   // Copies: four lanes a row of 64 bytes. Rows past M are past the end and become zeros, rows
   // of the next split meet zeros of dY, columns past K are not kept; steps past the last copy
@@ -95,17 +96,27 @@ __global__ __launch_bounds__(kThreads) void i8_few_channels_kernel(ChannelArgs g
 #pragma unroll
   for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
 
-  auto value = [&](int p, int h, int e) {
-    return 2 * (p * kLanes + pair) + h < left ? v[p][h][e] * s[p][h] : 0.0f;
-  };
-  uint32_t most[8] = {};
+  // Rows past the last are the last times zero: zeros, or a NaN in a channel that holds an
+  // infinity or a NaN there and so has no finite result. fmaxf passes over NaN: what a channel
+  // with one is scaled by does not matter.
+  float x[P][2][8];
+  float largest[8] = {};
 #pragma unroll
   for (int p = 0; p < P; ++p)
-    if (2 * p * kLanes < left)
+    if (2 * p * kLanes < left) {  // uniform
 #pragma unroll
       for (int h = 0; h < 2; ++h)
+        if (2 * (p * kLanes + pair) + h >= left) s[p][h] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most[e] = max(most[e], magnitude(value(p, h, e)));
+      for (int e = 0; e < 8; ++e) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[p][h][e] = v[p][h][e] * s[p][h];
+        largest[e] = fmaxf(fmaxf(largest[e], fabsf(x[p][0][e])), fabsf(x[p][1][e]));
+      }
+    }
+  uint32_t most[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) most[e] = magnitude(largest[e]);
   const int col = wave_max_of_eight<kPieces>(most);
   if (lane < N) big[wave][8 * half + col] = most[0];
   lds_only_barrier();
@@ -125,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void i8_few_channels_kernel(ChannelArgs g
       for (int e = 0; e < 8; ++e) {
         const float f = up[8 * half + e];
         *reinterpret_cast<half2v*>(a + (8 * half + e) * kPitch + 4 * (p * kLanes + pair)) =
-            half2v{(_Float16)(value(p, 0, e) * f), (_Float16)(value(p, 1, e) * f)};
+            half2v{(_Float16)(x[p][0][e] * f), (_Float16)(x[p][1][e] * f)};
       }
   lds_only_barrier();
 
