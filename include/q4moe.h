@@ -458,7 +458,7 @@ int i8_gemv(const float* x, const int8_t* W, const float* sw, float* y, int M, i
 
 /* Any number of rows: Y[m][n] = sx[m] * sw[n] * sum_k X[m][k] * W[n][k].
  *   X int8 [M][K], sx fp32 [M]     W int8 [N][K], sw fp32 [N]
- *   Y fp32, fp16 or bf16 [M][N] by `type`, formed in fp32 and rounded once */
+ *   Y fp32, fp16 or bf16 [M][N] by `type`, formed in fp32 as (sum * sx) * sw and rounded once */
 size_t i8_gemm_workspace_bytes(int M, int N, int K);
 int i8_gemm(const int8_t* X, const float* sx, const int8_t* W, const float* sw, void* Y, int type,
             int M, int N, int K, void* ws, size_t ws_bytes, void* stream);
@@ -468,8 +468,9 @@ int i8_gemm(const int8_t* X, const float* sx, const int8_t* W, const float* sw, 
  *   dY bf16 [M][N]     dX bf16 [M][K]
  * (quantizing passes it on unchanged). The products dY * sw of a row are scaled together
  * by a power of two to the range of fp16 and rounded to it, and the sum, in fp32, is scaled
- * back, so gradients need no loss scale. A row of dY with an infinity or a NaN has results
- * that are not finite, in every column; other rows are not touched by it. */
+ * back, so gradients need no loss scale. A row of dY with an infinity or a NaN, also one that
+ * a product dY * sw past fp32's range makes, has results that are not finite, in every
+ * column; other rows are not touched by it. */
 size_t i8_gemm_backward_workspace_bytes(int M, int N, int K);
 int i8_gemm_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint16_t* dX, int M,
                      int N, int K, void* ws, size_t ws_bytes, void* stream);
@@ -478,8 +479,8 @@ int i8_gemm_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint1
  * forward pass:
  *   dW[n][k] = sum_m dY[m][n] * sx[m] * X[m][k]
  *   dY bf16 [M][N]     X int8 [M][K], sx fp32 [M]     dW bf16 [N][K], overwritten
- * The products dY * sx of a column of dY are scaled and rounded as i8_gemm_backward does
- * those of a row. A column of dY with an infinity or a NaN has a row of dW that is not
+ * The products dY * sx of a column of dY (with up to 16 output channels: of a part of its
+ * rows) are scaled and rounded as i8_gemm_backward does those of a row. A column of dY with an infinity or a NaN has a row of dW that is not
  * finite; a token whose scale is a NaN leaves nothing finite. */
 size_t i8_gemm_backward_weight_workspace_bytes(int M, int N, int K);
 int i8_gemm_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx, uint16_t* dW,
@@ -487,7 +488,8 @@ int i8_gemm_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx
 
 /* Which kernel serves a shape of them (for inspection and tests; host arithmetic only).
  * form: whose call; M, N, K: as in it.
- *   rows, cols  of a tile of the result; rows is 0 for the kernel of few rows
+ *   rows, cols  of a tile of the result; 0 for the kernels of few rows (i8_gemm: M <= 16) and
+ *               of few output channels (the weights' gradient: N <= 16)
  *   splits      workgroups that share the contraction of a tile, 1 for none
  *   steps       K steps of a split (128 of i8_gemm's contraction, 64 of a gradient's)
  * Fails as the call does for M, N and K; Q4_EINVAL for another form or a null pointer. */

@@ -2,13 +2,21 @@
 //   dW[n][k] = sum_m (dY[m][n] * sx[m]) * X[m][k]
 // in one kernel. dY is little and X is much: a workgroup owns 64 columns of X, whose rows are on
 // their way into LDS while it makes its left operand: all of dY * sx, scaled column by column
-// and rounded to fp16 as for the tiles, transposed in LDS. Its eight waves then share out the
-// rows: each multiplies steps of 32 by v_mfma_f32_16x16x32_f16, copied memory -> LDS several
-// steps ahead into a part of its own, and their sums meet in LDS, in the order of the waves.
+// and rounded to fp16 as for the tiles, transposed in LDS. Its waves then share out the rows:
+// each multiplies steps of 32 by v_mfma_f32_16x16x32_f16, copied memory -> LDS several steps
+// ahead into a part of its own, and their sums meet in LDS, in the order of the waves.
 //
-// More rows than fit LDS are split over workgroups. Each split scales by the power of two of
-// its own rows and takes it back (exact), so splits are sums of their own, added in their
-// order by a second kernel.
+// Up to 2048 rows (4096 of eight channels) fit a workgroup of eight waves; more are split over
+// workgroups of four waves and half as many rows, two of which fit a CU. Each split scales by
+// the power of two of its own rows and takes it back (exact), so splits are sums of their own,
+// added in their order by a second kernel.
+//
+// What bounds it: rank 16 of 1999 rows of 11008 9.3 us, of which X takes 4.4 at a large copy's
+// rate; the rest is the start, dY's way from memory and its 32768 values' conversion (a
+// microsecond on a CU's four units), which the copies in flight only hide as far as they fit
+// LDS. By a transposing kernel and the tiles: 15.8. Rank 16 of 8192 rows of 4096 12.9 us by four
+// waves, 12.7 by eight, of 11008 27.8 and 29.2 (tiles 20.3 and 29.8), of 4096 rows of 4096 9.5
+// and 10.7 (14.6); of a row 5.3 (6.5). Past 64 splits the tiles take over.
 #include <algorithm>
 
 #include "i8_device.hpp"
@@ -19,13 +27,12 @@ namespace q4 {
 namespace {
 
 
-constexpr int kWaves = 8, kThreads = kWaves * kWaveSize;
 constexpr int kCols = 64;               // of X, a workgroup
 constexpr int kStepRows = 32;           // of X, a step of a wave
 constexpr int kStepCopy = kStepRows * kCols;
 constexpr int NS = 5;                   // steps of a wave in LDS
-constexpr int kValues = 32768;          // of dY in LDS: 64 KiB
-constexpr int kMaxSplits = 32;
+constexpr int kWaveValues = 4096;       // of dY in LDS, a wave
+constexpr int kMaxSplits = 64;
 
 struct ChannelArgs {
   const uint16_t* dY;
@@ -40,9 +47,11 @@ struct ChannelArgs {
 // read at once, 16 of one chunk, meet no bank twice.
 __device__ __forceinline__ int swz_step(int k) { return 2 * ((k >> 2) & 1) + ((k >> 3) & 1); }
 
-template <int N>  // output channels, 8 or 16
-__global__ __launch_bounds__(kThreads) void i8_few_channels_kernel(ChannelArgs g) {
-  constexpr int kRows = kValues / N;      // of dY
+// N: output channels, 8 or 16
+template <int N, int kWaves>
+__global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_channels_kernel(ChannelArgs g) {
+  constexpr int kThreads = kWaves * kWaveSize;
+  constexpr int kRows = kWaves * kWaveValues / N;  // of dY
   constexpr int kPitch = kRows * 2 + 16;  // bytes of a channel in LDS
   constexpr int kPieces = N / 8;          // of a row of dY
   constexpr int kLanes = kThreads / kPieces;
@@ -205,21 +214,21 @@ __global__ __launch_bounds__(kThreads) void i8_few_channels_kernel(ChannelArgs g
       make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
 }
 
-template <int N>
+template <int N, int WAVES>
 void launch(const ChannelArgs& g, hipStream_t st) {
-  hipLaunchKernelGGL(i8_few_channels_kernel<N>, dim3((unsigned)(g.tiles * g.S)), dim3(kThreads), 0,
-                     st, g);
+  hipLaunchKernelGGL((i8_few_channels_kernel<N, WAVES>), dim3((unsigned)(g.tiles * g.S)),
+                     dim3(WAVES * kWaveSize), 0, st, g);
 }
 
 }  // namespace
 
 bool plan_i8_few_channels(I8Plan& p, int M, int N, int K) {
   if (N > 16) return false;
-  const int most = kValues / N;
-  const int S = (M + most - 1) / most;
-  if (S > kMaxSplits) return false;
+  const int most = 4 * kWaveValues / N;
+  if (M > kMaxSplits * most) return false;
+  const int S = M <= 2 * most ? 1 : (M + most - 1) / most;
   p.strip = true;
-  p.kper = ((M + S - 1) / S + 63) / 64;  // of 64 rows, at most `most`
+  p.kper = ((M + S - 1) / S + 63) / 64;  // of 64 rows, at most what a workgroup takes
   p.S = (M + p.kper * 64 - 1) / (p.kper * 64);
   if (p.S > 1) p.ws_bytes = (size_t)p.S * N * K * sizeof(float);
   return true;
@@ -230,9 +239,9 @@ hipError_t launch_i8_few_channels(const uint16_t* dY, const int8_t* X, const flo
                                   hipStream_t st) {
   const ChannelArgs g{dY, sx, X, dW, part, M, K, (K + kCols - 1) / kCols, p.S, p.kper * 64};
   if (N == 8)
-    launch<8>(g, st);
+    p.S == 1 ? launch<8, 8>(g, st) : launch<8, 4>(g, st);
   else
-    launch<16>(g, st);
+    p.S == 1 ? launch<16, 8>(g, st) : launch<16, 4>(g, st);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;
   return launch_i8_gradient_finish(part, nullptr, dW, N, K, p.S, st);

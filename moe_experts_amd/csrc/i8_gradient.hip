@@ -14,7 +14,7 @@
 // What bounds it: 2048 rows of 4096 x 11008 take 181 us for the input (1.02 PFLOP/s) and 190 for
 // the weights, of which the matrix cores need 75 at the peak clock; the power limit holds it at
 // 1.5 to 1.7 GHz as for a plain bf16 product, whose library form takes 182 us at this
-// size. The row kernels in front take 21 and 28 us, at 4.3 and 4.8 TB/s of what they move.
+// size. The row kernels in front take 22 and 27 us, at 4.1 and 5.0 TB/s of what they move.
 #include <algorithm>
 
 #include "i8_device.hpp"
@@ -252,9 +252,9 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 // Tiles, measured (us, the product alone): 11008 x 4096 results over 2048: 128 x 256 190,
 // 128 x 128 197; 2048 x 4096 over 11008: 181, 192; 1536 x 5120 over 777: 26.2, 24.6; 150 x 11008
 // over 4096: 128 x 128 34, 64 x 128 36, 32 x 128 27; 130 x 4096 over 4096: 19.4 and 18.5 and
-// 16.6 in 3, 2 and 3 splits; 16 x 11008 over 1999: 32 x 128 in 2 splits 10.0. Of 256 x 256
-// no more than of 128 x 256: 192 and 181 (in 2 splits). Two stages do better than more where
-// two workgroups fit a CU by that: 128 x 256 in 3 stages 219 instead of 190.
+// 16.6 in 3, 2 and 3 splits. Of 256 x 256 no more than of 128 x 256: 192 and 181 (in 2 splits).
+// Two stages do better than more where two workgroups fit a CU by that: 128 x 256 in 3 stages
+// 219 instead of 190.
 constexpr I8Tile kTiles[] = {{128, 256, 0.80, 0.72, 0.25},
                              {128, 128, 0.30, 0.28, 0.27},
                              {64, 128, 0.26, 0.20, 0.12},
