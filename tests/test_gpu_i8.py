@@ -389,6 +389,55 @@ def test_few_broken_channels_stay_alone(M, N):
     assert torch.isnan(i8_gemm_backward_weight(dY, X, to_dev(sx)).float()).all()
 
 
+@pytest.mark.parametrize("N", [8, 24, 64, 1000, 2040, 2048, 2056, 4096, 4104, 6008, 16392])
+@pytest.mark.parametrize("M", [1, 7, 8, 9, 15, 16])
+def test_backward_of_few_rows(M, N):
+    from moe_experts_amd import i8_gemm_backward, i8_gemm_backward_workspace_bytes
+    K = (16, 48, 64, 80, 208)[(M + N // 8) % 5]
+    dY, W, sw = gradient(100, M, N), int8(101, N, K, low=-128), scales(102, N)
+    full, dX = guarded(M * K, torch.bfloat16, fill=7.0)
+    need = i8_gemm_backward_workspace_bytes(M, N, K)
+    wfull, ws = guarded_ws(need, fill=0xFF)
+    i8_gemm_backward(dY, to_dev(W), to_dev(sw), dX=dX.view(M, K), ws=ws)
+    want = ref.backward(host(dY), W, sw)
+    ref.check(host(dX.view(M, K)), want)
+    ref.check_norm(host(dX.view(M, K)), want[0])
+    assert guards_intact(full, M * K, fill=7.0) and ws_guards_intact(wfull, need, fill=0xFF)
+
+
+@pytest.mark.parametrize("M", [5, 8, 13, 16])
+@pytest.mark.parametrize("N", [72, 9000])
+def test_few_rows_of_far_sizes(M, N):
+    """Rows of any size beside one another, whose values fall by 2^40 on the way; a row of zeros."""
+    from moe_experts_amd import i8_gemm_backward
+    K = 80
+    r = datagen.rng(103)
+    W, sw = int8(104, N, K), scales(105, N)
+    size = 2.0 ** np.linspace(-60, 90, M)[:, None]
+    size[4] = 0
+    dY = typed(r.standard_normal((M, N)) * size * 2.0 ** np.linspace(0, -40, N), "bf16")
+    got = host(i8_gemm_backward(dY, to_dev(W), to_dev(sw)))
+    ref.check(got, ref.backward(host(dY), W, sw))
+    assert not got[4].any()
+
+
+@pytest.mark.parametrize("M", [5, 8, 13, 16])
+@pytest.mark.parametrize("N", [72, 9000])
+def test_few_broken_rows_stay_alone(M, N):
+    from moe_experts_amd import i8_gemm_backward
+    K = 272
+    dY, W, sw = gradient(106, M, N), to_dev(int8(107, N, K)), scales(108, N)
+    was = i8_gemm_backward(dY, W, to_dev(sw))
+    broken = dY.clone()
+    broken[3, 6], broken[1, N - 1] = float("inf"), float("nan")
+    got = i8_gemm_backward(broken, W, to_dev(sw))
+    keep = [m for m in range(M) if m not in (1, 3)]
+    assert not torch.isfinite(got[[1, 3]].float()).any()
+    assert torch.equal(got[keep], was[keep])
+    sw[N - 2] = np.nan
+    assert torch.isnan(i8_gemm_backward(dY, W, to_dev(sw)).float()).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(7, 24, 48), (64, 1032, 272), (150, 2048, 512), (300, 520, 4112),
                                    (4200, 136, 4112)])
 def test_gradients_pick_single_values(M, N, K):
