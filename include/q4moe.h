@@ -488,8 +488,7 @@ int i8_gemm_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx
 
 /* Which kernel serves a shape of them (for inspection and tests; host arithmetic only).
  * form: whose call; M, N, K: as in it.
- *   rows, cols  of a tile of the result; 0 for the kernels of few rows (i8_gemm: M <= 16) and
- *               of few output channels (the weights' gradient: N <= 16)
+ *   rows, cols  of a tile of the result; 0 for the kernels of up to 16 rows in the result
  *   splits      workgroups that share the contraction of a tile, 1 for none
  *   steps       K steps of a split (128 of i8_gemm's contraction, 64 of a gradient's)
  * Fails as the call does for M, N and K; Q4_EINVAL for another form or a null pointer. */

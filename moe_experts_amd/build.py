@@ -16,7 +16,7 @@ SOURCES = ["q4moe_api.cpp", "gemv_q4_0.hip", "gemv_mfma_q4_0.hip", "gemv_q8_0.hi
            "moe_q4_0.hip", "router_moe.hip", "moe_prefill.hip", "gemm_q4_0.hip",
            "gemv_noalloc.hip", "ffn_decode.hip", "ffn_gemm.hip", "ffn_rows.hip",
            "ffn_strip.hip", "i8_rows.hip", "i8_strip.hip", "i8_gemm.hip", "i8_gradient.hip",
-           "i8_channels.hip"]
+           "i8_few_gradient.hip"]
 # Per-source extra flags. The matrix-core tiles keep their accumulators in
 # ordinary VGPRs (MFMA "VGPR form"): with accumulation registers the
 # allocator rotated the accumulators between loop iterations (register copies
@@ -33,7 +33,7 @@ EXTRA = {"gemv_mfma_q4_0.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "i8_strip.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "i8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "i8_gradient.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-         "i8_channels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+         "i8_few_gradient.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,339 @@
+// Gradients of the 8-bit product with up to 16 rows in the result, in one kernel:
+//   weights, up to 16 output channels (the rank of an adapter)
+//     dW[n][k] = sum_m (dY[m][n] * sx[m]) * X[m][k]
+//   input, up to 16 tokens
+//     dX[m][k] = sum_n (dY[m][n] * sw[n]) * W[n][k]
+// or C[i][k] = sum_c A[i][c] * B[c][k]. A is little and B is much: a workgroup owns 64 columns of
+// B, whose rows are on their way into LDS while it makes A: all of dY times the scales, scaled
+// row by row of C and rounded to fp16 as for the tiles, in LDS with c contiguous. Its waves then
+// share out the rows of B: each multiplies steps of 32 by v_mfma_f32_16x16x32_f16, copied
+// memory -> LDS several steps ahead into a part of its own, and their sums meet in LDS, in the
+// order of the waves.
+//
+// A contraction of up to 2048 (4096 with up to 8 rows) fits a workgroup of eight waves; a longer
+// one (of the weights' gradient) is split over workgroups of four waves and half as much, two
+// of which fit a CU. Each split scales by the power of two of its own part and takes it back
+// (exact), so splits are sums of their own, added in their order by a second kernel.
+//
+// What bounds it: rank 16 of 1999 rows of 11008 9.3 us, of which B takes 4.4 at a large copy's
+// rate; the rest is the start, dY's way from memory and its 32768 values' conversion (a
+// microsecond on a CU's four units), which the copies in flight only hide as far as they fit
+// LDS. By a transposing kernel and the tiles: 15.8. Rank 16 of 8192 rows of 4096 12.9 us by four
+// waves, 12.7 by eight, of 11008 27.8 and 29.2 (tiles 20.3 and 29.8), of 4096 rows of 4096 9.5
+// and 10.7 (14.6); of a row 5.3 (6.5). Past 64 splits the tiles take over.
+//
+// The input's gradient takes it where no splits are needed: it saves the launch that rounds
+// dY, 3.8 us from a program that launches call by call (7.8 and 11.6 us a small call). On the
+// GPU alone 8 rows of 4096 x 11008 13.7 us (tiles 15.9), 4 of 1536 x 5120 7.3 (10.8), one of
+// 4096 x 4096 9.8 (9.5); split, 16 of 8192 x 16384 39.5 (31.4).
+#include <algorithm>
+
+#include "i8_device.hpp"
+#include "i8_internal.hpp"
+#include "i8_tile.hpp"
+
+namespace q4 {
+namespace {
+
+constexpr int kCols = 64;          // of B, a workgroup
+constexpr int kStepRows = 32;      // of B, a step of a wave
+constexpr int kStepCopy = kStepRows * kCols;
+constexpr int NS = 5;              // steps of a wave in LDS
+constexpr int kWaveValues = 4096;  // of A in LDS, a wave
+
+struct FewArgs {
+  const uint16_t* dY;  // [depth][rows], or of the input's gradient [rows][depth]
+  const float* scale;  // [depth]
+  const int8_t* B;     // [depth][cols]
+  uint16_t* out;       // [rows][cols]
+  float* part;         // fp32 [S][rows][cols]
+  int rows, depth, cols, tiles, S, chunk;
+};
+
+// Where the 16-byte chunk c of a step's row k stands: c ^ swz_step(k). The rows that 32 lanes
+// read at once, 16 of one chunk, meet no bank twice.
+__device__ __forceinline__ int swz_step(int k) { return 2 * ((k >> 2) & 1) + ((k >> 3) & 1); }
+
+// A workgroup's share of dY, 64 values a lane, [p][e], in registers. N rows of A, 8 or 16.
+// Parts past the end are the last times zero: zeros, or a NaN in a row of A that holds an
+// infinity or a NaN there and so has no finite result.
+//
+// For the weights dY is transposed on its way: value p, e of a lane is column 8 * half + e of its
+// row 2 * (p / 2 * kLanes + at) + p % 2; pairs of rows are a dword of A.
+template <int N, int THREADS>
+struct Transposed {
+  static constexpr int kPieces = N / 8, kLanes = THREADS / kPieces, kPer = 2 * kLanes;
+  Piece<Q4_TYPE_BF16> v[8];
+  float s[8];
+  int half, at;
+  __device__ __forceinline__ void load(const FewArgs& g, int c0, int left) {
+    half = threadIdx.x % kPieces;
+    at = threadIdx.x / kPieces;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int c = c0 + min(p / 2 * kPer + 2 * at + p % 2, left - 1);
+      v[p].load(g.dY + (size_t)c * N + 8 * half);
+      s[p] = g.scale[c];
+    }
+  }
+  // whether any lane's value p is of use; uniform
+  static __device__ __forceinline__ bool used(int p, const FewArgs&, int left) {
+    return p / 2 * kPer < left;
+  }
+  __device__ __forceinline__ void multiply(float (&x)[8], int p, int left) const {
+    const float f = p / 2 * kPer + 2 * at + p % 2 < left ? s[p] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = v[p][e] * f;
+  }
+  // the largest of every row of A in this wave
+  __device__ __forceinline__ void largest(const float (&x)[8][8], const FewArgs& g, int left,
+                                          uint32_t* big) const {
+    float m[8] = {};
+#pragma unroll
+    for (int p = 0; p < 8; p += 2)
+      if (used(p, g, left))
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] = fmaxf(fmaxf(m[e], fabsf(x[p][e])), fabsf(x[p + 1][e]));
+    uint32_t b[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = magnitude(m[e]);
+    const int e = wave_max_of_eight<kPieces>(b);
+    if ((threadIdx.x & 63) < N) big[8 * half + e] = b[0];
+  }
+  // the waves that hold values of row i
+  static __device__ __forceinline__ int first_wave(int) { return 0; }
+  static constexpr int kWavesOfRow = THREADS / kWaveSize;
+  __device__ __forceinline__ void store(const float (&x)[8][8], uint8_t* a, int pitch,
+                                        const float* up, const FewArgs& g, int left) const {
+#pragma unroll
+    for (int p = 0; p < 8; p += 2)
+      if (used(p, g, left))  // and so all of the last step
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f = up[8 * half + e];
+          *reinterpret_cast<half2v*>(a + (8 * half + e) * pitch + p * kPer + 4 * at) =
+              half2v{(_Float16)(x[p][e] * f), (_Float16)(x[p + 1][e] * f)};
+        }
+  }
+};
+
+// For the input dY stands as A does: value p, e of a lane is column 8 * at + e of row
+// p * kPieces + part. Rows past the last are not made: what stands there is not kept.
+template <int N, int THREADS>
+struct Straight {
+  static constexpr int kPieces = N / 8, kLanes = THREADS / kPieces;
+  Piece<Q4_TYPE_BF16> v[8];
+  float s[8];
+  int part, at;
+  __device__ __forceinline__ void load(const FewArgs& g, int c0, int left) {
+    part = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+    at = threadIdx.x % kLanes;
+    const int c = c0 + min(8 * at, left - 8);  // depth and left are multiples of 8
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      v[p].load(g.dY + (size_t)min(p * kPieces + part, g.rows - 1) * g.depth + c);
+    __builtin_memcpy(s, g.scale + c, sizeof(s));
+  }
+  __device__ __forceinline__ bool used(int p, const FewArgs& g, int) const {
+    return p * kPieces + part < g.rows;
+  }
+  __device__ __forceinline__ void multiply(float (&x)[8], int p, int left) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = v[p][e] * (8 * at < left ? s[e] : 0.0f);
+  }
+  __device__ __forceinline__ void largest(const float (&x)[8][8], const FewArgs& g, int left,
+                                          uint32_t* big) const {
+    uint32_t b[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      float m = 0.0f;
+      if (used(p, g, left))
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[p][e]));
+      b[p] = magnitude(m);
+    }
+    const int p = wave_max_of_eight<1>(b);
+    if ((threadIdx.x & 63) < 8) big[p * kPieces + part] = b[0];
+  }
+  static constexpr int kWavesOfRow = kLanes / kWaveSize;
+  static __device__ __forceinline__ int first_wave(int i) { return i % kPieces * kWavesOfRow; }
+  __device__ __forceinline__ void store(const float (&x)[8][8], uint8_t* a, int pitch,
+                                        const float* up, const FewArgs& g, int left) const {
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      if (used(p, g, left)) {
+        const float f = up[p * kPieces + part];
+        half8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = (_Float16)(x[p][e] * f);
+        *reinterpret_cast<half8*>(a + (p * kPieces + part) * pitch + 16 * at) = h;
+      }
+  }
+};
+
+template <class Dy, int N, int kWaves>
+__global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewArgs g) {
+  constexpr int kThreads = kWaves * kWaveSize;
+  constexpr int kDepth = kWaves * kWaveValues / N;  // of A
+  constexpr int kPitch = kDepth * 2 + 16;           // bytes of a row of A in LDS
+  static_assert(8 * 8 * kThreads == N * kDepth, "every value in one lane");
+  __shared__ __attribute__((aligned(16))) uint8_t a[N * kPitch];
+  __shared__ uint32_t big[kWaves][N];
+  __shared__ float up[N], down[N];
+  // The steps' stages are apart, so that the compiler can tell a copy into one from a read of
+  // another; in each every wave has its own part.
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[kWaves * kStepCopy], s1[kWaves * kStepCopy],
+      s2[kWaves * kStepCopy], s3[kWaves * kStepCopy], s4[kWaves * kStepCopy];
+  uint8_t* const st[NS] = {s0, s1, s2, s3, s4};
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  // neighbours, which share the lines of B, on one XCD
+  const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
+  const int sp = L / g.tiles, j0 = (L - sp * g.tiles) * kCols;
+  const int c0 = sp * g.chunk, left = min(g.depth - c0, g.chunk);  // 1 .. kDepth
+  const int nk = (left + kStepRows - 1) / kStepRows, per = (nk + kWaves - 1) / kWaves;
+  const int kb = min(nk, wave * per), ke = min(nk, kb + per);
+
+  // dY first, all of it at once: loads return in order, and B is much
+  Dy dy;
+  dy.load(g, c0, left);
+  asm volatile("" ::: "memory");  // the copies below stay below
+  __builtin_amdgcn_sched_barrier(0);
+
+  // Copies: four lanes a row of 64 bytes. Rows past the last are past the end and become
+  // zeros, rows of the next split meet zeros of A, columns past the last are not kept; steps
+  // past the last copy zeros, without an access of memory, and are not read.
+  const __amdgpu_buffer_rsrc_t rb =
+      make_rsrc(g.B + j0, (uint32_t)g.depth * (uint32_t)g.cols - (uint32_t)j0);
+  const uint32_t at = (uint32_t)(lane >> 2) * (uint32_t)g.cols +
+                      16u * (uint32_t)((lane & 3) ^ swz_step(lane >> 2));
+  auto issue = [&](uint8_t* stage, int k) __attribute__((always_inline)) {
+    uint8_t* mine = stage + wave * kStepCopy;
+    const uint32_t so = (uint32_t)(c0 + min(k, nk - 1) * kStepRows) * (uint32_t)g.cols;
+    copy16(rb, mine, k < ke ? at : kPastEnd, so);
+    copy16(rb, mine + kStepCopy / 2, k < ke ? at + 16u * (uint32_t)g.cols : kPastEnd, so);
+  };
+#pragma unroll
+  for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
+
+  // fmaxf passes over NaN: what a row with one is scaled by does not matter.
+  float x[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+    if (dy.used(p, g, left)) dy.multiply(x[p], p, left);
+  dy.largest(x, g, left, big[wave]);
+  lds_only_barrier();
+  if (t < N) {
+    uint32_t b = 0;
+#pragma unroll
+    for (int w = 0; w < Dy::kWavesOfRow; ++w) b = max(b, big[Dy::first_wave(t) + w][t]);
+    const PowerOfTwo f = to_fp16_range(b);
+    up[t] = f.up;
+    down[t] = f.down;
+  }
+  lds_only_barrier();
+  dy.store(x, a, kPitch, up, g, left);
+  lds_only_barrier();
+
+  float4v acc[kCols / 16];
+#pragma unroll
+  for (int j = 0; j < kCols / 16; ++j) acc[j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+  // Lane l takes row l % 16 of A and rows 8 * (l / 16) .. of a step; of eight rows the upper lanes
+  // repeat the lower and are not kept.
+  const uint8_t* ar = a + (lane & (N - 1)) * kPitch + 16 * (lane >> 4);
+  const int kr = 8 * (lane >> 4) + ((lane & 15) >> 1);
+  const int bo = wave * kStepCopy + kr * kCols + 8 * (lane & 1), bs = swz_step(kr);
+  auto step = [&](uint8_t* stage, int k) __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    // this wave's copies of the step have landed: vmcnt(2 * (NS - 1))
+    constexpr int kLeft = 2 * (NS - 1);
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (kLeft & 15) | (kLeft >> 4) << 14);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const half8 ax = *reinterpret_cast<const half8*>(ar + k * (2 * kStepRows));
+    int2v b[kCols / 16];
+#pragma unroll
+    for (int j = 0; j < kCols / 16; ++j)
+      b[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (__attribute__((address_space(3))) int2v*)(stage + bo + ((j ^ bs) << 4)));
+#pragma unroll
+    for (int j = 0; j < kCols / 16; ++j)
+      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_halves(b[j]), ax, acc[j], 0, 0, 0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is copied over
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    issue(stage, k + NS);
+  };
+  int k = kb;
+  for (; k + NS <= ke; k += NS)
+#pragma unroll
+    for (int u = 0; u < NS; ++u) step(st[u], k + u);
+#pragma unroll
+  for (int u = 0; u < NS - 1; ++u)
+    if (k + u < ke) step(st[u], k + u);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no copy lands after the workgroup ends
+
+  // lane l of a 16 x 16 result holds row l % 16 and four neighbouring columns
+  float4v* sums = reinterpret_cast<float4v*>(a);
+  static_assert(kWaves * kCols / 16 * kWaveSize * 16 <= N * kPitch, "sums fit");
+  __syncthreads();  // `a` has been read
+#pragma unroll
+  for (int j = 0; j < kCols / 16; ++j) sums[(wave * (kCols / 16) + j) * kWaveSize + lane] = acc[j];
+  __syncthreads();
+  const int n = lane & 15, c = j0 + 16 * wave + 4 * (lane >> 4);
+  if (wave >= kCols / 16 || n >= g.rows || c >= g.cols) return;
+  float4v sum = sums[wave * kWaveSize + lane];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) sum += sums[(w * (kCols / 16) + wave) * kWaveSize + lane];
+  sum *= down[n];
+  if (g.S > 1) {
+    *reinterpret_cast<float4v*>(g.part + ((size_t)sp * g.rows + n) * g.cols + c) = sum;
+    return;
+  }
+  uint32_t y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = i8_to_bf16(sum[e]);
+  *reinterpret_cast<uint2*>(g.out + (size_t)n * g.cols + c) =
+      make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
+}
+
+template <template <int, int> class Dy, int N, int WAVES>
+void launch(const FewArgs& g, hipStream_t st) {
+  hipLaunchKernelGGL((i8_few_gradient_kernel<Dy<N, WAVES * kWaveSize>, N, WAVES>),
+                     dim3((unsigned)(g.tiles * g.S)), dim3(WAVES * kWaveSize), 0, st, g);
+}
+
+}  // namespace
+
+bool plan_i8_few_gradient(I8Plan& p, int rows, int cols, int depth, int splits) {
+  if (rows > 16) return false;
+  const int most = 4 * kWaveValues / (rows <= 8 ? 8 : 16);  // of four waves
+  const int S = depth <= 2 * most ? 1 : (depth + most - 1) / most;
+  if (S > splits) return false;
+  p.strip = true;
+  p.kper = ((depth + S - 1) / S + 63) / 64;  // of 64, at most what a workgroup takes
+  p.S = (depth + p.kper * 64 - 1) / (p.kper * 64);
+  if (p.S > 1) p.ws_bytes = (size_t)p.S * rows * cols * sizeof(float);
+  return true;
+}
+
+hipError_t launch_i8_few_gradient(const uint16_t* dY, bool transposed, const float* scale,
+                                  const int8_t* B, uint16_t* out, int rows, int cols, int depth,
+                                  float* part, const I8Plan& p, hipStream_t st) {
+  const FewArgs g{dY,   scale, B,    out, part, rows, depth, cols, (cols + kCols - 1) / kCols,
+                  p.S, p.kper * 64};
+  if (!transposed)
+    rows <= 8 ? launch<Straight, 8, 8>(g, st) : launch<Straight, 16, 8>(g, st);
+  else if (rows == 8)
+    p.S == 1 ? launch<Transposed, 8, 8>(g, st) : launch<Transposed, 8, 4>(g, st);
+  else
+    p.S == 1 ? launch<Transposed, 16, 8>(g, st) : launch<Transposed, 16, 4>(g, st);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || p.S == 1) return err;
+  return launch_i8_gradient_finish(part, nullptr, out, rows, cols, p.S, st);
+}
+
+}  // namespace q4

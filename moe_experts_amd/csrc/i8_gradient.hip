@@ -309,10 +309,15 @@ hipError_t launch_tiles(const int8_t* B, uint16_t* out, int rows, int cols, int 
 
 }  // namespace
 
-I8Plan plan_i8_backward(int M, int N, int K) { return plan_gradient(M, K, N, 0); }
+I8Plan plan_i8_backward(int M, int N, int K) {
+  I8Plan p{};
+  if (plan_i8_few_gradient(p, M, K, N, 1)) return p;
+  return plan_gradient(M, K, N, 0);
+}
 
 hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint16_t* dX,
                               int M, int N, int K, void* ws, const I8Plan& p, hipStream_t st) {
+  if (p.strip) return launch_i8_few_gradient(dY, false, sw, W, dX, M, K, N, nullptr, p, st);
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipError_t err =
       launch_i8_gradient_rows(dY, sw, reinterpret_cast<uint16_t*>(w + p.off_a),
@@ -323,7 +328,7 @@ hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* 
 
 I8Plan plan_i8_backward_weight(int M, int N, int K) {
   I8Plan p{};
-  if (plan_i8_few_channels(p, M, N, K)) return p;
+  if (plan_i8_few_gradient(p, N, K, M, kFewSplits)) return p;
   return plan_gradient(N, K, M, i8_max_chunks(M, N));
 }
 
@@ -332,7 +337,7 @@ hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const 
                                      hipStream_t st) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   if (p.strip)
-    return launch_i8_few_channels(dY, X, sx, dW, M, N, K, reinterpret_cast<float*>(w), p, st);
+    return launch_i8_few_gradient(dY, true, sx, X, dW, N, K, M, reinterpret_cast<float*>(w), p, st);
   const hipError_t err = launch_i8_gradient_columns(
       dY, sx, reinterpret_cast<uint16_t*>(w + p.off_a), reinterpret_cast<float*>(w + p.off_rs),
       reinterpret_cast<uint32_t*>(w + p.off_max), M, N, p.ld, st);

@@ -104,12 +104,15 @@ hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const 
                                      uint16_t* dW, int M, int N, int K, void* ws, const I8Plan& p,
                                      hipStream_t st);
 
-// ---- few output channels (i8_channels.hip) --------------------------------------
-// Plans the weights' gradient of up to 16 output channels; false: by tiles.
-bool plan_i8_few_channels(I8Plan& p, int M, int N, int K);
-hipError_t launch_i8_few_channels(const uint16_t* dY, const int8_t* X, const float* sx,
-                                  uint16_t* dW, int M, int N, int K, float* part, const I8Plan& p,
-                                  hipStream_t st);
+// ---- gradients with few rows in the result (i8_few_gradient.hip) ------------------
+// Plans a gradient of up to 16 rows, rows x cols over `depth`, in at most `splits`; false: by
+// tiles.
+constexpr int kFewSplits = 64;
+bool plan_i8_few_gradient(I8Plan& p, int rows, int cols, int depth, int splits);
+// dY [depth][rows] (transposed) or [rows][depth], scale [depth], B [depth][cols]
+hipError_t launch_i8_few_gradient(const uint16_t* dY, bool transposed, const float* scale,
+                                  const int8_t* B, uint16_t* out, int rows, int cols, int depth,
+                                  float* part, const I8Plan& p, hipStream_t st);
 
 // ---- left operands of the gradients, sums of splits (i8_rows.hip) --------------
 // a[m][n] = fp16(dY[m][n] * sw[n] * 2^e), n < ld (zero past N), rs[m] = 2^-e

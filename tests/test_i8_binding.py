@@ -11,7 +11,7 @@ from tests.test_ffn_registers import OBJDUMP, descriptions, said_of_objects, unw
 
 #: kernels of the matrix cores, and how many variants of each are built
 KERNELS = {"i8_gemm_kernel": 18, "i8_gradient_kernel": 4, "i8_few_rows_kernel": 7,
-           "i8_few_channels_kernel": 4}
+           "i8_few_gradient_kernel": 6}
 
 
 @pytest.mark.parametrize("index", [0, 3])
