@@ -14,11 +14,16 @@
 //     them waiting for LDS (130 rows of 4096 x 4096 by 64 x 64: 11.3 -> 9.5 us).
 //
 // What bounds it: 2048 rows of 4096 x 11008 take 95 us, 1.95 POP/s. With all CUs busy the power
-// limit holds the clock at 1.5 to 1.7 GHz, at which the matrix cores are busy three quarters
-// of a tile's time: without LDS reads it takes 85 us, without copies 83, with neither 72. A
-// deeper ring of stages, registers in place of LDS-DMA, raised priorities and freer scheduling
-// all came out within 3 %. Where few tiles leave the clock at 2.4 GHz, 777 rows of 5120 x 1536,
-// a step of 64 x 128 takes 850 cycles, of which LDS is busy 700 (64 KiB read, 24 KiB written).
+// limit holds the clock at 1.5 to 1.7 GHz, at which the matrix cores' own cycles are 55 us;
+// without LDS reads it takes 85 us, without copies 83, with neither 72. A deeper ring of
+// stages, registers in place of LDS-DMA, raised priorities and freer scheduling all came out
+// within 3 %.
+//
+// Few tiles are bound by the rate at which a CU copies: one workgroup alone on the GPU takes
+// 0.25 us a step of 64 x 128, 0.18 of 64 x 64 and 0.31 of 128 x 128, that is 80 cycles a step and
+// 21 a KiB (at 64 bytes a cycle it were 16); a fourth stage or other waves over the tile change
+// nothing. 777 rows of 5120 x 1536 take 17.7 us of which 40 such steps are 11: 100 CUs have no
+// tile, and splits that give them one cost more (20.6 us in three).
 #include <algorithm>
 
 #include "i8_device.hpp"

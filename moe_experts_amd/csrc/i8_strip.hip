@@ -136,8 +136,8 @@ __global__ __launch_bounds__(kStripThreads) void i8_few_rows_kernel(StripArgs g)
     const uint32_t so = (uint32_t)min(s, nk - 1) * 128u;
     const int left = s < ke ? K - s * 128 : 0;
     const uint32_t o = chunk < left ? at : kPastEnd, o8 = chunk8 < left ? at8 : kPastEnd;
-    if constexpr (XROWS >= 8) copy16(rx, mine + 2048, o, so);
-    if constexpr (XROWS >= 16) copy16(rx, mine + 3072, o8, so);
+    if constexpr (XROWS >= 8) copy16(rx, mine + 2 * 1024, o, so);
+    if constexpr (XROWS >= 16) copy16(rx, mine + 3 * 1024, o8, so);
     copy16(rw, mine, o, so);
     copy16(rw, mine + 1024, o8, so);
   };
