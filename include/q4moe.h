@@ -479,16 +479,17 @@ int i8_gemm_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint1
  * forward pass:
  *   dW[n][k] = sum_m dY[m][n] * sx[m] * X[m][k]
  *   dY bf16 [M][N]     X int8 [M][K], sx fp32 [M]     dW bf16 [N][K], overwritten
- * The products dY * sx of a column of dY (with up to 16 output channels: of a part of its
- * rows) are scaled and rounded as i8_gemm_backward does those of a row. A column of dY with an infinity or a NaN has a row of dW that is not
- * finite; a token whose scale is a NaN leaves nothing finite. */
+ * The products dY * sx of a column of dY (with up to 16 output channels: of a part of it)
+ * are scaled and rounded as i8_gemm_backward does those of a row. A column of dY with an
+ * infinity or a NaN has a row of dW that is not finite; a token whose scale is a NaN leaves
+ * nothing finite. */
 size_t i8_gemm_backward_weight_workspace_bytes(int M, int N, int K);
 int i8_gemm_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx, uint16_t* dW,
                             int M, int N, int K, void* ws, size_t ws_bytes, void* stream);
 
 /* Which kernel serves a shape of them (for inspection and tests; host arithmetic only).
  * form: whose call; M, N, K: as in it.
- *   rows, cols  of a tile of the result; 0 for the kernels of up to 16 rows in the result
+ *   rows, cols  of a tile of the result; 0 for the kernels of few rows or little work
  *   splits      workgroups that share the contraction of a tile, 1 for none
  *   steps       K steps of a split (128 of i8_gemm's contraction, 64 of a gradient's)
  * Fails as the call does for M, N and K; Q4_EINVAL for another form or a null pointer. */

@@ -739,8 +739,8 @@ I8_FORMS = {"i8_gemm": 0, "i8_gemm_backward": 1, "i8_gemm_backward_weight": 2}
 
 
 def i8_gemm_plan(form: str, M: int, N: int, K: int):
-    """(rows and columns of a tile of the result, or 0 for the kernels of up to 16 rows; splits of the contraction; K steps of a split) by which the call `form` serves a
-    shape."""
+    """(rows and columns of a tile of the result, or 0 for the kernels of few rows or little work;
+    splits of the contraction; K steps of a split) by which the call `form` serves a shape."""
     if form not in I8_FORMS:
         raise ValueError(f"form must be one of {sorted(I8_FORMS)} (got {form!r})")
     _ints(M, N, K)

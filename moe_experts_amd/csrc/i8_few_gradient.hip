@@ -1,14 +1,14 @@
-// Gradients of the 8-bit product with up to 16 rows in the result, in one kernel:
-//   weights, up to 16 output channels (the rank of an adapter)
+// Gradients of the 8-bit product with few rows in the result, or little work, in one kernel:
+//   weights (an adapter's rank of output channels)
 //     dW[n][k] = sum_m (dY[m][n] * sx[m]) * X[m][k]
-//   input, up to 16 tokens
+//   input
 //     dX[m][k] = sum_n (dY[m][n] * sw[n]) * W[n][k]
-// or C[i][k] = sum_c A[i][c] * B[c][k]. A is little and B is much: a workgroup owns 64 columns of
-// B, whose rows are on their way into LDS while it makes A: all of dY times the scales, scaled
-// row by row of C and rounded to fp16 as for the tiles, in LDS with c contiguous. Its waves then
-// share out the rows of B: each multiplies steps of 32 by v_mfma_f32_16x16x32_f16, copied
-// memory -> LDS several steps ahead into a part of its own, and their sums meet in LDS, in the
-// order of the waves.
+// or C[i][k] = sum_c A[i][c] * B[c][k]. A workgroup makes 16 rows and 64 columns of C. Of B its
+// columns' rows are on their way into LDS while it makes its rows of A: dY times the scales,
+// scaled row by row of C and rounded to fp16 as for the tiles, in LDS with c contiguous. Its
+// waves then share out the rows of B: each multiplies steps of 32 by v_mfma_f32_16x16x32_f16,
+// copied memory -> LDS several steps ahead into a part of its own, and their sums meet in LDS,
+// in the order of the waves.
 //
 // A contraction of up to 2048 (4096 with up to 8 rows) fits a workgroup of eight waves; a longer
 // one (of the weights' gradient) is split over workgroups of four waves and half as much, two
@@ -22,10 +22,13 @@
 // waves, 12.7 by eight, of 11008 27.8 and 29.2 (tiles 20.3 and 29.8), of 4096 rows of 4096 9.5
 // and 10.7 (14.6); of a row 5.3 (6.5). Past 64 splits the tiles take over.
 //
-// The input's gradient takes it where no splits are needed: it saves the launch that rounds
-// dY, 3.8 us from a program that launches call by call (7.8 and 11.6 us a small call). On the
-// GPU alone 8 rows of 4096 x 11008 13.7 us (tiles 15.9), 4 of 1536 x 5120 7.3 (10.8), one of
-// 4096 x 4096 9.8 (9.5); split, 16 of 8192 x 16384 39.5 (31.4).
+// More than 16 rows, and the input's gradient, take it where no splits are needed, the former up
+// to kGroups workgroups, one a CU: it saves the launch that writes A, 2.7 us from a program that
+// launches call by call (6.6 and 9.3 us a small call). On the GPU alone, us, here and by tiles:
+// weights of 64 x 512 over 64 rows 5.5 and 6.6, 256 x 1024 over 1000 7.5 and 11.1, 64 x 4096 over
+// 2048 11.9 and 15.2; input, 4 rows of 1536 x 5120 7.3 and 10.8, 64 of 2048 x 4096 9.7 and 12.9,
+// 128 of 128 x 256 6.1 and 6.0, one of 4096 x 4096 10.2 and 9.5; split, 16 of 8192 x 16384 39.5
+// and 31.4.
 #include <algorithm>
 
 #include "i8_device.hpp"
@@ -40,6 +43,7 @@ constexpr int kStepRows = 32;      // of B, a step of a wave
 constexpr int kStepCopy = kStepRows * kCols;
 constexpr int NS = 5;              // steps of a wave in LDS
 constexpr int kWaveValues = 4096;  // of A in LDS, a wave
+constexpr int kGroups = 256;       // workgroups, where the result has more than 16 rows
 
 struct FewArgs {
   const uint16_t* dY;  // [depth][rows], or of the input's gradient [rows][depth]
@@ -47,7 +51,11 @@ struct FewArgs {
   const int8_t* B;     // [depth][cols]
   uint16_t* out;       // [rows][cols]
   float* part;         // fp32 [S][rows][cols]
-  int rows, depth, cols, tiles, S, chunk;
+  int rows, depth, cols, tiles, groups, S, chunk;
+};
+// The rows of the result that a workgroup makes: `count` from `first` on.
+struct Group {
+  int first, count;
 };
 
 // Where the 16-byte chunk c of a step's row k stands: c ^ swz_step(k). The rows that 32 lanes
@@ -66,18 +74,19 @@ struct Transposed {
   Piece<Q4_TYPE_BF16> v[8];
   float s[8];
   int half, at;
-  __device__ __forceinline__ void load(const FewArgs& g, int c0, int left) {
+  __device__ __forceinline__ void load(const FewArgs& g, const Group& r, int c0, int left) {
     half = threadIdx.x % kPieces;
     at = threadIdx.x / kPieces;
+    const uint16_t* y = g.dY + r.first + min(8 * half, r.count - 8);  // rows is a multiple of 8
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const int c = c0 + min(p / 2 * kPer + 2 * at + p % 2, left - 1);
-      v[p].load(g.dY + (size_t)c * N + 8 * half);
+      v[p].load(y + (size_t)c * g.rows);
       s[p] = g.scale[c];
     }
   }
   // whether any lane's value p is of use; uniform
-  static __device__ __forceinline__ bool used(int p, const FewArgs&, int left) {
+  static __device__ __forceinline__ bool used(int p, const Group&, int left) {
     return p / 2 * kPer < left;
   }
   __device__ __forceinline__ void multiply(float (&x)[8], int p, int left) const {
@@ -86,12 +95,12 @@ struct Transposed {
     for (int e = 0; e < 8; ++e) x[e] = v[p][e] * f;
   }
   // the largest of every row of A in this wave
-  __device__ __forceinline__ void largest(const float (&x)[8][8], const FewArgs& g, int left,
+  __device__ __forceinline__ void largest(const float (&x)[8][8], const Group& r, int left,
                                           uint32_t* big) const {
     float m[8] = {};
 #pragma unroll
     for (int p = 0; p < 8; p += 2)
-      if (used(p, g, left))
+      if (used(p, r, left))
 #pragma unroll
         for (int e = 0; e < 8; ++e) m[e] = fmaxf(fmaxf(m[e], fabsf(x[p][e])), fabsf(x[p + 1][e]));
     uint32_t b[8];
@@ -104,10 +113,10 @@ struct Transposed {
   static __device__ __forceinline__ int first_wave(int) { return 0; }
   static constexpr int kWavesOfRow = THREADS / kWaveSize;
   __device__ __forceinline__ void store(const float (&x)[8][8], uint8_t* a, int pitch,
-                                        const float* up, const FewArgs& g, int left) const {
+                                        const float* up, const Group& r, int left) const {
 #pragma unroll
     for (int p = 0; p < 8; p += 2)
-      if (used(p, g, left))  // and so all of the last step
+      if (used(p, r, left))  // and so all of the last step
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float f = up[8 * half + e];
@@ -118,36 +127,34 @@ struct Transposed {
 };
 
 // For the input dY stands as A does: value p, e of a lane is column 8 * at + e of row
-// p * kPieces + part. Rows past the last are not made: what stands there is not kept.
+// p * kPieces + part. Rows past the last repeat it and are not kept.
 template <int N, int THREADS>
 struct Straight {
   static constexpr int kPieces = N / 8, kLanes = THREADS / kPieces;
   Piece<Q4_TYPE_BF16> v[8];
   float s[8];
   int part, at;
-  __device__ __forceinline__ void load(const FewArgs& g, int c0, int left) {
+  __device__ __forceinline__ void load(const FewArgs& g, const Group& r, int c0, int left) {
     part = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
     at = threadIdx.x % kLanes;
     const int c = c0 + min(8 * at, left - 8);  // depth and left are multiples of 8
 #pragma unroll
     for (int p = 0; p < 8; ++p)
-      v[p].load(g.dY + (size_t)min(p * kPieces + part, g.rows - 1) * g.depth + c);
+      v[p].load(g.dY + (size_t)(r.first + min(p * kPieces + part, r.count - 1)) * g.depth + c);
     __builtin_memcpy(s, g.scale + c, sizeof(s));
   }
-  __device__ __forceinline__ bool used(int p, const FewArgs& g, int) const {
-    return p * kPieces + part < g.rows;
-  }
+  static __device__ __forceinline__ constexpr bool used(int, const Group&, int) { return true; }
   __device__ __forceinline__ void multiply(float (&x)[8], int p, int left) const {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = v[p][e] * (8 * at < left ? s[e] : 0.0f);
   }
-  __device__ __forceinline__ void largest(const float (&x)[8][8], const FewArgs& g, int left,
+  __device__ __forceinline__ void largest(const float (&x)[8][8], const Group& r, int left,
                                           uint32_t* big) const {
     uint32_t b[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       float m = 0.0f;
-      if (used(p, g, left))
+      if (used(p, r, left))
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[p][e]));
       b[p] = magnitude(m);
@@ -158,10 +165,10 @@ struct Straight {
   static constexpr int kWavesOfRow = kLanes / kWaveSize;
   static __device__ __forceinline__ int first_wave(int i) { return i % kPieces * kWavesOfRow; }
   __device__ __forceinline__ void store(const float (&x)[8][8], uint8_t* a, int pitch,
-                                        const float* up, const FewArgs& g, int left) const {
+                                        const float* up, const Group& r, int left) const {
 #pragma unroll
     for (int p = 0; p < 8; ++p)
-      if (used(p, g, left)) {
+      if (used(p, r, left)) {
         const float f = up[p * kPieces + part];
         half8 h;
 #pragma unroll
@@ -189,14 +196,16 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   // neighbours, which share the lines of B, on one XCD
   const int L = xcd_logical_tile(blockIdx.x, gridDim.x);
-  const int sp = L / g.tiles, j0 = (L - sp * g.tiles) * kCols;
+  const int sg = L / g.tiles, j0 = (L - sg * g.tiles) * kCols;
+  const int sp = sg / g.groups, first = (sg - sp * g.groups) * N;
+  const Group rows{first, min(N, g.rows - first)};
   const int c0 = sp * g.chunk, left = min(g.depth - c0, g.chunk);  // 1 .. kDepth
   const int nk = (left + kStepRows - 1) / kStepRows, per = (nk + kWaves - 1) / kWaves;
   const int kb = min(nk, wave * per), ke = min(nk, kb + per);
 
   // dY first, all of it at once: loads return in order, and B is much
   Dy dy;
-  dy.load(g, c0, left);
+  dy.load(g, rows, c0, left);
   asm volatile("" ::: "memory");  // the copies below stay below
   __builtin_amdgcn_sched_barrier(0);
 
@@ -220,8 +229,8 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   float x[8][8];
 #pragma unroll
   for (int p = 0; p < 8; ++p)
-    if (dy.used(p, g, left)) dy.multiply(x[p], p, left);
-  dy.largest(x, g, left, big[wave]);
+    if (dy.used(p, rows, left)) dy.multiply(x[p], p, left);
+  dy.largest(x, rows, left, big[wave]);
   lds_only_barrier();
   if (t < N) {
     uint32_t b = 0;
@@ -232,7 +241,7 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
     down[t] = f.down;
   }
   lds_only_barrier();
-  dy.store(x, a, kPitch, up, g, left);
+  dy.store(x, a, kPitch, up, rows, left);
   lds_only_barrier();
 
   float4v acc[kCols / 16];
@@ -284,35 +293,35 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   for (int j = 0; j < kCols / 16; ++j) sums[(wave * (kCols / 16) + j) * kWaveSize + lane] = acc[j];
   __syncthreads();
   const int n = lane & 15, c = j0 + 16 * wave + 4 * (lane >> 4);
-  if (wave >= kCols / 16 || n >= g.rows || c >= g.cols) return;
+  if (wave >= kCols / 16 || n >= rows.count || c >= g.cols) return;
   float4v sum = sums[wave * kWaveSize + lane];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) sum += sums[(w * (kCols / 16) + wave) * kWaveSize + lane];
   sum *= down[n];
   if (g.S > 1) {
-    *reinterpret_cast<float4v*>(g.part + ((size_t)sp * g.rows + n) * g.cols + c) = sum;
+    *reinterpret_cast<float4v*>(g.part + ((size_t)sp * g.rows + first + n) * g.cols + c) = sum;
     return;
   }
   uint32_t y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = i8_to_bf16(sum[e]);
-  *reinterpret_cast<uint2*>(g.out + (size_t)n * g.cols + c) =
+  *reinterpret_cast<uint2*>(g.out + (size_t)(first + n) * g.cols + c) =
       make_uint2(y[0] | (y[1] << 16), y[2] | (y[3] << 16));
 }
 
 template <template <int, int> class Dy, int N, int WAVES>
 void launch(const FewArgs& g, hipStream_t st) {
   hipLaunchKernelGGL((i8_few_gradient_kernel<Dy<N, WAVES * kWaveSize>, N, WAVES>),
-                     dim3((unsigned)(g.tiles * g.S)), dim3(WAVES * kWaveSize), 0, st, g);
+                     dim3((unsigned)(g.tiles * g.groups * g.S)), dim3(WAVES * kWaveSize), 0, st, g);
 }
 
 }  // namespace
 
 bool plan_i8_few_gradient(I8Plan& p, int rows, int cols, int depth, int splits) {
-  if (rows > 16) return false;
   const int most = 4 * kWaveValues / (rows <= 8 ? 8 : 16);  // of four waves
   const int S = depth <= 2 * most ? 1 : (depth + most - 1) / most;
-  if (S > splits) return false;
+  const long long workgroups = (long long)((rows + 15) / 16) * ((cols + kCols - 1) / kCols);
+  if (rows > 16 ? S > 1 || workgroups > kGroups : S > splits) return false;
   p.strip = true;
   p.kper = ((depth + S - 1) / S + 63) / 64;  // of 64, at most what a workgroup takes
   p.S = (depth + p.kper * 64 - 1) / (p.kper * 64);
@@ -324,7 +333,7 @@ hipError_t launch_i8_few_gradient(const uint16_t* dY, bool transposed, const flo
                                   const int8_t* B, uint16_t* out, int rows, int cols, int depth,
                                   float* part, const I8Plan& p, hipStream_t st) {
   const FewArgs g{dY,   scale, B,    out, part, rows, depth, cols, (cols + kCols - 1) / kCols,
-                  p.S, p.kper * 64};
+                  rows <= 8 ? 1 : (rows + 15) / 16, p.S, p.kper * 64};
   if (!transposed)
     rows <= 8 ? launch<Straight, 8, 8>(g, st) : launch<Straight, 16, 8>(g, st);
   else if (rows == 8)

@@ -104,9 +104,8 @@ hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const 
                                      uint16_t* dW, int M, int N, int K, void* ws, const I8Plan& p,
                                      hipStream_t st);
 
-// ---- gradients with few rows in the result (i8_few_gradient.hip) ------------------
-// Plans a gradient of up to 16 rows, rows x cols over `depth`, in at most `splits`; false: by
-// tiles.
+// ---- gradients of few rows or little work (i8_few_gradient.hip) -------------------
+// Plans a gradient of rows x cols over `depth`, in at most `splits`; false: by tiles.
 constexpr int kFewSplits = 64;
 bool plan_i8_few_gradient(I8Plan& p, int rows, int cols, int depth, int splits);
 // dY [depth][rows] (transposed) or [rows][depth], scale [depth], B [depth][cols]

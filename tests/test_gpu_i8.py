@@ -438,6 +438,30 @@ def test_few_broken_rows_stay_alone(M, N):
     assert torch.isnan(i8_gemm_backward(dY, W, to_dev(sw)).float()).all()
 
 
+@pytest.mark.parametrize("rows", [17, 23, 24, 31, 32, 33, 40, 104])
+@pytest.mark.parametrize("depth", [8, 264, 2040, 2048])
+def test_gradients_by_groups_of_rows(rows, depth):
+    """Results of more rows than a workgroup makes, the last group of any height."""
+    from moe_experts_amd import i8_gemm_backward, i8_gemm_backward_weight
+    K = (16, 80, 208)[rows % 3]
+    dY, B, s = gradient(110, rows, depth), int8(111, depth, K, low=-128), scales(112, depth)
+    full, out = guarded(rows * K, torch.bfloat16, fill=7.0)
+    i8_gemm_backward(dY, to_dev(B), to_dev(s), dX=out.view(rows, K))
+    want = ref.backward(host(dY), B, s)
+    ref.check(host(out.view(rows, K)), want)
+    ref.check_norm(host(out.view(rows, K)), want[0])
+    assert guards_intact(full, rows * K, fill=7.0)
+    rows += -rows % 8
+    depth -= depth // 16  # any length
+    dY, B, s = gradient(113, depth, rows), int8(114, depth, K, low=-128), scales(115, depth)
+    full, out = guarded(rows * K, torch.bfloat16, fill=7.0)
+    i8_gemm_backward_weight(dY, to_dev(B), to_dev(s), dW=out.view(rows, K))
+    want = ref.backward_weight(host(dY), B, s)
+    ref.check(host(out.view(rows, K)), want)
+    ref.check_norm(host(out.view(rows, K)), want[0])
+    assert guards_intact(full, rows * K, fill=7.0)
+
+
 @pytest.mark.parametrize("M,N,K", [(7, 24, 48), (64, 1032, 272), (150, 2048, 512), (300, 520, 4112),
                                    (4200, 136, 4112)])
 def test_gradients_pick_single_values(M, N, K):

@@ -32,7 +32,8 @@ BACKWARD = [(17, 16, 8), (17, 16, 72), (17, 16, 136), (17, 16, 200), (17, 16, 26
             (17, 32784, 8), (257, 11008, 72), (1300, 3088, 136), (1300, 3088, 200),
             (1300, 3088, 264), (3100, 400, 11008), (65, 11008, 8200),
             (1, 16, 8), (16, 16, 8), (9, 144, 72), (16, 16, 2048), (16, 16, 2056), (8, 80, 4096),
-            (8, 80, 4104), (3, 272, 11008), (16, 272, 11008), (16, 16, 70000), (8, 16, 140000)]
+            (8, 80, 4104), (3, 272, 11008), (16, 272, 11008), (16, 16, 70000), (8, 16, 140000),
+            (4200, 16, 24), (4200, 16, 72), (31, 80, 2048), (500, 512, 24)]
 WEIGHT = [(17, 16, 8), (65, 16, 8), (130, 16, 8), (200, 16, 8), (257, 16, 8), (1700, 16, 8),
           (2500, 16, 8), (2500, 144, 200), (2050, 272, 200),
           (17, 16, 8200), (65, 16, 8200), (130, 16, 8200), (200, 16, 8200), (257, 16, 8200),
@@ -42,7 +43,8 @@ WEIGHT = [(17, 16, 8), (65, 16, 8), (130, 16, 8), (200, 16, 8), (257, 16, 8), (1
           (17, 32784, 8), (65, 11008, 264), (130, 272, 11008), (200, 272, 11008), (257, 400, 8200),
           (64, 16, 24), (65, 16, 24), (400, 16, 24), (1700, 16, 24), (2500, 16, 24), (17, 32784, 24),
           (4097, 144, 8), (4200, 144, 8), (2048, 4096, 16), (2049, 4096, 16), (9000, 1040, 16),
-          (40000, 80, 16), (40000, 80, 8), (140000, 16, 8), (66000, 144, 16)]
+          (40000, 80, 16), (40000, 80, 8), (140000, 16, 8), (66000, 144, 16),
+          (17, 16, 4104), (96, 16, 4104), (2048, 80, 40), (31, 512, 488)]
 SHAPES = {"i8_gemm": GEMM, "i8_gemm_backward": BACKWARD, "i8_gemm_backward_weight": WEIGHT}
 
 

@@ -35,8 +35,8 @@ def lib():
 VALID = {
     "i8_gemv": ((4, 16, 4, 16), (8, 64, 11008)),
     "i8_gemm": ((16, 4, 16, 4, 16), (130, 64, 65536)),
-    "i8_gemm_backward": ((16, 16, 4, 16), (40, 128, 64)),
-    "i8_gemm_backward_weight": ((16, 16, 4, 16), (40, 128, 64)),
+    "i8_gemm_backward": ((16, 16, 4, 16), (40, 4096, 64)),
+    "i8_gemm_backward_weight": ((16, 16, 4, 16), (4096, 128, 64)),
 }
 
 
