@@ -34,7 +34,7 @@ hipError_t launch_i8_gemv(const float* x, const int8_t* W, const float* sw, floa
 // Result [rows][cols] by tiles of BM x BN, K steps of 128 bytes of the left operand, S splits of
 // the contraction (32-bit partial sums [S][rows][cols] in ws).
 struct I8Plan {
-  bool strip;      // few rows of the result, by a kernel of their own (BM is 0)
+  bool strip;      // few rows or little work, by a kernel of its own (BM is 0)
   int tile;        // of those compiled
   int BM, BN;
   int tiles_m, tiles_n;
