@@ -25,9 +25,9 @@
 // More than 16 rows, and the input's gradient, take it where no splits are needed, the former up
 // to kGroups workgroups, one a CU: it saves the launch that writes A, 2.7 us from a program that
 // launches call by call (6.6 and 9.3 us a small call). On the GPU alone, us, here and by tiles:
-// weights of 64 x 512 over 64 rows 5.5 and 6.6, 256 x 1024 over 1000 7.5 and 11.1, 64 x 4096 over
-// 2048 11.9 and 15.2; input, 4 rows of 1536 x 5120 7.3 and 10.8, 64 of 2048 x 4096 9.7 and 12.9,
-// 128 of 128 x 256 6.1 and 6.0, one of 4096 x 4096 10.2 and 9.5; split, 16 of 8192 x 16384 39.5
+// weights of 64 x 512 over 64 rows 5.5 and 6.6, 256 x 1024 over 1000 7.3 and 11.1, 64 x 4096 over
+// 2048 11.8 and 15.2; input, 4 rows of 1536 x 5120 7.3 and 10.8, 64 of 2048 x 4096 9.5 and 12.9,
+// 128 of 128 x 256 6.1 and 6.0, one of 4096 x 4096 10.0 and 9.5; split, 16 of 8192 x 16384 39.5
 // and 31.4.
 #include <algorithm>
 
@@ -252,11 +252,13 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   const uint8_t* ar = a + (lane & (N - 1)) * kPitch + 16 * (lane >> 4);
   const int kr = 8 * (lane >> 4) + ((lane & 15) >> 1);
   const int bo = wave * kStepCopy + kr * kCols + 8 * (lane & 1), bs = swz_step(kr);
-  auto step = [&](uint8_t* stage, int k) __attribute__((always_inline)) {
+  // tail: -1 where the step issues copies, else how many did not before it
+  auto step = [&](uint8_t* stage, int k, auto tail) __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    // this wave's copies of the step have landed: vmcnt(2 * (NS - 1))
-    constexpr int kLeft = 2 * (NS - 1);
+    // this wave's copies of the step have landed: all but those of the steps behind it
+    constexpr int kTail = decltype(tail)::value;
+    constexpr int kLeft = 2 * (NS - 1 - (kTail > 0 ? kTail : 0));
     __builtin_amdgcn_s_waitcnt(0x0f70 | (kLeft & 15) | (kLeft >> 4) << 14);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -269,6 +271,7 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
 #pragma unroll
     for (int j = 0; j < kCols / 16; ++j)
       acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_halves(b[j]), ax, acc[j], 0, 0, 0);
+    if constexpr (kTail >= 0) return;
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is copied over
@@ -279,10 +282,12 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   int k = kb;
   for (; k + NS <= ke; k += NS)
 #pragma unroll
-    for (int u = 0; u < NS; ++u) step(st[u], k + u);
-#pragma unroll
-  for (int u = 0; u < NS - 1; ++u)
-    if (k + u < ke) step(st[u], k + u);
+    for (int u = 0; u < NS; ++u) step(st[u], k + u, std::integral_constant<int, -1>{});
+  static_assert(NS == 5, "tail");
+  if (k < ke) step(s0, k, std::integral_constant<int, 0>{});
+  if (k + 1 < ke) step(s1, k + 1, std::integral_constant<int, 1>{});
+  if (k + 2 < ke) step(s2, k + 2, std::integral_constant<int, 2>{});
+  if (k + 3 < ke) step(s3, k + 3, std::integral_constant<int, 3>{});
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no copy lands after the workgroup ends
 
   // lane l of a 16 x 16 result holds row l % 16 and four neighbouring columns
