@@ -467,8 +467,11 @@ int i8_gemm(const int8_t* X, const float* sx, const int8_t* W, const float* sw, 
  *   dX[m][k] = sum_n dY[m][n] * sw[n] * W[n][k]
  *   dY bf16 [M][N]     dX bf16 [M][K]
  * (quantizing passes it on unchanged). The products dY * sw of a row are scaled together
- * by a power of two to the range of fp16 and rounded to it, and the sum, in fp32, is scaled
- * back, so gradients need no loss scale. A row of dY with an infinity or a NaN, also one that
+ * by a power of two to the range of fp16 and rounded to it (within 2^-11 of themselves), and
+ * the sum, in fp32, is scaled back, so gradients need no loss scale. Products too small for
+ * that beside their row's largest, by 2^27 and more, still count where the larger ones meet
+ * zeros of W: a result is within 2^-10 of its own terms' magnitudes added up, and its rounding
+ * to bf16, with terms down to 2^-139 of the row's largest. A row of dY with an infinity or a NaN, also one that
  * a product dY * sw past fp32's range makes, has results that are not finite, in every
  * column; other rows are not touched by it. */
 size_t i8_gemm_backward_workspace_bytes(int M, int N, int K);
@@ -480,7 +483,8 @@ int i8_gemm_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint1
  *   dW[n][k] = sum_m dY[m][n] * sx[m] * X[m][k]
  *   dY bf16 [M][N]     X int8 [M][K], sx fp32 [M]     dW bf16 [N][K], overwritten
  * The products dY * sx of a column of dY (with up to 16 output channels: of a part of it)
- * are scaled and rounded as i8_gemm_backward does those of a row. A column of dY with an
+ * are scaled, rounded and, where that loses what a result rests on, mended as
+ * i8_gemm_backward does those of a row. A column of dY with an
  * infinity or a NaN has a row of dW that is not finite; a token whose scale is a NaN leaves
  * nothing finite. */
 size_t i8_gemm_backward_weight_workspace_bytes(int M, int N, int K);

@@ -33,6 +33,7 @@
 
 #include "i8_device.hpp"
 #include "i8_internal.hpp"
+#include "i8_lost.hpp"
 #include "i8_tile.hpp"
 
 namespace q4 {
@@ -52,6 +53,7 @@ struct FewArgs {
   uint16_t* out;       // [rows][cols]
   float* part;         // fp32 [S][rows][cols]
   int rows, depth, cols, tiles, groups, S, chunk;
+  LeftSource left;
 };
 // The rows of the result that a workgroup makes: `count` from `first` on.
 struct Group {
@@ -94,15 +96,21 @@ struct Transposed {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = v[p][e] * f;
   }
-  // the largest of every row of A in this wave
+  // the largest of every row of A in this wave, the least of a lane's values of each (i8_lost.hpp)
+  uint32_t least[8];
   __device__ __forceinline__ void largest(const float (&x)[8][8], const Group& r, int left,
-                                          uint32_t* big) const {
+                                          uint32_t* big) {
     float m[8] = {};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) least[e] = kNoLeast;
 #pragma unroll
     for (int p = 0; p < 8; p += 2)
       if (used(p, r, left))
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] = fmaxf(fmaxf(m[e], fabsf(x[p][e])), fabsf(x[p + 1][e]));
+        for (int e = 0; e < 8; ++e) {
+          m[e] = fmaxf(fmaxf(m[e], fabsf(x[p][e])), fabsf(x[p + 1][e]));
+          least[e] = least_of(least_of(least[e], x[p][e]), x[p + 1][e]);
+        }
     uint32_t b[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) b[e] = magnitude(m[e]);
@@ -113,7 +121,8 @@ struct Transposed {
   static __device__ __forceinline__ int first_wave(int) { return 0; }
   static constexpr int kWavesOfRow = THREADS / kWaveSize;
   __device__ __forceinline__ void store(const float (&x)[8][8], uint8_t* a, int pitch,
-                                        const float* up, const Group& r, int left) const {
+                                        const float* up, uint32_t* lost, const Group& r,
+                                        int left) const {
 #pragma unroll
     for (int p = 0; p < 8; p += 2)
       if (used(p, r, left))  // and so all of the last step
@@ -123,6 +132,19 @@ struct Transposed {
           *reinterpret_cast<half2v*>(a + (8 * half + e) * pitch + p * kPer + 4 * at) =
               half2v{(_Float16)(x[p][e] * f), (_Float16)(x[p + 1][e] * f)};
         }
+    float low = 1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) low = fminf(low, scaled_least(least[e], up[8 * half + e]));
+    if (low >= kLeast16) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float f = up[8 * half + e];
+      float gone = 0.0f;
+#pragma unroll
+      for (int p = 0; p < 8; p += 2)
+        if (used(p, r, left)) gone += fabsf(lost16(x[p][e] * f)) + fabsf(lost16(x[p + 1][e] * f));
+      add_lost(&lost[8 * half + e], gone);
+    }
   }
 };
 
@@ -148,15 +170,20 @@ struct Straight {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = v[p][e] * (8 * at < left ? s[e] : 0.0f);
   }
+  uint32_t least[8];
   __device__ __forceinline__ void largest(const float (&x)[8][8], const Group& r, int left,
-                                          uint32_t* big) const {
+                                          uint32_t* big) {
     uint32_t b[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       float m = 0.0f;
+      least[p] = kNoLeast;
       if (used(p, r, left))
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[p][e]));
+        for (int e = 0; e < 8; ++e) {
+          m = fmaxf(m, fabsf(x[p][e]));
+          least[p] = least_of(least[p], x[p][e]);
+        }
       b[p] = magnitude(m);
     }
     const int p = wave_max_of_eight<1>(b);
@@ -165,7 +192,8 @@ struct Straight {
   static constexpr int kWavesOfRow = kLanes / kWaveSize;
   static __device__ __forceinline__ int first_wave(int i) { return i % kPieces * kWavesOfRow; }
   __device__ __forceinline__ void store(const float (&x)[8][8], uint8_t* a, int pitch,
-                                        const float* up, const Group& r, int left) const {
+                                        const float* up, uint32_t* lost, const Group& r,
+                                        int left) const {
 #pragma unroll
     for (int p = 0; p < 8; ++p)
       if (used(p, r, left)) {
@@ -175,6 +203,18 @@ struct Straight {
         for (int e = 0; e < 8; ++e) h[e] = (_Float16)(x[p][e] * f);
         *reinterpret_cast<half8*>(a + (p * kPieces + part) * pitch + 16 * at) = h;
       }
+    float low = 1.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      low = fminf(low, scaled_least(least[p], up[p * kPieces + part]));
+    if (low >= kLeast16) return;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      float gone = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gone += fabsf(lost16(x[p][e] * up[p * kPieces + part]));
+      add_lost(&lost[p * kPieces + part], gone);
+    }
   }
 };
 
@@ -187,6 +227,7 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   __shared__ __attribute__((aligned(16))) uint8_t a[N * kPitch];
   __shared__ uint32_t big[kWaves][N];
   __shared__ float up[N], down[N];
+  __shared__ uint32_t lost[N];
   // The steps' stages are apart, so that the compiler can tell a copy into one from a read of
   // another; in each every wave has its own part.
   __shared__ __attribute__((aligned(1024))) uint8_t s0[kWaves * kStepCopy], s1[kWaves * kStepCopy],
@@ -239,9 +280,10 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
     const PowerOfTwo f = to_fp16_range(b);
     up[t] = f.up;
     down[t] = f.down;
+    lost[t] = 0;
   }
   lds_only_barrier();
-  dy.store(x, a, kPitch, up, rows, left);
+  dy.store(x, a, kPitch, up, lost, rows, left);
   lds_only_barrier();
 
   float4v acc[kCols / 16];
@@ -298,10 +340,17 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   for (int j = 0; j < kCols / 16; ++j) sums[(wave * (kCols / 16) + j) * kWaveSize + lane] = acc[j];
   __syncthreads();
   const int n = lane & 15, c = j0 + 16 * wave + 4 * (lane >> 4);
-  if (wave >= kCols / 16 || n >= rows.count || c >= g.cols) return;
-  float4v sum = sums[wave * kWaveSize + lane];
+  if (wave >= kCols / 16) return;
+  float4v total[1][1];
+  float4v& sum = total[0][0];
+  sum = sums[wave * kWaveSize + lane];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) sum += sums[(w * (kCols / 16) + wave) * kWaveSize + lane];
+  const bool live = n < rows.count && c < g.cols;
+  const float limit[1] = {live ? lost_limit(lost[n & (N - 1)]) : 0.0f};
+  const float row_up[1] = {up[n & (N - 1)]};
+  mend_lost<16>(total, g.left, first, j0 + 16 * wave, c0, c0 + left, limit, row_up);
+  if (!live) return;
   sum *= down[n];
   if (g.S > 1) {
     *reinterpret_cast<float4v*>(g.part + ((size_t)sp * g.rows + first + n) * g.cols + c) = sum;
@@ -338,7 +387,8 @@ hipError_t launch_i8_few_gradient(const uint16_t* dY, bool transposed, const flo
                                   const int8_t* B, uint16_t* out, int rows, int cols, int depth,
                                   float* part, const I8Plan& p, hipStream_t st) {
   const FewArgs g{dY,   scale, B,    out, part, rows, depth, cols, (cols + kCols - 1) / kCols,
-                  rows <= 8 ? 1 : (rows + 15) / 16, p.S, p.kper * 64};
+                  rows <= 8 ? 1 : (rows + 15) / 16, p.S, p.kper * 64,
+                  {dY, scale, B, transposed ? 1 : depth, transposed ? rows : 1, cols}};
   if (!transposed)
     rows <= 8 ? launch<Straight, 8, 8>(g, st) : launch<Straight, 16, 8>(g, st);
   else if (rows == 8)
@@ -347,7 +397,7 @@ hipError_t launch_i8_few_gradient(const uint16_t* dY, bool transposed, const flo
     p.S == 1 ? launch<Transposed, 16, 8>(g, st) : launch<Transposed, 16, 4>(g, st);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;
-  return launch_i8_gradient_finish(part, nullptr, out, rows, cols, p.S, st);
+  return launch_i8_gradient_finish(part, nullptr, nullptr, g.left, out, rows, depth, p.S, st);
 }
 
 }  // namespace q4

@@ -19,6 +19,7 @@
 
 #include "i8_device.hpp"
 #include "i8_internal.hpp"
+#include "i8_lost.hpp"
 #include "i8_tile.hpp"
 
 namespace q4 {
@@ -32,6 +33,8 @@ struct GradArgs {
   const uint16_t* A;  // fp16 [rows][ld]
   const int8_t* B;    // [depth][cols]
   const float* rs;
+  const uint32_t* lost;
+  LeftSource left;    // what A was made of
   uint16_t* out;      // bf16 [rows][cols]
   int rows, cols, depth, ld;
   int tiles_m, tiles_n, nk, S, kper;
@@ -68,8 +71,9 @@ struct ByteCopy {
   }
 };
 
-template <int BM, int BN, int WM, int WN, int NS, bool WHOLE>
-__global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs g) {
+// WAVES a SIMD: what the stages leave room for.
+template <int BM, int BN, int WM, int WN, int NS, bool WHOLE, int WAVES>
+__global__ __launch_bounds__(WM* WN* kWaveSize, WAVES) void i8_gradient_kernel(GradArgs g) {
   constexpr int kThreads = WM * WN * kWaveSize;
   constexpr int WR = BM / WM, WC = BN / WN;
   constexpr int MI = WR / 32, NJ = WC / 32;
@@ -171,8 +175,17 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  // whether a row of this wave has lost anything; loads return in order, so that nothing is
+  // waited for that the first products do not need
+  const int iw = i0 + wm * WR, rlive = rows - wm * WR;
+  uint32_t lost = 0;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) lost |= g.lost[min(iw + 32 * i + (lane & 31), g.rows - 1)];
+  asm volatile("" ::: "memory");  // the copies below stay below
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
+  const bool any_lost = __any(lost != 0);
   tile_hand_over<kCopies*(NS - 1)>();
 #pragma unroll
   for (int q = 0; q < (WHOLE ? Q : 1); ++q) read(o[q], s0, q);
@@ -188,9 +201,20 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
   tile_hand_over<0>();  // the last copies have landed before results go where they went
 
   // Lane l holds row l % 32 of A, register r column 8 * (r / 4) + 4 * (l / 32) + r % 4.
-  const int iw = i0 + wm * WR, rlive = rows - wm * WR;
   const int jw = j0 + wn * WC;
   const int lr = lane & 31, l4 = 4 * (lane >> 5);
+  if (any_lost && g.S == 1) {  // sums of splits are mended where they are whole
+    int again = lr;  // so that no address is kept from the loads before the loop
+    asm volatile("" : "+v"(again));
+    float limit[MI], up[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int row = min(iw + 32 * i + again, g.rows - 1);
+      limit[i] = 32 * i + lr < rlive ? lost_limit(g.lost[row]) : 0.0f;
+      up[i] = 1.0f / g.rs[row];  // a power of two
+    }
+    mend_lost<32>(acc, g.left, iw, jw, 0, g.depth, limit, up);
+  }
   if (g.S > 1) {
     float* dst = g.part + (size_t)sp * g.rows * g.cols;
 #pragma unroll
@@ -240,9 +264,9 @@ __global__ __launch_bounds__(WM* WN* kWaveSize) void i8_gradient_kernel(GradArgs
   }
 }
 
-template <int BM, int BN, int WM, int WN, int NS, bool WHOLE>
+template <int BM, int BN, int WM, int WN, int NS, bool WHOLE, int WAVES>
 void launch_tile(const GradArgs& g, hipStream_t st) {
-  hipLaunchKernelGGL((i8_gradient_kernel<BM, BN, WM, WN, NS, WHOLE>),
+  hipLaunchKernelGGL((i8_gradient_kernel<BM, BN, WM, WN, NS, WHOLE, WAVES>),
                      dim3((unsigned)(g.tiles_m * g.tiles_n * g.S)), dim3(WM * WN * kWaveSize), 0,
                      st, g);
 }
@@ -273,18 +297,22 @@ I8Plan plan_gradient(int rows, int cols, int depth, int chunks) {
   };
   p.off_a = take((size_t)rows * p.ld * 2);
   p.off_rs = take((size_t)rows * sizeof(float));
+  p.off_lost = take((size_t)rows * sizeof(uint32_t));
   p.off_max = take((size_t)chunks * rows * sizeof(uint32_t));
   p.off_part = take(p.S > 1 ? (size_t)p.S * rows * cols * sizeof(float) : 0);
   p.ws_bytes = at;
   return p;
 }
 
-hipError_t launch_tiles(const int8_t* B, uint16_t* out, int rows, int cols, int depth, uint8_t* w,
+hipError_t launch_tiles(const LeftSource& left, uint16_t* out, int rows, int depth, uint8_t* w,
                         const I8Plan& p, hipStream_t st) {
+  const int cols = left.cols;
   if ((long long)p.tiles_m * p.tiles_n * p.S > 0x3fffffLL) return hipErrorInvalidValue;
   GradArgs g{reinterpret_cast<const uint16_t*>(w + p.off_a),
-             B,
+             left.B,
              reinterpret_cast<const float*>(w + p.off_rs),
+             reinterpret_cast<const uint32_t*>(w + p.off_lost),
+             left,
              out,
              rows,
              cols,
@@ -297,14 +325,14 @@ hipError_t launch_tiles(const int8_t* B, uint16_t* out, int rows, int cols, int 
              p.kper,
              reinterpret_cast<float*>(w + p.off_part)};
   switch (p.tile) {
-    case 0: launch_tile<128, 256, 2, 4, 2, false>(g, st); break;
-    case 1: launch_tile<128, 128, 2, 4, 2, false>(g, st); break;
-    case 2: launch_tile<64, 128, 2, 4, 4, true>(g, st); break;
-    default: launch_tile<32, 128, 1, 4, 4, true>(g, st);
+    case 0: launch_tile<128, 256, 2, 4, 2, false, 4>(g, st); break;
+    case 1: launch_tile<128, 128, 2, 4, 2, false, 6>(g, st); break;
+    case 2: launch_tile<64, 128, 2, 4, 4, true, 4>(g, st); break;
+    default: launch_tile<32, 128, 1, 4, 4, true, 3>(g, st);
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;
-  return launch_i8_gradient_finish(g.part, g.rs, out, rows, cols, p.S, st);
+  return launch_i8_gradient_finish(g.part, g.rs, g.lost, left, out, rows, depth, p.S, st);
 }
 
 }  // namespace
@@ -321,9 +349,10 @@ hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* 
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipError_t err =
       launch_i8_gradient_rows(dY, sw, reinterpret_cast<uint16_t*>(w + p.off_a),
-                              reinterpret_cast<float*>(w + p.off_rs), M, N, p.ld, st);
+                              reinterpret_cast<float*>(w + p.off_rs),
+                              reinterpret_cast<uint32_t*>(w + p.off_lost), M, N, p.ld, st);
   if (err != hipSuccess) return err;
-  return launch_tiles(W, dX, M, K, N, w, p, st);
+  return launch_tiles({dY, sw, W, N, 1, K}, dX, M, N, w, p, st);
 }
 
 I8Plan plan_i8_backward_weight(int M, int N, int K) {
@@ -340,9 +369,10 @@ hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const 
     return launch_i8_few_gradient(dY, true, sx, X, dW, N, K, M, reinterpret_cast<float*>(w), p, st);
   const hipError_t err = launch_i8_gradient_columns(
       dY, sx, reinterpret_cast<uint16_t*>(w + p.off_a), reinterpret_cast<float*>(w + p.off_rs),
-      reinterpret_cast<uint32_t*>(w + p.off_max), M, N, p.ld, st);
+      reinterpret_cast<uint32_t*>(w + p.off_lost), reinterpret_cast<uint32_t*>(w + p.off_max), M, N,
+      p.ld, st);
   if (err != hipSuccess) return err;
-  return launch_tiles(X, dW, N, K, M, w, p, st);
+  return launch_tiles({dY, sx, X, 1, N, K}, dW, N, M, w, p, st);
 }
 
 }  // namespace q4

@@ -17,6 +17,7 @@
 
 #include "i8_device.hpp"
 #include "i8_internal.hpp"
+#include "i8_lost.hpp"
 
 namespace q4 {
 namespace {
@@ -134,9 +135,10 @@ __global__ __launch_bounds__(kRowThreads) void i8_dequantize_short_kernel(
 template <int THREADS, int V, bool LOOP>
 __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
     const uint16_t* __restrict__ dY, const float* __restrict__ sw, _Float16* __restrict__ a,
-    float* __restrict__ rs, int M, int N, int ld) {
-  __shared__ uint32_t at[THREADS / kWaveSize];
+    float* __restrict__ rs, uint32_t* __restrict__ lost, int M, int N, int ld) {
+  __shared__ uint32_t at[THREADS / kWaveSize], units;
   for (int m = blockIdx.x; m < M; m += gridDim.x) {
+    if (threadIdx.x == 0) units = 0;
     const uint16_t* yr = dY + (size_t)m * N;
     _Float16* ar = a + (size_t)m * ld;
     float x[V][8];
@@ -156,17 +158,21 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
         for (int e = 0; e < 8; ++e) x[v][e] = in ? y[v][e] * x[v][e] : 0.0f;
       }
     };
-    uint32_t big = 0;
+    uint32_t big = 0, least = kNoLeast;
     for (int n0 = 0; n0 < N; n0 += THREADS * 8 * V) {
       load(n0);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) big = max(big, magnitude(x[v][e]));
+        for (int e = 0; e < 8; ++e) {
+          big = max(big, magnitude(x[v][e]));
+          least = least_of(least, x[v][e]);
+        }
       if (!LOOP) break;
     }
     const PowerOfTwo p = to_fp16_range(workgroup_max<THREADS>(big, at));
     if (threadIdx.x == 0) rs[m] = p.down;
+    const bool losing = may_lose(least, p.up);
     for (int n0 = 0; n0 < ld; n0 += THREADS * 8 * V) {
       if (LOOP) load(n0);
 #pragma unroll
@@ -177,10 +183,17 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = (_Float16)(x[v][e] * p.up);
         *reinterpret_cast<half8*>(ar + n) = h;
+        if (losing) {
+          float gone = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) gone += fabsf(lost16(x[v][e] * p.up));
+          add_lost(&units, gone);
+        }
       }
       if (!LOOP) break;
     }
-    if (THREADS > kWaveSize) __syncthreads();
+    lds_only_barrier();
+    if (threadIdx.x == 0) lost[m] = units;
   }
 }
 
@@ -199,9 +212,9 @@ bool columns_once(int M, int N) { return M <= kOnceRows && N <= kOnceCols; }
 template <int THREADS, int P>
 __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
     const uint16_t* __restrict__ dY, const float* __restrict__ sx, _Float16* __restrict__ a,
-    float* __restrict__ rs, int M, int N, int ld) {
+    float* __restrict__ rs, uint32_t* __restrict__ lost, int M, int N, int ld) {
   constexpr int kWaves = THREADS / kWaveSize;
-  __shared__ uint32_t at[kWaves][8];
+  __shared__ uint32_t at[kWaves][8], units[8];
   __shared__ float factor[8];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int n = xcd_logical_tile(blockIdx.x, gridDim.x) * 8;
@@ -219,13 +232,19 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
   auto value = [&](int p, int h, int e) {
     return 2 * (p * THREADS + t) + h < M ? v[p][h][e] * s[p][h] : 0.0f;
   };
-  uint32_t big[8] = {};
+  uint32_t big[8] = {}, least[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) least[e] = kNoLeast;
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) big[e] = max(big[e], magnitude(value(p, h, e)));
+      for (int e = 0; e < 8; ++e) {
+        const float f = value(p, h, e);
+        big[e] = max(big[e], magnitude(f));
+        least[e] = least_of(least[e], f);
+      }
   const int e = wave_max_of_eight<1>(big);
   if (lane < 8) at[wave][e] = big[0];
   __syncthreads();
@@ -240,9 +259,11 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
     if (lane < 8) {
       factor[lane] = f.up;
       rs[n + lane] = f.down;
+      units[lane] = 0;
     }
   }
   __syncthreads();
+  float low = 1.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float up = factor[e];
@@ -253,7 +274,19 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
         *reinterpret_cast<half2v*>(a + (size_t)(n + e) * ld + m) =
             half2v{(_Float16)(value(p, 0, e) * up), (_Float16)(value(p, 1, e) * up)};
     }
+    low = fminf(low, scaled_least(least[e], up));
   }
+  if (low < kLeast16)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float gone = 0.0f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        gone += fabsf(lost16(value(p, 0, e) * factor[e])) + fabsf(lost16(value(p, 1, e) * factor[e]));
+      add_lost(&units[e], gone);
+    }
+  lds_only_barrier();
+  if (t < 8) lost[n + t] = units[t];
 }
 
 // Largest |dY * sx| of 64 columns in a chunk of the rows. Every workgroup of the second kernel
@@ -268,7 +301,7 @@ int max_rows(int M) {  // of a chunk
 
 __global__ __launch_bounds__(kRowThreads) void i8_column_max_kernel(
     const uint16_t* __restrict__ dY, const float* __restrict__ sx, uint32_t* __restrict__ big,
-    int M, int N, int tiles_n, int chunk_rows) {
+    uint32_t* __restrict__ lost, int M, int N, int tiles_n, int chunk_rows) {
   __shared__ uint32_t at[kRowLanes][kCols];
   const int c8 = (int)threadIdx.x % kColLanes, r = (int)threadIdx.x / kColLanes;
   const int n = ((int)blockIdx.x % tiles_n) * kCols + c8 * 8;
@@ -294,6 +327,7 @@ __global__ __launch_bounds__(kRowThreads) void i8_column_max_kernel(
     for (int i = 0; i < kRowLanes; ++i) v = max(v, at[i][threadIdx.x]);
     const int col = ((int)blockIdx.x % tiles_n) * kCols + (int)threadIdx.x;
     if (col < N) big[(size_t)chunk * N + col] = v;
+    if (col < N && chunk == 0) lost[col] = 0;  // for the second kernel
   }
 }
 
@@ -302,12 +336,13 @@ __global__ __launch_bounds__(kRowThreads) void i8_column_max_kernel(
 // column.
 __global__ __launch_bounds__(kRowThreads) void i8_gradient_columns_kernel(
     const uint16_t* __restrict__ dY, const float* __restrict__ sx,
-    const uint32_t* __restrict__ big, _Float16* __restrict__ a, float* __restrict__ rs, int M,
-    int N, int ld, int tiles_n, int chunks) {
+    const uint32_t* __restrict__ big, _Float16* __restrict__ a, float* __restrict__ rs,
+    uint32_t* __restrict__ lost, int M, int N, int ld, int tiles_n, int chunks) {
   constexpr int kPairs = kChunkRows / 2 / kRowLanes;  // of a lane
   constexpr int kPitch = 64 + 1;  // dwords of a column: eight columns on are eight banks on
   __shared__ uint32_t tile[kCols * kPitch];
   __shared__ float up[kCols];
+  __shared__ uint32_t units[kCols];
   const int n0 = ((int)blockIdx.x % tiles_n) * kCols;
   const int m0 = (int)blockIdx.x / tiles_n * kChunkRows;
   const int c8 = (int)threadIdx.x % kColLanes, r = (int)threadIdx.x / kColLanes;
@@ -329,28 +364,38 @@ __global__ __launch_bounds__(kRowThreads) void i8_gradient_columns_kernel(
       for (int c = 0; c < chunks; ++c) b = max(b, big[(size_t)c * N + col]);
     const PowerOfTwo f = to_fp16_range(b);
     up[threadIdx.x] = f.up;
+    units[threadIdx.x] = 0;
     if (col < N && m0 == 0) rs[col] = f.down;
   }
   __syncthreads();
   float u[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) u[e] = up[c8 * 8 + e];
+  const bool live = n0 + c8 * 8 < N;
 #pragma unroll
   for (int p = 0; p < kPairs; p += 2) {
     const int mt = m0 + 2 * p * kRowLanes;  // first of the 128 rows
     if (mt >= ld) break;                    // uniform
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int e = 0; e < 8; ++e) {
+      float f[2][2];
+      uint32_t least = kNoLeast;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-          half2v h;
+      for (int i = 0; i < 2; ++i) {
+        half2v h;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          h[j] = m0 + 2 * ((p + i) * kRowLanes + r) + j < M
-                     ? (_Float16)(v[p + i][j][e] * s[p + i][j] * u[e])
-                     : (_Float16)0.0f;
+        for (int j = 0; j < 2; ++j) {
+          const bool in = m0 + 2 * ((p + i) * kRowLanes + r) + j < M;
+          f[i][j] = in ? v[p + i][j][e] * s[p + i][j] * u[e] : 0.0f;
+          h[j] = (_Float16)f[i][j];
+          least = least_of(least, f[i][j]);
+        }
         tile[(c8 * 8 + e) * kPitch + i * kRowLanes + r] = __builtin_bit_cast(uint32_t, h);
       }
+      if (live && may_lose(least, 1.0f))
+        add_lost(&units[c8 * 8 + e], fabsf(lost16(f[0][0])) + fabsf(lost16(f[0][1])) +
+                                         fabsf(lost16(f[1][0])) + fabsf(lost16(f[1][1])));
+    }
     __syncthreads();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -361,6 +406,9 @@ __global__ __launch_bounds__(kRowThreads) void i8_gradient_columns_kernel(
     }
     __syncthreads();
   }
+  // the loop's last barrier is behind the last addition
+  if (threadIdx.x < kCols && units[threadIdx.x] != 0)  // of a column before the last
+    atomicAdd(&lost[n0 + (int)threadIdx.x], units[threadIdx.x]);
 }
 
 // ---------------------------------------------------------------------------
@@ -396,13 +444,33 @@ __global__ __launch_bounds__(kRowThreads) void i8_finish_kernel(
   __builtin_memcpy(__builtin_assume_aligned(Y + i, sizeof(y)), y, sizeof(y));
 }
 
+// lost: what is mended of sums that need it (i8_lost.hpp), here and not split by split, where the
+// largest terms may all lie in another split
 __global__ __launch_bounds__(kRowThreads) void i8_gradient_finish_kernel(
-    const float* __restrict__ part, const float* __restrict__ rs, uint16_t* __restrict__ out,
-    size_t mn, int cols, int S) {
+    const float* __restrict__ part, const float* __restrict__ rs,
+    const uint32_t* __restrict__ lost, LeftSource left, uint16_t* __restrict__ out, size_t mn,
+    int depth, int S) {
   const size_t i = ((size_t)blockIdx.x * kRowThreads + threadIdx.x) * 4;
+  if (i - (threadIdx.x & 63) * 4 >= mn) return;  // whole waves
+  const size_t at = min(i, mn - 4);              // lanes behind the last repeat it
+  const int row = (int)(at / left.cols), col = (int)(at - (size_t)row * left.cols);
+  float4v v = sum_splits(reinterpret_cast<const float4v*>(part + at), mn / 4, S);
+  const float s = rs ? rs[row] : 1.0f;
+  const float limit = lost && i < mn ? lost_limit(lost[row]) : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    for (uint64_t low = __ballot(fabsf(v[e]) < limit); low != 0; low &= low - 1) {
+      const int l = __builtin_ctzll(low);
+      auto of_lane = [&](auto x) {
+        return __builtin_bit_cast(decltype(x),
+                                  __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
+      };
+      const float sum = lost_sum(left, of_lane(row), 1.0f / of_lane(s), of_lane(limit),
+                                 of_lane(col) + e, 0, depth);
+      if ((int)(threadIdx.x & 63) == l) v[e] += sum;
+    }
+  }
   if (i >= mn) return;
-  const float4v v = sum_splits(reinterpret_cast<const float4v*>(part + i), mn / 4, S);
-  const float s = rs ? rs[i / cols] : 1.0f;
   uint16_t y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = (uint16_t)i8_to_bf16(v[e] * s);
@@ -417,10 +485,10 @@ void quantize(const void* X, int8_t* Q, float* scale, int M, int K, hipStream_t 
 }
 
 template <int THREADS, int V, bool LOOP>
-void gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs, int M, int N,
-                   int ld, hipStream_t st) {
+void gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs, uint32_t* lost,
+                   int M, int N, int ld, hipStream_t st) {
   hipLaunchKernelGGL((i8_gradient_rows_kernel<THREADS, V, LOOP>), dim3(row_grid(M)),
-                     dim3(THREADS), 0, st, dY, sw, reinterpret_cast<_Float16*>(a), rs, M, N, ld);
+                     dim3(THREADS), 0, st, dY, sw, reinterpret_cast<_Float16*>(a), rs, lost, M, N, ld);
 }
 
 }  // namespace
@@ -480,21 +548,21 @@ hipError_t launch_i8_dequantize(const int8_t* Q, const float* scale, void* X, in
 }
 
 hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs,
-                                   int M, int N, int ld, hipStream_t st) {
+                                   uint32_t* lost, int M, int N, int ld, hipStream_t st) {
   if (ld <= 512)
-    gradient_rows<64, 1, false>(dY, sw, a, rs, M, N, ld, st);
+    gradient_rows<64, 1, false>(dY, sw, a, rs, lost, M, N, ld, st);
   else if (ld <= 2048)
-    gradient_rows<256, 1, false>(dY, sw, a, rs, M, N, ld, st);
+    gradient_rows<256, 1, false>(dY, sw, a, rs, lost, M, N, ld, st);
   else if (ld <= 4096)
-    gradient_rows<256, 2, false>(dY, sw, a, rs, M, N, ld, st);
+    gradient_rows<256, 2, false>(dY, sw, a, rs, lost, M, N, ld, st);
   else if (ld <= 8192)
-    gradient_rows<256, 4, false>(dY, sw, a, rs, M, N, ld, st);
+    gradient_rows<256, 4, false>(dY, sw, a, rs, lost, M, N, ld, st);
   else if (ld <= 12288)
-    gradient_rows<256, 6, false>(dY, sw, a, rs, M, N, ld, st);
+    gradient_rows<256, 6, false>(dY, sw, a, rs, lost, M, N, ld, st);
   else if (ld <= 16384)
-    gradient_rows<256, 8, false>(dY, sw, a, rs, M, N, ld, st);
+    gradient_rows<256, 8, false>(dY, sw, a, rs, lost, M, N, ld, st);
   else
-    gradient_rows<256, 4, true>(dY, sw, a, rs, M, N, ld, st);
+    gradient_rows<256, 4, true>(dY, sw, a, rs, lost, M, N, ld, st);
   return hipGetLastError();
 }
 
@@ -503,13 +571,14 @@ int i8_max_chunks(int M, int N) {
 }
 
 hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint16_t* a, float* rs,
-                                      uint32_t* big, int M, int N, int ld, hipStream_t st) {
+                                      uint32_t* lost, uint32_t* big, int M, int N, int ld,
+                                      hipStream_t st) {
   if (columns_once(M, N)) {
     auto go = [&](auto threads, auto pairs) {
       constexpr int T = decltype(threads)::value;
       hipLaunchKernelGGL((i8_gradient_columns_once_kernel<T, decltype(pairs)::value>),
                          dim3((unsigned)(N / 8)), dim3(T), 0, st, dY, sx,
-                         reinterpret_cast<_Float16*>(a), rs, M, N, ld);
+                         reinterpret_cast<_Float16*>(a), rs, lost, M, N, ld);
     };
     typedef std::integral_constant<int, 1> One;
     typedef std::integral_constant<int, 1024> Widest;
@@ -531,9 +600,9 @@ hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint1
   const long long grid = (long long)tiles_n * ((M + kChunkRows - 1) / kChunkRows);
   if (grid > 0xffffffLL) return hipErrorInvalidValue;  // below 2^32 lanes
   hipLaunchKernelGGL(i8_column_max_kernel, dim3((unsigned)(tiles_n * maxima)), dim3(kRowThreads), 0,
-                     st, dY, sx, big, M, N, tiles_n, max_rows(M));
+                     st, dY, sx, big, lost, M, N, tiles_n, max_rows(M));
   hipLaunchKernelGGL(i8_gradient_columns_kernel, dim3((unsigned)grid), dim3(kRowThreads), 0, st,
-                     dY, sx, big, reinterpret_cast<_Float16*>(a), rs, M, N, ld, tiles_n, maxima);
+                     dY, sx, big, reinterpret_cast<_Float16*>(a), rs, lost, M, N, ld, tiles_n, maxima);
   return hipGetLastError();
 }
 
@@ -549,12 +618,13 @@ hipError_t launch_i8_finish(const int32_t* part, const float* sx, const float* s
   return hipGetLastError();
 }
 
-hipError_t launch_i8_gradient_finish(const float* part, const float* rs, uint16_t* out, int rows,
-                                     int cols, int S, hipStream_t st) {
-  const size_t mn = (size_t)rows * cols;
+hipError_t launch_i8_gradient_finish(const float* part, const float* rs, const uint32_t* lost,
+                                     const LeftSource& left, uint16_t* out, int rows, int depth,
+                                     int S, hipStream_t st) {
+  const size_t mn = (size_t)rows * left.cols;
   const unsigned grid = (unsigned)((mn / 4 + kRowThreads - 1) / kRowThreads);
-  hipLaunchKernelGGL(i8_gradient_finish_kernel, dim3(grid), dim3(kRowThreads), 0, st, part, rs, out,
-                     mn, cols, S);
+  hipLaunchKernelGGL(i8_gradient_finish_kernel, dim3(grid), dim3(kRowThreads), 0, st, part, rs,
+                     lost, left, out, mn, depth, S);
   return hipGetLastError();
 }
 

@@ -66,17 +66,6 @@ __device__ __forceinline__ void tile_hand_over() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// A barrier for LDS alone: copies from memory stay in flight over it.
-__device__ __forceinline__ void lds_only_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 // Tiles of one pass over the GPU in an order that lets those of an XCD share operands:
 // kGroupRows tile rows go down before the next tile column begins.
 constexpr int kGroupRows = 8;

@@ -1,0 +1,146 @@
+"""Gradients of the 8-bit product whose terms lie far apart: results that rest on terms far below
+their row's largest, because the largest meet zeros, are as near as any other.
+
+The bound holds no part of a row's largest value: each term within half a step of fp16 of itself,
+what lies below fp16's range within as much of a result's terms together, sums in fp32 and the
+result's rounding to bf16. Terms stay above 2^-139 of a row's largest, the documented limit."""
+import numpy as np
+import pytest
+import torch
+
+from moe_experts_amd import datagen
+from tests import i8_ref as ref
+from tests.gpu_util import dev, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.detach().float().cpu().numpy()
+
+
+def bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).bfloat16().to(dev())
+
+
+def near(t, b):
+    """sum_c t[i][c] * b[c][j] and its bound."""
+    b = b.astype(np.float64)
+    v, size = t @ b, np.abs(t) @ np.abs(b)
+    # the product dY * scale in fp32, the rounding to fp16, what falls below it, fp32 sums
+    e = (ref.E32 + 2 * ref.E16 * (1 + ref.E32) + (t.shape[1] + 16) * ref.E32 * (1 + 2 * ref.E16)) * size
+    rel, sub = ref.HALF_STEP["bf16"]
+    return v, e + rel * (np.abs(v) + e) + sub
+
+
+def spread(seed, rows, depth, gap):
+    """Values [rows][depth]: a few of each row 2^gap above the rest, and which columns those are;
+    "all": every size from 1 to 2^-110."""
+    r = datagen.rng(seed)
+    v = r.standard_normal((rows, depth))
+    v = np.where(np.abs(v) < 0.05, 0.5, v)
+    large = np.zeros(depth, dtype=bool)
+    large[r.choice(depth, max(1, depth // 40), replace=False)] = True
+    if gap == "all":
+        return v * 2.0 ** r.permutation(np.linspace(0, -110, depth)), large
+    return np.where(large, v, v * 2.0 ** -gap), large
+
+
+def operand(seed, depth, cols, large):
+    """int8 [depth][cols] that has zeros for the large terms in two of three columns, and is sparse
+    in one."""
+    r = datagen.rng(seed)
+    b = r.integers(-128, 128, (depth, cols)).astype(np.int8)
+    b[np.ix_(large, np.arange(cols) % 3 != 0)] = 0
+    thin = np.flatnonzero(np.arange(cols) % 3 == 2)
+    b[:, thin] *= r.random((depth, len(thin))) < 0.01
+    return b
+
+
+GAPS = [20, 27, 30, 34, 40, 60, 110, "all"]
+#: rows, depth, cols and whether tiles serve the input's and the weights' gradient: few rows, groups
+#: of rows, tiles with and without splits, transposed by one kernel and by two
+SHAPES = [(1, 64, 48, False, None), (5, 200, 80, False, None), (8, 4096, 272, False, False),
+          (16, 2048, 144, False, False), (40, 1000, 272, False, False),
+          (40, 4104, 272, True, True), (72, 2056, 4112, True, True), (264, 512, 1040, True, True),
+          (264, 136, 4112, True, True), (136, 8200, 272, True, True), (4112, 264, 144, True, True),
+          (2104, 72, 8208, True, True), (1032, 200, 6032, True, True)]
+
+
+def tiled(form, M, N, K):
+    from moe_experts_amd import i8_gemm_plan
+    return i8_gemm_plan(form, M, N, K)[0] > 0
+
+
+@pytest.mark.parametrize("gap", GAPS)
+@pytest.mark.parametrize("rows,depth,cols,tiles", [s[:4] for s in SHAPES])
+def test_input(rows, depth, cols, tiles, gap):
+    from moe_experts_amd import i8_gemm_backward
+    assert tiled("i8_gemm_backward", rows, depth, cols) == tiles
+    v, large = spread(1, rows, depth, gap)
+    W = operand(2, depth, cols, large)
+    sw = np.exp(datagen.rng(3).standard_normal(depth) - 4).astype(np.float32)
+    dY = bf16(v * 2.0 ** datagen.rng(4).integers(-30, 30, (rows, 1)))
+    got = i8_gemm_backward(dY, to_dev(W), to_dev(sw))
+    ref.check(host(got), near(host(dY).astype(np.float64) * sw.astype(np.float64), W))
+
+
+@pytest.mark.parametrize("gap", GAPS)
+@pytest.mark.parametrize("rows,depth,cols,tiles", [(*s[:3], s[4]) for s in SHAPES if s[4] is not None]
+                         + [(8, 777, 80, False), (16, 9001, 80, False), (16, 70000, 16, True),
+                            (8, 33, 48, False), (264, 1, 16, False), (264, 131, 4112, True)])
+def test_weights(rows, depth, cols, tiles, gap):
+    from moe_experts_amd import i8_gemm_backward_weight
+    assert tiled("i8_gemm_backward_weight", depth, rows, cols) == tiles
+    v, large = spread(5, rows, depth, gap)
+    X = operand(6, depth, cols, large)
+    sx = np.exp(datagen.rng(7).standard_normal(depth) - 4).astype(np.float32)
+    dY = bf16((v * 2.0 ** datagen.rng(8).integers(-30, 30, (rows, 1))).T)
+    got = i8_gemm_backward_weight(dY, to_dev(X), to_dev(sx))
+    t = np.ascontiguousarray((host(dY).astype(np.float64) * sx.astype(np.float64)[:, None]).T)
+    ref.check(host(got), near(t, X))
+
+
+@pytest.mark.parametrize("rows,depth,cols", [s[:3] for s in SHAPES if s[0] > 1])
+def test_far_terms_stay_with_their_row(rows, depth, cols):
+    """One row with far terms among rows without: those are what they are beside any other, and
+    a call is what it is when it is repeated, bitwise."""
+    from moe_experts_amd import i8_gemm_backward, i8_gemm_backward_weight
+    r = datagen.rng(9)
+    v, large = spread(10, rows, depth, 40)
+    B = to_dev(operand(11, depth, cols, large))
+    s = to_dev(np.exp(r.standard_normal(depth) - 4).astype(np.float32))
+    plain = np.where(np.abs(v) < 2.0 ** -20, v * 2.0 ** 40, v)
+    mixed = plain.copy()
+    mixed[rows // 2] = v[rows // 2]
+    keep = [i for i in range(rows) if i != rows // 2]
+    was, got = (i8_gemm_backward(bf16(a), B, s) for a in (plain, mixed))
+    assert torch.equal(was[keep], got[keep]) and not torch.equal(was, got)
+    assert torch.equal(got, i8_gemm_backward(bf16(mixed), B, s))
+    if rows % 8 == 0:
+        was, got = (i8_gemm_backward_weight(bf16(a.T), B, s) for a in (plain, mixed))
+        assert torch.equal(was[keep], got[keep]) and not torch.equal(was, got)
+        assert torch.equal(got, i8_gemm_backward_weight(bf16(mixed.T), B, s))
+
+
+@pytest.mark.parametrize("gap", [40, "all"])
+@pytest.mark.parametrize("rows,depth,cols", [(16, 2048, 144), (40, 4104, 272), (72, 2056, 4112),
+                                             (264, 512, 1040), (136, 8200, 272)])
+def test_dead_channels(rows, depth, cols, gap):
+    """Columns of zeros beside others, under rows with far terms: exact zeros, and their neighbours
+    what they are without them."""
+    from moe_experts_amd import i8_gemm_backward, i8_gemm_backward_weight
+    v, large = spread(12, rows, depth, gap)
+    B = operand(13, depth, cols, large)
+    dead = datagen.rng(14).random(cols) < 0.3
+    dead[[0, cols - 1]] = True
+    D = B.copy()
+    D[:, dead] = 0
+    s = to_dev(np.exp(datagen.rng(15).standard_normal(depth) - 4).astype(np.float32))
+    calls = [lambda b: i8_gemm_backward(bf16(v), to_dev(b), s)]
+    if rows % 8 == 0:
+        calls.append(lambda b: i8_gemm_backward_weight(bf16(v.T), to_dev(b), s))
+    for call in calls:
+        was, got = host(call(B)), host(call(D))
+        assert not got[:, dead].any() and np.array_equal(got[:, ~dead], was[:, ~dead])
