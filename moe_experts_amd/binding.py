@@ -19,6 +19,7 @@ import os
 import threading
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libq4moe.so")
@@ -451,10 +452,20 @@ def _act(act: str) -> int:
     return a
 
 
+def _no_tangent(t, name: str):
+    if (isinstance(t, torch.Tensor) and torch._C._is_fwd_grad_enabled()
+            and _forward.unpack_dual(t).tangent is not None):
+        raise ValueError(f"{name} has a tangent, which this call does not carry on: call it in the "
+                         "forward of a torch.autograd.Function with a jvp")
+
+
 def _ptr(t, name: str, dtype, numel: int, index: int) -> int:
     """Address of a contiguous tensor of this type and size on device `index`. These calls record
     nothing for torch's autograd: on a tensor that requires a gradient their results would
-    quietly have none, so that is refused while torch records."""
+    quietly have none, so that is refused while torch records; and so are tensors with a tangent
+    of forward-mode differentiation."""
+    if _forward._current_level >= 0:
+        _no_tangent(t, name)
     if (isinstance(t, torch.Tensor) and t.get_device() == index >= 0 and t.dtype is dtype
             and t.numel() == numel and t.is_contiguous() and not t.requires_grad):
         return t.data_ptr()
