@@ -695,6 +695,7 @@ def q4_0_gemm_lora(X: torch.Tensor, B: torch.Tensor, N: int, A: torch.Tensor, Bl
 #: Types of activations and results.
 I8_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _TOO_BIG = -6  # Q4_ETOOBIG
+_NOT_POSITIVE = -1  # Q4_EINVAL
 
 
 def _type(dtype, name: str) -> int:
@@ -709,6 +710,8 @@ def _ints(*sizes):
     shape."""
     if max(sizes) > 0x7fffffff:
         raise Q4Error(_TOO_BIG)
+    if min(sizes) < -0x80000000:
+        raise Q4Error(_NOT_POSITIVE)
 
 
 def _call(f, index: int, *args):
