@@ -15,8 +15,6 @@
 // while its first weights are on their way: a row of 4096 for 4096 x 4096 6.5 us, against
 // 4.7 and 3.2 for a launch that quantizes and the time between the two. With more values it
 // takes longer than that launch (4 rows of 4096: 11.0 against 8.9).
-#include <algorithm>
-
 #include "i8_device.hpp"
 #include "i8_internal.hpp"
 #include "i8_tile.hpp"
@@ -37,7 +35,6 @@ struct StripArgs {
   const float* sw;
   void* Y;
   int M, N, K;
-  int blocks;
 };
 
 // Fused: all of x in registers, the largest of each row by LDS, int8 into xq, rows `pitch`
@@ -113,9 +110,7 @@ __global__ __launch_bounds__(kStripThreads) void i8_few_rows_kernel(StripArgs g)
   uint8_t* const st[4] = {s0, s1, s2, s3};
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int block = (int)(blockIdx.y * gridDim.x + blockIdx.x);
-  if (block >= g.blocks) return;  // the whole workgroup, before any barrier
-  const int n0 = block * 16;
+  const int n0 = (int)blockIdx.x * 16;
   const int K = g.K;
   const int nk = (K + 127) / 128, per = (nk + kWaves - 1) / kWaves;
   const int kb = min(nk, wave * per), ke = min(nk, kb + per);
@@ -207,11 +202,9 @@ __global__ __launch_bounds__(kStripThreads) void i8_few_rows_kernel(StripArgs g)
 }
 
 template <int TYPE, int XROWS, int NS>
-hipError_t launch(StripArgs g, hipStream_t st) {
-  g.blocks = (g.N + 15) / 16;
-  // two dimensions: one of the widest matrices' workgroups would pass 2^32 lanes
-  const int x = std::min(g.blocks, 1 << 20);
-  hipLaunchKernelGGL((i8_few_rows_kernel<TYPE, XROWS, NS>), dim3(x, (g.blocks + x - 1) / x),
+hipError_t launch(const StripArgs& g, hipStream_t st) {
+  // N * K < 2^31 and K >= 16: at most 2^23 workgroups
+  hipLaunchKernelGGL((i8_few_rows_kernel<TYPE, XROWS, NS>), dim3((unsigned)((g.N + 15) / 16)),
                      dim3(kStripThreads), 0, st, g);
   return hipGetLastError();
 }
@@ -222,7 +215,7 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 hipError_t launch_i8_strip(const int8_t* X, const float* sx, const int8_t* W, const float* sw,
                            void* Y, int type, int M, int N, int K, hipStream_t st) {
-  const StripArgs g{X, nullptr, sx, W, sw, Y, M, N, K, 0};
+  const StripArgs g{X, nullptr, sx, W, sw, Y, M, N, K};
   hipError_t err = hipSuccess;
   i8_by_type(type, [&](auto t) {
     if (M <= 8)
@@ -246,7 +239,7 @@ I8GemvPlan plan_i8_gemv(int M, int, int K) {
 hipError_t launch_i8_gemv(const float* x, const int8_t* W, const float* sw, float* y, int M, int N,
                           int K, void* ws, const I8GemvPlan& p, hipStream_t st) {
   if (p.fused) {
-    const StripArgs g{nullptr, x, nullptr, W, sw, y, M, N, K, 0};
+    const StripArgs g{nullptr, x, nullptr, W, sw, y, M, N, K};
     return launch<Q4_TYPE_F32, 0, 3>(g, st);
   }
   int8_t* q = static_cast<int8_t*>(ws);
