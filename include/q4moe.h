@@ -504,6 +504,19 @@ typedef enum q4_i8_form {
 } q4_i8_form;
 int i8_gemm_plan(int form, int M, int N, int K, int* rows, int* cols, int* splits, int* steps);
 
+/* Which form of a row kernel serves a shape, likewise. form: i8_quantize (M rows of K values of 16
+ * bits; N is not looked at), or the kernel that makes the left operand of a gradient's tiles.
+ *   threads  of a workgroup; 0 where a gradient has no such kernel
+ *   pieces   of eight values that a lane holds at once (0: rows of fewer than eight)
+ *   passes   over the data
+ * Fails as the call does for M, N and K; Q4_EINVAL for another form or a null pointer. */
+typedef enum q4_i8_rows_form {
+  Q4_I8_QUANTIZE_ROWS = 0,
+  Q4_I8_BACKWARD_ROWS = 1,
+  Q4_I8_BACKWARD_WEIGHT_ROWS = 2
+} q4_i8_rows_form;
+int i8_rows_plan(int form, int M, int N, int K, int* threads, int* pieces, int* passes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,7 @@ _EXPORTS = ("q4_0_gemv", "q8_0_gemv", "q8_0_gemv_workspace_bytes", "q4_0_gemm", 
             "i8_quantize", "i8_dequantize", "i8_gemv", "i8_gemv_workspace_bytes", "i8_gemm",
             "i8_gemm_workspace_bytes", "i8_gemm_backward", "i8_gemm_backward_workspace_bytes",
             "i8_gemm_backward_weight", "i8_gemm_backward_weight_workspace_bytes", "i8_gemm_plan",
+            "i8_rows_plan",
             "Q4Error")
 
 

@@ -101,6 +101,8 @@ for _name, _ptrs in (("i8_gemv", 4), ("i8_gemm", 5), ("i8_gemm_backward", 4),
     _f.argtypes = [_P] * _ptrs + [_I] * (4 if _name == "i8_gemm" else 3) + [_P, _Z, _P]
 _lib.i8_gemm_plan.restype = _I
 _lib.i8_gemm_plan.argtypes = [_I] * 4 + [ctypes.POINTER(_I)] * 4
+_lib.i8_rows_plan.restype = _I
+_lib.i8_rows_plan.argtypes = [_I] * 4 + [ctypes.POINTER(_I)] * 3
 _lib.i8_quantize.restype = _I
 _lib.i8_quantize.argtypes = [_P, _I, _P, _P, _I, _I, _P]
 _lib.i8_dequantize.restype = _I
@@ -760,6 +762,22 @@ def i8_gemm_plan(form: str, M: int, N: int, K: int):
     _ints(M, N, K)
     v = [_I() for _ in range(4)]
     _check(_lib.i8_gemm_plan(I8_FORMS[form], M, N, K, *[ctypes.byref(i) for i in v]))
+    return tuple(i.value for i in v)
+
+
+#: Calls whose row kernel i8_rows_plan tells.
+I8_ROWS_FORMS = {"i8_quantize": 0, "i8_gemm_backward": 1, "i8_gemm_backward_weight": 2}
+
+
+def i8_rows_plan(form: str, M: int, N: int, K: int):
+    """(threads of a workgroup, pieces of eight values that a lane holds, passes over the data) of
+    the row kernel by which `form` serves a shape: i8_quantize's own (of 16-bit values; N is not
+    looked at), or the one that makes the left operand of a gradient's tiles (0 threads: none)."""
+    if form not in I8_ROWS_FORMS:
+        raise ValueError(f"form must be one of {sorted(I8_ROWS_FORMS)} (got {form!r})")
+    _ints(M, N, K)
+    v = [_I() for _ in range(3)]
+    _check(_lib.i8_rows_plan(I8_ROWS_FORMS[form], M, N, K, *[ctypes.byref(i) for i in v]))
     return tuple(i.value for i in v)
 
 

@@ -343,6 +343,11 @@ I8Plan plan_i8_backward(int M, int N, int K) {
   return plan_gradient(M, K, N, 0);
 }
 
+I8RowsPlan plan_i8_backward_rows(int M, int N, int K) {
+  const I8Plan p = plan_i8_backward(M, N, K);
+  return p.strip ? I8RowsPlan{} : plan_i8_gradient_rows(p.ld);
+}
+
 hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint16_t* dX,
                               int M, int N, int K, void* ws, const I8Plan& p, hipStream_t st) {
   if (p.strip) return launch_i8_few_gradient(dY, false, sw, W, dX, M, K, N, nullptr, p, st);
@@ -359,6 +364,11 @@ I8Plan plan_i8_backward_weight(int M, int N, int K) {
   I8Plan p{};
   if (plan_i8_few_gradient(p, N, K, M, kFewSplits)) return p;
   return plan_gradient(N, K, M, i8_max_chunks(M, N));
+}
+
+I8RowsPlan plan_i8_backward_weight_rows(int M, int N, int K) {
+  const I8Plan p = plan_i8_backward_weight(M, N, K);
+  return p.strip ? I8RowsPlan{} : plan_i8_gradient_columns(M, N, p.ld);
 }
 
 hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx,

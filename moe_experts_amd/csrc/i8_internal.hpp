@@ -11,6 +11,14 @@
 namespace q4 {
 
 // ---- rows (i8_rows.hip) ------------------------------------------------------
+// Which form of a row kernel serves a shape: threads of a workgroup, pieces of eight values that
+// a lane holds, passes over the data.
+struct I8RowsPlan {
+  int threads, pieces, passes;
+};
+I8RowsPlan plan_i8_quantize(int M, int K);
+I8RowsPlan plan_i8_gradient_rows(int ld);
+I8RowsPlan plan_i8_gradient_columns(int M, int N, int ld);
 hipError_t launch_i8_quantize(const void* X, int type, int8_t* Q, float* scale, int M, int K,
                               hipStream_t st);
 hipError_t launch_i8_dequantize(const int8_t* Q, const float* scale, void* X, int type, int M,
@@ -97,10 +105,13 @@ hipError_t launch_i8_gemm(const int8_t* X, const float* sx, const int8_t* W, con
                           hipStream_t st);
 
 I8Plan plan_i8_backward(int M, int N, int K);
+// the row kernel in front of the tiles; zeros where there is none
+I8RowsPlan plan_i8_backward_rows(int M, int N, int K);
 hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* sw, uint16_t* dX,
                               int M, int N, int K, void* ws, const I8Plan& p, hipStream_t st);
 
 I8Plan plan_i8_backward_weight(int M, int N, int K);
+I8RowsPlan plan_i8_backward_weight_rows(int M, int N, int K);
 hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const float* sx,
                                      uint16_t* dW, int M, int N, int K, void* ws, const I8Plan& p,
                                      hipStream_t st);

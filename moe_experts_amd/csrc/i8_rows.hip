@@ -491,37 +491,71 @@ void gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs, 
                      dim3(THREADS), 0, st, dY, sw, reinterpret_cast<_Float16*>(a), rs, lost, M, N, ld);
 }
 
+// The compiled forms of a kernel: threads, pieces of eight values a lane, passes over the data.
+template <int THREADS, int PIECES, int PASSES>
+struct Form {
+  static constexpr int kThreads = THREADS, kPieces = PIECES, kPasses = PASSES;
+};
+template <class... F>
+struct Forms {};
+typedef Forms<Form<64, 1, 1>, Form<256, 1, 1>, Form<256, 2, 1>, Form<256, 4, 1>, Form<256, 6, 1>,
+              Form<256, 8, 1>, Form<256, 4, 2>>
+    RowForms;
+typedef Forms<Form<64, 1, 1>, Form<256, 1, 1>, Form<256, 2, 1>, Form<256, 4, 1>, Form<256, 6, 1>,
+              Form<256, 8, 1>, Form<256, 4, 2>, Form<1024, 1, 1>, Form<1024, 2, 1>>
+    QuantizeForms;
+typedef Forms<Form<64, 2, 1>, Form<256, 2, 1>, Form<512, 2, 1>, Form<1024, 2, 1>, Form<1024, 4, 1>,
+              Form<1024, 8, 1>>
+    ColumnForms;
+
+// Calls `go` with the form that a plan names; false if there is none.
+template <class Go, class... F>
+bool by_form(const I8RowsPlan& p, Forms<F...>, Go&& go) {
+  auto one = [&](auto form) {
+    using T = decltype(form);
+    if (p.threads != T::kThreads || p.pieces != T::kPieces || p.passes != T::kPasses) return false;
+    go(form);
+    return true;
+  };
+  return (one(F{}) || ...);
+}
+
 }  // namespace
+
+// Rows of fewer than eight values have a kernel of their own (pieces 0).
+I8RowsPlan plan_i8_quantize(int M, int K) {
+  if (K < 8) return {kRowThreads, 0, 1};
+  if (K <= 512) return {64, 1, 1};
+  if (K <= 2048) return {256, 1, 1};
+  if (M <= kFewRows && K <= 8192) return {1024, 1, 1};
+  if (M <= kFewRows && K <= 16384) return {1024, 2, 1};
+  if (K <= 4096) return {256, 2, 1};
+  if (K <= 8192) return {256, 4, 1};
+  if (K <= 12288) return {256, 6, 1};
+  if (K <= 16384) return {256, 8, 1};
+  return {256, 4, 2};
+}
 
 hipError_t launch_i8_quantize(const void* X, int type, int8_t* Q, float* scale, int M, int K,
                               hipStream_t st) {
+  const I8RowsPlan p = plan_i8_quantize(M, K);
+  bool found = false;
   i8_by_type(type, [&](auto t) {
     constexpr int TYPE = decltype(t)::value;
-    if (K < 8)
+    if (p.pieces == 0) {
+      found = true;
       hipLaunchKernelGGL((i8_quantize_short_kernel<TYPE>),
                          dim3(row_grid(((long long)M + kRowThreads - 1) / kRowThreads)),
                          dim3(kRowThreads), 0, st, static_cast<const typename Val<TYPE>::T*>(X), Q,
                          scale, M, K);
-    else if (K <= 512)
-      quantize<TYPE, 64, 1, false>(X, Q, scale, M, K, st);
-    else if (K <= 2048)
-      quantize<TYPE, 256, 1, false>(X, Q, scale, M, K, st);
-    else if (M <= kFewRows && K <= 8192)
-      quantize<TYPE, 1024, 1, false>(X, Q, scale, M, K, st);
-    else if (M <= kFewRows && K <= 16384)
-      quantize<TYPE, 1024, 2, false>(X, Q, scale, M, K, st);
-    else if (K <= 4096)
-      quantize<TYPE, 256, 2, false>(X, Q, scale, M, K, st);
-    else if (K <= 8192)
-      quantize<TYPE, 256, 4, false>(X, Q, scale, M, K, st);
-    else if (K <= 12288)
-      quantize<TYPE, 256, 6, false>(X, Q, scale, M, K, st);
-    else if (K <= 16384)
-      quantize<TYPE, 256, 8, false>(X, Q, scale, M, K, st);
-    else
-      quantize<TYPE, 256, 4, true>(X, Q, scale, M, K, st);
+      return;
+    }
+    found = by_form(p, QuantizeForms{}, [&](auto form) {
+      using F = decltype(form);
+      quantize<TYPE, F::kThreads, F::kPieces, F::kPasses == 2>(X, Q, scale, M, K, st);
+    });
   });
-  return hipGetLastError();
+  return found ? hipGetLastError() : hipErrorInvalidValue;
 }
 
 hipError_t launch_i8_dequantize(const int8_t* Q, const float* scale, void* X, int type, int M,
@@ -547,23 +581,34 @@ hipError_t launch_i8_dequantize(const int8_t* Q, const float* scale, void* X, in
   return hipGetLastError();
 }
 
+I8RowsPlan plan_i8_gradient_rows(int ld) {
+  if (ld <= 512) return {64, 1, 1};
+  if (ld <= 2048) return {256, 1, 1};
+  if (ld <= 4096) return {256, 2, 1};
+  if (ld <= 8192) return {256, 4, 1};
+  if (ld <= 12288) return {256, 6, 1};
+  if (ld <= 16384) return {256, 8, 1};
+  return {256, 4, 2};
+}
+
 hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs,
                                    uint32_t* lost, int M, int N, int ld, hipStream_t st) {
-  if (ld <= 512)
-    gradient_rows<64, 1, false>(dY, sw, a, rs, lost, M, N, ld, st);
-  else if (ld <= 2048)
-    gradient_rows<256, 1, false>(dY, sw, a, rs, lost, M, N, ld, st);
-  else if (ld <= 4096)
-    gradient_rows<256, 2, false>(dY, sw, a, rs, lost, M, N, ld, st);
-  else if (ld <= 8192)
-    gradient_rows<256, 4, false>(dY, sw, a, rs, lost, M, N, ld, st);
-  else if (ld <= 12288)
-    gradient_rows<256, 6, false>(dY, sw, a, rs, lost, M, N, ld, st);
-  else if (ld <= 16384)
-    gradient_rows<256, 8, false>(dY, sw, a, rs, lost, M, N, ld, st);
-  else
-    gradient_rows<256, 4, true>(dY, sw, a, rs, lost, M, N, ld, st);
-  return hipGetLastError();
+  const bool found = by_form(plan_i8_gradient_rows(ld), RowForms{}, [&](auto form) {
+    using F = decltype(form);
+    gradient_rows<F::kThreads, F::kPieces, F::kPasses == 2>(dY, sw, a, rs, lost, M, N, ld, st);
+  });
+  return found ? hipGetLastError() : hipErrorInvalidValue;
+}
+
+// Pieces: of a lane, in pairs of rows where one kernel does it all.
+I8RowsPlan plan_i8_gradient_columns(int M, int N, int ld) {
+  if (!columns_once(M, N)) return {kRowThreads, kChunkRows / kRowLanes, 2};
+  if (ld <= 128) return {64, 2, 1};
+  if (ld <= 512) return {256, 2, 1};
+  if (ld <= 1024) return {512, 2, 1};
+  if (ld <= 2048) return {1024, 2, 1};
+  if (ld <= 4096) return {1024, 4, 1};
+  return {1024, 8, 1};
 }
 
 int i8_max_chunks(int M, int N) {
@@ -573,28 +618,15 @@ int i8_max_chunks(int M, int N) {
 hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint16_t* a, float* rs,
                                       uint32_t* lost, uint32_t* big, int M, int N, int ld,
                                       hipStream_t st) {
-  if (columns_once(M, N)) {
-    auto go = [&](auto threads, auto pairs) {
-      constexpr int T = decltype(threads)::value;
-      hipLaunchKernelGGL((i8_gradient_columns_once_kernel<T, decltype(pairs)::value>),
-                         dim3((unsigned)(N / 8)), dim3(T), 0, st, dY, sx,
+  const I8RowsPlan p = plan_i8_gradient_columns(M, N, ld);
+  if (p.passes == 1) {
+    const bool found = by_form(p, ColumnForms{}, [&](auto form) {
+      using F = decltype(form);
+      hipLaunchKernelGGL((i8_gradient_columns_once_kernel<F::kThreads, F::kPieces / 2>),
+                         dim3((unsigned)(N / 8)), dim3(F::kThreads), 0, st, dY, sx,
                          reinterpret_cast<_Float16*>(a), rs, lost, M, N, ld);
-    };
-    typedef std::integral_constant<int, 1> One;
-    typedef std::integral_constant<int, 1024> Widest;
-    if (ld <= 128)
-      go(std::integral_constant<int, 64>{}, One{});
-    else if (ld <= 512)
-      go(std::integral_constant<int, 256>{}, One{});
-    else if (ld <= 1024)
-      go(std::integral_constant<int, 512>{}, One{});
-    else if (ld <= 2048)
-      go(Widest{}, One{});
-    else if (ld <= 4096)
-      go(Widest{}, std::integral_constant<int, 2>{});
-    else
-      go(Widest{}, std::integral_constant<int, 4>{});
-    return hipGetLastError();
+    });
+    return found ? hipGetLastError() : hipErrorInvalidValue;
   }
   const int tiles_n = (N + kCols - 1) / kCols, maxima = i8_max_chunks(M, N);
   const long long grid = (long long)tiles_n * ((M + kChunkRows - 1) / kChunkRows);

@@ -635,4 +635,24 @@ int i8_gemm_plan(int form, int M, int N, int K, int* rows, int* cols, int* split
   return Q4_OK;
 }
 
+int i8_rows_plan(int form, int M, int N, int K, int* threads, int* pieces, int* passes) {
+  if (!threads || !pieces || !passes) return Q4_EINVAL;
+  if (form < Q4_I8_QUANTIZE_ROWS || form > Q4_I8_BACKWARD_WEIGHT_ROWS) return Q4_EINVAL;
+  q4::I8RowsPlan p;
+  if (form == Q4_I8_QUANTIZE_ROWS) {
+    if (M <= 0 || K <= 0) return Q4_EINVAL;
+    if ((long long)M * K > kMaxBytes / 2 || (long long)M * 4 > kMaxBytes) return Q4_ETOOBIG;
+    p = q4::plan_i8_quantize(M, K);
+  } else {
+    const bool input = form == Q4_I8_BACKWARD_ROWS;
+    const int rc = check_i8_gradient_shape(M, N, K, input ? M : N);
+    if (rc != Q4_OK) return rc;
+    p = input ? q4::plan_i8_backward_rows(M, N, K) : q4::plan_i8_backward_weight_rows(M, N, K);
+  }
+  *threads = p.threads;
+  *pieces = p.pieces;
+  *passes = p.passes;
+  return Q4_OK;
+}
+
 }  // extern "C"
