@@ -175,12 +175,13 @@ __global__ __launch_bounds__(WM* WN* kWaveSize, WAVES) void i8_gradient_kernel(G
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // whether a row of this wave has lost anything; loads return in order, so that nothing is
-  // waited for that the first products do not need
+  // whether a row of this wave has lost anything (sums of splits are mended where they are added);
+  // loads return in order, so that nothing is waited for that the first products do not need
   const int iw = i0 + wm * WR, rlive = rows - wm * WR;
   uint32_t lost = 0;
+  if (g.S == 1)
 #pragma unroll
-  for (int i = 0; i < MI; ++i) lost |= g.lost[min(iw + 32 * i + (lane & 31), g.rows - 1)];
+    for (int i = 0; i < MI; ++i) lost |= g.lost[min(iw + 32 * i + (lane & 31), g.rows - 1)];
   asm volatile("" ::: "memory");  // the copies below stay below
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(WM* WN* kWaveSize, WAVES) void i8_gradient_kernel(G
   // Lane l holds row l % 32 of A, register r column 8 * (r / 4) + 4 * (l / 32) + r % 4.
   const int jw = j0 + wn * WC;
   const int lr = lane & 31, l4 = 4 * (lane >> 5);
-  if (any_lost && g.S == 1) {  // sums of splits are mended where they are whole
+  if (any_lost) {
     int again = lr;  // so that no address is kept from the loads before the loop
     asm volatile("" : "+v"(again));
     float limit[MI], up[MI];
