@@ -15,20 +15,25 @@
 // of which fit a CU. Each split scales by the power of two of its own part and takes it back
 // (exact), so splits are sums of their own, added in their order by a second kernel.
 //
-// What bounds it: rank 16 of 1999 rows of 11008 9.3 us, of which B takes 4.4 at a large copy's
+// What bounds it: rank 16 of 1999 rows of 11008 9.9 us, of which B takes 4.4 at a large copy's
 // rate; the rest is the start, dY's way from memory and its 32768 values' conversion (a
-// microsecond on a CU's four units), which the copies in flight only hide as far as they fit
-// LDS. By a transposing kernel and the tiles: 15.8. Rank 16 of 8192 rows of 4096 12.9 us by four
-// waves, 12.7 by eight, of 11008 27.8 and 29.2 (tiles 20.3 and 29.8), of 4096 rows of 4096 9.5
-// and 10.7 (14.6); of a row 5.3 (6.5). Past 64 splits the tiles take over.
+// microsecond on a CU's four units, and 0.4 for the search for what it loses, i8_lost.hpp), which
+// the copies in flight only hide as far as they fit LDS. By a transposing kernel and the tiles:
+// 16.6. Rank 16 of 8192 rows of 4096 14.7 us (tiles 21.5), of 11008 31.5 (31.2), of 4096 rows of
+// 4096 11.2 (16.6), of a row 5.9 (7.2). Four waves and eight took the same at rank 16 of 8192 rows
+// of 4096 (12.9 and 12.7, without the search), four less at 11008 (27.8 and 29.2) and at 4096 rows
+// (9.5 and 10.7). Past 64 splits the tiles take over.
 //
 // More than 16 rows, and the input's gradient, take it where no splits are needed, the former up
-// to kGroups workgroups, one a CU: it saves the launch that writes A, 2.7 us from a program that
-// launches call by call (6.6 and 9.3 us a small call). On the GPU alone, us, here and by tiles:
-// weights of 64 x 512 over 64 rows 5.5 and 6.6, 256 x 1024 over 1000 7.3 and 11.1, 64 x 4096 over
-// 2048 11.8 and 15.2; input, 4 rows of 1536 x 5120 7.3 and 10.8, 64 of 2048 x 4096 9.5 and 12.9,
-// 128 of 128 x 256 6.1 and 6.0, one of 4096 x 4096 10.0 and 9.5; split, 16 of 8192 x 16384 39.5
-// and 31.4.
+// to kGroups workgroups, one a CU (eight waves' LDS leaves no room for two, and four waves hold
+// half the contraction): it saves the launch that writes A, 2.7 us from a program that launches
+// call by call. On the GPU alone, us, here and by tiles: weights of 64 x 512 over 64 rows 5.8 and
+// 7.3, 256 x 1024 over 1000 8.2 and 11.9, 64 x 4096 over 2048 (256 workgroups) 12.9 and 17.4; input,
+// 4 rows of 1536 x 5120 8.8 and 11.5, 64 of 2048 x 4096 (256) 11.2 and 13.4, 128 of 128 x 256 6.3 and
+// 6.5, one of 4096 x 4096 12.9 and 11.6. With more workgroups than CUs: weights of 24 x 11008 over
+// 1999 (344) 19.4 and 16.9, 32 x 11008 20.0 and 17.7, 72 x 4096 over 2000 (320) 21.1 and 17.3,
+// 512 x 1024 over 1000 (512) 14.8 and 12.2; input, 80 rows of 2048 x 4096 (320) 17.8 and 13.7. The
+// input's split: 16 of 8192 x 16384 39.5 and 31.4, without the search.
 #include <algorithm>
 
 #include "i8_device.hpp"

@@ -11,19 +11,21 @@
 //     (256 x 384, one pass of 232 tiles over the CUs: 95 us too, registers spilled).
 //   * Small tiles (WHOLE) read all of the next step's operands before they multiply this
 //     step's: with 64 to 128 cycles of products a quarter, reading one quarter ahead left
-//     them waiting for LDS (130 rows of 4096 x 4096 by 64 x 64: 11.3 -> 9.5 us).
+//     them waiting for LDS (130 rows of 4096 x 4096 by 64 x 64: 11.3 -> 9.5 us; 9.8 now).
 //
-// What bounds it: 2048 rows of 4096 x 11008 take 95 us, 1.95 POP/s. With all CUs busy the power
-// limit holds the clock at 1.5 to 1.7 GHz, at which the matrix cores' own cycles are 55 us;
-// without LDS reads it takes 85 us, without copies 83, with neither 72. A deeper ring of
+// What bounds it: 2048 rows of 4096 x 11008 take 94 to 105 us, from GPU to GPU, 1.76 to 1.96 POP/s.
+// With all CUs busy the power limit holds the clock at 1.69 to 1.72 GHz call after call (2.0 to
+// 2.3 in the 777-row product below, which leaves CUs idle), at which the matrix cores' own cycles
+// are 52 us; where the whole took 95, it took 85 us without LDS reads, 83 without copies, 72 with
+// neither. A deeper ring of
 // stages, registers in place of LDS-DMA, raised priorities and freer scheduling all came out
 // within 3 %.
 //
 // Few tiles are bound by the rate at which a CU copies: one workgroup alone on the GPU takes
 // 0.25 us a step of 64 x 128, 0.18 of 64 x 64 and 0.31 of 128 x 128, that is 80 cycles a step and
 // 21 a KiB (at 64 bytes a cycle it were 16); a fourth stage or other waves over the tile change
-// nothing. 777 rows of 5120 x 1536 take 17.7 us of which 40 such steps are 11: 100 CUs have no
-// tile, and splits that give them one cost more (20.6 us in three).
+// nothing. 777 rows of 5120 x 1536 take 17.5 us of which 40 such steps are 11: 100 CUs have no
+// tile, and splits that give them one cost more (22.8 us in two).
 #include <algorithm>
 
 #include "i8_device.hpp"
@@ -239,11 +241,12 @@ void launch_tile(const GemmArgs& g, int type, hipStream_t st) {
 
 }  // namespace
 
-// Tiles, measured (us a call, bf16 results): 2048 rows of 4096 x 11008: 256 x 192 95, 128 x 256
-// 104, 128 x 128 121; of 4096 x 4096: 46, 39, 45; 777 of 4096 x 4096: 35, 30, 21, and 64 x 128
-// 23; of 5120 x 1536: 64 x 128 17.7, 128 x 128 22 (in 3 splits 20.8), 64 x 64 20; 130 of
-// 4096 x 4096: 12.4, 15, 9.5; 33 of 4096 x 11008: 64 x 64 13.9, 32 x 128 15.5; 20 of 4096 x 4096:
-// 32 x 64 8.0.
+// Tiles, measured (us a call on the GPU, bf16 results): 2048 rows of 4096 x 11008: 256 x 192 101 to
+// 106, 128 x 256 102 to 103, 128 x 128 121 (on another GPU 95, 104 and 121); of 4096 x 4096: 44,
+// 37.4, 44; 777 of 4096 x 4096: 38.5, 27.5, 20.8, and 64 x 128 22.9; of 5120 x 1536: 64 x 128 17.5,
+// 128 x 128 in 3 splits 21.9, 64 x 64 19.7; 130 of 4096 x 4096: 64 x 64 9.8, 64 x 128 12.9,
+// 128 x 128 in 4 splits 18.2; 33 of 4096 x 11008: 64 x 64 10.4, 32 x 64 12.2, 64 x 128 in 2 splits
+// 13.5; 20 of 4096 x 4096: 32 x 64 8.5, 64 x 64 in 4 splits 8.7.
 constexpr I8Tile kTiles[] = {{256, 192, 0.90, 0.90, 0.50},
                              {128, 256, 0.70, 0.70, 0.30},
                              {128, 128, 0.46, 0.46, 0.14},

@@ -11,10 +11,11 @@
 // sign bit turned, a byte behind 0x64 is the half 1024 + 128 + q. Otherwise as the 8-bit
 // product's tiles (64 of the contraction a step).
 //
-// What bounds it: 2048 rows of 4096 x 11008 take 181 us for the input (1.02 PFLOP/s) and 190 for
-// the weights, of which the matrix cores need 75 at the peak clock; the power limit holds it at
-// 1.5 to 1.7 GHz as for a plain bf16 product, whose library form takes 182 us at this
-// size. The row kernels in front take 22 and 27 us, at 4.1 and 5.0 TB/s of what they move.
+// What bounds it: 2048 rows of 4096 x 11008 take 163 to 189 us for the input and 171 to 192 for the
+// weights, from GPU to GPU, of which the matrix cores need 75 at the peak clock; the power limit
+// holds it at 1.67 to 1.81 and 1.44 to 1.53 GHz call after call. A plain bf16 product of the
+// library takes 161 us where these take 163 and 171. The row kernels in front take 22 and 27 us,
+// at 4.1 and 5.0 TB/s of what they move.
 #include <algorithm>
 
 #include "i8_device.hpp"
@@ -274,12 +275,12 @@ void launch_tile(const GradArgs& g, hipStream_t st) {
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Tiles, measured (us, the product alone): 11008 x 4096 results over 2048: 128 x 256 190,
-// 128 x 128 197; 2048 x 4096 over 11008: 181, 192; 1536 x 5120 over 777: 26.2, 24.6; 150 x 11008
-// over 4096: 128 x 128 34, 64 x 128 36, 32 x 128 27; 130 x 4096 over 4096: 19.4 and 18.5 and
-// 16.6 in 3, 2 and 3 splits. Of 256 x 256 no more than of 128 x 256: 192 and 181 (in 2 splits).
-// Two stages do better than more where two workgroups fit a CU by that: 128 x 256 in 3 stages
-// 219 instead of 190.
+// Tiles, measured (us a call on the GPU, with the row kernel): 11008 x 4096 results over 2048:
+// 128 x 256 211, 128 x 128 214; 2048 x 4096 over 11008: 195, 203; 1536 x 5120 over 777: 27.2, 27.6,
+// and 64 x 128 31.3; 150 x 11008 over 4096: 128 x 128 39.8, 64 x 128 39.9, 32 x 128 30.8; 130 x 4096
+// over 4096: 128 x 128 in 4 splits 24.8, 64 x 128 in 2 23.4, 32 x 128 22.2. Two stages do better
+// than more where two workgroups fit a CU by that: 128 x 256 in 3 stages 219 instead of 190, the
+// product alone.
 constexpr I8Tile kTiles[] = {{128, 256, 0.80, 0.72, 0.25},
                              {128, 128, 0.30, 0.28, 0.27},
                              {64, 128, 0.26, 0.20, 0.12},

@@ -22,7 +22,6 @@
 namespace q4 {
 namespace {
 
-
 constexpr int kRowThreads = 256;
 constexpr int kFewRows = 256;       // rows by wider workgroups: no more than one a CU
 constexpr int kMaxGrid = 1 << 20;  // workgroups; each takes every kMaxGrid-th row after its own
@@ -202,9 +201,10 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
 // registers, so that dY is read once for the search and the rounding. A lane has P pairs of
 // neighbouring rows; a pair's values of a column are one dword of the result, and 64 lanes
 // store 256 bytes of a column together. The 16 bytes of a row share their line with those of
-// seven other workgroups, which run on the same XCD. Against the two kernels below, in us:
-// 777 x 1536 4.4 and 9.2, 2048 x 4096 11.3 and 13.9, 8192 x 4096 32 and 50; but 2048 x 11008,
-// which comes from memory, 37 and 28: hence kOnceCols.
+// seven other workgroups, which run on the same XCD. Against the two kernels below, us a call of the
+// gradient on the GPU: 777 rows of 5120 x 1536 27.0 and 33.0, 2048 of 4096 x 4096 81.3 and 86.1, 8192
+// of 4096 x 4096 306 and 304; but 2048 of 4096 x 11008, whose dY comes from memory, 222 and 215, of
+// 1024 x 11008 79.7 and 78.8: hence kOnceCols.
 // ---------------------------------------------------------------------------
 constexpr int kOnceRows = 8192, kOnceCols = 4096;
 bool columns_once(int M, int N) { return M <= kOnceRows && N <= kOnceCols; }

@@ -9,10 +9,17 @@
 //
 // Bound by the weights' way from memory. With the weights loaded straight into the matrix
 // instruction's registers (16 rows of 64 bytes a load): 8 rows of 11008 x 4096 12.1 us, by
-// copies (8 rows of 128 bytes each) 10.2, 4.4 TB/s; a row of 4096 x 4096 4.9 and 4.6.
+// copies (8 rows of 128 bytes each) 9.2 to 9.7, 4.7 to 4.9 TB/s; a row of 4096 x 4096 4.9 and 4.6
+// to 4.9.
+//
+// Stages: 48 KiB of them, so that three workgroups fit a CU: four steps of up to 8 rows, three of
+// 16. A fourth step of 16 rows leaves two workgroups (4096 x 11008 9.55 -> 10.5 us; 11008 x 4096
+// the same, 10.4), a third of 8 does no better (11008 x 4096 9.7 both, one row 9.3 and 9.2), two
+// do worse (10.3, 10.7 of 16 rows). With the quantized rows in LDS two to four steps are the same
+// (a row of 4096 x 4096 6.1 to 6.2, of 8192 x 4096 10.3 to 10.6).
 //
 // fp32 rows of up to kFusedValues values in all are quantized by every workgroup for itself
-// while its first weights are on their way: a row of 4096 for 4096 x 4096 6.5 us, against
+// while its first weights are on their way: a row of 4096 for 4096 x 4096 6.2 to 6.5 us, against
 // 4.7 and 3.2 for a launch that quantizes and the time between the two. With more values it
 // takes longer than that launch (4 rows of 4096: 11.0 against 8.9).
 #include "i8_device.hpp"
