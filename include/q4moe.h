@@ -470,8 +470,10 @@ int i8_gemm(const int8_t* X, const float* sx, const int8_t* W, const float* sw, 
  * by a power of two to the range of fp16 and rounded to it (within 2^-11 of themselves), and
  * the sum, in fp32, is scaled back, so gradients need no loss scale. Products too small for
  * that beside their row's largest, by 2^27 and more, still count where the larger ones meet
- * zeros of W: a result is within 2^-10 of its own terms' magnitudes added up, and its rounding
- * to bf16, with terms down to 2^-139 of the row's largest. A row of dY with an infinity or a NaN, also one that
+ * zeros of W, within 2^-8 of themselves and down to 2^-139 of the row's largest: apart from
+ * them a result is within 2^-10 of its own terms' magnitudes added up, and its rounding to
+ * bf16, whatever else its row holds. Where they count the call takes up to two and a half
+ * times as long. A row of dY with an infinity or a NaN, also one that
  * a product dY * sw past fp32's range makes, has results that are not finite, in every
  * column; other rows are not touched by it. */
 size_t i8_gemm_backward_workspace_bytes(int M, int N, int K);

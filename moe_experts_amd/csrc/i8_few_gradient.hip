@@ -15,9 +15,9 @@
 // of which fit a CU. Each split scales by the power of two of its own part and takes it back
 // (exact), so splits are sums of their own, added in their order by a second kernel.
 //
-// What bounds it: rank 16 of 1999 rows of 11008 9.9 us, of which B takes 4.4 at a large copy's
+// What bounds it: rank 16 of 1999 rows of 11008 10.1 us, of which B takes 4.4 at a large copy's
 // rate; the rest is the start, dY's way from memory and its 32768 values' conversion (a
-// microsecond on a CU's four units, and 0.4 for the search for what it loses, i8_lost.hpp), which
+// microsecond on a CU's four units, and 0.35 for the search for what it loses, i8_lost.hpp), which
 // the copies in flight only hide as far as they fit LDS. By a transposing kernel and the tiles:
 // 16.6. Rank 16 of 8192 rows of 4096 14.7 us (tiles 21.5), of 11008 31.5 (31.2), of 4096 rows of
 // 4096 11.2 (16.6), of a row 5.9 (7.2). Four waves and eight took the same at rank 16 of 8192 rows
@@ -58,7 +58,6 @@ struct FewArgs {
   uint16_t* out;       // [rows][cols]
   float* part;         // fp32 [S][rows][cols]
   int rows, depth, cols, tiles, groups, S, chunk;
-  LeftSource left;
 };
 // The rows of the result that a workgroup makes: `count` from `first` on.
 struct Group {
@@ -151,6 +150,19 @@ struct Transposed {
       add_lost(&lost[8 * half + e], gone);
     }
   }
+  // what store() has lost, as bf16 numbers
+  __device__ __forceinline__ void store_lost(const float (&x)[8][8], uint8_t* a, int pitch,
+                                             const float* up, const Group& r, int left) const {
+#pragma unroll
+    for (int p = 0; p < 8; p += 2)
+      if (used(p, r, left))
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f = up[8 * half + e];
+          *reinterpret_cast<uint32_t*>(a + (8 * half + e) * pitch + p * kPer + 4 * at) =
+              lost_bf16(x[p][e] * f) | lost_bf16(x[p + 1][e] * f) << 16;
+        }
+  }
 };
 
 // For the input dY stands as A does: value p, e of a lane is column 8 * at + e of row
@@ -221,6 +233,19 @@ struct Straight {
       add_lost(&lost[p * kPieces + part], gone);
     }
   }
+  __device__ __forceinline__ void store_lost(const float (&x)[8][8], uint8_t* a, int pitch,
+                                             const float* up, const Group& r, int left) const {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float f = up[p * kPieces + part];
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = lost_bf16(x[p][2 * i] * f) | lost_bf16(x[p][2 * i + 1] * f) << 16;
+      *reinterpret_cast<uint4*>(a + (p * kPieces + part) * pitch + 16 * at) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
 };
 
 template <class Dy, int N, int kWaves>
@@ -232,7 +257,8 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   __shared__ __attribute__((aligned(16))) uint8_t a[N * kPitch];
   __shared__ uint32_t big[kWaves][N];
   __shared__ float up[N], down[N];
-  __shared__ uint32_t lost[N];
+  __shared__ uint32_t lost[N], at_risk[kCols / 16];
+  __shared__ uint64_t live[kWaves];  // a bit a column of B that holds more than zeros in a wave's part
   // The steps' stages are apart, so that the compiler can tell a copy into one from a read of
   // another; in each every wave has its own part.
   __shared__ __attribute__((aligned(1024))) uint8_t s0[kWaves * kStepCopy], s1[kWaves * kStepCopy],
@@ -249,12 +275,6 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
   const int nk = (left + kStepRows - 1) / kStepRows, per = (nk + kWaves - 1) / kWaves;
   const int kb = min(nk, wave * per), ke = min(nk, kb + per);
 
-  // dY first, all of it at once: loads return in order, and B is much
-  Dy dy;
-  dy.load(g, rows, c0, left);
-  asm volatile("" ::: "memory");  // the copies below stay below
-  __builtin_amdgcn_sched_barrier(0);
-
   // Copies: four lanes a row of 64 bytes. Rows past the last are past the end and become
   // zeros, rows of the next split meet zeros of A, columns past the last are not kept; steps
   // past the last copy zeros, without an access of memory, and are not read.
@@ -268,94 +288,161 @@ __global__ __launch_bounds__(kWaves* kWaveSize) void i8_few_gradient_kernel(FewA
     copy16(rb, mine, k < ke ? at : kPastEnd, so);
     copy16(rb, mine + kStepCopy / 2, k < ke ? at + 16u * (uint32_t)g.cols : kPastEnd, so);
   };
+  // dY first, all of it at once: loads return in order, and B is much; then the first copies of B,
+  // then dY times the scales
+  Dy dy;
+  auto begin = [&](float (&x)[8][8]) __attribute__((always_inline)) {
+    dy.load(g, rows, c0, left);
+    asm volatile("" ::: "memory");  // the copies below stay below
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
+    for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      if (dy.used(p, rows, left)) dy.multiply(x[p], p, left);
+  };
 
-  // fmaxf passes over NaN: what a row with one is scaled by does not matter.
-  float x[8][8];
-#pragma unroll
-  for (int p = 0; p < 8; ++p)
-    if (dy.used(p, rows, left)) dy.multiply(x[p], p, left);
-  dy.largest(x, rows, left, big[wave]);
-  lds_only_barrier();
-  if (t < N) {
-    uint32_t b = 0;
-#pragma unroll
-    for (int w = 0; w < Dy::kWavesOfRow; ++w) b = max(b, big[Dy::first_wave(t) + w][t]);
-    const PowerOfTwo f = to_fp16_range(b);
-    up[t] = f.up;
-    down[t] = f.down;
-    lost[t] = 0;
-  }
-  lds_only_barrier();
-  dy.store(x, a, kPitch, up, lost, rows, left);
-  lds_only_barrier();
-
-  float4v acc[kCols / 16];
-#pragma unroll
-  for (int j = 0; j < kCols / 16; ++j) acc[j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
   // Lane l takes row l % 16 of A and rows 8 * (l / 16) .. of a step; of eight rows the upper lanes
   // repeat the lower and are not kept.
   const uint8_t* ar = a + (lane & (N - 1)) * kPitch + 16 * (lane >> 4);
   const int kr = 8 * (lane >> 4) + ((lane & 15) >> 1);
   const int bo = wave * kStepCopy + kr * kCols + 8 * (lane & 1), bs = swz_step(kr);
-  // tail: -1 where the step issues copies, else how many did not before it
-  auto step = [&](uint8_t* stage, int k, auto tail) __attribute__((always_inline)) {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    // this wave's copies of the step have landed: all but those of the steps behind it
-    constexpr int kTail = decltype(tail)::value;
-    constexpr int kLeft = 2 * (NS - 1 - (kTail > 0 ? kTail : 0));
-    __builtin_amdgcn_s_waitcnt(0x0f70 | (kLeft & 15) | (kLeft >> 4) << 14);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    const half8 ax = *reinterpret_cast<const half8*>(ar + k * (2 * kStepRows));
-    int2v b[kCols / 16];
+  float4v acc[kCols / 16];
+  uint32_t seen[kCols / 16] = {};  // what a column of B holds, one bit over another
+  // The wave's part of the contraction, by the left operand, fp16 in LDS, or by what it has lost.
+  auto contract = [&](auto second) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < kCols / 16; ++j)
-      b[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-          (__attribute__((address_space(3))) int2v*)(stage + bo + ((j ^ bs) << 4)));
+    for (int j = 0; j < kCols / 16; ++j) acc[j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    // tail: -1 where the step issues copies, else how many did not before it
+    auto step = [&](uint8_t* stage, int k, auto tail) __attribute__((always_inline)) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      // this wave's copies of the step have landed: all but those of the steps behind it
+      constexpr int kTail = decltype(tail)::value;
+      constexpr int kLeft = 2 * (NS - 1 - (kTail > 0 ? kTail : 0));
+      __builtin_amdgcn_s_waitcnt(0x0f70 | (kLeft & 15) | (kLeft >> 4) << 14);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      const half8 ax = *reinterpret_cast<const half8*>(ar + k * (2 * kStepRows));
+      int2v b[kCols / 16];
 #pragma unroll
-    for (int j = 0; j < kCols / 16; ++j)
-      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_halves(b[j]), ax, acc[j], 0, 0, 0);
-    if constexpr (kTail >= 0) return;
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is copied over
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    issue(stage, k + NS);
+      for (int j = 0; j < kCols / 16; ++j)
+        b[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) int2v*)(stage + bo + ((j ^ bs) << 4)));
+#pragma unroll
+      for (int j = 0; j < kCols / 16; ++j) {
+        if constexpr (second) {
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              to_bf16s(b[j]), __builtin_bit_cast(bf16x8, ax), acc[j], 0, 0, 0);
+        } else {
+          seen[j] |= (uint32_t)(b[j][0] | b[j][1]);
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_halves(b[j]), ax, acc[j], 0, 0, 0);
+        }
+      }
+      if constexpr (kTail >= 0) return;
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read before it is copied over
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      issue(stage, k + NS);
+    };
+    int k = kb;
+    for (; k + NS <= ke; k += NS)
+#pragma unroll
+      for (int u = 0; u < NS; ++u) step(st[u], k + u, std::integral_constant<int, -1>{});
+    static_assert(NS == 5, "tail");
+    if (k < ke) step(s0, k, std::integral_constant<int, 0>{});
+    if (k + 1 < ke) step(s1, k + 1, std::integral_constant<int, 1>{});
+    if (k + 2 < ke) step(s2, k + 2, std::integral_constant<int, 2>{});
+    if (k + 3 < ke) step(s3, k + 3, std::integral_constant<int, 3>{});
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no copy lands behind this
   };
-  int k = kb;
-  for (; k + NS <= ke; k += NS)
-#pragma unroll
-    for (int u = 0; u < NS; ++u) step(st[u], k + u, std::integral_constant<int, -1>{});
-  static_assert(NS == 5, "tail");
-  if (k < ke) step(s0, k, std::integral_constant<int, 0>{});
-  if (k + 1 < ke) step(s1, k + 1, std::integral_constant<int, 1>{});
-  if (k + 2 < ke) step(s2, k + 2, std::integral_constant<int, 2>{});
-  if (k + 3 < ke) step(s3, k + 3, std::integral_constant<int, 3>{});
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no copy lands after the workgroup ends
-
-  // lane l of a 16 x 16 result holds row l % 16 and four neighbouring columns
+  // The waves' sums of 16 columns, for one of the first four waves: lane l of a 16 x 16 result holds
+  // row l % 16 and four neighbouring columns.
   float4v* sums = reinterpret_cast<float4v*>(a);
   static_assert(kWaves * kCols / 16 * kWaveSize * 16 <= N * kPitch, "sums fit");
-  __syncthreads();  // `a` has been read
+  auto exchange = [&]() __attribute__((always_inline)) {
+    __syncthreads();  // `a` has been read
 #pragma unroll
-  for (int j = 0; j < kCols / 16; ++j) sums[(wave * (kCols / 16) + j) * kWaveSize + lane] = acc[j];
-  __syncthreads();
+    for (int j = 0; j < kCols / 16; ++j)
+      sums[(wave * (kCols / 16) + j) * kWaveSize + lane] = acc[j];
+    __syncthreads();
+    const int own = min(wave, kCols / 16 - 1);
+    float4v sum = sums[own * kWaveSize + lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) sum += sums[(w * (kCols / 16) + own) * kWaveSize + lane];
+    return sum;
+  };
+
+  // fmaxf passes over NaN: what a row with one is scaled by does not matter.
+  {
+    float x[8][8];
+    begin(x);
+    dy.largest(x, rows, left, big[wave]);
+    lds_only_barrier();
+    if (t < N) {
+      uint32_t b = 0;
+#pragma unroll
+      for (int w = 0; w < Dy::kWavesOfRow; ++w) b = max(b, big[Dy::first_wave(t) + w][t]);
+      const PowerOfTwo f = to_fp16_range(b);
+      up[t] = f.up;
+      down[t] = f.down;
+      lost[t] = 0;
+    }
+    lds_only_barrier();
+    dy.store(x, a, kPitch, up, lost, rows, left);
+    lds_only_barrier();
+  }
+  const uint32_t my_lost = lost[lane & (N - 1)];  // row l % N's
+  contract(std::false_type{});
   const int n = lane & 15, c = j0 + 16 * wave + 4 * (lane >> 4);
-  if (wave >= kCols / 16) return;
-  float4v total[1][1];
-  float4v& sum = total[0][0];
-  sum = sums[wave * kWaveSize + lane];
+  const bool alive = wave < kCols / 16 && n < rows.count && c < g.cols;
+  const bool losing = __any(my_lost != 0);  // the same in all waves
+  if (losing) {
+    uint64_t columns = 0;
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) sum += sums[(w * (kCols / 16) + wave) * kWaveSize + lane];
-  const bool live = n < rows.count && c < g.cols;
-  const float limit[1] = {live ? lost_limit(lost[n & (N - 1)]) : 0.0f};
-  const float row_up[1] = {up[n & (N - 1)]};
-  mend_lost<16>(total, g.left, first, j0 + 16 * wave, c0, c0 + left, limit, row_up);
-  if (!live) return;
+    for (int j = 0; j < kCols / 16; ++j) {  // lane l has seen a quarter of column l % 16
+      uint64_t m = __ballot(seen[j] != 0);
+      m |= m >> 32;
+      m |= m >> 16;
+      columns |= (m & 0xffffu) << (16 * j);
+    }
+    if (lane == 0) live[wave] = columns;
+  }
+  float4v sum = exchange();
+  // What the left operand has lost, where a result may rest on it (i8_lost.hpp).
+  if (losing) {
+    uint64_t columns = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) columns |= live[w];
+    const float limit = alive ? lost_limit(my_lost) : 0.0f;
+    bool low = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      low |= fabsf(sum[e]) < limit && (columns >> ((c - j0 + e) & 63) & 1u);
+    const uint64_t mine = __ballot(low);
+    if (wave < kCols / 16 && lane == 0) at_risk[wave] = mine != 0;
+    lds_only_barrier();
+    uint32_t any = 0;
+#pragma unroll
+    for (int w = 0; w < kCols / 16; ++w) any |= at_risk[w];
+    if (__builtin_amdgcn_readfirstlane(any) != 0) {
+      {
+        float x[8][8];
+        begin(x);
+        dy.store_lost(x, a, kPitch, up, rows, left);
+        lds_only_barrier();
+      }
+      contract(std::true_type{});
+      const float4v more = exchange();
+      // of rows at risk in these 16 columns alone, whatever the others hold
+      uint64_t row = mine | mine >> 32;
+      row |= row >> 16;
+      if (row >> n & 1u) sum += more;
+    }
+  }
+  if (!alive) return;
   sum *= down[n];
   if (g.S > 1) {
     *reinterpret_cast<float4v*>(g.part + ((size_t)sp * g.rows + first + n) * g.cols + c) = sum;
@@ -392,8 +479,7 @@ hipError_t launch_i8_few_gradient(const uint16_t* dY, bool transposed, const flo
                                   const int8_t* B, uint16_t* out, int rows, int cols, int depth,
                                   float* part, const I8Plan& p, hipStream_t st) {
   const FewArgs g{dY,   scale, B,    out, part, rows, depth, cols, (cols + kCols - 1) / kCols,
-                  rows <= 8 ? 1 : (rows + 15) / 16, p.S, p.kper * 64,
-                  {dY, scale, B, transposed ? 1 : depth, transposed ? rows : 1, cols}};
+                  rows <= 8 ? 1 : (rows + 15) / 16, p.S, p.kper * 64};
   if (!transposed)
     rows <= 8 ? launch<Straight, 8, 8>(g, st) : launch<Straight, 16, 8>(g, st);
   else if (rows == 8)
@@ -402,7 +488,7 @@ hipError_t launch_i8_few_gradient(const uint16_t* dY, bool transposed, const flo
     p.S == 1 ? launch<Transposed, 16, 8>(g, st) : launch<Transposed, 16, 4>(g, st);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;
-  return launch_i8_gradient_finish(part, nullptr, nullptr, g.left, out, rows, depth, p.S, st);
+  return launch_i8_gradient_finish(part, nullptr, out, rows, cols, p.S, st);
 }
 
 }  // namespace q4

@@ -4,7 +4,8 @@
 // Both are C[i][j] = rs[i] * sum_c A[i][c] * B[c][j] with A fp16 (the bracket, scaled; written
 // by a row kernel, for the weights transposed) and B the int8 operand as it stands in memory,
 // its rows along the contraction: one kernel on the fp16 matrix cores with fp32 sums. Every
-// int8 is an fp16 number, so only A is rounded.
+// int8 is an fp16 number, so only A is rounded; what its smallest values lose by it comes back where a
+// result may rest on it (i8_lost.hpp).
 //
 // B's step is copied into LDS as bytes; ds_read_b64_tr_b8 gives a lane eight values of one
 // column, that is of the contraction, which become halves in ten instructions: with the
@@ -30,12 +31,19 @@ typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr int BK = kStepBytes / 2;  // of the contraction in a step
 
+// How a tile goes over the contraction (i8_lost.hpp): by the left operand; the same, looking which
+// columns of B hold more than zeros, where a row has lost anything (an instruction for every eight
+// values, 1.6 % of a large tile's time); by what the left operand has lost.
+enum Pass { kPlain, kLooking, kLost };
+template <int P>
+using PassTag = std::integral_constant<int, P>;
+
 struct GradArgs {
   const uint16_t* A;  // fp16 [rows][ld]
   const int8_t* B;    // [depth][cols]
   const float* rs;
+  const uint16_t* A2;  // bf16 [rows][ld], what A lost, where lost[row] is not 0
   const uint32_t* lost;
-  LeftSource left;    // what A was made of
   uint16_t* out;      // bf16 [rows][cols]
   int rows, cols, depth, ld;
   int tiles_m, tiles_n, nk, S, kper;
@@ -103,12 +111,6 @@ __global__ __launch_bounds__(WM* WN* kWaveSize, WAVES) void i8_gradient_kernel(G
   ca.init(g.A + (size_t)i0 * g.ld, rows, (uint32_t)g.ld * 2u, t);
   cb.init(g, j0, t);
   constexpr int kCopies = ca.kInstr + cb.kInstr;  // of a wave in a step
-  // steps past the last copy zeros, without an access of memory, and are not read
-  auto issue = [&](uint8_t* stage, int ks) __attribute__((always_inline)) {
-    const int k = min(ks, ke - 1);
-    ca.issue(stage, k, ks < ke ? kStepBytes : 0, wave);  // ld is whole steps
-    cb.issue(stage + kA, k, ks < ke, wave);
-  };
 
   float16v acc[MI][NJ];
 #pragma unroll
@@ -118,7 +120,7 @@ __global__ __launch_bounds__(WM* WN* kWaveSize, WAVES) void i8_gradient_kernel(G
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   struct Operands {
-    half8 a[MI];
+    half8 a[MI];  // or the bits of bf16 numbers
     int2v b[NJ];
   };
   const int ra = wm * WR + (lane & 31);
@@ -139,83 +141,163 @@ __global__ __launch_bounds__(WM* WN* kWaveSize, WAVES) void i8_gradient_kernel(G
           (__attribute__((address_space(3))) int2v*)(stage + bo + q * 16 * BN +
                                                      (((bc + 2 * j) ^ bs) << 4)));
   };
-  auto multiply = [&](const Operands& o) __attribute__((always_inline)) {
+  uint32_t live[NJ] = {};  // what a column of B holds, one bit over another
+  auto multiply = [&](const Operands& o, auto pass) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const half8 b = to_halves(o.b[j]);
+      if constexpr (pass == kLooking) live[j] |= (uint32_t)(o.b[j][0] | o.b[j][1]);
+      if constexpr (pass == kLost) {
+        const bf16x8 b = to_bf16s(o.b[j]);
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, o.a[i], acc[i][j], 0, 0, 0);
-    }
-  };
-  constexpr int Q = BK / 16;
-  Operands o[WHOLE ? 2 * Q : 2];
-  auto step = [&](uint8_t* cur, uint8_t* next, int ks, int half) __attribute__((always_inline)) {
-    if constexpr (WHOLE) {
-      tile_hand_over<kCopies*(NS - 2)>();
+        for (int i = 0; i < MI; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              b, __builtin_bit_cast(bf16x8, o.a[i]), acc[i][j], 0, 0, 0);
+      } else {
+        const half8 b = to_halves(o.b[j]);
 #pragma unroll
-      for (int q = 0; q < Q; ++q) read(o[Q * (1 - half) + q], next, q);
-      issue(cur, ks + NS);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int q = 0; q < Q; ++q) multiply(o[Q * half + q]);
-      __builtin_amdgcn_sched_barrier(0);
-    } else {
-#pragma unroll
-      for (int q = 0; q < Q - 1; ++q) {
-        read(o[(q + 1) & 1], cur, q + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(o[q & 1]);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < MI; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, o.a[i], acc[i][j], 0, 0, 0);
       }
-      tile_hand_over<kCopies*(NS - 2)>();
-      read(o[0], next, 0);
-      issue(cur, ks + NS);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(o[1]);
-      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // whether a row of this wave has lost anything (sums of splits are mended where they are added);
-  // loads return in order, so that nothing is waited for that the first products do not need
-  const int iw = i0 + wm * WR, rlive = rows - wm * WR;
+  // whether a row of the tile has lost anything; loads return in order, so that nothing is waited
+  // for that the first products do not need
   uint32_t lost = 0;
-  if (g.S == 1)
 #pragma unroll
-    for (int i = 0; i < MI; ++i) lost |= g.lost[min(iw + 32 * i + (lane & 31), g.rows - 1)];
+  for (int i = 0; i < BM; i += kWaveSize) lost |= g.lost[min(i0 + i + lane, g.rows - 1)];
   asm volatile("" ::: "memory");  // the copies below stay below
   __builtin_amdgcn_sched_barrier(0);
+  // steps past the last copy zeros, without an access of memory, and are not read
+  auto issue = [&](const RowCopy<BM, kThreads>& left, uint8_t* stage, int ks)
+                   __attribute__((always_inline)) {
+    const int k = min(ks, ke - 1);
+    left.issue(stage, k, ks < ke ? kStepBytes : 0, wave);  // ld is whole steps
+    cb.issue(stage + kA, k, ks < ke, wave);
+  };
+  auto begin = [&](const RowCopy<BM, kThreads>& left) __attribute__((always_inline)) {
 #pragma unroll
-  for (int u = 0; u < NS; ++u) issue(st[u], kb + u);
-  const bool any_lost = __any(lost != 0);
-  tile_hand_over<kCopies*(NS - 1)>();
+    for (int u = 0; u < NS; ++u) issue(left, st[u], kb + u);
+  };
+  // the contraction from kb to ke, behind begin()
+  constexpr int Q = BK / 16;
+  auto contract = [&](const RowCopy<BM, kThreads>& left, auto pass)
+                      __attribute__((always_inline)) {
+    Operands o[WHOLE ? 2 * Q : 2];
+    auto step = [&](uint8_t* cur, uint8_t* next, int ks, int half) __attribute__((always_inline)) {
+      if constexpr (WHOLE) {
+        tile_hand_over<kCopies*(NS - 2)>();
 #pragma unroll
-  for (int q = 0; q < (WHOLE ? Q : 1); ++q) read(o[q], s0, q);
-  // stages and operand sets alternate at compile time
-  constexpr int U = WHOLE && NS % 2 ? 2 * NS : NS;
-  int ks = kb;
-  for (; ks + U <= ke; ks += U)
+        for (int q = 0; q < Q; ++q) read(o[Q * (1 - half) + q], next, q);
+        issue(left, cur, ks + NS);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) step(st[u % NS], st[(u + 1) % NS], ks + u, u & 1);
+        for (int q = 0; q < Q; ++q) multiply(o[Q * half + q], pass);
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
 #pragma unroll
-  for (int u = 0; u < U - 1; ++u)
-    if (ks + u < ke) step(st[u % NS], st[(u + 1) % NS], ks + u, u & 1);
-  tile_hand_over<0>();  // the last copies have landed before results go where they went
+        for (int q = 0; q < Q - 1; ++q) {
+          read(o[(q + 1) & 1], cur, q + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(o[q & 1], pass);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        tile_hand_over<kCopies*(NS - 2)>();
+        read(o[0], next, 0);
+        issue(left, cur, ks + NS);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(o[1], pass);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    tile_hand_over<kCopies*(NS - 1)>();
+#pragma unroll
+    for (int q = 0; q < (WHOLE ? Q : 1); ++q) read(o[q], s0, q);
+    // stages and operand sets alternate at compile time
+    constexpr int U = WHOLE && NS % 2 ? 2 * NS : NS;
+    int ks = kb;
+    for (; ks + U <= ke; ks += U)
+#pragma unroll
+      for (int u = 0; u < U; ++u) step(st[u % NS], st[(u + 1) % NS], ks + u, u & 1);
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u)
+      if (ks + u < ke) step(st[u % NS], st[(u + 1) % NS], ks + u, u & 1);
+    tile_hand_over<0>();  // the last copies have landed before their places are used again
+  };
+  begin(ca);
+  const bool losing = __any(lost != 0);  // the same in all waves
+  if (losing)
+    contract(ca, PassTag<kLooking>{});
+  else
+    contract(ca, PassTag<kPlain>{});
 
   // Lane l holds row l % 32 of A, register r column 8 * (r / 4) + 4 * (l / 32) + r % 4.
+  const int iw = i0 + wm * WR, rlive = rows - wm * WR;
   const int jw = j0 + wn * WC;
   const int lr = lane & 31, l4 = 4 * (lane >> 5);
-  if (any_lost) {
-    int again = lr;  // so that no address is kept from the loads before the loop
-    asm volatile("" : "+v"(again));
-    float limit[MI], up[MI];
+  // What the left operand has lost, where a result may rest on it (i8_lost.hpp): all waves of the
+  // workgroup agree on the rows, a bit each.
+  if (losing) {
+    __shared__ uint32_t at_risk[WN][BM / 32];
+    uint32_t low[MI][NJ];  // a bit a result
+    uint32_t any_low = 0;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int row = min(iw + 32 * i + again, g.rows - 1);
-      limit[i] = 32 * i + lr < rlive ? lost_limit(g.lost[row]) : 0.0f;
-      up[i] = 1.0f / g.rs[row];  // a power of two
+      const float limit =
+          32 * i + lr < rlive ? lost_limit(g.lost[min(iw + 32 * i + lr, g.rows - 1)]) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        low[i][j] = 0;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          low[i][j] |= fabsf(acc[i][j][r]) < limit ? 1u << r : 0u;
+        // held as bits, not as a mask of lanes for every result
+        asm volatile("" : "+v"(low[i][j]));
+        any_low |= low[i][j];
+      }
     }
-    mend_lost<32>(acc, g.left, iw, jw, 0, g.depth, limit, up);
+    uint32_t rows_low[MI] = {};
+    if (__any(any_low != 0)) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        // unless their columns are zeros, or none of the result's: lane l has seen half of
+        // column l % 32
+        const uint64_t seen = __ballot(live[j] != 0);
+        const int left = g.cols - (jw + 32 * j);
+        const uint32_t in = left <= 0 ? 0u : left < 32 ? (1u << left) - 1u : ~0u;
+        const uint32_t columns = (((uint32_t)seen | (uint32_t)(seen >> 32)) & in) >> l4;
+        // the columns of a lane's results, in the order of its registers
+        const uint32_t own = (columns & 15u) | (columns >> 4 & 0xf0u) | (columns >> 8 & 0xf00u) |
+                             (columns >> 12 & 0xf000u);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const uint64_t lanes = __ballot((low[i][j] & own) != 0);
+          rows_low[i] |= (uint32_t)lanes | (uint32_t)(lanes >> 32);
+        }
+      }
+    }
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < MI; ++i) at_risk[wn][wm * MI + i] = rows_low[i];
+    lds_only_barrier();
+    uint32_t any = 0;
+#pragma unroll
+    for (int w = 0; w < WN; ++w)
+#pragma unroll
+      for (int i = 0; i < BM / 32; ++i) any |= at_risk[w][i];
+    if (__builtin_amdgcn_readfirstlane(any) != 0) {
+      RowCopy<BM, kThreads> c2;
+      c2.init(g.A2 + (size_t)i0 * g.ld, rows, (uint32_t)g.ld * 2u, t);
+#pragma unroll
+      for (int i = 0; i < c2.kInstr; ++i) {
+        const int row = (i * kThreads + t) / c2.kChunks;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int w = 0; w < WN; ++w) bits |= at_risk[w][row >> 5];
+        if (!(bits >> (row & 31) & 1u)) c2.off[i] = kPastEnd;
+      }
+      begin(c2);
+      contract(c2, PassTag<kLost>{});
+    }
   }
   if (g.S > 1) {
     float* dst = g.part + (size_t)sp * g.rows * g.cols;
@@ -298,23 +380,29 @@ I8Plan plan_gradient(int rows, int cols, int depth, int chunks) {
     return o;
   };
   p.off_a = take((size_t)rows * p.ld * 2);
+  p.off_a2 = take((size_t)rows * p.ld * 2);
   p.off_rs = take((size_t)rows * sizeof(float));
   p.off_lost = take((size_t)rows * sizeof(uint32_t));
-  p.off_max = take((size_t)chunks * rows * sizeof(uint32_t));
+  p.off_max = take((size_t)2 * chunks * rows * sizeof(uint32_t));
   p.off_part = take(p.S > 1 ? (size_t)p.S * rows * cols * sizeof(float) : 0);
   p.ws_bytes = at;
   return p;
 }
 
-hipError_t launch_tiles(const LeftSource& left, uint16_t* out, int rows, int depth, uint8_t* w,
+LeftOperand left_operand(uint8_t* w, const I8Plan& p) {
+  return {reinterpret_cast<uint16_t*>(w + p.off_a), reinterpret_cast<uint16_t*>(w + p.off_a2),
+          reinterpret_cast<float*>(w + p.off_rs), reinterpret_cast<uint32_t*>(w + p.off_lost), p.ld};
+}
+
+hipError_t launch_tiles(const int8_t* B, uint16_t* out, int rows, int cols, int depth, uint8_t* w,
                         const I8Plan& p, hipStream_t st) {
-  const int cols = left.cols;
   if ((long long)p.tiles_m * p.tiles_n * p.S > 0x3fffffLL) return hipErrorInvalidValue;
-  GradArgs g{reinterpret_cast<const uint16_t*>(w + p.off_a),
-             left.B,
-             reinterpret_cast<const float*>(w + p.off_rs),
-             reinterpret_cast<const uint32_t*>(w + p.off_lost),
-             left,
+  const LeftOperand l = left_operand(w, p);
+  GradArgs g{l.a,
+             B,
+             l.rs,
+             l.a2,
+             l.lost,
              out,
              rows,
              cols,
@@ -334,7 +422,7 @@ hipError_t launch_tiles(const LeftSource& left, uint16_t* out, int rows, int dep
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.S == 1) return err;
-  return launch_i8_gradient_finish(g.part, g.rs, g.lost, left, out, rows, depth, p.S, st);
+  return launch_i8_gradient_finish(g.part, g.rs, out, rows, cols, p.S, st);
 }
 
 }  // namespace
@@ -354,12 +442,9 @@ hipError_t launch_i8_backward(const uint16_t* dY, const int8_t* W, const float* 
                               int M, int N, int K, void* ws, const I8Plan& p, hipStream_t st) {
   if (p.strip) return launch_i8_few_gradient(dY, false, sw, W, dX, M, K, N, nullptr, p, st);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const hipError_t err =
-      launch_i8_gradient_rows(dY, sw, reinterpret_cast<uint16_t*>(w + p.off_a),
-                              reinterpret_cast<float*>(w + p.off_rs),
-                              reinterpret_cast<uint32_t*>(w + p.off_lost), M, N, p.ld, st);
+  const hipError_t err = launch_i8_gradient_rows(dY, sw, left_operand(w, p), M, N, st);
   if (err != hipSuccess) return err;
-  return launch_tiles({dY, sw, W, N, 1, K}, dX, M, N, w, p, st);
+  return launch_tiles(W, dX, M, K, N, w, p, st);
 }
 
 I8Plan plan_i8_backward_weight(int M, int N, int K) {
@@ -380,11 +465,9 @@ hipError_t launch_i8_backward_weight(const uint16_t* dY, const int8_t* X, const 
   if (p.strip)
     return launch_i8_few_gradient(dY, true, sx, X, dW, N, K, M, reinterpret_cast<float*>(w), p, st);
   const hipError_t err = launch_i8_gradient_columns(
-      dY, sx, reinterpret_cast<uint16_t*>(w + p.off_a), reinterpret_cast<float*>(w + p.off_rs),
-      reinterpret_cast<uint32_t*>(w + p.off_lost), reinterpret_cast<uint32_t*>(w + p.off_max), M, N,
-      p.ld, st);
+      dY, sx, left_operand(w, p), reinterpret_cast<uint32_t*>(w + p.off_max), M, N, st);
   if (err != hipSuccess) return err;
-  return launch_tiles({dY, sx, X, 1, N, K}, dW, N, M, w, p, st);
+  return launch_tiles(X, dW, N, K, M, w, p, st);
 }
 
 }  // namespace q4

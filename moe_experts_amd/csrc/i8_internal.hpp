@@ -50,8 +50,9 @@ struct I8Plan {
   int S, kper;     // splits, K steps of one
   size_t off_a;    // gradients: the left operand, fp16 [rows][ld]
   size_t off_rs;   // gradients: fp32 [rows], what a row of the product is multiplied by
-  size_t off_lost; // gradients: uint32 [rows], what rounding a row to fp16 has lost
-  size_t off_max;  // weight gradient: uint32 [chunks of M][N]
+  size_t off_a2;   // gradients: what that has lost, bf16 [rows][ld], of the rows that have lost any
+  size_t off_lost; // gradients: uint32 [rows], the sum of it
+  size_t off_max;  // weight gradient: uint32 [2][chunks of M][N]
   size_t off_part;
   int ld;          // gradients: values of a row of the left operand
   size_t ws_bytes;
@@ -126,29 +127,26 @@ hipError_t launch_i8_few_gradient(const uint16_t* dY, bool transposed, const flo
                                   float* part, const I8Plan& p, hipStream_t st);
 
 // ---- left operands of the gradients, sums of splits (i8_rows.hip) --------------
-// The left operand's origin: dY's value of row i, place c of the contraction at
-// i * row_step + c * step.
-struct LeftSource {
-  const uint16_t* dY;
-  const float* scale;  // [depth]
-  const int8_t* B;     // [depth][cols]
-  int row_step, step, cols;
+struct LeftOperand {
+  uint16_t* a;     // fp16 [rows][ld]
+  uint16_t* a2;    // what its values below fp16's normal range lost (i8_lost.hpp), bf16 [rows][ld],
+                   // where lost[row] is not 0
+  float* rs;       // [rows]
+  uint32_t* lost;  // [rows]
+  int ld;
 };
-// a[m][n] = fp16(dY[m][n] * sw[n] * 2^e), n < ld (zero past N), rs[m] = 2^-e, lost[m]: what the
-// values below fp16's normal range lost by it (i8_lost.hpp)
-hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs,
-                                   uint32_t* lost, int M, int N, int ld, hipStream_t st);
-// a[n][m] = fp16(dY[m][n] * sx[m] * 2^e), m < ld (zero past M), rs[n] = 2^-e, lost[n]; big:
-// scratch, the largest magnitudes of a column in each of i8_max_chunks(M, N) chunks of the rows
+// a[m][n] = fp16(dY[m][n] * sw[n] * 2^e), n < ld (zero past N), rs[m] = 2^-e
+hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, const LeftOperand& l, int M,
+                                   int N, hipStream_t st);
+// a[n][m] = fp16(dY[m][n] * sx[m] * 2^e), m < ld (zero past M), rs[n] = 2^-e; scratch: the largest
+// and the least magnitudes of a column in each of i8_max_chunks(M, N) chunks of the rows
 int i8_max_chunks(int M, int N);
-hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint16_t* a, float* rs,
-                                      uint32_t* lost, uint32_t* big, int M, int N, int ld,
-                                      hipStream_t st);
+hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, const LeftOperand& l,
+                                      uint32_t* scratch, int M, int N, hipStream_t st);
 hipError_t launch_i8_finish(const int32_t* part, const float* sx, const float* sw, void* Y,
                             int type, int M, int N, int S, hipStream_t st);
-// rs and lost may be null: sums as they are
-hipError_t launch_i8_gradient_finish(const float* part, const float* rs, const uint32_t* lost,
-                                     const LeftSource& left, uint16_t* out, int rows, int depth,
-                                     int S, hipStream_t st);
+// rs may be null: sums as they are
+hipError_t launch_i8_gradient_finish(const float* part, const float* rs, uint16_t* out, int rows,
+                                     int cols, int S, hipStream_t st);
 
 }  // namespace q4

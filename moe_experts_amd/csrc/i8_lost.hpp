@@ -6,22 +6,25 @@
 // operands hold many zeros: where all larger terms meet one, a result rests on what was lost.
 //
 // So whoever rounds a row adds up what its values lose, L. A result's sum is off by no more than
-// 128 L for it. If its terms' magnitudes add up to 2^18 L, that is within 2^-11 of them, as much as
-// the rounding of every term to fp16 is, and it stands. The sum itself tells that of nearly all
-// results. For any other a wave adds up its terms' magnitudes, which in a few steps is enough for
-// nearly all of these, and else the lost parts' products, from dY in fp32. Which results those are
-// depends on their own row and column alone, so rows stay independent of one another. Splits of
-// tiles are mended where they are added; splits of few rows, which are scaled each by itself, each
-// by itself. Terms down to 2^-139 of a row's largest count, where the scaled value leaves fp32's
-// normal range.
+// 128 L for it; if the sum is at least 2^18 L, that is within 2^-11 of it, a rounding of fp16 more,
+// and it stands. Otherwise, unless its column of the int8 operand holds nothing but zeros, its row
+// is multiplied once more: the lost parts, as bf16 numbers (8 bits, fp32's range), are a second left
+// operand, and the tile (or the workgroup of a gradient of few rows) goes over the contraction
+// again with those rows of it, the others zero. A lost part that counts is within 2^-8 of itself,
+// down to 2^-139 of its row's largest, where the scaled value leaves fp32's normal range.
 //
-// Rows whose values lie near one another pay for the search alone: 150 rows of 11008 x 4096 29.3 ->
-// 29.8 us, rank 16 of 1999 rows 9.5 -> 9.9, 777 rows of 5120 x 1536 25.8 -> 26.4, 2048 of 4096 x
-// 11008 202 -> 203 (input) and 212 -> 214 (weights). Gradients of a softmax over 32000 channels,
-// 2048 rows of 4096, whose values cover hundreds of binades (logits of standard deviation 5 and 9):
-// input 583 -> 959 and 527 -> 1475 us, weights 603 -> 639 and 531 -> 604; with one channel of 20
-// dead 596 -> 1106. Added instead to all results of a block of 32 x 32 with one to mend, by the
-// matrix cores and without the early end, the same took 1240 to 10400.
+// Which rows those are depends on the row itself and the int8 operand, so rows stay independent of
+// one another, and no data take more than the contraction twice.
+//
+// Rows whose values lie near one another pay for the search alone, old and new in us: 2048 rows of
+// 4096 x 11008 193.5 and 195.4 (input), 205.4 and 209.8 (weights), 150 rows of 11008 x 4096 29.7 and
+// 30.1, 777 rows of 5120 x 1536 26.2 and 27.4, rank 16 of 1999 rows 9.6 and 10.1; channels of zeros
+// cost nothing more. One token 2^40 above the rest: weights of 4096 x 11008 over 2048 rows 171 and
+// 421, 5120 x 1536 over 777 26.0 and 58.2. Gradients of a softmax over 32000 channels, 2048 rows of
+// 4096, whose values cover hundreds of binades (logits of standard deviation 5 and 9): input 554 and
+// 1011, 480 and 930, weights 573 and 965, 517 and 977. Mended one result at a time by a wave, the
+// softmaxes took less (951, 1466, 623, 596), but what one token or channels of zeros can put at risk
+// up to seconds.
 #pragma once
 
 #include "i8_device.hpp"
@@ -46,147 +49,37 @@ __device__ __forceinline__ bool may_lose(uint32_t least, float up) {
   return scaled_least(least, up) < kLeast16;
 }
 
-// what v loses as fp16
+// what v loses as fp16; exact
 __device__ __forceinline__ float lost16(float v) {
   return fabsf(v) < kLeast16 ? v - (float)(_Float16)v : 0.0f;
+}
+// the same as a bf16 number, to nearest (it is finite)
+__device__ __forceinline__ uint32_t lost_bf16(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, lost16(v));
+  return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
 // Sums over lanes are kept in whole units, rounded up: added in any order they are the same. At most
 // 16 units a value, and fewer than 2^27 values a row.
 __device__ __forceinline__ void add_lost(uint32_t* units, float lost) {
   if (lost > 0.0f) atomicAdd(units, (uint32_t)ceilf(lost * (1.0f / kLostUnit)));
 }
-// below this a result's sum is mended
+// a sum below this does not stand
 __device__ __forceinline__ float lost_limit(uint32_t units) {
   return (float)units * (kLostUnit * kLostLimit);
 }
 
-// Which of R columns of B from col0 on are not all zeros from c0 to c1, a bit each, among those that
-// are wanted; the same for all lanes of the wave. Columns that hold nothing (dead channels) would
-// otherwise be searched to their end for every row.
-template <int R>
-__device__ __forceinline__ uint32_t live_columns(const LeftSource& s, int col0, uint32_t wanted,
-                                                 int c0, int c1) {
-  constexpr int kPieces = R / 16, kPlaces = kWaveSize / kPieces;  // of a load
-  const int lane = threadIdx.x & 63, piece = 16 * (lane % kPieces);
-  uint32_t live = 0;
-#pragma unroll 1
-  for (int c = c0; c < c1 && (wanted & ~live) != 0; c += 8 * kPlaces) {
-    uint32_t any[4] = {};
-    if (col0 + piece < s.cols)
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// Eight int8 as bf16 numbers, exactly.
+__device__ __forceinline__ bf16x8 to_bf16s(int2v q) {
+  uint32_t h[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int at = min(c + u * kPlaces + lane / kPieces, c1 - 1);
-        uint32_t w[4];
-        __builtin_memcpy(w, __builtin_assume_aligned(s.B + (size_t)at * s.cols + col0 + piece, 16), 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) any[i] |= w[i];
-      }
-    uint32_t bits = 0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) bits |= (any[e / 4] >> (8 * (e % 4)) & 255u) != 0 ? 1u << e : 0u;
-    bits <<= piece;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) bits |= (uint32_t)__shfl_xor((int)bits, o);
-    live |= bits;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = (uint32_t)q[i / 2] >> (16 * (i % 2));
+    const float lo = (float)(int8_t)w, hi = (float)(int8_t)(w >> 8);
+    h[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo),
+                                 0x07060302u);
   }
-  return __builtin_amdgcn_readfirstlane(live & wanted);
-}
-
-// Sum of the products of what a row, scaled by `up`, lost from c0 to c1, or 0 as soon as its terms'
-// magnitudes have reached `limit`. Row and column are the same for all lanes of the wave, and so is
-// the result.
-__device__ __forceinline__ float lost_sum(const LeftSource& s, int row, float up, float limit,
-                                          int col, int c0, int c1) {
-  float sum = 0.0f, size = 0.0f;
-  const uint16_t* y = s.dY + (size_t)row * s.row_step;
-#pragma unroll 1
-  for (int c = c0; c < c1; c += 4 * kWaveSize) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int place = c + u * kWaveSize + (int)(threadIdx.x & 63);
-      const size_t at = min(place, c1 - 1);
-      const float v = Val<Q4_TYPE_BF16>::get(y[at * s.step]) * s.scale[at] * up;
-      const float q = place < c1 ? (float)s.B[at * s.cols + col] : 0.0f;
-      size += fabsf(v * q);
-      sum += lost16(v) * q;
-    }
-    if (__any(size >= limit)) return 0.0f;
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-  return sum;
-}
-
-// Mends a wave's MI x NJ blocks of R x R results as the matrix instructions of R rows leave them:
-// lane l holds row row0 + R * i + l % R, register r of block j column col0 + R * j + 8 * (r / 4) +
-// 4 * (l / R) + r % 4. limit and up are the rows', limit 0 for one that is not to be touched. One
-// copy of the loop serves all blocks: the tiles have no registers for more.
-template <int R, int MI, int NJ, class V>
-__device__ __forceinline__ void mend_lost(V (&acc)[MI][NJ], const LeftSource& s, int row0, int col0,
-                                          int c0, int c1, const float (&limit)[MI],
-                                          const float (&up)[MI]) {
-  constexpr int kRegs = R * R / kWaveSize;
-  const int lane = threadIdx.x & 63;
-  uint32_t low[MI * NJ];
-  uint32_t any = 0;
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int r = 0; r < kRegs; ++r)
-        if (col0 + R * j + 8 * (r / 4) + 4 * (lane / R) + r % 4 < s.cols &&
-            fabsf(acc[i][j][r]) < limit[i])
-          bits |= 1u << r;
-      low[i * NJ + j] = bits;
-      any |= bits;
-    }
-  if (!__any(any)) return;
-#pragma unroll 1
-  for (int block = 0; block < MI * NJ; ++block) {
-    uint32_t bits = low[0];
-    float block_limit = limit[0], block_up = up[0];
-#pragma unroll
-    for (int b = 1; b < MI * NJ; ++b)
-      if (block == b) {
-        bits = low[b];
-        block_limit = limit[b / NJ];
-        block_up = up[b / NJ];
-      }
-    // lanes with a result to look at in column `in`, in register `reg`
-    auto rows_of = [&](int in, int& reg) {
-      reg = R == 32 ? in / 8 * 4 + in % 4 : in % 4;
-      return __ballot((bits >> reg & 1u) && lane / R == (R == 32 ? in / 4 % 2 : in / 4));
-    };
-    const int first = col0 + block % NJ * R;
-    int reg;
-    uint32_t wanted = 0;
-#pragma unroll 1
-    for (int in = 0; in < R; ++in) wanted |= rows_of(in, reg) != 0 ? 1u << in : 0u;
-    if (wanted != 0) wanted = live_columns<R>(s, first, wanted, c0, c1);
-#pragma unroll 1
-    for (; wanted != 0; wanted &= wanted - 1) {
-      const int in = __builtin_ctz(wanted);
-#pragma unroll 1
-      for (uint64_t rows = rows_of(in, reg); rows != 0; rows &= rows - 1) {
-        const int l = __builtin_ctzll(rows);
-        auto of_row = [&](float f) {
-          return __builtin_bit_cast(float,
-                                    __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), l));
-        };
-        const float sum = lost_sum(s, row0 + block / NJ * R + l % R, of_row(block_up),
-                                   of_row(block_limit), first + in, c0, c1);
-#pragma unroll
-        for (int b = 0; b < MI * NJ; ++b)
-#pragma unroll
-          for (int r = 0; r < kRegs; ++r) {
-            const float v = acc[b / NJ][b % NJ][r];
-            acc[b / NJ][b % NJ][r] = lane == l && b == block && r == reg ? v + sum : v;
-          }
-      }
-    }
-  }
+  return __builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3]));
 }
 
 }  // namespace q4

@@ -133,13 +133,13 @@ __global__ __launch_bounds__(kRowThreads) void i8_dequantize_short_kernel(
 // One workgroup a row of dY; N and ld are multiples of 8.
 template <int THREADS, int V, bool LOOP>
 __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
-    const uint16_t* __restrict__ dY, const float* __restrict__ sw, _Float16* __restrict__ a,
-    float* __restrict__ rs, uint32_t* __restrict__ lost, int M, int N, int ld) {
+    const uint16_t* __restrict__ dY, const float* __restrict__ sw, LeftOperand l, int M, int N) {
   __shared__ uint32_t at[THREADS / kWaveSize], units;
+  const int ld = l.ld;
   for (int m = blockIdx.x; m < M; m += gridDim.x) {
     if (threadIdx.x == 0) units = 0;
     const uint16_t* yr = dY + (size_t)m * N;
-    _Float16* ar = a + (size_t)m * ld;
+    uint16_t* ar = l.a + (size_t)m * ld;
     float x[V][8];
     // products of the pieces from n0 on, zeros behind the row
     auto load = [&](int n0) {
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
       if (!LOOP) break;
     }
     const PowerOfTwo p = to_fp16_range(workgroup_max<THREADS>(big, at));
-    if (threadIdx.x == 0) rs[m] = p.down;
+    if (threadIdx.x == 0) l.rs[m] = p.down;
     const bool losing = may_lose(least, p.up);
     for (int n0 = 0; n0 < ld; n0 += THREADS * 8 * V) {
       if (LOOP) load(n0);
@@ -192,7 +192,23 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_rows_kernel(
       if (!LOOP) break;
     }
     lds_only_barrier();
-    if (threadIdx.x == 0) lost[m] = units;
+    const uint32_t sum = units;
+    if (threadIdx.x == 0) l.lost[m] = sum;
+    for (int n0 = 0; sum != 0 && n0 < ld; n0 += THREADS * 8 * V) {
+      if (LOOP) load(n0);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int n = n0 + (v * THREADS + (int)threadIdx.x) * 8;
+        if (n >= ld) continue;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = lost_bf16(x[v][2 * e] * p.up) | lost_bf16(x[v][2 * e + 1] * p.up) << 16;
+        *reinterpret_cast<uint4*>(l.a2 + (size_t)m * ld + n) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (!LOOP) break;
+    }
+    lds_only_barrier();  // `units` is read before the next row clears it
   }
 }
 
@@ -211,8 +227,8 @@ bool columns_once(int M, int N) { return M <= kOnceRows && N <= kOnceCols; }
 
 template <int THREADS, int P>
 __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
-    const uint16_t* __restrict__ dY, const float* __restrict__ sx, _Float16* __restrict__ a,
-    float* __restrict__ rs, uint32_t* __restrict__ lost, int M, int N, int ld) {
+    const uint16_t* __restrict__ dY, const float* __restrict__ sx, LeftOperand l, int M, int N) {
+  const int ld = l.ld;
   constexpr int kWaves = THREADS / kWaveSize;
   __shared__ uint32_t at[kWaves][8], units[8];
   __shared__ float factor[8];
@@ -258,7 +274,7 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
     const PowerOfTwo f = to_fp16_range(b);
     if (lane < 8) {
       factor[lane] = f.up;
-      rs[n + lane] = f.down;
+      l.rs[n + lane] = f.down;
       units[lane] = 0;
     }
   }
@@ -271,7 +287,7 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
     for (int p = 0; p < P; ++p) {
       const int m = 2 * (p * THREADS + t);  // ld is even
       if (m < ld)
-        *reinterpret_cast<half2v*>(a + (size_t)(n + e) * ld + m) =
+        *reinterpret_cast<half2v*>(l.a + (size_t)(n + e) * ld + m) =
             half2v{(_Float16)(value(p, 0, e) * up), (_Float16)(value(p, 1, e) * up)};
     }
     low = fminf(low, scaled_least(least[e], up));
@@ -286,11 +302,22 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
       add_lost(&units[e], gone);
     }
   lds_only_barrier();
-  if (t < 8) lost[n + t] = units[t];
+  if (t < 8) l.lost[n + t] = units[t];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (units[e] == 0) continue;  // uniform
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int m = 2 * (p * THREADS + t);
+      if (m < ld)
+        *reinterpret_cast<uint32_t*>(l.a2 + (size_t)(n + e) * ld + m) =
+            lost_bf16(value(p, 0, e) * factor[e]) | lost_bf16(value(p, 1, e) * factor[e]) << 16;
+    }
+  }
 }
 
-// Largest |dY * sx| of 64 columns in a chunk of the rows. Every workgroup of the second kernel
-// reads all chunks' values of its columns, so there are at most kMaxChunks.
+// Largest and least |dY * sx| (i8_lost.hpp) of 64 columns in a chunk of the rows. Every workgroup of
+// the second kernel reads all chunks' values of its columns, so there are at most kMaxChunks.
 constexpr int kCols = 64, kColLanes = kCols / 8, kRowLanes = kRowThreads / kColLanes;
 constexpr int kChunkRows = 256, kMaxChunks = 64;
 
@@ -301,12 +328,15 @@ int max_rows(int M) {  // of a chunk
 
 __global__ __launch_bounds__(kRowThreads) void i8_column_max_kernel(
     const uint16_t* __restrict__ dY, const float* __restrict__ sx, uint32_t* __restrict__ big,
-    uint32_t* __restrict__ lost, int M, int N, int tiles_n, int chunk_rows) {
-  __shared__ uint32_t at[kRowLanes][kCols];
+    uint32_t* __restrict__ least, uint32_t* __restrict__ lost, int M, int N, int tiles_n,
+    int chunk_rows) {
+  __shared__ uint32_t at[2][kRowLanes][kCols];
   const int c8 = (int)threadIdx.x % kColLanes, r = (int)threadIdx.x / kColLanes;
   const int n = ((int)blockIdx.x % tiles_n) * kCols + c8 * 8;
   const int chunk = (int)blockIdx.x / tiles_n;
-  uint32_t b[8] = {};
+  uint32_t b[8] = {}, s8[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s8[e] = kNoLeast;
   if (n < N) {
     const int m1 = (int)min((long long)M, (long long)(chunk + 1) * chunk_rows);
 #pragma unroll 8
@@ -315,19 +345,32 @@ __global__ __launch_bounds__(kRowThreads) void i8_column_max_kernel(
       __builtin_memcpy(v, __builtin_assume_aligned(dY + (size_t)m * N + n, 16), 16);
       const float s = sx[m];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = max(b[e], magnitude(Val<Q4_TYPE_BF16>::get(v[e]) * s));
+      for (int e = 0; e < 8; ++e) {
+        const float f = Val<Q4_TYPE_BF16>::get(v[e]) * s;
+        b[e] = max(b[e], magnitude(f));
+        s8[e] = least_of(s8[e], f);
+      }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) at[r][c8 * 8 + e] = b[e];
+  for (int e = 0; e < 8; ++e) {
+    at[0][r][c8 * 8 + e] = b[e];
+    at[1][r][c8 * 8 + e] = s8[e];
+  }
   __syncthreads();
   if (threadIdx.x < kCols) {
-    uint32_t v = 0;
+    uint32_t v = 0, s = kNoLeast;
 #pragma unroll
-    for (int i = 0; i < kRowLanes; ++i) v = max(v, at[i][threadIdx.x]);
+    for (int i = 0; i < kRowLanes; ++i) {
+      v = max(v, at[0][i][threadIdx.x]);
+      s = min(s, at[1][i][threadIdx.x]);
+    }
     const int col = ((int)blockIdx.x % tiles_n) * kCols + (int)threadIdx.x;
-    if (col < N) big[(size_t)chunk * N + col] = v;
-    if (col < N && chunk == 0) lost[col] = 0;  // for the second kernel
+    if (col < N) {
+      big[(size_t)chunk * N + col] = v;
+      least[(size_t)chunk * N + col] = s;
+      if (chunk == 0) lost[col] = 0;  // for the second kernel
+    }
   }
 }
 
@@ -336,13 +379,15 @@ __global__ __launch_bounds__(kRowThreads) void i8_column_max_kernel(
 // column.
 __global__ __launch_bounds__(kRowThreads) void i8_gradient_columns_kernel(
     const uint16_t* __restrict__ dY, const float* __restrict__ sx,
-    const uint32_t* __restrict__ big, _Float16* __restrict__ a, float* __restrict__ rs,
-    uint32_t* __restrict__ lost, int M, int N, int ld, int tiles_n, int chunks) {
+    const uint32_t* __restrict__ big, const uint32_t* __restrict__ least, LeftOperand l, int M,
+    int N, int tiles_n, int chunks) {
+  const int ld = l.ld;
   constexpr int kPairs = kChunkRows / 2 / kRowLanes;  // of a lane
   constexpr int kPitch = 64 + 1;  // dwords of a column: eight columns on are eight banks on
   __shared__ uint32_t tile[kCols * kPitch];
   __shared__ float up[kCols];
   __shared__ uint32_t units[kCols];
+  __shared__ uint64_t losing;  // a bit a column
   const int n0 = ((int)blockIdx.x % tiles_n) * kCols;
   const int m0 = (int)blockIdx.x / tiles_n * kChunkRows;
   const int c8 = (int)threadIdx.x % kColLanes, r = (int)threadIdx.x / kColLanes;
@@ -359,56 +404,84 @@ __global__ __launch_bounds__(kRowThreads) void i8_gradient_columns_kernel(
     }
   if (threadIdx.x < kCols) {
     const int col = n0 + (int)threadIdx.x;
-    uint32_t b = 0;
+    uint32_t b = 0, low = kNoLeast;
     if (col < N)
-      for (int c = 0; c < chunks; ++c) b = max(b, big[(size_t)c * N + col]);
+      for (int c = 0; c < chunks; ++c) {
+        b = max(b, big[(size_t)c * N + col]);
+        low = min(low, least[(size_t)c * N + col]);
+      }
     const PowerOfTwo f = to_fp16_range(b);
     up[threadIdx.x] = f.up;
     units[threadIdx.x] = 0;
-    if (col < N && m0 == 0) rs[col] = f.down;
+    if (col < N && m0 == 0) l.rs[col] = f.down;
+    const uint64_t some = __ballot(may_lose(low, f.up));
+    if (threadIdx.x == 0) losing = some;
   }
   __syncthreads();
   float u[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) u[e] = up[c8 * 8 + e];
-  const bool live = n0 + c8 * 8 < N;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int p = 0; p < kPairs; p += 2) {
     const int mt = m0 + 2 * p * kRowLanes;  // first of the 128 rows
     if (mt >= ld) break;                    // uniform
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float f[2][2];
-      uint32_t least = kNoLeast;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int e = 0; e < 8; ++e) {
         half2v h;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bool in = m0 + 2 * ((p + i) * kRowLanes + r) + j < M;
-          f[i][j] = in ? v[p + i][j][e] * s[p + i][j] * u[e] : 0.0f;
-          h[j] = (_Float16)f[i][j];
-          least = least_of(least, f[i][j]);
-        }
+        for (int j = 0; j < 2; ++j)
+          h[j] = m0 + 2 * ((p + i) * kRowLanes + r) + j < M
+                     ? (_Float16)(v[p + i][j][e] * s[p + i][j] * u[e])
+                     : (_Float16)0.0f;
         tile[(c8 * 8 + e) * kPitch + i * kRowLanes + r] = __builtin_bit_cast(uint32_t, h);
       }
-      if (live && may_lose(least, 1.0f))
-        add_lost(&units[c8 * 8 + e], fabsf(lost16(f[0][0])) + fabsf(lost16(f[0][1])) +
-                                         fabsf(lost16(f[1][0])) + fabsf(lost16(f[1][1])));
-    }
     __syncthreads();
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int i = 0; i < kCols; i += kRowThreads / kWaveSize) {
       const int col = i + wave, m = mt + 2 * lane;  // ld is even
       if (n0 + col < N && m < ld)
-        *reinterpret_cast<uint32_t*>(a + (size_t)(n0 + col) * ld + m) = tile[col * kPitch + lane];
+        *reinterpret_cast<uint32_t*>(l.a + (size_t)(n0 + col) * ld + m) = tile[col * kPitch + lane];
     }
     __syncthreads();
   }
-  // the loop's last barrier is behind the last addition
+  const uint64_t some = losing;
+  if (some == 0) return;  // uniform
+  // Columns that have, in this chunk or another, something to lose: all chunks write what theirs do,
+  // a lane one row, four columns at a time. (By LDS as above 11008 columns, of which 22 lose a
+  // value, took 27 us instead of 18.)
+  static_assert(kChunkRows == kRowThreads, "a row a lane");
+  const int m = m0 + (int)threadIdx.x;
+  const float f = m < M ? sx[m] : 0.0f;
+#pragma unroll 1
+  for (uint64_t left = some; left != 0;) {
+    int col[4];
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // the last again where fewer are left
+      col[i] = left != 0 || i == 0 ? __builtin_ctzll(left) : col[i ? i - 1 : 0];
+      left &= left - 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = Val<Q4_TYPE_BF16>::get(dY[(size_t)min(m, M - 1) * N + n0 + col[i]]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i > 0 && col[i] == col[i - 1]) break;  // uniform
+      const float v = m < M ? x[i] * f * up[col[i]] : 0.0f;
+      if (m < ld) l.a2[(size_t)(n0 + col[i]) * ld + m] = (uint16_t)lost_bf16(v);
+      float gone = fabsf(lost16(v));
+      if (!__any(gone > 0.0f)) continue;
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) gone += __shfl_xor(gone, o);
+      if (lane == 0) add_lost(&units[col[i]], gone);
+    }
+  }
+  lds_only_barrier();
   if (threadIdx.x < kCols && units[threadIdx.x] != 0)  // of a column before the last
-    atomicAdd(&lost[n0 + (int)threadIdx.x], units[threadIdx.x]);
+    atomicAdd(&l.lost[n0 + (int)threadIdx.x], units[threadIdx.x]);
 }
 
 // ---------------------------------------------------------------------------
@@ -444,33 +517,13 @@ __global__ __launch_bounds__(kRowThreads) void i8_finish_kernel(
   __builtin_memcpy(__builtin_assume_aligned(Y + i, sizeof(y)), y, sizeof(y));
 }
 
-// lost: what is mended of sums that need it (i8_lost.hpp), here and not split by split, where the
-// largest terms may all lie in another split
 __global__ __launch_bounds__(kRowThreads) void i8_gradient_finish_kernel(
-    const float* __restrict__ part, const float* __restrict__ rs,
-    const uint32_t* __restrict__ lost, LeftSource left, uint16_t* __restrict__ out, size_t mn,
-    int depth, int S) {
+    const float* __restrict__ part, const float* __restrict__ rs, uint16_t* __restrict__ out,
+    size_t mn, int cols, int S) {
   const size_t i = ((size_t)blockIdx.x * kRowThreads + threadIdx.x) * 4;
-  if (i - (threadIdx.x & 63) * 4 >= mn) return;  // whole waves
-  const size_t at = min(i, mn - 4);              // lanes behind the last repeat it
-  const int row = (int)(at / left.cols), col = (int)(at - (size_t)row * left.cols);
-  float4v v = sum_splits(reinterpret_cast<const float4v*>(part + at), mn / 4, S);
-  const float s = rs ? rs[row] : 1.0f;
-  const float limit = lost && i < mn ? lost_limit(lost[row]) : 0.0f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    for (uint64_t low = __ballot(fabsf(v[e]) < limit); low != 0; low &= low - 1) {
-      const int l = __builtin_ctzll(low);
-      auto of_lane = [&](auto x) {
-        return __builtin_bit_cast(decltype(x),
-                                  __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
-      };
-      const float sum = lost_sum(left, of_lane(row), 1.0f / of_lane(s), of_lane(limit),
-                                 of_lane(col) + e, 0, depth);
-      if ((int)(threadIdx.x & 63) == l) v[e] += sum;
-    }
-  }
   if (i >= mn) return;
+  const float4v v = sum_splits(reinterpret_cast<const float4v*>(part + i), mn / 4, S);
+  const float s = rs ? rs[i / cols] : 1.0f;
   uint16_t y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = (uint16_t)i8_to_bf16(v[e] * s);
@@ -485,10 +538,10 @@ void quantize(const void* X, int8_t* Q, float* scale, int M, int K, hipStream_t 
 }
 
 template <int THREADS, int V, bool LOOP>
-void gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs, uint32_t* lost,
-                   int M, int N, int ld, hipStream_t st) {
+void gradient_rows(const uint16_t* dY, const float* sw, const LeftOperand& l, int M, int N,
+                   hipStream_t st) {
   hipLaunchKernelGGL((i8_gradient_rows_kernel<THREADS, V, LOOP>), dim3(row_grid(M)),
-                     dim3(THREADS), 0, st, dY, sw, reinterpret_cast<_Float16*>(a), rs, lost, M, N, ld);
+                     dim3(THREADS), 0, st, dY, sw, l, M, N);
 }
 
 // The compiled forms of a kernel: threads, pieces of eight values a lane, passes over the data.
@@ -591,11 +644,11 @@ I8RowsPlan plan_i8_gradient_rows(int ld) {
   return {256, 4, 2};
 }
 
-hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, uint16_t* a, float* rs,
-                                   uint32_t* lost, int M, int N, int ld, hipStream_t st) {
-  const bool found = by_form(plan_i8_gradient_rows(ld), RowForms{}, [&](auto form) {
+hipError_t launch_i8_gradient_rows(const uint16_t* dY, const float* sw, const LeftOperand& l, int M,
+                                   int N, hipStream_t st) {
+  const bool found = by_form(plan_i8_gradient_rows(l.ld), RowForms{}, [&](auto form) {
     using F = decltype(form);
-    gradient_rows<F::kThreads, F::kPieces, F::kPasses == 2>(dY, sw, a, rs, lost, M, N, ld, st);
+    gradient_rows<F::kThreads, F::kPieces, F::kPasses == 2>(dY, sw, l, M, N, st);
   });
   return found ? hipGetLastError() : hipErrorInvalidValue;
 }
@@ -615,26 +668,26 @@ int i8_max_chunks(int M, int N) {
   return columns_once(M, N) ? 0 : (M + max_rows(M) - 1) / max_rows(M);
 }
 
-hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, uint16_t* a, float* rs,
-                                      uint32_t* lost, uint32_t* big, int M, int N, int ld,
-                                      hipStream_t st) {
-  const I8RowsPlan p = plan_i8_gradient_columns(M, N, ld);
+hipError_t launch_i8_gradient_columns(const uint16_t* dY, const float* sx, const LeftOperand& l,
+                                      uint32_t* scratch, int M, int N, hipStream_t st) {
+  const I8RowsPlan p = plan_i8_gradient_columns(M, N, l.ld);
   if (p.passes == 1) {
     const bool found = by_form(p, ColumnForms{}, [&](auto form) {
       using F = decltype(form);
       hipLaunchKernelGGL((i8_gradient_columns_once_kernel<F::kThreads, F::kPieces / 2>),
-                         dim3((unsigned)(N / 8)), dim3(F::kThreads), 0, st, dY, sx,
-                         reinterpret_cast<_Float16*>(a), rs, lost, M, N, ld);
+                         dim3((unsigned)(N / 8)), dim3(F::kThreads), 0, st, dY, sx, l, M, N);
     });
     return found ? hipGetLastError() : hipErrorInvalidValue;
   }
   const int tiles_n = (N + kCols - 1) / kCols, maxima = i8_max_chunks(M, N);
   const long long grid = (long long)tiles_n * ((M + kChunkRows - 1) / kChunkRows);
   if (grid > 0xffffffLL) return hipErrorInvalidValue;  // below 2^32 lanes
+  uint32_t* big = scratch;
+  uint32_t* least = scratch + (size_t)maxima * N;
   hipLaunchKernelGGL(i8_column_max_kernel, dim3((unsigned)(tiles_n * maxima)), dim3(kRowThreads), 0,
-                     st, dY, sx, big, lost, M, N, tiles_n, max_rows(M));
+                     st, dY, sx, big, least, l.lost, M, N, tiles_n, max_rows(M));
   hipLaunchKernelGGL(i8_gradient_columns_kernel, dim3((unsigned)grid), dim3(kRowThreads), 0, st,
-                     dY, sx, big, reinterpret_cast<_Float16*>(a), rs, lost, M, N, ld, tiles_n, maxima);
+                     dY, sx, big, least, l, M, N, tiles_n, maxima);
   return hipGetLastError();
 }
 
@@ -650,13 +703,12 @@ hipError_t launch_i8_finish(const int32_t* part, const float* sx, const float* s
   return hipGetLastError();
 }
 
-hipError_t launch_i8_gradient_finish(const float* part, const float* rs, const uint32_t* lost,
-                                     const LeftSource& left, uint16_t* out, int rows, int depth,
-                                     int S, hipStream_t st) {
-  const size_t mn = (size_t)rows * left.cols;
+hipError_t launch_i8_gradient_finish(const float* part, const float* rs, uint16_t* out, int rows,
+                                     int cols, int S, hipStream_t st) {
+  const size_t mn = (size_t)rows * cols;
   const unsigned grid = (unsigned)((mn / 4 + kRowThreads - 1) / kRowThreads);
-  hipLaunchKernelGGL(i8_gradient_finish_kernel, dim3(grid), dim3(kRowThreads), 0, st, part, rs,
-                     lost, left, out, mn, depth, S);
+  hipLaunchKernelGGL(i8_gradient_finish_kernel, dim3(grid), dim3(kRowThreads), 0, st, part, rs, out,
+                     mn, cols, S);
   return hipGetLastError();
 }
 

@@ -1,9 +1,11 @@
 """Gradients of the 8-bit product whose terms lie far apart: results that rest on terms far below
 their row's largest, because the largest meet zeros, are as near as any other.
 
-The bound holds no part of a row's largest value: each term within half a step of fp16 of itself,
-what lies below fp16's range within as much of a result's terms together, sums in fp32 and the
-result's rounding to bf16. Terms stay above 2^-139 of a row's largest, the documented limit."""
+The bound holds no part of a row's largest value: each term within half a step of fp16 of itself;
+what fp16 loses of terms below 2^-27 of their row's largest (its normal range ends there at the
+latest) either left out, where it is as little of a result's terms together, or within half a step
+of bf16 of itself, which is at most that of the term; sums in fp32 and the result's rounding to
+bf16. Terms stay above 2^-139 of a row's largest, the documented limit."""
 import numpy as np
 import pytest
 import torch
@@ -29,7 +31,9 @@ def near(t, b):
     b = b.astype(np.float64)
     v, size = t @ b, np.abs(t) @ np.abs(b)
     # the product dY * scale in fp32, the rounding to fp16, what falls below it, fp32 sums
+    small = np.where(np.abs(t) < 2.0 ** -27 * np.abs(t).max(axis=1, keepdims=True), np.abs(t), 0)
     e = (ref.E32 + 2 * ref.E16 * (1 + ref.E32) + (t.shape[1] + 16) * ref.E32 * (1 + 2 * ref.E16)) * size
+    e += ref.EBF * (1 + ref.E32) * (small @ np.abs(b))
     rel, sub = ref.HALF_STEP["bf16"]
     return v, e + rel * (np.abs(v) + e) + sub
 
@@ -129,18 +133,36 @@ def test_far_terms_stay_with_their_row(rows, depth, cols):
                                              (264, 512, 1040), (136, 8200, 272)])
 def test_dead_channels(rows, depth, cols, gap):
     """Columns of zeros beside others, under rows with far terms: exact zeros, and their neighbours
-    what they are without them."""
+    within the bound."""
     from moe_experts_amd import i8_gemm_backward, i8_gemm_backward_weight
     v, large = spread(12, rows, depth, gap)
     B = operand(13, depth, cols, large)
     dead = datagen.rng(14).random(cols) < 0.3
     dead[[0, cols - 1]] = True
-    D = B.copy()
-    D[:, dead] = 0
-    s = to_dev(np.exp(datagen.rng(15).standard_normal(depth) - 4).astype(np.float32))
-    calls = [lambda b: i8_gemm_backward(bf16(v), to_dev(b), s)]
+    B[:, dead] = 0
+    s = np.exp(datagen.rng(15).standard_normal(depth) - 4).astype(np.float32)
+    dY = bf16(v)
+    want = near(host(dY).astype(np.float64) * s.astype(np.float64), B)
+    results = [i8_gemm_backward(dY, to_dev(B), to_dev(s))]
     if rows % 8 == 0:
-        calls.append(lambda b: i8_gemm_backward_weight(bf16(v.T), to_dev(b), s))
-    for call in calls:
-        was, got = host(call(B)), host(call(D))
-        assert not got[:, dead].any() and np.array_equal(got[:, ~dead], was[:, ~dead])
+        results.append(i8_gemm_backward_weight(dY.T.contiguous(), to_dev(B), to_dev(s)))
+    for got in map(host, results):
+        ref.check(got, want)
+        assert not got[:, dead].any()
+
+
+def test_all_results_rest_on_far_terms():
+    """A token whose row is zeros, 2^40 above the rest in the gradient: every result of both kernels
+    rests on what fp16 loses, and takes the contraction twice, not more."""
+    from moe_experts_amd import i8_gemm_backward_weight
+    for M, N, K in ((777, 1536, 1040), (1999, 16, 272), (9001, 72, 272)):
+        r = datagen.rng(16)
+        X = r.integers(-127, 128, (M, K)).astype(np.int8)
+        X[M // 2] = 0
+        v = r.standard_normal((M, N))
+        v[M // 2] *= 2.0 ** 40
+        sx = np.exp(r.standard_normal(M) - 4).astype(np.float32)
+        dY = bf16(v)
+        got = host(i8_gemm_backward_weight(dY, to_dev(X), to_dev(sx)))
+        t = np.ascontiguousarray((host(dY).astype(np.float64) * sx.astype(np.float64)[:, None]).T)
+        ref.check(got, near(t, X))
