@@ -8,7 +8,8 @@
 // scaled row by row of C and rounded to fp16 as for the tiles, in LDS with c contiguous. Its
 // waves then share out the rows of B: each multiplies steps of 32 by v_mfma_f32_16x16x32_f16,
 // copied memory -> LDS several steps ahead into a part of its own, and their sums meet in LDS,
-// in the order of the waves.
+// in the order of the waves. Where a result may rest on what the rounding of A has lost, the
+// workgroup goes over the contraction a second time with that in A's place (i8_lost.hpp).
 //
 // A contraction of up to 2048 (4096 with up to 8 rows) fits a workgroup of eight waves; a longer
 // one (of the weights' gradient) is split over workgroups of four waves and half as much, two

@@ -18,7 +18,7 @@
 //
 // Rows whose values lie near one another pay for the search alone, old and new in us: 2048 rows of
 // 4096 x 11008 193.5 and 195.4 (input), 205.4 and 209.8 (weights), 150 rows of 11008 x 4096 29.7 and
-// 30.1, 777 rows of 5120 x 1536 26.2 and 27.4, rank 16 of 1999 rows 9.6 and 10.1; channels of zeros
+// 30.1, 777 rows of 5120 x 1536 26.2 and 27.2, rank 16 of 1999 rows 9.6 and 10.1; channels of zeros
 // cost nothing more. One token 2^40 above the rest: weights of 4096 x 11008 over 2048 rows 171 and
 // 421, 5120 x 1536 over 777 26.0 and 58.2. Gradients of a softmax over 32000 channels, 2048 rows of
 // 4096, whose values cover hundreds of binades (logits of standard deviation 5 and 9): input 554 and

@@ -302,7 +302,9 @@ __global__ __launch_bounds__(THREADS) void i8_gradient_columns_once_kernel(
       add_lost(&units[e], gone);
     }
   lds_only_barrier();
-  if (t < 8) l.lost[n + t] = units[t];
+  const uint32_t sum = units[lane & 7];
+  if (t < 8) l.lost[n + t] = sum;
+  if (!__any(sum != 0)) return;  // the same in all waves
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     if (units[e] == 0) continue;  // uniform

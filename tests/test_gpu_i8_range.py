@@ -12,7 +12,8 @@ import torch
 
 from moe_experts_amd import datagen
 from tests import i8_ref as ref
-from tests.gpu_util import dev, to_dev
+from tests.gpu_util import (dev, guarded, guarded_ws, guards_intact, to_dev,
+                            ws_guards_intact)
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +167,85 @@ def test_all_results_rest_on_far_terms():
         got = host(i8_gemm_backward_weight(dY, to_dev(X), to_dev(sx)))
         t = np.ascontiguousarray((host(dY).astype(np.float64) * sx.astype(np.float64)[:, None]).T)
         ref.check(got, near(t, X))
+
+
+@pytest.mark.parametrize("rows,depth,cols", [(8, 4096, 272), (40, 1000, 272), (40, 4104, 272),
+                                             (72, 2056, 4112), (136, 8200, 272), (4112, 264, 144),
+                                             (2104, 72, 8208), (264, 131, 4112)])
+def test_memory_around_is_left_alone(rows, depth, cols):
+    """The second left operand is written and read within the workspace, whatever that holds before;
+    results are bitwise those of another."""
+    import moe_experts_amd as q4
+    v, large = spread(17, rows, depth, "all")
+    B = to_dev(operand(18, depth, cols, large))
+    s = to_dev(np.exp(datagen.rng(19).standard_normal(depth) - 4).astype(np.float32))
+    forms = [("i8_gemm_backward", bf16(v), (rows, depth, cols), "dX")] if depth % 8 == 0 else []
+    forms.append(("i8_gemm_backward_weight", bf16(v.T), (depth, rows, cols), "dW"))
+    for form, dY, (M, N, K), out in forms:
+        if N % 8:
+            continue
+        need = getattr(q4, form + "_workspace_bytes")(M, N, K)
+        seen = []
+        for fill in (0xFF, 0x00):
+            full, y = guarded(rows * cols, torch.bfloat16, fill=7.0)
+            wfull, ws = guarded_ws(need, fill=fill)
+            getattr(q4, form)(dY, B, s, **{out: y.view(rows, cols)}, ws=ws)
+            seen.append(y.clone())
+            assert guards_intact(full, rows * cols, fill=7.0)
+            assert ws_guards_intact(wfull, need, fill=fill)
+        assert torch.equal(*seen)
+
+
+@pytest.mark.parametrize("rows,depth,cols", [(8, 4096, 272), (40, 4104, 272), (264, 512, 1040),
+                                             (136, 8200, 272)])
+def test_replays_with_and_without_far_terms(rows, depth, cols):
+    """A captured call whose inputs come to have far terms, lose them and have them again: every
+    replay is the eager call, bitwise."""
+    from moe_experts_amd import i8_gemm_backward, i8_gemm_backward_weight
+    v, large = spread(20, rows, depth, 40)
+    plain = np.where(np.abs(v) < 2.0 ** -20, v * 2.0 ** 40, v)
+    B = to_dev(operand(21, depth, cols, large))
+    s = to_dev(np.exp(datagen.rng(22).standard_normal(depth) - 4).astype(np.float32))
+    inputs = [bf16(plain), bf16(v)]
+    dY = inputs[0].clone()
+    dYt = dY.T.contiguous()
+    dX = torch.zeros((rows, cols), dtype=torch.bfloat16, device=dev())
+    dW = torch.zeros_like(dX)
+
+    def call():
+        i8_gemm_backward(dY, B, s, dX=dX)
+        i8_gemm_backward_weight(dYt, B, s, dW=dW)
+
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for which in (1, 0, 1, 1, 0):
+        dY.copy_(inputs[which])
+        dYt.copy_(inputs[which].T)
+        dX.fill_(77)
+        dW.fill_(77)
+        g.replay()
+        got = dX.clone(), dW.clone()
+        call()
+        assert torch.equal(got[0], dX) and torch.equal(got[1], dW)
+
+
+@pytest.mark.parametrize("rows,depth,cols", [(8, 4096, 272), (40, 1000, 272), (40, 4104, 272),
+                                             (264, 512, 1040), (136, 8200, 272)])
+def test_broken_rows_beside_far_terms(rows, depth, cols):
+    """Rows with an infinity or a NaN among rows with far terms: none of their results is finite, and
+    the others are what they were."""
+    from moe_experts_amd import i8_gemm_backward, i8_gemm_backward_weight
+    v, large = spread(23, rows, depth, "all")
+    B = to_dev(operand(24, depth, cols, large))
+    s = to_dev(np.exp(datagen.rng(25).standard_normal(depth) - 4).astype(np.float32))
+    broken = v.copy()
+    broken[2, depth // 2], broken[5, 0] = np.inf, np.nan
+    keep = [i for i in range(rows) if i not in (2, 5)]
+    for call in (lambda a: i8_gemm_backward(bf16(a), B, s),
+                 lambda a: i8_gemm_backward_weight(bf16(a.T), B, s)):
+        was, got = call(v), call(broken)
+        assert torch.equal(got[keep], was[keep])
+        assert not torch.isfinite(got[[2, 5]].float()).any()
